@@ -12,6 +12,8 @@
  *   pa_mla_absorb_q                MLA: absorbed query [W_UK_h q_nope | q_pe]
  *   pa_mla_decode_attention        MLA: decode attention over the paged latent cache
  *   pa_mla_project_out             MLA: latent output times W_UV_h
+ *   pa_reshape_and_cache_q4        scatter per-token K/V into a 4-bit paged cache
+ *   pa_gather_cache_q4             read 4-bit cache rows back as bf16, fp16 or fp32
  *
  * Common rules
  *   - Every pointer argument except the `*_host` ones is a DEVICE pointer on
@@ -58,7 +60,8 @@ typedef enum {
   PA_BF16 = 0,
   PA_FP16 = 1,
   PA_FP32 = 2,
-  PA_FP8_E4M3 = 3 /* OCP FP8 E4M3 (max 448, no inf, 0x7F/0xFF NaN) */
+  PA_FP8_E4M3 = 3, /* OCP FP8 E4M3 (max 448, no inf, 0x7F/0xFF NaN) */
+  PA_Q4 = 4        /* rows of 4-bit groups (pa_reshape_and_cache_q4); only where a call says so */
 } pa_dtype;
 
 /* Bits of the device-side error word (first 4 bytes of a decode workspace). */
@@ -434,6 +437,73 @@ pa_status pa_mla_decode_attention(void *out_latent, const void *q_latent,
 pa_status pa_mla_project_out(void *out, const void *out_latent, const void *w_uv,
                              int32_t num_seqs, int32_t num_heads, int32_t latent_dim,
                              int32_t v_head_dim, pa_stream_t stream);
+
+/* ========================================================================
+ * A long context in less memory: the 4-bit cache, and eviction
+ *
+ * No counterpart in the paper's pages: they hold K/V at 16 or 8 bits and
+ * keep every token.  The paged layout, slot mapping and block tables are
+ * theirs.
+ *
+ * 4-bit rows (PA_Q4).  A kv head's row of head_size elements is cut into
+ * groups of 32 consecutive elements.  Per group, in fp32:
+ *     m    = fp16(min x), saturated to +-65504
+ *     s    = fp16(clamp((max x - m) / 15, 0, 1023))
+ *     code = clamp(rne((x - m) / s), 0, 15)          (0 where s = 0)
+ * (all IEEE, round to nearest even) and an element stands for m + s * code.
+ * A span (max x - m) above 1023 * 15 saturates.  A group that holds a NaN or an
+ * infinity stands for NaN in all its elements (s and m are stored as NaN).
+ * The row's bytes: head_size / 2 code bytes (element 2i in the low, 2i + 1
+ * in the high nibble of byte i), then head_size / 32 pairs (s, m) of fp16:
+ * 5 * head_size / 8 bytes (80 for head_size 128, 0.31 of bf16).
+ * ====================================================================== */
+
+/* ------------------------------------------------------------------------
+ * pa_reshape_and_cache_q4 -- pa_reshape_and_cache into a 4-bit cache.
+ *
+ * Slots, the SWA table and skips as in pa_reshape_and_cache.
+ * key, value: [num_tokens, num_heads, head_size] of src_dtype (PA_BF16,
+ *   PA_FP16 or PA_FP32), key_stride/value_stride elements between tokens;
+ *   value and value_cache may both be NULL (K-only).
+ * key_cache, value_cache: [num_blocks, block_size, num_heads,
+ *   5 * head_size / 8] bytes, block_stride BYTES between blocks, the rest
+ *   contiguous.
+ * head_size: a multiple of 32.  Alignment: key/value/caches 16-byte
+ *   aligned; key_stride and value_stride multiples of 8 elements,
+ *   block_stride a multiple of 4 bytes.
+ * Errors: PA_ERR_INVALID, PA_ERR_UNSUPPORTED (dtype, head_size),
+ *   PA_ERR_ALIGN, PA_ERR_CUDA.
+ * ---------------------------------------------------------------------- */
+pa_status pa_reshape_and_cache_q4(const void *key, const void *value, pa_dtype src_dtype,
+                                  int64_t num_tokens, int32_t num_heads, int32_t head_size,
+                                  int64_t key_stride, int64_t value_stride, void *key_cache,
+                                  void *value_cache, int64_t num_blocks, int32_t block_size,
+                                  int64_t block_stride, const int64_t *slot_mapping,
+                                  const int64_t *swa_slot_mapping, int64_t swa_len,
+                                  pa_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * pa_gather_cache_q4 -- read rows of a 4-bit cache back.
+ *
+ * For every t with 0 <= s = slot_mapping[t] < num_blocks * block_size:
+ *     key[t, h, i] = cast(m + s * code)  of  key_cache[slot s, head h]
+ * and the same for value; other rows of key and value are left as they
+ * were.  The value is formed in fp32 with one rounding (a fused multiply-
+ * add) and cast to dst_dtype (PA_BF16, PA_FP16 or PA_FP32) by round to
+ * nearest even.  This is how a cached prefix is handed to the prefill
+ * attention, which reads a bf16 cache: rows gathered to consecutive t are a
+ * [num_blocks, block_size, num_heads, head_size] cache with an identity
+ * block table.
+ * key, value: [num_tokens, num_heads, head_size], key_stride/value_stride
+ *   elements between tokens.  value and value_cache may both be NULL.
+ * Other arguments, alignment and errors as for pa_reshape_and_cache_q4.
+ * ---------------------------------------------------------------------- */
+pa_status pa_gather_cache_q4(void *key, void *value, pa_dtype dst_dtype, int64_t num_tokens,
+                             int32_t num_heads, int32_t head_size, int64_t key_stride,
+                             int64_t value_stride, const void *key_cache,
+                             const void *value_cache, int64_t num_blocks, int32_t block_size,
+                             int64_t block_stride, const int64_t *slot_mapping,
+                             pa_stream_t stream);
 
 /* Diagnostic of the failure path every pipeline kernel shares: launches one
  * CTA whose threads wait, with the same bounded wait the pipelines use, on a

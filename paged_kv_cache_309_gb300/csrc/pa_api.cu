@@ -84,6 +84,44 @@ pa_status check_decode(void* out, const void* q, const void* k_cache, const void
   return PA_OK;
 }
 
+// Checks shared by the 4-bit cache's write and gather; fills *a on PA_OK
+// (num_tokens 0 returns PA_OK with nothing to launch).
+pa_status check_q4(const void* key, const void* value, pa_dtype dtype, int64_t num_tokens,
+                   int32_t num_heads, int32_t head_size, int64_t key_stride, int64_t value_stride,
+                   const void* key_cache, const void* value_cache, int64_t num_blocks,
+                   int32_t block_size, int64_t block_stride, const int64_t* slot_mapping,
+                   pa_detail::Q4CacheArgs* a) {
+  if (num_tokens < 0 || num_heads <= 0 || head_size <= 0 || block_size <= 0 || num_blocks < 0)
+    return PA_ERR_INVALID;
+  if (num_tokens == 0) return PA_OK;  // nothing to do; pointers may be null
+  if (key == nullptr || key_cache == nullptr || slot_mapping == nullptr) return PA_ERR_INVALID;
+  if ((value == nullptr) != (value_cache == nullptr)) return PA_ERR_INVALID;
+  if (!is_src_dtype(dtype) || head_size % 32 != 0) return PA_ERR_UNSUPPORTED;
+  const int64_t row = static_cast<int64_t>(num_heads) * head_size;
+  if (row >= (1ll << 31)) return PA_ERR_UNSUPPORTED;
+  if (key_stride % 8 != 0 || (value && value_stride % 8 != 0) || block_stride % 4 != 0)
+    return PA_ERR_ALIGN;
+  if (num_tokens > 1 && (key_stride < row || (value && value_stride < row))) return PA_ERR_INVALID;
+  if (num_blocks > 1 && block_stride < row / 8 * 5 * block_size) return PA_ERR_INVALID;
+  if (!aligned(key, 16) || !aligned(key_cache, 16) || !aligned(value, 16) ||
+      !aligned(value_cache, 16))
+    return PA_ERR_ALIGN;
+  a->key = key;
+  a->value = value;
+  a->key_cache = const_cast<void*>(key_cache);
+  a->value_cache = const_cast<void*>(value_cache);
+  a->slot_mapping = slot_mapping;
+  a->num_tokens = num_tokens;
+  a->key_stride = key_stride;
+  a->value_stride = value ? value_stride : 0;
+  a->block_stride = block_stride;
+  a->num_slots = num_blocks * block_size;
+  a->row_chunks = static_cast<int32_t>(row / 8);
+  a->chunks_per_head = head_size / 8;
+  a->block_size = block_size;
+  return PA_OK;
+}
+
 // One CTA waits on a barrier nothing arrives on: the bounded wait gives up
 // after its limit and the error bit is set, as in any pipeline kernel.
 __global__ void selftest_bounded_wait_kernel(unsigned* err) {
@@ -504,6 +542,38 @@ pa_status pa_mla_project_out(void* out, const void* out_latent, const void* w_uv
   if (!aligned(out, 16) || !aligned(out_latent, 16) || !aligned(w_uv, 16)) return PA_ERR_ALIGN;
   return pa_detail::launch_mla_project_out(out, out_latent, w_uv, num_seqs, num_heads, latent_dim,
                                            v_head_dim, reinterpret_cast<cudaStream_t>(stream));
+}
+
+pa_status pa_reshape_and_cache_q4(const void* key, const void* value, pa_dtype src_dtype,
+                                  int64_t num_tokens, int32_t num_heads, int32_t head_size,
+                                  int64_t key_stride, int64_t value_stride, void* key_cache,
+                                  void* value_cache, int64_t num_blocks, int32_t block_size,
+                                  int64_t block_stride, const int64_t* slot_mapping,
+                                  const int64_t* swa_slot_mapping, int64_t swa_len,
+                                  pa_stream_t stream) {
+  if (swa_slot_mapping != nullptr && swa_len < 0) return PA_ERR_INVALID;
+  pa_detail::Q4CacheArgs a{};
+  const pa_status st =
+      check_q4(key, value, src_dtype, num_tokens, num_heads, head_size, key_stride, value_stride,
+               key_cache, value_cache, num_blocks, block_size, block_stride, slot_mapping, &a);
+  if (st != PA_OK || num_tokens == 0) return st;
+  a.swa = swa_slot_mapping;
+  a.swa_len = swa_slot_mapping ? swa_len : 0;
+  return pa_detail::launch_reshape_and_cache_q4(a, src_dtype,
+                                                reinterpret_cast<cudaStream_t>(stream));
+}
+
+pa_status pa_gather_cache_q4(void* key, void* value, pa_dtype dst_dtype, int64_t num_tokens,
+                             int32_t num_heads, int32_t head_size, int64_t key_stride,
+                             int64_t value_stride, const void* key_cache, const void* value_cache,
+                             int64_t num_blocks, int32_t block_size, int64_t block_stride,
+                             const int64_t* slot_mapping, pa_stream_t stream) {
+  pa_detail::Q4CacheArgs a{};
+  const pa_status st =
+      check_q4(key, value, dst_dtype, num_tokens, num_heads, head_size, key_stride, value_stride,
+               key_cache, value_cache, num_blocks, block_size, block_stride, slot_mapping, &a);
+  if (st != PA_OK || num_tokens == 0) return st;
+  return pa_detail::launch_gather_cache_q4(a, dst_dtype, reinterpret_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

@@ -562,6 +562,29 @@ struct ReshapeArgs {
 pa_status launch_reshape_and_cache(const ReshapeArgs& a, pa_dtype src, pa_dtype dst,
                                    cudaStream_t stream);
 
+// 4-bit cache (cache_q4.cu): the write reads key/value and fills the caches,
+// the gather reads the caches and fills key/value.
+struct Q4CacheArgs {
+  const void* key;
+  const void* value;  // null: K only
+  void* key_cache;
+  void* value_cache;
+  const int64_t* slot_mapping;
+  const int64_t* swa;
+  int64_t swa_len;
+  int64_t num_tokens;
+  int64_t key_stride;    // elements
+  int64_t value_stride;  // elements
+  int64_t block_stride;  // bytes
+  int64_t num_slots;
+  int32_t row_chunks;       // (num_heads * head_size) / 8
+  int32_t chunks_per_head;  // head_size / 8
+  int32_t block_size;
+  int32_t groups;  // warps per token (set by the launcher)
+};
+pa_status launch_reshape_and_cache_q4(Q4CacheArgs a, pa_dtype src, cudaStream_t stream);
+pa_status launch_gather_cache_q4(Q4CacheArgs a, pa_dtype dst, cudaStream_t stream);
+
 struct ConcatArgs {
   void* k;
   const void* k_nope;

@@ -18,7 +18,7 @@ LIB_PATH = os.path.join(HERE, "libpa.so")
 HEADER = os.path.join(os.path.dirname(HERE), "include", "pa.h")
 
 PA_OK, PA_ERR_INVALID, PA_ERR_UNSUPPORTED, PA_ERR_ALIGN, PA_ERR_WORKSPACE, PA_ERR_CUDA = range(6)
-PA_BF16, PA_FP16, PA_FP32, PA_FP8_E4M3 = range(4)
+PA_BF16, PA_FP16, PA_FP32, PA_FP8_E4M3, PA_Q4 = range(5)
 PA_DEVERR_WAIT_TIMEOUT = 0x1
 PA_DEVERR_CONTEXT_CLIPPED = 0x2
 PA_DEVERR_SLOT_MISMATCH = 0x4
@@ -88,6 +88,11 @@ def _load():
     lib.pa_mla_project_out.restype = E
     lib.pa_selftest_bounded_wait.argtypes = [P, P]
     lib.pa_selftest_bounded_wait.restype = E
+    lib.pa_reshape_and_cache_q4.argtypes = [P, P, E, I64, I32, I32, I64, I64, P, P, I64, I32, I64,
+                                            P, P, I64, P]
+    lib.pa_reshape_and_cache_q4.restype = E
+    lib.pa_gather_cache_q4.argtypes = [P, P, E, I64, I32, I32, I64, I64, P, P, I64, I32, I64, P, P]
+    lib.pa_gather_cache_q4.restype = E
     _lib = lib
     return lib
 
@@ -514,3 +519,72 @@ def pa_mla_project_out(out, out_latent, w_uv, stream=None):
     _need(out.shape[:2] == (B, H) and w_uv.shape == (dc, H * dv), "shape mismatch")
     _check(_load().pa_mla_project_out(_ptr(out), _ptr(out_latent), _ptr(w_uv), B, H, dc, dv,
                                       _stream(stream)), "pa_mla_project_out")
+
+
+# ------------------------------------------------------------ 4-bit cache --
+def q4_row_bytes(head_size):
+    """Bytes of a kv head's row in a 4-bit cache: head_size / 2 of codes, then
+    an fp16 (scale, minimum) pair for each group of 32 elements."""
+    if head_size <= 0 or head_size % 32 != 0:
+        raise ValueError("head_size must be a multiple of 32")
+    return 5 * head_size // 8
+
+
+def _q4_shapes(key, value, key_cache, value_cache, slot_mapping):
+    """Checks shared by the 4-bit write and gather: (N, H, d, num_blocks, bs)."""
+    N, H, d = key.shape
+    for t, name in ((key, "key"), (value, "value")):
+        if t is not None and (t.shape != key.shape or t.dtype != key.dtype or t.stride(2) != 1
+                              or t.stride(1) != d):
+            raise ValueError(f"{name}: [N, H, d] with heads and elements contiguous expected")
+    if (value is None) != (value_cache is None):
+        raise ValueError("give both value and value_cache, or neither")
+    nb, bs, Hc, rb = key_cache.shape
+    if key_cache.dtype != torch.uint8 or (Hc, rb) != (H, q4_row_bytes(d)) \
+            or key_cache.stride(3) != 1 or key_cache.stride(2) != rb \
+            or key_cache.stride(1) != H * rb:
+        raise ValueError("key_cache must be uint8 [num_blocks, bs, H, 5 * d / 8], contiguous "
+                         "inside a block")
+    if value_cache is not None and (value_cache.shape != key_cache.shape
+                                    or value_cache.stride() != key_cache.stride()
+                                    or value_cache.dtype != key_cache.dtype):
+        raise ValueError("value_cache must match key_cache")
+    if slot_mapping.dtype != torch.int64 or slot_mapping.numel() != N \
+            or not slot_mapping.is_contiguous():
+        raise ValueError("slot_mapping must be int64 [N]")
+    return N, H, d, nb, bs
+
+
+def pa_reshape_and_cache_q4(key, value, key_cache, value_cache, slot_mapping,
+                            swa_slot_mapping=None, stream=None):
+    """key/value [N, H, d] (token stride free) quantised into 4-bit caches
+    uint8 [num_blocks, bs, H, 5 * d / 8] (block stride free); slot_mapping [N]
+    int64, optional swa table int64.  value and value_cache may be None."""
+    _on_device(key=key, value=value, key_cache=key_cache, value_cache=value_cache,
+               slot_mapping=slot_mapping, swa_slot_mapping=swa_slot_mapping)
+    N, H, d, nb, bs = _q4_shapes(key, value, key_cache, value_cache, slot_mapping)
+    swa_len = 0
+    if swa_slot_mapping is not None:
+        if swa_slot_mapping.dtype != torch.int64 or not swa_slot_mapping.is_contiguous():
+            raise ValueError("swa_slot_mapping must be int64, contiguous")
+        swa_len = swa_slot_mapping.numel()
+    st = _load().pa_reshape_and_cache_q4(
+        _ptr(key), _ptr(value), _dtype(key), N, H, d, key.stride(0),
+        0 if value is None else value.stride(0), _ptr(key_cache), _ptr(value_cache), nb, bs,
+        key_cache.stride(0), _ptr(slot_mapping), _ptr(swa_slot_mapping), swa_len,
+        _stream(stream))
+    _check(st, "pa_reshape_and_cache_q4")
+
+
+def pa_gather_cache_q4(key, value, key_cache, value_cache, slot_mapping, stream=None):
+    """key/value [N, H, d] bf16, fp16 or fp32 (written) <- the rows of the
+    4-bit caches at slot_mapping [N] int64; rows of negative or out-of-pool
+    slots are left as they were.  value and value_cache may be None."""
+    _on_device(key=key, value=value, key_cache=key_cache, value_cache=value_cache,
+               slot_mapping=slot_mapping)
+    N, H, d, nb, bs = _q4_shapes(key, value, key_cache, value_cache, slot_mapping)
+    st = _load().pa_gather_cache_q4(
+        _ptr(key), _ptr(value), _dtype(key), N, H, d, key.stride(0),
+        0 if value is None else value.stride(0), _ptr(key_cache), _ptr(value_cache), nb, bs,
+        key_cache.stride(0), _ptr(slot_mapping), _stream(stream))
+    _check(st, "pa_gather_cache_q4")
