@@ -14,6 +14,7 @@
  *   pa_mla_project_out             MLA: latent output times W_UV_h
  *   pa_reshape_and_cache_q4        scatter per-token K/V into a 4-bit paged cache
  *   pa_gather_cache_q4             read 4-bit cache rows back as bf16, fp16 or fp32
+ *   pa_paged_decode_attention_q4   decode attention over a 4-bit cache
  *
  * Common rules
  *   - Every pointer argument except the `*_host` ones is a DEVICE pointer on
@@ -504,6 +505,29 @@ pa_status pa_gather_cache_q4(void *key, void *value, pa_dtype dst_dtype, int64_t
                              const void *value_cache, int64_t num_blocks, int32_t block_size,
                              int64_t block_stride, const int64_t *slot_mapping,
                              pa_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * pa_paged_decode_attention_q4 -- decode attention over a 4-bit cache.
+ *
+ * The attention of pa_paged_decode_attention with K and V the values that
+ * the 4-bit rows stand for.  k_cache, v_cache: [num_blocks, block_size,
+ * num_kv_heads, 80] bytes, contiguous, 16-byte aligned.  Other arguments,
+ * limits, the workspace (pa_paged_decode_workspace_size) and the error word
+ * as for pa_paged_decode_attention.  q values must be finite.  A token whose
+ * row stands for NaN makes the outputs of its heads NaN.
+ * Numerics: scores in fp32 from exact products of the codes with q (q in
+ * fp16 after a power-of-two prescale: exact, but for elements below 2^-24
+ * of a head's largest); fp32 softmax; the weights and s * code enter the
+ * weighted sum rounded to fp16, the sum is fp32.
+ * ---------------------------------------------------------------------- */
+pa_status pa_paged_decode_attention_q4(void *out, const void *q, const void *k_cache,
+                                       const void *v_cache, const int32_t *block_tables,
+                                       const int32_t *context_lens, int32_t num_seqs,
+                                       int32_t num_q_heads, int32_t num_kv_heads,
+                                       int32_t head_size, int32_t block_size,
+                                       int32_t max_blocks_per_seq, int64_t num_blocks,
+                                       float scale, int32_t max_context_len, void *workspace,
+                                       size_t workspace_bytes, pa_stream_t stream);
 
 /* Diagnostic of the failure path every pipeline kernel shares: launches one
  * CTA whose threads wait, with the same bounded wait the pipelines use, on a

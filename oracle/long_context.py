@@ -13,7 +13,7 @@ GROUP = 32
 def q4_quantise(x):
     """uint8 rows [..., 5 * d / 8] of float32 values x [..., d]."""
     x = np.asarray(x, np.float32)
-    g = x.reshape(*x.shape[:-1], -1, GROUP)
+    g = x.reshape(*x.shape[:-1], x.shape[-1] // GROUP, GROUP)
     bad = ~np.isfinite(g).all(-1)
     g = np.where(bad[..., None], np.float32(0), g)
     m = np.clip(g.min(-1), np.float32(-65504), np.float32(65504)).astype(np.float16)
@@ -26,7 +26,7 @@ def q4_quantise(x):
     m = np.where(bad, np.float16(np.nan), m)
     code = np.where(bad[..., None], 0, code).astype(np.uint8).reshape(x.shape)
     packed = code[..., 0::2] | (code[..., 1::2] << 4)
-    pairs = np.stack([s, m], -1).reshape(*x.shape[:-1], -1)
+    pairs = np.stack([s, m], -1).reshape(*x.shape[:-1], x.shape[-1] // GROUP * 2)
     return np.concatenate([packed, pairs.view(np.uint8)], -1)
 
 

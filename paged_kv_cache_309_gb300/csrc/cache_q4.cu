@@ -21,17 +21,6 @@ constexpr int kWarps = 8;
 constexpr int kChunksPerLane = 4;
 constexpr int kChunksPerWarp = 32 * kChunksPerLane;
 
-__device__ __forceinline__ float min_nan(float a, float b) {
-  float d;
-  asm("min.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
-  return d;
-}
-__device__ __forceinline__ float max_nan(float a, float b) {
-  float d;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
-  return d;
-}
-
 // Byte offsets of chunk c of a row (head c / cph): its codes and its group's
 // (s, m) pair.
 struct RowPlace {

@@ -43,60 +43,15 @@
 #include <atomic>
 #include <cmath>
 
-#include "pa_internal.cuh"
+#include "decode_common.cuh"
 
 namespace pa_detail {
 namespace {
 
 using namespace pa;
 
-constexpr int kD = 128;                 // head size handled by this kernel
 constexpr int kTile = 64;               // tokens per pipeline stage
-constexpr int kConsumerWarps = 4;
-constexpr int kThreads = (kConsumerWarps + 1) * 32;
 constexpr int kRowBytes = kD * 2;       // one bf16 row of one KV head (tensor map stride)
-constexpr float kRescaleLog2 = 8.0f;    // lazy-rescale threshold (base-2 units)
-constexpr size_t kWorkspaceHeader = 256;  // error word + padding
-
-struct DecodeParams {
-  __nv_bfloat16* out;
-  const __nv_bfloat16* q;
-  const int32_t* block_tables;
-  const int32_t* context_lens;
-  float* ws_lse;
-  float* ws_o;
-  unsigned* counters;  // [B, H_KV] split arrivals, zero between calls
-  unsigned* err;
-  int64_t num_blocks;
-  int32_t num_q_heads;
-  int32_t num_kv_heads;
-  int32_t block_size;
-  int32_t log2_bs;
-  int32_t max_blocks_per_seq;
-  int32_t num_splits;
-  int32_t tokens_per_split;
-  float scale_log2;
-  const float* k_scale;  // quantised cache: code * k_scale is the value (else null)
-  const float* v_scale;
-  // fused decode step (else null): each sequence's newest K/V row
-  // [B, H_KV, d] bf16, written at slot_mapping[b] before it is attended to
-  const __nv_bfloat16* new_k;
-  const __nv_bfloat16* new_v;
-  const int64_t* slot_mapping;
-  void* k_cache;
-  void* v_cache;
-};
-
-
-// context length used by both kernels: clipped to the plan and the table
-__device__ __forceinline__ int effective_len(const DecodeParams& p, int b, bool* clipped) {
-  int L = __ldg(p.context_lens + b);
-  L = L < 0 ? 0 : L;
-  const int64_t cap = min(static_cast<int64_t>(p.max_blocks_per_seq) * p.block_size,
-                          static_cast<int64_t>(p.num_splits) * p.tokens_per_split);
-  *clipped = static_cast<int64_t>(L) > cap;
-  return *clipped ? static_cast<int>(cap) : L;
-}
 
 // ===================================================== tensor-core consumer
 // The same split kernel with the grouped products on the tensor cores
@@ -126,61 +81,6 @@ struct TcLayout {
   static constexpr int kBytes = kBarOffset + 3 * kStages * 8 + 16;  // full, empty, mask, flags
   static constexpr int kAlloc = kBytes + 1024;  // room to align the base to 1 KB
 };
-
-// Merge of one (sequence, query head) by one warp: weights 2^(lse_s - max)
-// over the n splits that hold tokens, out = sum_s w_s o_s / sum_s w_s,
-// rounded to bf16.  Partials are read through L2 (__ldcg): other CTAs wrote
-// them during this launch.
-__device__ __forceinline__ void merge_splits_warp(const DecodeParams& p, int64_t bh, int n,
-                                                  int lane) {
-  const float* lse = p.ws_lse + bh * p.num_splits;
-  const float* o = p.ws_o + bh * p.num_splits * kD;
-  float M = -INFINITY;
-  for (int s = lane; s < n; s += 32) M = fmaxf(M, __ldcg(lse + s));
-#pragma unroll
-  for (int off = 16; off >= 1; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  float W = 0.f;
-  if (M != -INFINITY) {
-    for (int s0 = 0; s0 < n; s0 += 32) {
-      const int my = s0 + lane;
-      const float wl = my < n ? exp2f(__ldcg(lse + my) - M) : 0.f;
-      const int cnt = min(32, n - s0);
-      int k = 0;
-      for (; k + 8 <= cnt; k += 8) {
-        float4 v[8];
-        float w[8];
-#pragma unroll
-        for (int u = 0; u < 8; ++u) {
-          v[u] = __ldcg(reinterpret_cast<const float4*>(o + static_cast<int64_t>(s0 + k + u) * kD) +
-                        lane);
-          w[u] = __shfl_sync(0xffffffffu, wl, k + u);
-        }
-#pragma unroll
-        for (int u = 0; u < 8; ++u) {
-          W += w[u];
-          acc.x += w[u] * v[u].x;
-          acc.y += w[u] * v[u].y;
-          acc.z += w[u] * v[u].z;
-          acc.w += w[u] * v[u].w;
-        }
-      }
-      for (; k < cnt; ++k) {
-        const float4 v =
-            __ldcg(reinterpret_cast<const float4*>(o + static_cast<int64_t>(s0 + k) * kD) + lane);
-        const float w = __shfl_sync(0xffffffffu, wl, k);
-        W += w;
-        acc.x += w * v.x;
-        acc.y += w * v.y;
-        acc.z += w * v.z;
-        acc.w += w * v.w;
-      }
-    }
-  }
-  const float inv = W > 0.f ? 1.f / W : 0.f;
-  *reinterpret_cast<uint2*>(p.out + bh * kD + lane * 4) =
-      make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
-}
 
 // Decode step, fused write: the warp that owns row L-1 of the last tile
 // converts the sequence's new K (lanes 0-15) and V (lanes 16-31) row exactly
@@ -666,28 +566,7 @@ __global__ void __launch_bounds__(kThreads, (kFp8 && NT == 1) ? 4 : TcLayout<kFp
   }
   if (p.num_splits == 1) return;
 
-  // ------------------------------------------------- split count and merge
-  // The CTA that completes the count of its (sequence, kv head) merges the
-  // splits of its G query heads and returns the counter to zero.
-  __syncthreads();  // every partial of this CTA is written
-  int* last_flag = abort_ptr + 1;
-  const int n_valid = (L + p.tokens_per_split - 1) / p.tokens_per_split;
-  if (threadIdx.x == 0) {
-    __threadfence();
-    unsigned* ctr = p.counters + static_cast<int64_t>(b) * p.num_kv_heads + g;
-    const unsigned prev = atomicAdd(ctr, 1u);
-    const bool last = prev + 1u == static_cast<unsigned>(n_valid);
-    if (last) {
-      atomicExch(ctr, 0u);
-      __threadfence();
-    }
-    *last_flag = last ? 1 : 0;
-  }
-  __syncthreads();
-  if (*last_flag) {
-    for (int h = warp; h < G; h += kThreads / 32)
-      merge_splits_warp(p, static_cast<int64_t>(b) * p.num_q_heads + hq0 + h, n_valid, lane);
-  }
+  count_and_merge(p, b, g, hq0, G, L, abort_ptr + 1, warp, lane);
 }
 
 // Epilogue of the tensor-core split kernel: merge the consumer warps'
@@ -844,6 +723,26 @@ bool make_kv_map_fp8(CUtensorMap* map, const void* base, int64_t rows, int32_t n
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// [rows, H_KV, 80] bytes of 4-bit rows; box = a whole row x 1 head x box_rows
+// rows, packed at 80 bytes.
+bool make_kv_map_q4(CUtensorMap* map, const void* base, int64_t rows, int32_t num_kv_heads,
+                    int32_t box_rows) {
+  auto enc = encode_fn();
+  if (enc == nullptr) return false;
+  constexpr int kQ4Row = kD / 2 + kD / 8;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(kQ4Row),
+                              static_cast<cuuint64_t>(num_kv_heads),
+                              static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(kQ4Row),
+                                 static_cast<cuuint64_t>(kQ4Row) * num_kv_heads};
+  const cuuint32_t box[3] = {static_cast<cuuint32_t>(kQ4Row), 1u,
+                             static_cast<cuuint32_t>(box_rows)};
+  const cuuint32_t es[3] = {1u, 1u, 1u};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, es,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // Scratch of the allocation-free decode entry point.  Every GPU that loads
 // this library holds these 16 MiB for the life of the process.  Host code
 // must not use the name as an address: static_decode_scratch_address() asks
@@ -914,20 +813,7 @@ size_t decode_workspace_bytes(int32_t num_seqs, int32_t num_q_heads, int32_t num
   return bytes;
 }
 
-pa_status launch_paged_decode(const DecodeArgs& a, cudaStream_t stream) {
-  if (a.num_seqs == 0) return PA_OK;
-  const int32_t G = a.num_q_heads / a.num_kv_heads;
-  const int64_t rows = a.num_blocks * a.block_size;
-  const int32_t box_rows = a.block_size < kTile ? a.block_size : kTile;
-  const bool fp8 = a.cache_dtype == PA_FP8_E4M3;
-  CUtensorMap mk, mv;
-  const bool maps_ok =
-      fp8 ? make_kv_map_fp8(&mk, a.k_cache, rows, a.num_kv_heads, box_rows) &&
-                make_kv_map_fp8(&mv, a.v_cache, rows, a.num_kv_heads, box_rows)
-          : make_kv_map_swizzled(&mk, a.k_cache, rows, a.num_kv_heads, box_rows) &&
-                make_kv_map_swizzled(&mv, a.v_cache, rows, a.num_kv_heads, box_rows);
-  if (!maps_ok) return PA_ERR_CUDA;
-
+DecodeParams make_decode_params(const DecodeArgs& a) {
   DecodeParams p;
   p.out = static_cast<__nv_bfloat16*>(a.out);
   p.q = static_cast<const __nv_bfloat16*>(a.q);
@@ -958,7 +844,24 @@ pa_status launch_paged_decode(const DecodeArgs& a, cudaStream_t stream) {
   p.slot_mapping = a.slot_mapping;
   p.k_cache = const_cast<void*>(a.k_cache);
   p.v_cache = const_cast<void*>(a.v_cache);
+  return p;
+}
 
+pa_status launch_paged_decode(const DecodeArgs& a, cudaStream_t stream) {
+  if (a.num_seqs == 0) return PA_OK;
+  const int32_t G = a.num_q_heads / a.num_kv_heads;
+  const int64_t rows = a.num_blocks * a.block_size;
+  const int32_t box_rows = a.block_size < kTile ? a.block_size : kTile;
+  const bool fp8 = a.cache_dtype == PA_FP8_E4M3;
+  CUtensorMap mk, mv;
+  const bool maps_ok =
+      fp8 ? make_kv_map_fp8(&mk, a.k_cache, rows, a.num_kv_heads, box_rows) &&
+                make_kv_map_fp8(&mv, a.v_cache, rows, a.num_kv_heads, box_rows)
+          : make_kv_map_swizzled(&mk, a.k_cache, rows, a.num_kv_heads, box_rows) &&
+                make_kv_map_swizzled(&mv, a.v_cache, rows, a.num_kv_heads, box_rows);
+  if (!maps_ok) return PA_ERR_CUDA;
+
+  const DecodeParams p = make_decode_params(a);
   if (a.plan.num_splits > 65535 || a.num_seqs > 65535) return PA_ERR_UNSUPPORTED;
   const dim3 grid(static_cast<unsigned>(a.num_kv_heads), static_cast<unsigned>(a.plan.num_splits),
                   static_cast<unsigned>(a.num_seqs));

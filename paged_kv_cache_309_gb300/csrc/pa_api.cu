@@ -36,14 +36,14 @@ bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p
 bool is_src_dtype(pa_dtype d) { return d == PA_BF16 || d == PA_FP16 || d == PA_FP32; }
 bool is_any_dtype(pa_dtype d) { return is_src_dtype(d) || d == PA_FP8_E4M3; }
 
-// Host-side checks shared by both decode entry points; fills *a (all but the
+// Host-side checks shared by the decode entry points; fills *a (all but the
 // workspace) on success.
 pa_status check_decode(void* out, const void* q, const void* k_cache, const void* v_cache,
                        pa_dtype cache_dtype, const int32_t* block_tables,
                        const int32_t* context_lens, int32_t num_seqs, int32_t num_q_heads,
                        int32_t num_kv_heads, int32_t head_size, int32_t block_size,
                        int32_t max_blocks_per_seq, int64_t num_blocks, float scale,
-                       int32_t max_context_len, pa_detail::DecodeArgs* a) {
+                       int32_t max_context_len, pa_detail::DecodeArgs* a, bool allow_q4 = false) {
   if (num_seqs < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || head_size <= 0 ||
       block_size <= 0 || max_blocks_per_seq <= 0 || num_blocks <= 0 || max_context_len < 0 ||
       max_context_len > (1 << 30))
@@ -53,7 +53,8 @@ pa_status check_decode(void* out, const void* q, const void* k_cache, const void
     return PA_ERR_INVALID;
   if (num_q_heads % num_kv_heads != 0) return PA_ERR_INVALID;
   if (!std::isfinite(scale)) return PA_ERR_INVALID;
-  if (cache_dtype != PA_BF16 && cache_dtype != PA_FP8_E4M3) return PA_ERR_UNSUPPORTED;
+  if (cache_dtype != PA_BF16 && cache_dtype != PA_FP8_E4M3 && !(allow_q4 && cache_dtype == PA_Q4))
+    return PA_ERR_UNSUPPORTED;
   if (head_size != 128) return PA_ERR_UNSUPPORTED;
   const int32_t G = num_q_heads / num_kv_heads;
   if (G != 1 && G != 2 && G != 4 && G != 8 && G != 16) return PA_ERR_UNSUPPORTED;
@@ -574,6 +575,29 @@ pa_status pa_gather_cache_q4(void* key, void* value, pa_dtype dst_dtype, int64_t
                key_cache, value_cache, num_blocks, block_size, block_stride, slot_mapping, &a);
   if (st != PA_OK || num_tokens == 0) return st;
   return pa_detail::launch_gather_cache_q4(a, dst_dtype, reinterpret_cast<cudaStream_t>(stream));
+}
+
+pa_status pa_paged_decode_attention_q4(void* out, const void* q, const void* k_cache,
+                                       const void* v_cache, const int32_t* block_tables,
+                                       const int32_t* context_lens, int32_t num_seqs,
+                                       int32_t num_q_heads, int32_t num_kv_heads,
+                                       int32_t head_size, int32_t block_size,
+                                       int32_t max_blocks_per_seq, int64_t num_blocks,
+                                       float scale, int32_t max_context_len, void* workspace,
+                                       size_t workspace_bytes, pa_stream_t stream) {
+  pa_detail::DecodeArgs a{};
+  const pa_status st = check_decode(out, q, k_cache, v_cache, PA_Q4, block_tables, context_lens,
+                                    num_seqs, num_q_heads, num_kv_heads, head_size, block_size,
+                                    max_blocks_per_seq, num_blocks, scale, max_context_len, &a,
+                                    /*allow_q4=*/true);
+  if (st != PA_OK) return st;
+  const size_t need =
+      pa_detail::decode_workspace_bytes(num_seqs, num_q_heads, num_kv_heads, head_size, a.plan);
+  if (workspace == nullptr || workspace_bytes < need) return PA_ERR_WORKSPACE;
+  if (!aligned(workspace, 256)) return PA_ERR_ALIGN;
+  a.workspace = workspace;
+  a.error_word = nullptr;
+  return pa_detail::launch_paged_decode_q4(a, reinterpret_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

@@ -280,6 +280,18 @@ __device__ __forceinline__ void div8_for_e4m3(const Vec8<S>& v, float (&f)[8], c
   }
 }
 
+// minimum and maximum that carry a NaN
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float d;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+
 __device__ __forceinline__ float div_rn(float x, const Divisor& d) {
   const float ax = fabsf(x);
   if (d.fast && ax >= 0x1p-60f && ax <= 0x1p60f) {
@@ -534,6 +546,9 @@ bool make_kv_map_swizzled(CUtensorMap* map, const void* base, int64_t rows, int3
                           int32_t box_rows);
 bool make_kv_map_fp8(CUtensorMap* map, const void* base, int64_t rows, int32_t num_kv_heads,
                      int32_t box_rows);
+// The same over a [rows, H_KV, 80] 4-bit cache: whole 80-byte rows, no swizzle.
+bool make_kv_map_q4(CUtensorMap* map, const void* base, int64_t rows, int32_t num_kv_heads,
+                    int32_t box_rows);
 
 struct ReshapeArgs {
   const void* key;
@@ -628,6 +643,7 @@ struct DecodeArgs {
   const int64_t* slot_mapping;
 };
 pa_status launch_paged_decode(const DecodeArgs& a, cudaStream_t stream);
+pa_status launch_paged_decode_q4(const DecodeArgs& a, cudaStream_t stream);  // decode_q4.cu
 
 struct PrefillArgs {
   void* out;

@@ -93,6 +93,9 @@ def _load():
     lib.pa_reshape_and_cache_q4.restype = E
     lib.pa_gather_cache_q4.argtypes = [P, P, E, I64, I32, I32, I64, I64, P, P, I64, I32, I64, P, P]
     lib.pa_gather_cache_q4.restype = E
+    lib.pa_paged_decode_attention_q4.argtypes = [P, P, P, P, P, P, I32, I32, I32, I32, I32, I32,
+                                                 I64, F32, I32, P, SZ, P]
+    lib.pa_paged_decode_attention_q4.restype = E
     _lib = lib
     return lib
 
@@ -588,3 +591,41 @@ def pa_gather_cache_q4(key, value, key_cache, value_cache, slot_mapping, stream=
         0 if value is None else value.stride(0), _ptr(key_cache), _ptr(value_cache), nb, bs,
         key_cache.stride(0), _ptr(slot_mapping), _stream(stream))
     _check(st, "pa_gather_cache_q4")
+
+
+def _decode_shapes(out, q, k_cache, v_cache, block_tables, context_lens, workspace):
+    """Checks shared by the calls below: (B, H_Q, H_KV, d, block_size, num_blocks)."""
+    _on_device(out=out, q=q, k_cache=k_cache, v_cache=v_cache, block_tables=block_tables,
+               context_lens=context_lens)
+    _workspace(workspace)
+    B, HQ, d = q.shape
+    nb, bs, HKV, row = k_cache.shape
+    for t, name in ((q, "q"), (out, "out"), (k_cache, "k_cache"), (v_cache, "v_cache"),
+                    (block_tables, "block_tables"), (context_lens, "context_lens")):
+        _need(t.is_contiguous(), f"{name} must be contiguous")
+    _need(out.shape == q.shape and q.dtype == torch.bfloat16 and out.dtype == torch.bfloat16,
+          "q and out must be bf16 [B, H_Q, d]")
+    _need(v_cache.shape == k_cache.shape and v_cache.dtype == k_cache.dtype,
+          "v_cache must match k_cache")
+    _need(row == (q4_row_bytes(d) if k_cache.dtype == torch.uint8 else d),
+          "cache rows must be d elements, or 5 * d / 8 bytes of a 4-bit cache (uint8)")
+    _need(block_tables.dtype == torch.int32 and context_lens.dtype == torch.int32,
+          "block_tables and context_lens must be int32")
+    _need(block_tables.dim() == 2 and block_tables.shape[0] == B and context_lens.numel() == B,
+          "block_tables must be [B, max_blocks_per_seq], context_lens [B]")
+    return B, HQ, HKV, d, bs, nb
+
+
+def pa_paged_decode_attention_q4(out, q, k_cache, v_cache, block_tables, context_lens, scale,
+                                 max_context_len, workspace, stream=None):
+    """out/q [B, H_Q, 128] bf16; 4-bit caches uint8 [num_blocks, bs, H_KV, 80],
+    contiguous; block_tables [B, max_blocks_per_seq] int32; context_lens [B]
+    int32; workspace from decode_workspace."""
+    B, HQ, HKV, d, bs, nb = _decode_shapes(out, q, k_cache, v_cache, block_tables, context_lens,
+                                           workspace)
+    _need(k_cache.dtype == torch.uint8, "a 4-bit cache (uint8 rows) is expected")
+    st = _load().pa_paged_decode_attention_q4(
+        _ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables), _ptr(context_lens),
+        B, HQ, HKV, d, bs, block_tables.shape[1], nb, float(scale), int(max_context_len),
+        _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream))
+    _check(st, "pa_paged_decode_attention_q4")

@@ -124,3 +124,61 @@ def test_binding_refuses_wrong_shapes(monkeypatch):
                     (x, x, c.transpose(1, 2), c, s), (x, x, c, c, torch.zeros(8, dtype=torch.int64)[::2])):
             with pytest.raises(ValueError):
                 fn(*bad)
+
+
+# ------------------------------------------------------- decode over 4 bits --
+def _dec(lib, **kw):
+    a = dict(out=FAKE, q=FAKE, kc=FAKE, vc=FAKE, bt=FAKE, cl=FAKE, B=4, HQ=32, HKV=8, d=128, bs=16,
+             mbps=8, nb=64, scale=0.088, maxctx=128, ws=FAKE, wsb=1 << 30)
+    a.update(kw)
+    return lib.pa_paged_decode_attention_q4(
+        a["out"], a["q"], a["kc"], a["vc"], a["bt"], a["cl"], a["B"], a["HQ"], a["HKV"], a["d"],
+        a["bs"], a["mbps"], a["nb"], a["scale"], a["maxctx"], a["ws"], a["wsb"], None)
+
+
+def test_decode_q4_rejects(lib):
+    assert _dec(lib, B=0) == pa.PA_OK
+    for bad in (dict(out=None), dict(q=None), dict(kc=None), dict(vc=None), dict(bt=None),
+                dict(cl=None), dict(B=-1), dict(HQ=12), dict(HKV=0), dict(nb=0), dict(mbps=0),
+                dict(scale=float("inf")), dict(scale=float("nan")), dict(maxctx=-1)):
+        assert _dec(lib, **bad) == pa.PA_ERR_INVALID, bad
+    for bad in (dict(d=64), dict(HQ=24), dict(HQ=256), dict(bs=4), dict(bs=24), dict(bs=512),
+                dict(nb=1 << 28), dict(B=65536)):
+        assert _dec(lib, **bad) == pa.PA_ERR_UNSUPPORTED, bad
+    for bad in (dict(out=FAKE_MIS), dict(q=FAKE_MIS), dict(kc=FAKE_MIS), dict(vc=FAKE_MIS),
+                dict(ws=P(0x100010))):
+        assert _dec(lib, **bad) == pa.PA_ERR_ALIGN, bad
+    for bad in (dict(ws=None), dict(wsb=16)):
+        assert _dec(lib, **bad) == pa.PA_ERR_WORKSPACE, bad
+
+
+def _decode_tensors(row=80, dtype=torch.uint8):
+    q = torch.zeros(2, 8, 128, dtype=torch.bfloat16)
+    c = torch.zeros(4, 16, 4, row, dtype=dtype)
+    return dict(out=q.clone(), q=q, k_cache=c, v_cache=c.clone(),
+                block_tables=torch.zeros(2, 3, dtype=torch.int32),
+                context_lens=torch.zeros(2, dtype=torch.int32), scale=0.1, max_context_len=16,
+                workspace=torch.zeros(256, dtype=torch.uint8))
+
+
+def _bad_decode_tensors(good):
+    q, c = good["q"], good["k_cache"]
+    return [dict(q=q.float()), dict(out=q.half()), dict(out=q[:1]), dict(v_cache=c[:3]),
+            dict(v_cache=c.to(torch.int16)), dict(k_cache=c[..., :79], v_cache=c[..., :79]),
+            dict(block_tables=torch.zeros(2, 3, dtype=torch.int64)),
+            dict(block_tables=torch.zeros(3, 3, dtype=torch.int32)),
+            dict(context_lens=torch.zeros(3, dtype=torch.int32)),
+            dict(context_lens=torch.zeros(2, dtype=torch.int64)),
+            dict(k_cache=c.transpose(1, 2)), dict(q=q.transpose(0, 1))]
+
+
+def test_decode_q4_binding_refusals(monkeypatch):
+    good = _decode_tensors()
+    with pytest.raises(ValueError, match="CUDA tensor"):
+        pa.pa_paged_decode_attention_q4(**good)
+    monkeypatch.setattr(pa, "_on_device", lambda **kw: None)
+    monkeypatch.setattr(pa, "_load", lambda: pytest.fail("reached the library"))
+    bf16 = torch.zeros(4, 16, 4, 128, dtype=torch.bfloat16)
+    for bad in _bad_decode_tensors(good) + [dict(k_cache=bf16, v_cache=bf16)]:
+        with pytest.raises(ValueError):
+            pa.pa_paged_decode_attention_q4(**{**good, **bad})
