@@ -15,6 +15,8 @@
  *   pa_reshape_and_cache_q4        scatter per-token K/V into a 4-bit paged cache
  *   pa_gather_cache_q4             read 4-bit cache rows back as bf16, fp16 or fp32
  *   pa_paged_decode_attention_q4   decode attention over a 4-bit cache
+ *   pa_paged_decode_attention_scored  decode attention that also adds up each cached
+ *                                  token's attention weight
  *
  * Common rules
  *   - Every pointer argument except the `*_host` ones is a DEVICE pointer on
@@ -528,6 +530,41 @@ pa_status pa_paged_decode_attention_q4(void *out, const void *q, const void *k_c
                                        int32_t max_blocks_per_seq, int64_t num_blocks,
                                        float scale, int32_t max_context_len, void *workspace,
                                        size_t workspace_bytes, pa_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * pa_paged_decode_attention_scored -- decode attention that also adds up
+ * each cached token's attention weight, per kv head:
+ *     w[b, g, t]        = sum over the G query heads h of kv head g of
+ *                         softmax_t(scale q[b, h] . K_t)
+ *     sums_out[b, g, t] = (t >= L - num_new ? 0 : sums_in[b, g, t]) + w[b, g, t]
+ * for t < min(L, sums_len); other elements of sums_out are left as they
+ * were.  num_new >= 0: the sequence's last num_new tokens joined the cache
+ * since the last call, so their sums start here (1 in a decode loop; any
+ * value >= L starts every sum).  A token of a dropped block has weight 0.
+ *
+ * sums_in, sums_out: [num_seqs, num_kv_heads, sums_len] fp32, contiguous;
+ *   the same array (updated in place) or two that do not overlap.
+ * cache_dtype: PA_BF16 (k_scale, v_scale NULL), PA_FP8_E4M3 (scales as in
+ *   pa_paged_decode_attention_fp8) or PA_Q4 (scales NULL; caches as in
+ *   pa_paged_decode_attention_q4).  out is what the decode call of that
+ *   cache gives.
+ * workspace: at least pa_paged_decode_scored_workspace_size(...) bytes (the
+ *   decode workspace, then one fp32 score for each query head and token and
+ *   a log-sum-exp for each query head); otherwise as for
+ *   pa_paged_decode_attention.  Two launches on `stream`.
+ * ---------------------------------------------------------------------- */
+size_t pa_paged_decode_scored_workspace_size(int32_t num_seqs, int32_t num_q_heads,
+                                             int32_t num_kv_heads, int32_t head_size,
+                                             int32_t max_context_len);
+
+pa_status pa_paged_decode_attention_scored(
+    void *out, float *sums_out, const float *sums_in, int32_t sums_len, int32_t num_new,
+    const void *q, const void *k_cache, const void *v_cache, pa_dtype cache_dtype,
+    const float *k_scale, const float *v_scale, const int32_t *block_tables,
+    const int32_t *context_lens, int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads,
+    int32_t head_size, int32_t block_size, int32_t max_blocks_per_seq, int64_t num_blocks,
+    float scale, int32_t max_context_len, void *workspace, size_t workspace_bytes,
+    pa_stream_t stream);
 
 /* Diagnostic of the failure path every pipeline kernel shares: launches one
  * CTA whose threads wait, with the same bounded wait the pipelines use, on a

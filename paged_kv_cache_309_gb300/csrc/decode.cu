@@ -129,14 +129,15 @@ __device__ __forceinline__ bool fused_token_write(const DecodeParams& p, int b, 
   return here;
 }
 
-template <int NT, bool kPairRows>
+template <int NT, bool kPairRows, bool kScored>
 __device__ __forceinline__ void epilogue_tc(const DecodeParams& p, uint8_t* smem,
                                             float (&o)[8][NT][4], float (&m)[NT][2],
                                             float (&l)[NT][2], int b, int split, int hq0, int G,
                                             int warp, int lane, float out_scale);
 
-// NT: n-tiles of 8 query heads (G <= 8 -> 1, G = 16 -> 2); kFp8: e4m3 cache.
-template <int NT, bool kFp8>
+// NT: n-tiles of 8 query heads (G <= 8 -> 1, G = 16 -> 2); kFp8: e4m3 cache;
+// kScored: also store the scores and each query head's log2-sum-exp.
+template <int NT, bool kFp8, bool kScored>
 __global__ void __launch_bounds__(kThreads, (kFp8 && NT == 1) ? 4 : TcLayout<kFp8>::kCtasPerSm)
     paged_decode_split_tc_kernel(const __grid_constant__ CUtensorMap tm_k,
                                  const __grid_constant__ CUtensorMap tm_v, const DecodeParams p,
@@ -174,6 +175,8 @@ __global__ void __launch_bounds__(kThreads, (kFp8 && NT == 1) ? 4 : TcLayout<kFp
         reinterpret_cast<uint4*>(p.out + (static_cast<int64_t>(b) * p.num_q_heads + hq0 + h) *
                                              kD)[c] = make_uint4(0u, 0u, 0u, 0u);
       }
+      if (kScored && threadIdx.x < G)
+        p.final_lse[static_cast<int64_t>(b) * p.num_q_heads + hq0 + threadIdx.x] = -INFINITY;
     }
     return;
   }
@@ -440,6 +443,10 @@ __global__ void __launch_bounds__(kThreads, (kFp8 && NT == 1) ? 4 : TcLayout<kFp
           for (int c = 0; c < 4; ++c) s[c] = (s0[nt][c] + s1[nt][c]) * score_scale;
           if (!v0) s[0] = s[1] = -INFINITY;
           if (!v1) s[2] = s[3] = -INFINITY;
+          if constexpr (kScored) {
+            const int tok0 = tok_begin + t * kTile + r0;
+            store_scores(p, b, g, G, tok0, gq, tok_end - tok0, nt * 8 + 2 * tq, s);
+          }
           float mx[2] = {fmaxf(s[0], s[2]), fmaxf(s[1], s[3])};
 #pragma unroll
           for (int off = 4; off <= 16; off <<= 1) {
@@ -540,6 +547,15 @@ __global__ void __launch_bounds__(kThreads, (kFp8 && NT == 1) ? 4 : TcLayout<kFp
             fence_proxy_async_smem();  // generic writes before the next TMA
         }
       }
+      if constexpr (kScored) {
+        if (mask16 == 0u) {  // no token of the slice is there
+          const float none[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          const int tok0 = tok_begin + t * kTile + r0;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+            store_scores(p, b, g, G, tok0, gq, tok_end - tok0, nt * 8 + 2 * tq, none);
+        }
+      }
       __syncwarp();
       if (lane == 0) mbar_arrive(&empty[stage]);
     }
@@ -562,11 +578,11 @@ __global__ void __launch_bounds__(kThreads, (kFp8 && NT == 1) ? 4 : TcLayout<kFp
                split] = -INFINITY;
   } else {
     const float out_scale = (kFp8 && p.v_scale != nullptr) ? __ldg(p.v_scale) : 1.f;
-    epilogue_tc<NT, kFp8>(p, smem, o, m, l, b, split, hq0, G, warp, lane, out_scale);
+    epilogue_tc<NT, kFp8, kScored>(p, smem, o, m, l, b, split, hq0, G, warp, lane, out_scale);
   }
   if (p.num_splits == 1) return;
 
-  count_and_merge(p, b, g, hq0, G, L, abort_ptr + 1, warp, lane);
+  count_and_merge<kScored>(p, b, g, hq0, G, L, abort_ptr + 1, warp, lane);
 }
 
 // Epilogue of the tensor-core split kernel: merge the consumer warps'
@@ -574,7 +590,7 @@ __global__ void __launch_bounds__(kThreads, (kFp8 && NT == 1) ? 4 : TcLayout<kFp
 // several splits write an fp32 partial and its log2-sum-exp.  kPairRows:
 // accumulator rows gq / gq + 8 of m-tile mt hold head elements 16mt + 2gq
 // and 16mt + 2gq + 1 (fp8 cache) instead of 16mt + gq and 16mt + gq + 8.
-template <int NT, bool kPairRows>
+template <int NT, bool kPairRows, bool kScored>
 __device__ __forceinline__ void epilogue_tc(const DecodeParams& p, uint8_t* smem,
                                             float (&o)[8][NT][4], float (&m)[NT][2],
                                             float (&l)[NT][2], int b, int split, int hq0, int G,
@@ -653,19 +669,23 @@ __device__ __forceinline__ void epilogue_tc(const DecodeParams& p, uint8_t* smem
     if (p.num_splits == 1) {
       *reinterpret_cast<uint2*>(p.out + row * kD + e0) =
           make_uint2(pack_bf16x2(acc4.x, acc4.y), pack_bf16x2(acc4.z, acc4.w));
+      if (kScored && e0 == 0)
+        p.final_lse[row] = Ls == 0.f ? -INFINITY : fin[2 * h] + log2f(Ls);
     } else {
       const int64_t slot = row * p.num_splits + split;
       *reinterpret_cast<float4*>(p.ws_o + slot * kD + e0) = acc4;
-      if (e0 == 0) p.ws_lse[slot] = Ls > 0.f ? fin[2 * h] + log2f(Ls) : -INFINITY;
+      // (scored: a NaN sum is carried to the weights)
+      if (e0 == 0)
+        p.ws_lse[slot] = (kScored ? Ls != 0.f : Ls > 0.f) ? fin[2 * h] + log2f(Ls) : -INFINITY;
     }
   }
 }
 
-template <int NT, bool kFp8>
+template <int NT, bool kFp8, bool kScored>
 pa_status launch_split_tc(const CUtensorMap& mk, const CUtensorMap& mv, const DecodeParams& p,
                           dim3 grid, int G, cudaStream_t stream) {
   static std::atomic<uint64_t> smem_raised{0};
-  auto kern = paged_decode_split_tc_kernel<NT, kFp8>;
+  auto kern = paged_decode_split_tc_kernel<NT, kFp8, kScored>;
   constexpr int kSmem = TcLayout<kFp8>::kAlloc;
   if (!ensure_smem_limit(kern, kSmem, smem_raised)) return PA_ERR_CUDA;
   kern<<<grid, kThreads, kSmem, stream>>>(mk, mv, p, G);
@@ -844,6 +864,9 @@ DecodeParams make_decode_params(const DecodeArgs& a) {
   p.slot_mapping = a.slot_mapping;
   p.k_cache = const_cast<void*>(a.k_cache);
   p.v_cache = const_cast<void*>(a.v_cache);
+  p.scores = a.scores;
+  p.final_lse = a.final_lse;
+  p.score_len = static_cast<int64_t>(a.plan.num_splits) * a.plan.tokens_per_split;
   return p;
 }
 
@@ -865,19 +888,20 @@ pa_status launch_paged_decode(const DecodeArgs& a, cudaStream_t stream) {
   if (a.plan.num_splits > 65535 || a.num_seqs > 65535) return PA_ERR_UNSUPPORTED;
   const dim3 grid(static_cast<unsigned>(a.num_kv_heads), static_cast<unsigned>(a.plan.num_splits),
                   static_cast<unsigned>(a.num_seqs));
-  pa_status st;
-  switch (G) {
-    case 1: case 2: case 4: case 8:
-      st = fp8 ? launch_split_tc<1, true>(mk, mv, p, grid, G, stream)
-               : launch_split_tc<1, false>(mk, mv, p, grid, G, stream);
-      break;
-    case 16:
-      st = fp8 ? launch_split_tc<2, true>(mk, mv, p, grid, G, stream)
-               : launch_split_tc<2, false>(mk, mv, p, grid, G, stream);
-      break;
-    default: return PA_ERR_UNSUPPORTED;
+  const bool scored = a.scores != nullptr;
+  if (G == 16) {
+    if (scored)
+      return fp8 ? launch_split_tc<2, true, true>(mk, mv, p, grid, G, stream)
+                 : launch_split_tc<2, false, true>(mk, mv, p, grid, G, stream);
+    return fp8 ? launch_split_tc<2, true, false>(mk, mv, p, grid, G, stream)
+               : launch_split_tc<2, false, false>(mk, mv, p, grid, G, stream);
   }
-  return st;
+  if (G > 8) return PA_ERR_UNSUPPORTED;
+  if (scored)
+    return fp8 ? launch_split_tc<1, true, true>(mk, mv, p, grid, G, stream)
+               : launch_split_tc<1, false, true>(mk, mv, p, grid, G, stream);
+  return fp8 ? launch_split_tc<1, true, false>(mk, mv, p, grid, G, stream)
+             : launch_split_tc<1, false, false>(mk, mv, p, grid, G, stream);
 }
 
 }  // namespace pa_detail

@@ -42,6 +42,12 @@ struct DecodeParams {
   const int64_t* slot_mapping;
   void* k_cache;
   void* v_cache;
+  // accumulated attention weights (else null): the scores in base 2, -inf
+  // where there is no token, [B, H_KV, score_len, G]; and each query head's
+  // log2-sum-exp [B, H_Q]
+  float* scores;
+  float* final_lse;
+  int64_t score_len;
 };
 
 
@@ -55,6 +61,26 @@ __device__ __forceinline__ int effective_len(const DecodeParams& p, int b, bool*
   return *clipped ? static_cast<int>(cap) : L;
 }
 
+// Scores of one 16-token slice, from the accumulator layout of the score
+// products: this lane holds tokens row and row + 8 of heads h, h + 1 (s[0],
+// s[1] and s[2], s[3]).  Rows at or past `rows` belong to another range.
+__device__ __forceinline__ void store_scores(const DecodeParams& p, int b, int g, int G, int tok0,
+                                             int row, int rows, int h, const float (&s)[4]) {
+  if (h >= G) return;
+  float* dst =
+      p.scores +
+      ((static_cast<int64_t>(b) * p.num_kv_heads + g) * p.score_len + tok0 + row) * G + h;
+#pragma unroll
+  for (int i = 0; i < 2; ++i, dst += 8 * G) {
+    if (row + 8 * i >= rows) break;
+    if (G == 1) {
+      dst[0] = s[2 * i];
+    } else {  // G and h are even
+      *reinterpret_cast<float2*>(dst) = make_float2(s[2 * i], s[2 * i + 1]);
+    }
+  }
+}
+
 // The parameters of a call (workspace split up, scale in base 2).
 DecodeParams make_decode_params(const DecodeArgs& a);
 
@@ -62,6 +88,7 @@ DecodeParams make_decode_params(const DecodeArgs& a);
 // over the n splits that hold tokens, out = sum_s w_s o_s / sum_s w_s,
 // rounded to bf16.  Partials are read through L2 (__ldcg): other CTAs wrote
 // them during this launch.
+template <bool kScored>
 __device__ __forceinline__ void merge_splits_warp(const DecodeParams& p, int64_t bh, int n,
                                                   int lane) {
   const float* lse = p.ws_lse + bh * p.num_splits;
@@ -109,6 +136,7 @@ __device__ __forceinline__ void merge_splits_warp(const DecodeParams& p, int64_t
       }
     }
   }
+  if (kScored && lane == 0) p.final_lse[bh] = W == 0.f ? -INFINITY : M + log2f(W);
   const float inv = W > 0.f ? 1.f / W : 0.f;
   *reinterpret_cast<uint2*>(p.out + bh * kD + lane * 4) =
       make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
@@ -118,6 +146,7 @@ __device__ __forceinline__ void merge_splits_warp(const DecodeParams& p, int64_t
 // completes the count merges the splits of its G query heads and returns the
 // counter to zero.  Every thread of the CTA calls it; last_flag: one int of
 // shared memory nothing else uses.
+template <bool kScored>
 __device__ __forceinline__ void count_and_merge(const DecodeParams& p, int b, int g, int hq0, int G,
                                                 int L, int* last_flag, int warp, int lane) {
   __syncthreads();  // every partial of this CTA is written
@@ -136,7 +165,7 @@ __device__ __forceinline__ void count_and_merge(const DecodeParams& p, int b, in
   __syncthreads();
   if (*last_flag) {
     for (int h = warp; h < G; h += kThreads / 32)
-      merge_splits_warp(p, static_cast<int64_t>(b) * p.num_q_heads + hq0 + h, n_valid, lane);
+      merge_splits_warp<kScored>(p, static_cast<int64_t>(b) * p.num_q_heads + hq0 + h, n_valid, lane);
   }
 }
 

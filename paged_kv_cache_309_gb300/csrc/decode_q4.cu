@@ -67,8 +67,9 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   return d;
 }
 
-// NT: n-tiles of 8 query heads (G <= 8 -> 1, G = 16 -> 2).
-template <int NT>
+// NT: n-tiles of 8 query heads (G <= 8 -> 1, G = 16 -> 2); kScored: also
+// store the scores and each query head's log2-sum-exp.
+template <int NT, bool kScored>
 __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2)
     paged_decode_split_q4_kernel(const __grid_constant__ CUtensorMap tm_k,
                                  const __grid_constant__ CUtensorMap tm_v, const DecodeParams p,
@@ -102,6 +103,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2)
       for (int i = threadIdx.x; i < G * (kD / 8); i += kThreads)
         reinterpret_cast<uint4*>(p.out + (static_cast<int64_t>(b) * p.num_q_heads + hq0) * kD)[i] =
             make_uint4(0u, 0u, 0u, 0u);
+      if (kScored && threadIdx.x < G)
+        p.final_lse[static_cast<int64_t>(b) * p.num_q_heads + hq0 + threadIdx.x] = -INFINITY;
     }
     return;
   }
@@ -269,8 +272,17 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2)
 #pragma unroll 1
       for (int sl = 0; sl < 2; ++sl) {
         const uint32_t mask16 = (mask32 >> (16 * sl)) & 0xFFFFu;
-        if (mask16 == 0u) continue;
         const int r0 = 32 * warp + 16 * sl;
+        const int tok0 = tok_begin + t * kTile + r0;
+        if (mask16 == 0u) {  // no token of the slice is there
+          if constexpr (kScored) {
+            const float none[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+              store_scores(p, b, g, G, tok0, gq, tok_end - tok0, nt * 8 + 2 * tq, none);
+          }
+          continue;
+        }
         if (mask16 != 0xFFFFu) {
           // rows without a token: s = m = 0 makes their values 0 (the ring's
           // leftovers could be NaN, and 0 x NaN would poison the sums)
@@ -339,6 +351,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2)
           }
           if (!v0) s[0] = s[1] = -INFINITY;
           if (!v1) s[2] = s[3] = -INFINITY;
+          if constexpr (kScored)
+            store_scores(p, b, g, G, tok0, gq, tok_end - tok0, nt * 8 + 2 * tq, s);
           float mx[2] = {fmaxf(s[0], s[2]), fmaxf(s[1], s[3])};
 #pragma unroll
           for (int off = 4; off <= 16; off <<= 1) {
@@ -516,6 +530,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2)
       if (p.num_splits == 1) {
         *reinterpret_cast<uint2*>(p.out + row * kD + e0) =
             make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
+        if (kScored && e0 == 0)
+          p.final_lse[row] = Ls == 0.f ? -INFINITY : fin[2 * h] + log2f(Ls);
       } else {
         const int64_t slot = row * p.num_splits + split;
         *reinterpret_cast<float4*>(p.ws_o + slot * kD + e0) = acc;
@@ -524,14 +540,14 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2)
     }
   }
   if (p.num_splits == 1) return;
-  count_and_merge(p, b, g, hq0, G, L, abort_ptr + 1, warp, lane);
+  count_and_merge<kScored>(p, b, g, hq0, G, L, abort_ptr + 1, warp, lane);
 }
 
-template <int NT>
+template <int NT, bool kScored>
 pa_status launch_split_q4(const CUtensorMap& mk, const CUtensorMap& mv, const DecodeParams& p,
                           dim3 grid, int G, cudaStream_t stream) {
   static std::atomic<uint64_t> smem_raised{0};
-  auto kern = paged_decode_split_q4_kernel<NT>;
+  auto kern = paged_decode_split_q4_kernel<NT, kScored>;
   if (!ensure_smem_limit(kern, Lay::kAlloc, smem_raised)) return PA_ERR_CUDA;
   kern<<<grid, kThreads, Lay::kAlloc, stream>>>(mk, mv, p, G);
   return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
@@ -552,8 +568,11 @@ pa_status launch_paged_decode_q4(const DecodeArgs& a, cudaStream_t stream) {
   const DecodeParams p = make_decode_params(a);
   const dim3 grid(static_cast<unsigned>(a.num_kv_heads), static_cast<unsigned>(a.plan.num_splits),
                   static_cast<unsigned>(a.num_seqs));
-  return G <= 8 ? launch_split_q4<1>(mk, mv, p, grid, G, stream)
-                : launch_split_q4<2>(mk, mv, p, grid, G, stream);
+  if (a.scores != nullptr)
+    return G <= 8 ? launch_split_q4<1, true>(mk, mv, p, grid, G, stream)
+                  : launch_split_q4<2, true>(mk, mv, p, grid, G, stream);
+  return G <= 8 ? launch_split_q4<1, false>(mk, mv, p, grid, G, stream)
+                : launch_split_q4<2, false>(mk, mv, p, grid, G, stream);
 }
 
 }  // namespace pa_detail

@@ -600,4 +600,50 @@ pa_status pa_paged_decode_attention_q4(void* out, const void* q, const void* k_c
   return pa_detail::launch_paged_decode_q4(a, reinterpret_cast<cudaStream_t>(stream));
 }
 
+size_t pa_paged_decode_scored_workspace_size(int32_t num_seqs, int32_t num_q_heads,
+                                             int32_t num_kv_heads, int32_t head_size,
+                                             int32_t max_context_len) {
+  if (num_seqs < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || head_size <= 0 ||
+      max_context_len < 0 || max_context_len > (1 << 30))
+    return 0;
+  const pa_detail::DecodePlan plan = pa_detail::make_decode_plan(
+      num_seqs, num_kv_heads, max_context_len, pa_detail::num_sms_current_device());
+  return pa_detail::scored_workspace_bytes(num_seqs, num_q_heads, num_kv_heads, head_size, plan);
+}
+
+pa_status pa_paged_decode_attention_scored(
+    void* out, float* sums_out, const float* sums_in, int32_t sums_len, int32_t num_new,
+    const void* q, const void* k_cache, const void* v_cache, pa_dtype cache_dtype,
+    const float* k_scale, const float* v_scale, const int32_t* block_tables,
+    const int32_t* context_lens, int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads,
+    int32_t head_size, int32_t block_size, int32_t max_blocks_per_seq, int64_t num_blocks,
+    float scale, int32_t max_context_len, void* workspace, size_t workspace_bytes,
+    pa_stream_t stream) {
+  if ((k_scale == nullptr) != (v_scale == nullptr)) return PA_ERR_INVALID;
+  if (k_scale != nullptr && cache_dtype != PA_FP8_E4M3) return PA_ERR_INVALID;
+  if (sums_out == nullptr || sums_in == nullptr || sums_len <= 0 || num_new < 0)
+    return PA_ERR_INVALID;
+  pa_detail::DecodeArgs a{};
+  const pa_status st = check_decode(out, q, k_cache, v_cache, cache_dtype, block_tables,
+                                    context_lens, num_seqs, num_q_heads, num_kv_heads, head_size,
+                                    block_size, max_blocks_per_seq, num_blocks, scale,
+                                    max_context_len, &a, /*allow_q4=*/true);
+  if (st != PA_OK) return st;
+  if (!aligned(sums_out, 4) || !aligned(sums_in, 4)) return PA_ERR_ALIGN;
+  // in place or apart: a partial overlap would read sums already written
+  const uintptr_t size = static_cast<uintptr_t>(num_seqs) * num_kv_heads * sums_len * 4;
+  const uintptr_t o = reinterpret_cast<uintptr_t>(sums_out), i = reinterpret_cast<uintptr_t>(sums_in);
+  if (o != i && o < i + size && i < o + size) return PA_ERR_INVALID;
+  const size_t need =
+      pa_detail::scored_workspace_bytes(num_seqs, num_q_heads, num_kv_heads, head_size, a.plan);
+  if (workspace == nullptr || workspace_bytes < need) return PA_ERR_WORKSPACE;
+  if (!aligned(workspace, 256)) return PA_ERR_ALIGN;
+  a.workspace = workspace;
+  a.error_word = nullptr;
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
+  return pa_detail::launch_paged_decode_scored(a, sums_out, sums_in, sums_len, num_new,
+                                               reinterpret_cast<cudaStream_t>(stream));
+}
+
 }  // extern "C"

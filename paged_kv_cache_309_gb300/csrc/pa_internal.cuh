@@ -641,9 +641,16 @@ struct DecodeArgs {
   const void* new_k;       // fused decode step: [B, H_KV, d] bf16 (else null)
   const void* new_v;
   const int64_t* slot_mapping;
+  float* scores;           // accumulated weights (else null): see DecodeParams
+  float* final_lse;
 };
 pa_status launch_paged_decode(const DecodeArgs& a, cudaStream_t stream);
 pa_status launch_paged_decode_q4(const DecodeArgs& a, cudaStream_t stream);  // decode_q4.cu
+// decode_scored.cu: the decode call of a's cache type, then the weights added up
+size_t scored_workspace_bytes(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads,
+                              int32_t head_size, const DecodePlan& plan);
+pa_status launch_paged_decode_scored(DecodeArgs a, float* sums_out, const float* sums_in,
+                                     int32_t sums_len, int32_t num_new, cudaStream_t stream);
 
 struct PrefillArgs {
   void* out;

@@ -96,6 +96,12 @@ def _load():
     lib.pa_paged_decode_attention_q4.argtypes = [P, P, P, P, P, P, I32, I32, I32, I32, I32, I32,
                                                  I64, F32, I32, P, SZ, P]
     lib.pa_paged_decode_attention_q4.restype = E
+    lib.pa_paged_decode_scored_workspace_size.argtypes = [I32, I32, I32, I32, I32]
+    lib.pa_paged_decode_scored_workspace_size.restype = SZ
+    lib.pa_paged_decode_attention_scored.argtypes = [P, P, P, I32, I32, P, P, P, E, P, P, P, P, I32,
+                                                     I32, I32, I32, I32, I32, I64, F32, I32, P, SZ,
+                                                     P]
+    lib.pa_paged_decode_attention_scored.restype = E
     _lib = lib
     return lib
 
@@ -629,3 +635,51 @@ def pa_paged_decode_attention_q4(out, q, k_cache, v_cache, block_tables, context
         B, HQ, HKV, d, bs, block_tables.shape[1], nb, float(scale), int(max_context_len),
         _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream))
     _check(st, "pa_paged_decode_attention_q4")
+
+
+# ------------------------------------------------ attention weights, eviction --
+def pa_paged_decode_scored_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_size,
+                                          max_context_len):
+    return int(_load().pa_paged_decode_scored_workspace_size(num_seqs, num_q_heads, num_kv_heads,
+                                                             head_size, max_context_len))
+
+
+def decode_scored_workspace(num_seqs, num_q_heads, num_kv_heads, head_size, max_context_len,
+                            device=None):
+    """A zeroed device workspace for pa_paged_decode_attention_scored (allocated by torch)."""
+    n = pa_paged_decode_scored_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_size,
+                                              max_context_len)
+    return torch.zeros(max(n, 256), dtype=torch.uint8, device=device or "cuda")
+
+
+def _sums(t, name, B, H):
+    _on_device(**{name: t})
+    _need(t.dtype == torch.float32 and t.dim() == 3 and t.shape[:2] == (B, H) and t.is_contiguous(),
+          f"{name} must be float32 [B, H_KV, tokens], contiguous")
+
+
+def pa_paged_decode_attention_scored(out, sums_out, sums, num_new, q, k_cache, v_cache,
+                                     block_tables, context_lens, scale, max_context_len, workspace,
+                                     k_scale=None, v_scale=None, stream=None):
+    """Decode attention (bf16, float8_e4m3fn with optional scales, or uint8
+    4-bit caches) that also adds each token's attention weight, summed over a
+    kv head's query heads: sums_out [B, H_KV, T] <- sums + weights, the last
+    num_new tokens of a sequence starting from 0.  sums_out may be sums.
+    workspace from decode_scored_workspace."""
+    B, HQ, HKV, d, bs, nb = _decode_shapes(out, q, k_cache, v_cache, block_tables, context_lens,
+                                           workspace)
+    _scales(k_scale, v_scale)
+    _sums(sums, "sums", B, HKV)
+    _sums(sums_out, "sums_out", B, HKV)
+    _need(sums.shape == sums_out.shape, "sums_out must match sums")
+    _need(0 <= num_new, "num_new must not be negative")
+    _need(k_scale is None or k_cache.dtype == torch.float8_e4m3fn,
+          "k_scale/v_scale apply to an e4m3 cache")
+    dtype = PA_Q4 if k_cache.dtype == torch.uint8 else _dtype(k_cache)
+    st = _load().pa_paged_decode_attention_scored(
+        _ptr(out), _ptr(sums_out), _ptr(sums), sums.shape[2], min(int(num_new), 2 ** 31 - 1),
+        _ptr(q), _ptr(k_cache), _ptr(v_cache), dtype, _ptr(k_scale), _ptr(v_scale),
+        _ptr(block_tables), _ptr(context_lens), B, HQ, HKV, d, bs, block_tables.shape[1], nb,
+        float(scale), int(max_context_len), _ptr(workspace),
+        workspace.numel() * workspace.element_size(), _stream(stream))
+    _check(st, "pa_paged_decode_attention_scored")

@@ -182,3 +182,53 @@ def test_decode_q4_binding_refusals(monkeypatch):
     for bad in _bad_decode_tensors(good) + [dict(k_cache=bf16, v_cache=bf16)]:
         with pytest.raises(ValueError):
             pa.pa_paged_decode_attention_q4(**{**good, **bad})
+
+
+# ------------------------------------------------------- accumulated weights --
+def _scored(lib, **kw):
+    a = dict(out=FAKE, so=FAKE, si=FAKE, T=128, new=1, q=FAKE, kc=FAKE, vc=FAKE, cd=pa.PA_BF16,
+             ks=None, vs=None, bt=FAKE, cl=FAKE, B=4, HQ=32, HKV=8, d=128, bs=16, mbps=8, nb=64,
+             scale=0.088, maxctx=128, ws=FAKE, wsb=1 << 30)
+    a.update(kw)
+    return lib.pa_paged_decode_attention_scored(
+        a["out"], a["so"], a["si"], a["T"], a["new"], a["q"], a["kc"], a["vc"], a["cd"], a["ks"],
+        a["vs"], a["bt"], a["cl"], a["B"], a["HQ"], a["HKV"], a["d"], a["bs"], a["mbps"], a["nb"],
+        a["scale"], a["maxctx"], a["ws"], a["wsb"], None)
+
+
+def test_scored_rejects(lib):
+    for cd in (pa.PA_BF16, pa.PA_FP8_E4M3, pa.PA_Q4):
+        assert _scored(lib, B=0, cd=cd) == pa.PA_OK
+    for bad in (dict(so=None), dict(si=None), dict(T=0), dict(T=-1), dict(new=-1), dict(ks=FAKE),
+                dict(ks=FAKE, vs=FAKE), dict(ks=FAKE, vs=FAKE, cd=pa.PA_Q4), dict(q=None),
+                dict(HQ=12), dict(so=P(0x100000 + 64)), dict(si=P(0x100000 + 4 * 8 * 128 * 4 - 4))):
+        assert _scored(lib, **bad) == pa.PA_ERR_INVALID, bad
+    for bad in (dict(cd=pa.PA_FP16), dict(cd=pa.PA_FP32), dict(cd=9), dict(d=64), dict(bs=12),
+                dict(HQ=24), dict(B=65536, wsb=1 << 50)):
+        assert _scored(lib, **bad) == pa.PA_ERR_UNSUPPORTED, bad
+    for bad in (dict(so=P(0x100002), si=P(0x100002)), dict(out=FAKE_MIS), dict(ws=P(0x100010))):
+        assert _scored(lib, **bad) == pa.PA_ERR_ALIGN, bad
+    # the decode workspace alone is too small
+    small = lib.pa_paged_decode_workspace_size(4, 32, 8, 128, 128)
+    assert _scored(lib, wsb=small) == pa.PA_ERR_WORKSPACE
+    need = lib.pa_paged_decode_scored_workspace_size(4, 32, 8, 128, 128)
+    assert need >= small + 4 * 32 * 128 * 4
+    assert _scored(lib, wsb=need - 1) == pa.PA_ERR_WORKSPACE
+    assert lib.pa_paged_decode_scored_workspace_size(-1, 32, 8, 128, 128) == 0
+    assert lib.pa_paged_decode_scored_workspace_size(4, 32, 0, 128, 128) == 0
+
+
+def test_scored_binding_refusals(monkeypatch):
+    sums = torch.zeros(2, 4, 30)
+    good = dict(_decode_tensors(128, torch.bfloat16), sums_out=sums, sums=sums, num_new=1)
+    with pytest.raises(ValueError, match="CUDA tensor"):
+        pa.pa_paged_decode_attention_scored(**good)
+    monkeypatch.setattr(pa, "_on_device", lambda **kw: None)
+    monkeypatch.setattr(pa, "_load", lambda: pytest.fail("reached the library"))
+    one = torch.zeros(1)
+    for bad in _bad_decode_tensors(good) + [
+            dict(sums=sums.double(), sums_out=sums.double()), dict(sums=sums[:, :2]),
+            dict(sums_out=sums[:, :, :20].contiguous()), dict(sums=sums.transpose(1, 2)),
+            dict(num_new=-1), dict(k_scale=one), dict(k_scale=one, v_scale=one)]:
+        with pytest.raises(ValueError):
+            pa.pa_paged_decode_attention_scored(**{**good, **bad})
