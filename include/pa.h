@@ -17,6 +17,8 @@
  *   pa_paged_decode_attention_q4   decode attention over a 4-bit cache
  *   pa_paged_decode_attention_scored  decode attention that also adds up each cached
  *                                  token's attention weight
+ *   pa_evict_select                which tokens of a row to keep, by those weights
+ *   pa_cache_compact               move the kept rows together through block tables
  *
  * Common rules
  *   - Every pointer argument except the `*_host` ones is a DEVICE pointer on
@@ -565,6 +567,60 @@ pa_status pa_paged_decode_attention_scored(
     int32_t head_size, int32_t block_size, int32_t max_blocks_per_seq, int64_t num_blocks,
     float scale, int32_t max_context_len, void *workspace, size_t workspace_bytes,
     pa_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * pa_evict_select -- which tokens each (sequence, kv head) keeps.
+ *
+ * With L = context_lens[b], clipped to [0, sums_len], row (b, g) keeps
+ * n = min(L, budget) tokens: first the protected ones (t < num_sink or
+ * t >= L - num_recent), then those of the largest sums[b, g, t]; of equal
+ * ones the lowest t.  A NaN sum counts as smaller than every number; +0 and
+ * -0 are equal.
+ *     keep[b, g, 0..n)     = the kept t, ascending; keep[b, g, n..budget) = -1
+ *     new_lens[b]          = n
+ *     sums_out[b, g, j]    = sums_in[b, g, keep[b, g, j]]  for j < n, other
+ *                            elements left as they were
+ * sums_in [num_seqs, num_kv_heads, sums_len] fp32 contiguous; sums_out NULL,
+ *   the same array, or another of the same shape that does not overlap it.
+ * keep [num_seqs, num_kv_heads, budget] int32 contiguous; new_lens
+ *   [num_seqs] int32, not context_lens itself (PA_ERR_INVALID).
+ * budget >= 1; num_sink, num_recent >= 0, num_sink + num_recent <= budget
+ *   (else PA_ERR_INVALID).  num_seqs * num_kv_heads of 2^27 or more:
+ *   PA_ERR_UNSUPPORTED.
+ * ---------------------------------------------------------------------- */
+pa_status pa_evict_select(int32_t *keep, int32_t *new_lens, float *sums_out,
+                          const float *sums_in, const int32_t *context_lens, int32_t num_seqs,
+                          int32_t num_kv_heads, int32_t sums_len, int32_t budget,
+                          int32_t num_sink, int32_t num_recent, pa_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * pa_cache_compact -- move the kept rows together.
+ *
+ * For every (b, g), j < min(keep_lens[b], keep_len) and t = keep[b, g, j]:
+ *     row j of sequence b, kv head g, read through dst_block_tables
+ *         <- row t, read through src_block_tables
+ * in k_cache and v_cache (v_cache may be NULL: a K-only or MLA latent cache).
+ * A row whose index or block is out of range (t < 0, past a table, a block id outside
+ * the pool) is not moved.  All other rows of the pool are left as they were.
+ *
+ * In place: pass the same pointer for both tables; keep must then be
+ * ascending in each row with keep[b, g, j] >= j (as pa_evict_select writes
+ * it) and no two sequences share blocks.  Otherwise the destination blocks
+ * must be distinct from each other and from every source block.
+ * k_cache, v_cache: [num_blocks, block_size, num_kv_heads, row_bytes],
+ *   contiguous, any element type; row_bytes a multiple of 16 (256 bf16, 128
+ *   e4m3, 80 PA_Q4 at head_size 128; 1152 an MLA latent row, one head).
+ * keep: [num_seqs, num_kv_heads, keep_len] int32, contiguous; keep_lens
+ *   [num_seqs] int32.  block_size >= 1.  Tables [num_seqs, src/dst_max_blocks]
+ *   int32.  num_seqs or num_kv_heads above 65535: PA_ERR_UNSUPPORTED.
+ * Alignment: caches 16 bytes.
+ * ---------------------------------------------------------------------- */
+pa_status pa_cache_compact(void *k_cache, void *v_cache, int32_t row_bytes, const int32_t *keep,
+                           const int32_t *keep_lens, int32_t keep_len,
+                           const int32_t *src_block_tables, int32_t src_max_blocks,
+                           const int32_t *dst_block_tables, int32_t dst_max_blocks,
+                           int32_t num_seqs, int32_t num_kv_heads, int32_t block_size,
+                           int64_t num_blocks, pa_stream_t stream);
 
 /* Diagnostic of the failure path every pipeline kernel shares: launches one
  * CTA whose threads wait, with the same bounded wait the pipelines use, on a

@@ -33,6 +33,12 @@ namespace {
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
+// whether two arrays of `size` bytes share part of their range but not all of it
+bool partly_overlap(const void* x, const void* y, uintptr_t size) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(x), b = reinterpret_cast<uintptr_t>(y);
+  return a != b && a < b + size && b < a + size;
+}
+
 bool is_src_dtype(pa_dtype d) { return d == PA_BF16 || d == PA_FP16 || d == PA_FP32; }
 bool is_any_dtype(pa_dtype d) { return is_src_dtype(d) || d == PA_FP8_E4M3; }
 
@@ -631,9 +637,9 @@ pa_status pa_paged_decode_attention_scored(
   if (st != PA_OK) return st;
   if (!aligned(sums_out, 4) || !aligned(sums_in, 4)) return PA_ERR_ALIGN;
   // in place or apart: a partial overlap would read sums already written
-  const uintptr_t size = static_cast<uintptr_t>(num_seqs) * num_kv_heads * sums_len * 4;
-  const uintptr_t o = reinterpret_cast<uintptr_t>(sums_out), i = reinterpret_cast<uintptr_t>(sums_in);
-  if (o != i && o < i + size && i < o + size) return PA_ERR_INVALID;
+  if (partly_overlap(sums_out, sums_in,
+                     static_cast<uintptr_t>(num_seqs) * num_kv_heads * sums_len * 4))
+    return PA_ERR_INVALID;
   const size_t need =
       pa_detail::scored_workspace_bytes(num_seqs, num_q_heads, num_kv_heads, head_size, a.plan);
   if (workspace == nullptr || workspace_bytes < need) return PA_ERR_WORKSPACE;
@@ -644,6 +650,78 @@ pa_status pa_paged_decode_attention_scored(
   a.v_scale = v_scale;
   return pa_detail::launch_paged_decode_scored(a, sums_out, sums_in, sums_len, num_new,
                                                reinterpret_cast<cudaStream_t>(stream));
+}
+
+pa_status pa_evict_select(int32_t* keep, int32_t* new_lens, float* sums_out,
+                          const float* sums_in, const int32_t* context_lens, int32_t num_seqs,
+                          int32_t num_kv_heads, int32_t sums_len, int32_t budget,
+                          int32_t num_sink, int32_t num_recent, pa_stream_t stream) {
+  if (num_seqs < 0 || num_kv_heads <= 0 || sums_len <= 0 || budget < 1 || num_sink < 0 ||
+      num_recent < 0 || static_cast<int64_t>(num_sink) + num_recent > budget)
+    return PA_ERR_INVALID;
+  if (num_seqs == 0) return PA_OK;
+  if (keep == nullptr || new_lens == nullptr || sums_in == nullptr || context_lens == nullptr ||
+      new_lens == context_lens)
+    return PA_ERR_INVALID;
+  const int64_t rows = static_cast<int64_t>(num_seqs) * num_kv_heads;
+  if (rows >= (1ll << 27)) return PA_ERR_UNSUPPORTED;
+  if (!aligned(keep, 4) || !aligned(new_lens, 4) || !aligned(sums_in, 4) ||
+      !aligned(sums_out, 4) || !aligned(context_lens, 4))
+    return PA_ERR_ALIGN;
+  if (sums_out != nullptr &&
+      partly_overlap(sums_out, sums_in, static_cast<uintptr_t>(rows) * sums_len * 4))
+    return PA_ERR_INVALID;
+  pa_detail::SelectArgs a{};
+  a.keep = keep;
+  a.new_lens = new_lens;
+  a.sums_out = sums_out;
+  a.sums_in = sums_in;
+  a.context_lens = context_lens;
+  a.num_seqs = num_seqs;
+  a.num_kv_heads = num_kv_heads;
+  a.sums_len = sums_len;
+  a.budget = budget;
+  a.num_sink = num_sink;
+  a.num_recent = num_recent;
+  return pa_detail::launch_evict_select(a, reinterpret_cast<cudaStream_t>(stream));
+}
+
+pa_status pa_cache_compact(void* k_cache, void* v_cache, int32_t row_bytes, const int32_t* keep,
+                           const int32_t* keep_lens, int32_t keep_len,
+                           const int32_t* src_block_tables, int32_t src_max_blocks,
+                           const int32_t* dst_block_tables, int32_t dst_max_blocks,
+                           int32_t num_seqs, int32_t num_kv_heads, int32_t block_size,
+                           int64_t num_blocks, pa_stream_t stream) {
+  if (row_bytes <= 0 || keep_len < 0 || src_max_blocks <= 0 || dst_max_blocks <= 0 ||
+      num_seqs < 0 || num_kv_heads <= 0 || block_size <= 0 || num_blocks < 0)
+    return PA_ERR_INVALID;
+  if (num_seqs == 0 || keep_len == 0 || num_blocks == 0) return PA_OK;  // nothing to move
+  if (k_cache == nullptr || keep == nullptr || keep_lens == nullptr ||
+      src_block_tables == nullptr || dst_block_tables == nullptr)
+    return PA_ERR_INVALID;
+  const bool in_place = src_block_tables == dst_block_tables;
+  if (in_place && src_max_blocks != dst_max_blocks) return PA_ERR_INVALID;
+  if (num_seqs > 65535 || num_kv_heads > 65535) return PA_ERR_UNSUPPORTED;
+  if (row_bytes % 16 != 0 || !aligned(k_cache, 16) || !aligned(v_cache, 16) ||
+      !aligned(keep, 4) || !aligned(keep_lens, 4) || !aligned(src_block_tables, 4) ||
+      !aligned(dst_block_tables, 4))
+    return PA_ERR_ALIGN;
+  pa_detail::CompactArgs a{};
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  a.keep = keep;
+  a.keep_lens = keep_lens;
+  a.src_table = src_block_tables;
+  a.dst_table = dst_block_tables;
+  a.keep_len = keep_len;
+  a.src_max_blocks = src_max_blocks;
+  a.dst_max_blocks = dst_max_blocks;
+  a.num_seqs = num_seqs;
+  a.num_kv_heads = num_kv_heads;
+  a.block_size = block_size;
+  a.row_units = row_bytes / 16;
+  a.num_blocks = num_blocks;
+  return pa_detail::launch_cache_compact(a, in_place, reinterpret_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

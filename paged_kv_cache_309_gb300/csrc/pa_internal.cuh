@@ -652,6 +652,30 @@ size_t scored_workspace_bytes(int32_t num_seqs, int32_t num_q_heads, int32_t num
 pa_status launch_paged_decode_scored(DecodeArgs a, float* sums_out, const float* sums_in,
                                      int32_t sums_len, int32_t num_new, cudaStream_t stream);
 
+struct SelectArgs {  // evict.cu
+  int32_t* keep;
+  int32_t* new_lens;
+  float* sums_out;  // null: not wanted
+  const float* sums_in;
+  const int32_t* context_lens;
+  int32_t num_seqs, num_kv_heads, sums_len, budget, num_sink, num_recent;
+};
+pa_status launch_evict_select(const SelectArgs& a, cudaStream_t stream);
+
+struct CompactArgs {  // evict.cu
+  void* k_cache;
+  void* v_cache;  // null: K only
+  const int32_t* keep;
+  const int32_t* keep_lens;
+  const int32_t* src_table;
+  const int32_t* dst_table;
+  int32_t keep_len, src_max_blocks, dst_max_blocks, num_seqs, num_kv_heads, block_size;
+  int32_t row_units;  // 16-byte units of a row
+  int64_t num_blocks;
+  int32_t rows_per_cta, units_per_cta;  // set by the launcher
+};
+pa_status launch_cache_compact(CompactArgs a, bool in_place, cudaStream_t stream);
+
 struct PrefillArgs {
   void* out;
   const void* q;

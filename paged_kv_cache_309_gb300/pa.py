@@ -102,6 +102,10 @@ def _load():
                                                      I32, I32, I32, I32, I32, I64, F32, I32, P, SZ,
                                                      P]
     lib.pa_paged_decode_attention_scored.restype = E
+    lib.pa_evict_select.argtypes = [P, P, P, P, P, I32, I32, I32, I32, I32, I32, P]
+    lib.pa_evict_select.restype = E
+    lib.pa_cache_compact.argtypes = [P, P, I32, P, P, I32, P, I32, P, I32, I32, I32, I32, I64, P]
+    lib.pa_cache_compact.restype = E
     _lib = lib
     return lib
 
@@ -683,3 +687,54 @@ def pa_paged_decode_attention_scored(out, sums_out, sums, num_new, q, k_cache, v
         float(scale), int(max_context_len), _ptr(workspace),
         workspace.numel() * workspace.element_size(), _stream(stream))
     _check(st, "pa_paged_decode_attention_scored")
+
+
+def pa_evict_select(keep, new_lens, sums_out, sums, context_lens, budget, num_sink, num_recent,
+                    stream=None):
+    """keep [B, H_KV, budget] int32 <- the tokens of each row to keep, ascending,
+    -1 behind them: the first num_sink and last num_recent, then the largest
+    sums [B, H_KV, T] float32 (ties to the lowest token); new_lens [B] int32 <-
+    their number; sums_out (None, sums itself or another like it) <- their sums."""
+    _on_device(keep=keep, new_lens=new_lens, context_lens=context_lens)
+    _need(keep.dtype == torch.int32 and keep.dim() == 3 and keep.is_contiguous(),
+          "keep must be int32 [B, H_KV, budget], contiguous")
+    B, H, budget_dim = keep.shape
+    _need(budget_dim == budget, "keep must be [B, H_KV, budget]")
+    _sums(sums, "sums", B, H)
+    if sums_out is not None:
+        _sums(sums_out, "sums_out", B, H)
+        _need(sums_out.shape == sums.shape, "sums_out must match sums")
+    for t, name in ((new_lens, "new_lens"), (context_lens, "context_lens")):
+        _need(t.dtype == torch.int32 and t.numel() == B and t.is_contiguous(),
+              f"{name} must be int32 [B]")
+    _check(_load().pa_evict_select(_ptr(keep), _ptr(new_lens), _ptr(sums_out), _ptr(sums),
+                                   _ptr(context_lens), B, H, sums.shape[2], budget, num_sink,
+                                   num_recent, _stream(stream)), "pa_evict_select")
+
+
+def pa_cache_compact(k_cache, v_cache, keep, keep_lens, src_block_tables, dst_block_tables,
+                     stream=None):
+    """Row j of each (sequence, kv head), read through dst_block_tables, <- its
+    row keep[b, g, j], read through src_block_tables, for j < keep_lens[b];
+    caches [num_blocks, bs, H_KV, row] of any type (v_cache may be None), rows
+    of a multiple of 16 bytes.  In place: pass one table twice (keep
+    ascending)."""
+    _on_device(k_cache=k_cache, v_cache=v_cache, keep=keep, keep_lens=keep_lens,
+               src_block_tables=src_block_tables, dst_block_tables=dst_block_tables)
+    _need(k_cache.dim() == 4 and k_cache.is_contiguous(),
+          "k_cache must be [num_blocks, bs, H_KV, row], contiguous")
+    _need(v_cache is None or (v_cache.shape == k_cache.shape and v_cache.dtype == k_cache.dtype
+                              and v_cache.is_contiguous()), "v_cache must match k_cache")
+    nb, bs, H, row = k_cache.shape
+    _need(keep.dtype == torch.int32 and keep.dim() == 3 and keep.shape[1] == H
+          and keep.is_contiguous(), "keep must be int32 [B, H_KV, n], contiguous")
+    B = keep.shape[0]
+    _need(keep_lens.dtype == torch.int32 and keep_lens.numel() == B and keep_lens.is_contiguous(),
+          "keep_lens must be int32 [B]")
+    for t, name in ((src_block_tables, "src_block_tables"), (dst_block_tables, "dst_block_tables")):
+        _need(t.dtype == torch.int32 and t.dim() == 2 and t.shape[0] == B and t.is_contiguous(),
+              f"{name} must be int32 [B, blocks], contiguous")
+    _check(_load().pa_cache_compact(
+        _ptr(k_cache), _ptr(v_cache), row * k_cache.element_size(), _ptr(keep), _ptr(keep_lens),
+        keep.shape[2], _ptr(src_block_tables), src_block_tables.shape[1], _ptr(dst_block_tables),
+        dst_block_tables.shape[1], B, H, bs, nb, _stream(stream)), "pa_cache_compact")

@@ -232,3 +232,85 @@ def test_scored_binding_refusals(monkeypatch):
             dict(num_new=-1), dict(k_scale=one), dict(k_scale=one, v_scale=one)]:
         with pytest.raises(ValueError):
             pa.pa_paged_decode_attention_scored(**{**good, **bad})
+
+
+# ------------------------------------------------------------------ eviction --
+def test_oracle_selection_by_hand():
+    nan = np.nan
+    sums = np.array([[[5., 1., 3., 3., nan, 3., 0., 9.]]], np.float32)
+    keep, new = lc.evict_select(sums, [8], 4, 0, 0)
+    assert keep.tolist() == [[[0, 2, 3, 7]]] and new.tolist() == [4]
+    keep, _ = lc.evict_select(sums, [8], 4, 2, 1)
+    assert keep.tolist() == [[[0, 1, 2, 7]]]
+    keep, new = lc.evict_select(sums, [3], 4, 1, 1)
+    assert keep.tolist() == [[[0, 1, 2, -1]]] and new.tolist() == [3]
+
+
+def _select(lib, **kw):
+    a = dict(keep=FAKE, new=FAKE, so=P(0x900000), si=P(0x300000), cl=P(0x200000), B=4, H=8, T=128,
+             budget=64, sink=4, recent=16)
+    a.update(kw)
+    return lib.pa_evict_select(a["keep"], a["new"], a["so"], a["si"], a["cl"], a["B"], a["H"],
+                               a["T"], a["budget"], a["sink"], a["recent"], None)
+
+
+def test_select_rejects(lib):
+    assert _select(lib, B=0) == pa.PA_OK
+    for bad in (dict(keep=None), dict(new=None), dict(si=None), dict(cl=None), dict(cl=FAKE),
+                dict(B=-1), dict(H=0), dict(T=0), dict(budget=0), dict(sink=-1), dict(recent=-1),
+                dict(sink=60), dict(sink=2 ** 31 - 1, recent=2 ** 31 - 1),
+                dict(so=P(0x300000 + 4)), dict(so=P(0x300000 - 4))):
+        assert _select(lib, **bad) == pa.PA_ERR_INVALID, bad
+    assert _select(lib, B=1 << 24) == pa.PA_ERR_UNSUPPORTED
+    for n in ("keep", "new", "so", "si", "cl"):
+        assert _select(lib, **{n: P(0x100002)}) == pa.PA_ERR_ALIGN, n
+
+
+def _compact(lib, **kw):
+    a = dict(k=FAKE, v=FAKE, row=256, keep=FAKE, lens=FAKE, n=64, src=P(0x200000), sm=8,
+             dst=P(0x300000), dm=4, B=4, H=8, bs=16, nb=64)
+    a.update(kw)
+    return lib.pa_cache_compact(a["k"], a["v"], a["row"], a["keep"], a["lens"], a["n"], a["src"],
+                                a["sm"], a["dst"], a["dm"], a["B"], a["H"], a["bs"], a["nb"], None)
+
+
+def test_compact_rejects(lib):
+    for ok in (dict(B=0), dict(n=0), dict(nb=0), dict(B=0, k=None)):
+        assert _compact(lib, **ok) == pa.PA_OK, ok
+    for bad in (dict(k=None), dict(keep=None), dict(lens=None), dict(src=None), dict(dst=None),
+                dict(row=0), dict(n=-1), dict(sm=0), dict(dm=0), dict(B=-1), dict(H=0), dict(bs=0),
+                dict(nb=-1), dict(src=FAKE, dst=FAKE)):
+        assert _compact(lib, **bad) == pa.PA_ERR_INVALID, bad
+    for bad in (dict(B=65536), dict(H=65536)):
+        assert _compact(lib, **bad) == pa.PA_ERR_UNSUPPORTED, bad
+    for bad in (dict(row=72), dict(k=FAKE_MIS), dict(v=FAKE_MIS), dict(keep=P(0x100002)),
+                dict(src=P(0x100002))):
+        assert _compact(lib, **bad) == pa.PA_ERR_ALIGN, bad
+
+
+def test_eviction_binding_refusals(monkeypatch):
+    sums = torch.zeros(2, 4, 30)
+    i32 = lambda *s: torch.zeros(*s, dtype=torch.int32)
+    sel = dict(keep=i32(2, 4, 10), new_lens=i32(2), sums_out=sums.clone(), sums=sums,
+               context_lens=i32(2), budget=10, num_sink=1, num_recent=2)
+    c = torch.zeros(6, 16, 4, 80, dtype=torch.uint8)
+    com = dict(k_cache=c, v_cache=c.clone(), keep=i32(2, 4, 10), keep_lens=i32(2),
+               src_block_tables=i32(2, 3), dst_block_tables=i32(2, 2))
+    with pytest.raises(ValueError, match="CUDA tensor"):
+        pa.pa_evict_select(**sel)
+    with pytest.raises(ValueError, match="CUDA tensor"):
+        pa.pa_cache_compact(**com)
+    monkeypatch.setattr(pa, "_on_device", lambda **kw: None)
+    monkeypatch.setattr(pa, "_load", lambda: pytest.fail("reached the library"))
+    for bad in (dict(budget=11), dict(keep=i32(2, 4, 10).long()), dict(keep=i32(2, 10)),
+                dict(keep=i32(2, 10, 4).transpose(1, 2)), dict(sums=sums.half()),
+                dict(sums_out=sums[:, :, :20].contiguous()), dict(sums=sums[:1]), dict(new_lens=i32(3)),
+                dict(context_lens=i32(2).long()), dict(context_lens=i32(4)[::2])):
+        with pytest.raises(ValueError):
+            pa.pa_evict_select(**{**sel, **bad})
+    for bad in (dict(v_cache=c[:5]), dict(v_cache=c.char()), dict(k_cache=c.transpose(1, 2)),
+                dict(keep=i32(2, 3, 10)), dict(keep=i32(2, 4, 10).long()), dict(keep_lens=i32(3)),
+                dict(src_block_tables=i32(3, 3)), dict(dst_block_tables=i32(2, 2).long()),
+                dict(src_block_tables=i32(3, 2).T), dict(keep_lens=i32(2).long())):
+        with pytest.raises(ValueError):
+            pa.pa_cache_compact(**{**com, **bad})
