@@ -123,8 +123,8 @@ pa_status check_q4(const void* key, const void* value, pa_dtype dtype, int64_t n
   a->value_stride = value ? value_stride : 0;
   a->block_stride = block_stride;
   a->num_slots = num_blocks * block_size;
-  a->row_chunks = static_cast<int32_t>(row / 8);
-  a->chunks_per_head = head_size / 8;
+  a->row_units = static_cast<int32_t>(row / 16);
+  a->units_per_head = head_size / 16;
   a->block_size = block_size;
   return PA_OK;
 }

@@ -592,10 +592,11 @@ struct Q4CacheArgs {
   int64_t value_stride;  // elements
   int64_t block_stride;  // bytes
   int64_t num_slots;
-  int32_t row_chunks;       // (num_heads * head_size) / 8
-  int32_t chunks_per_head;  // head_size / 8
+  int32_t row_units;       // (num_heads * head_size) / 16
+  int32_t units_per_head;  // head_size / 16
   int32_t block_size;
-  int32_t groups;  // warps per token (set by the launcher)
+  int32_t groups;  // warps per token; 8-byte code accesses (set by the launcher)
+  bool wide;
 };
 pa_status launch_reshape_and_cache_q4(Q4CacheArgs a, pa_dtype src, cudaStream_t stream);
 pa_status launch_gather_cache_q4(Q4CacheArgs a, pa_dtype dst, cudaStream_t stream);
