@@ -43,21 +43,60 @@ template <typename S>
 struct Unit {
   Vec8<S> v[2];
 };
-// (through L1: the two 16-byte halves of a 32-byte sector are two loads)
-__device__ __forceinline__ uint4 ld16(const void* p) {
-  return __ldg(static_cast<const uint4*>(p));
+// 32 bytes in one access where the address allows it: two accesses of 16
+// bytes each touch every 32-byte sector twice.
+struct U8 {
+  uint4 a, b;
+};
+__device__ __forceinline__ U8 ld32(const void* p, bool whole) {
+  U8 v;
+  if (whole) {
+    asm volatile("ld.global.nc.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(v.a.x), "=r"(v.a.y), "=r"(v.a.z), "=r"(v.a.w), "=r"(v.b.x), "=r"(v.b.y),
+                   "=r"(v.b.z), "=r"(v.b.w)
+                 : "l"(p));
+  } else {
+    v.a = __ldg(static_cast<const uint4*>(p));
+    v.b = __ldg(static_cast<const uint4*>(p) + 1);
+  }
+  return v;
+}
+__device__ __forceinline__ void st32(void* p, const U8& v, bool whole) {
+  if (whole) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(v.a.x),
+                 "r"(v.a.y), "r"(v.a.z), "r"(v.a.w), "r"(v.b.x), "r"(v.b.y), "r"(v.b.z),
+                 "r"(v.b.w)
+                 : "memory");
+  } else {
+    static_cast<uint4*>(p)[0] = v.a;
+    static_cast<uint4*>(p)[1] = v.b;
+  }
 }
 template <typename S>
-__device__ __forceinline__ Unit<S> load_unit(const S* p) {
+__device__ __forceinline__ Unit<S> load_unit(const S* p, bool whole) {
   Unit<S> u;
   if constexpr (sizeof(S) == 2) {
-    u.v[0].u = ld16(p);
-    u.v[1].u = ld16(p + 8);
+    const U8 x = ld32(p, whole);
+    u.v[0].u = x.a;
+    u.v[1].u = x.b;
   } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) u.v[i >> 1].u[i & 1] = ld16(p + 4 * i);
+    for (int i = 0; i < 2; ++i) {
+      const U8 x = ld32(p + 8 * i, whole);
+      u.v[i].u[0] = x.a;
+      u.v[i].u[1] = x.b;
+    }
   }
   return u;
+}
+template <typename S>
+__device__ __forceinline__ void store_unit(S* p, const Unit<S>& u, bool whole) {
+  if constexpr (sizeof(S) == 2) {
+    st32(p, U8{u.v[0].u, u.v[1].u}, whole);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) st32(p + 8 * i, U8{u.v[i].u[0], u.v[i].u[1]}, whole);
+  }
 }
 
 __device__ __forceinline__ uint32_t min2(uint32_t a, uint32_t b, bf16) {
@@ -128,30 +167,9 @@ __device__ __forceinline__ float2 group_min_max(const Unit<S>& u) {
   }
 }
 
-// Quantises the lane's unit together with its neighbour's: two code words and
-// the group's (s, m) as fp16 bits, s in the low half.
-template <typename S>
-__device__ __forceinline__ uint2 quantise(const Unit<S>& u, uint32_t& meta) {
-  const float2 mm = group_min_max(u);
-  const float mn = mm.x, mx = mm.y;
-  const bool fine = mn >= -3.4028235e38f && mx <= 3.4028235e38f;  // no NaN, no infinity
-  const __half mh = __float2half_rn(fminf(fmaxf(mn, -65504.f), 65504.f));
-  const float m = __half2float(mh);
-  Divisor by15;
-  by15.s = 15.f;
-  by15.r = 0x1.111112p-4f;  // RN(1 / 15)
-  by15.fast = true;
-  const __half sh = __float2half_rn(fminf(fmaxf(div_rn(mx - m, by15), 0.f), 1023.f));
-  const float s = __half2float(sh);
-  float r;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
-  r = s > 0.f ? r : 0.f;  // s = 0: every code 0
-  meta = fine ? static_cast<uint32_t>(__half_as_ushort(sh)) |
-                    (static_cast<uint32_t>(__half_as_ushort(mh)) << 16)
-              : 0x7FFF7FFFu;
-  // codes outside [0, 15] before the clamp: the minimum's rounding, a
-  // subnormal or saturated scale -- the same answer in both lanes of a group
-  const bool clamp = (mx - m) * r > 15.49f || (mn - m) * r < -0.49f;
+// The codes of a unit.  kClamp: some lie outside [0, 15] before the clamp.
+template <bool kClamp, typename S>
+__device__ __forceinline__ uint2 codes_of(const Unit<S>& u, float m, float s, float r) {
   const float2 nm = make_float2(-m, -m), r2 = make_float2(r, r), ns = make_float2(-s, -s);
   // 1.5 * 2^23: the sum's last bit counts 1 (also just below 0), rounded to even
   const float2 magic = make_float2(12582912.f, 12582912.f);
@@ -166,7 +184,7 @@ __device__ __forceinline__ uint2 quantise(const Unit<S>& u, uint32_t& meta) {
       const float2 t = add2_rn(make_float2(f[e], f[e + 1]), nm);
       float2 y = mul2_rn(t, r2);
       y = fma2_rn(fma2_rn(ns, y, t), r2, y);
-      if (clamp) {
+      if (kClamp) {
         y.x = fminf(fmaxf(y.x, 0.f), 15.f);
         y.y = fminf(fmaxf(y.y, 0.f), 15.f);
       }
@@ -175,9 +193,43 @@ __device__ __forceinline__ uint2 quantise(const Unit<S>& u, uint32_t& meta) {
       w = (w << 4) + __float_as_uint(c.y);
       w = (w << 4) + __float_as_uint(c.x);
     }
-    w -= 0x4B400000u + 0xB4000000u + 0x40000000u;  // shifted by 0, 4 and 8; the rest fell out
-    (half ? word.y : word.x) = fine ? w : 0u;
+    // shifted by 0, 4 and 8; the rest fell out of the word
+    (half ? word.y : word.x) = w - (0x4B400000u + 0xB4000000u + 0x40000000u);
   }
+  return word;
+}
+
+// Quantises the lane's unit together with its neighbour's: two code words and
+// the group's (s, m) as fp16 bits, s in the low half.
+template <typename S>
+__device__ __forceinline__ uint2 quantise(const Unit<S>& u, uint32_t& meta) {
+  const float2 mm = group_min_max(u);
+  const float mn = mm.x, mx = mm.y;
+  const bool fine = mn >= -3.4028235e38f && mx <= 3.4028235e38f;  // no NaN, no infinity
+  const __half mh = __float2half_rn(fminf(fmaxf(mn, -65504.f), 65504.f));
+  const float m = __half2float(mh);
+  // span / 15: RN(1 / 15) and one correction, as for the codes (15 has 4 bits)
+  const float span = mx - m;
+  float q = __fmul_rn(span, 0x1.111112p-4f);
+  q = __fmaf_rn(__fmaf_rn(-15.f, q, span), 0x1.111112p-4f, q);
+  const __half sh = __float2half_rn(fminf(fmaxf(q, 0.f), 1023.f));
+  const float s = __half2float(sh);
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
+  r = s > 0.f ? r : 0.f;  // s = 0: every code 0
+  // codes outside [0, 15] before the clamp: the minimum's rounding, a
+  // subnormal or saturated scale, values that are not finite
+  const bool clamp = !(span * r <= 15.49f && (mn - m) * r >= -0.49f);
+  uint2 word;
+  if (__any_sync(0xffffffffu, clamp)) {
+    word = codes_of<true>(u, m, s, r);
+    meta = 0x7FFF7FFFu;
+    if (!fine) return make_uint2(0u, 0u);
+  } else {
+    word = codes_of<false>(u, m, s, r);
+  }
+  meta = static_cast<uint32_t>(__half_as_ushort(sh)) |
+         (static_cast<uint32_t>(__half_as_ushort(mh)) << 16);
   return word;
 }
 
@@ -220,8 +272,8 @@ __global__ void __launch_bounds__(kWarps * 32) reshape_and_cache_q4_kernel(Q4Cac
   const bool mine = c < a.row_units, has_v = a.value != nullptr;
   Unit<S> k{}, v{};
   if (mine) {
-    k = load_unit(static_cast<const S*>(a.key) + t * a.key_stride + 16 * c);
-    if (has_v) v = load_unit(static_cast<const S*>(a.value) + t * a.value_stride + 16 * c);
+    k = load_unit(static_cast<const S*>(a.key) + t * a.key_stride + 16 * c, a.whole32);
+    if (has_v) v = load_unit(static_cast<const S*>(a.value) + t * a.value_stride + 16 * c, a.whole32);
   }
   const RowPlace p = row_place(c, a.units_per_head);
   const int64_t dst = row_of(a, s);
@@ -294,15 +346,20 @@ __global__ void __launch_bounds__(kWarps * 32) gather_cache_q4_kernel(Q4CacheArg
              t * (tensor ? a.value_stride : a.key_stride) + 16 * c;
     const float2 sm = widen(meta[tensor], f16{});
     const float2 s2 = make_float2(sm.x, sm.x), m2 = make_float2(sm.y, sm.y);
-    store8(dst, restore<D>(word[tensor].x, s2, m2));
-    store8(dst + 8, restore<D>(word[tensor].y, s2, m2));
+    store_unit(dst, Unit<D>{{restore<D>(word[tensor].x, s2, m2), restore<D>(word[tensor].y, s2, m2)}},
+               a.whole32);
   }
 }
 
-pa_status grid_of(Q4CacheArgs& a, unsigned* grid) {
+pa_status grid_of(Q4CacheArgs& a, int64_t elem_bytes, unsigned* grid) {
   a.groups = (a.row_units + 31) / 32;
   // 8-byte accesses to the codes: head rows (10 * units bytes) and blocks on multiples of 8
   a.wide = a.units_per_head % 4 == 0 && a.block_stride % 8 == 0;
+  // 32-byte accesses to the rows
+  const int64_t key_step = a.key_stride * elem_bytes, value_step = a.value_stride * elem_bytes;
+  a.whole32 = ((reinterpret_cast<uintptr_t>(a.key) | reinterpret_cast<uintptr_t>(a.value) |
+                static_cast<uintptr_t>(key_step) | static_cast<uintptr_t>(value_step)) &
+               31u) == 0u;
   const int64_t blocks = (a.num_tokens * a.groups + kWarps - 1) / kWarps;
   if (blocks > 0x7FFFFFFFll) return PA_ERR_UNSUPPORTED;
   *grid = static_cast<unsigned>(blocks);
@@ -313,7 +370,7 @@ pa_status grid_of(Q4CacheArgs& a, unsigned* grid) {
 
 pa_status launch_reshape_and_cache_q4(Q4CacheArgs a, pa_dtype src, cudaStream_t stream) {
   unsigned grid = 0;
-  const pa_status st = grid_of(a, &grid);
+  const pa_status st = grid_of(a, src == PA_FP32 ? 4 : 2, &grid);
   if (st != PA_OK) return st;
   switch (src) {
     case PA_BF16: reshape_and_cache_q4_kernel<bf16><<<grid, kWarps * 32, 0, stream>>>(a); break;
@@ -326,7 +383,7 @@ pa_status launch_reshape_and_cache_q4(Q4CacheArgs a, pa_dtype src, cudaStream_t 
 
 pa_status launch_gather_cache_q4(Q4CacheArgs a, pa_dtype dst, cudaStream_t stream) {
   unsigned grid = 0;
-  const pa_status st = grid_of(a, &grid);
+  const pa_status st = grid_of(a, dst == PA_FP32 ? 4 : 2, &grid);
   if (st != PA_OK) return st;
   switch (dst) {
     case PA_BF16: gather_cache_q4_kernel<bf16><<<grid, kWarps * 32, 0, stream>>>(a); break;

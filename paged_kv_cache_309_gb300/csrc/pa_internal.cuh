@@ -595,8 +595,10 @@ struct Q4CacheArgs {
   int32_t row_units;       // (num_heads * head_size) / 16
   int32_t units_per_head;  // head_size / 16
   int32_t block_size;
-  int32_t groups;  // warps per token; 8-byte code accesses (set by the launcher)
-  bool wide;
+  // set by the launcher: warps per token; whether codes can be accessed by 8
+  // bytes and the rows of key/value by 32
+  int32_t groups;
+  bool wide, whole32;
 };
 pa_status launch_reshape_and_cache_q4(Q4CacheArgs a, pa_dtype src, cudaStream_t stream);
 pa_status launch_gather_cache_q4(Q4CacheArgs a, pa_dtype dst, cudaStream_t stream);
