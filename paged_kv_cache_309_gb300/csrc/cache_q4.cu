@@ -261,7 +261,7 @@ __device__ __forceinline__ int64_t row_of(const Q4CacheArgs& a, int64_t s) {
 }
 
 template <typename S>
-__global__ void __launch_bounds__(kWarps * 32) reshape_and_cache_q4_kernel(Q4CacheArgs a) {
+__global__ void __launch_bounds__(kWarps * 32, sizeof(S) == 2 ? 8 : 4) reshape_and_cache_q4_kernel(Q4CacheArgs a) {
   const int lane = threadIdx.x & 31;
   const int64_t wid = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
   const int64_t t = a.groups == 1 ? wid : wid / a.groups;
