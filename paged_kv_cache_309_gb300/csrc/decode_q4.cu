@@ -41,6 +41,7 @@
 // set, the remaining pieces end empty (so the counts complete), the copies in
 // flight are waited for, and the CTA exits.
 #include <atomic>
+#include <type_traits>
 
 #include "decode_common.cuh"
 
@@ -101,6 +102,14 @@ __device__ __forceinline__ float ex2(float x) {
   float d;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(d) : "f"(x));
   return d;
+}
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
 }
 // 8x8 transpose of a 16-bit fragment across the warp
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
@@ -418,10 +427,14 @@ __global__ void __launch_bounds__(kThreads, Lay<NT>::kCtasPerSm)
   // (lane & 15), column u + (lane >> 4); the (s, m) pairs: rows (lane & 15)
   const uint32_t frag = static_cast<uint32_t>((32 * warp + (lane & 15)) * kRow + 16 * (lane >> 4));
   const uint32_t meta_frag = static_cast<uint32_t>((32 * warp + (lane & 15)) * kRow + 64);
+  // (s, m) rows read directly: K row gq, V row 2tq
+  const uint32_t k_meta = static_cast<uint32_t>((32 * warp + gq) * kRow + 64);
+  const uint32_t v_meta = static_cast<uint32_t>(kTensorBytes + (32 * warp + 2 * tq) * kRow + 64);
   const uint32_t smem_base = smem_u32(smem);
   Walk walk(sched);
   Piece pc;
-  int u = 0;  // tiles consumed
+  int stage = 0;  // of the next tile
+  uint32_t phase = 0u;
   bool ok = true;
   while (next_piece(qp, walk, pc)) {
     float o[8][NT][4];         // head elements 32u + 4gq + 2h (+1) of m-tile 2u + h
@@ -496,202 +509,209 @@ __global__ void __launch_bounds__(kThreads, Lay<NT>::kCtasPerSm)
       }
     }
 
-    for (int tok = pc.tok_begin; ok && tok < pc.tok_end; tok += kTile, ++u) {
-      const int stage = u % kStages;
-      const bool w_ok = mbar_wait_bounded(&full[stage], (u / kStages) & 1, abort_flag);
+    // One 16-token slice of a tile (sl 0 or 1).  kFull: every row is a token.
+    auto slice = [&](auto full_tag, const int sl, const int tok, const uint32_t st,
+                     const uint32_t mask32) {
+      constexpr bool kFull = decltype(full_tag)::value;
+      const int r0 = 32 * warp + 16 * sl;
+      const uint32_t mask16 = (mask32 >> (16 * sl)) & 0xFFFFu;
+      if (!kFull && mask16 == 0u) {  // no token of the slice is there
+        if constexpr (kScored) {
+          const float none[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+            store_scores(p, pc.b, g, G, tok + r0, gq, pc.tok_end - tok - r0, nt * 8 + 2 * tq,
+                         none);
+        }
+        return;
+      }
+      const uint32_t kbase = st + sl * 16 * kRow;
+      const uint32_t kaddr = kbase + frag;
+      const uint32_t vaddr = kaddr + kTensorBytes;
+      // ---- S_u = codes . q, and the minima's sum
+      float su[NT][4][4], zk[NT][4];
+#pragma unroll
+      for (int u2 = 0; u2 < 4; u2 += 2) {
+        uint32_t r[4];  // (row gq, u2), (row gq + 8, u2), (row gq, u2 + 1), (row gq + 8, u2 + 1)
+        ldsm_x4(kaddr + 16 * u2, r);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint32_t lo = r[2 * i], hi = r[2 * i + 1];
+          const uint32_t lo8 = lo >> 8, hi8 = hi >> 8;
+          const uint32_t a0[4] = {lo & 0x000F000Fu, hi & 0x000F000Fu, lo & 0x00F000F0u,
+                                  hi & 0x00F000F0u};
+          const uint32_t a1[4] = {lo8 & 0x000F000Fu, hi8 & 0x000F000Fu, lo8 & 0x00F000F0u,
+                                  hi8 & 0x00F000F0u};
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            mma_f16_first(su[nt][u2 + i], a0, qb[nt][u2 + i][0], qb[nt][u2 + i][1]);
+            mma_f16_16816(su[nt][u2 + i], a1, qb[nt][u2 + i][2], qb[nt][u2 + i][3]);
+          }
+        }
+      }
+      {
+        uint32_t r[4];  // (s, m) of group tq, rows gq and gq + 8
+        ldsm_x4(kbase + meta_frag, r);
+        const uint32_t a[4] = {r[0], r[1], r[0], r[1]};
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) mma_f16_first(zk[nt], a, qz[nt][0], qz[nt][1]);
+      }
+      float ss[2][4];  // s_u of rows gq, gq + 8
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const uint4 w = lds128(kbase + k_meta + 8 * i * kRow);
+        ss[i][0] = low_f32(w.x);
+        ss[i][1] = low_f32(w.y);
+        ss[i][2] = low_f32(w.z);
+        ss[i][3] = low_f32(w.w);
+      }
+      const bool v0 = kFull || ((mask16 >> gq) & 1u);        // token r0 + gq
+      const bool v1 = kFull || ((mask16 >> (gq + 8)) & 1u);  // token r0 + gq + 8
+      // ---- scores relative to the running maximum (first: to -inf, so +inf)
+      float a[NT][4], sr[NT][4];
+      bool high = false;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          a[nt][i] = ss[i >> 1][0] * su[nt][0][i];
+#pragma unroll
+          for (int v = 1; v < 4; ++v) a[nt][i] = fmaf(ss[i >> 1][v], su[nt][v][i], a[nt][i]);
+          sr[nt][i] = fmaf(a[nt][i], sscale[nt][i & 1],
+                           fmaf(zk[nt][i], zscale[nt][i & 1], -m[nt][i & 1]));
+        }
+        if (!v0) sr[nt][0] = sr[nt][1] = -INFINITY;
+        if (!v1) sr[nt][2] = sr[nt][3] = -INFINITY;
+        high |= fmaxf(fmaxf(sr[nt][0], sr[nt][1]), fmaxf(sr[nt][2], sr[nt][3])) >
+                kLift + kRescaleLog2;
+      }
+      if (kScored || __any_sync(0xffffffffu, high)) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          float s[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            s[i] = fmaf(a[nt][i], sscale[nt][i & 1], zk[nt][i] * zscale[nt][i & 1]);
+          if (!v0) s[0] = s[1] = -INFINITY;
+          if (!v1) s[2] = s[3] = -INFINITY;
+          if constexpr (kScored)
+            store_scores(p, pc.b, g, G, tok + r0, gq, pc.tok_end - tok - r0, nt * 8 + 2 * tq, s);
+          if (kScored && !__any_sync(0xffffffffu, high)) continue;
+          float mx[2] = {fmaxf(s[0], s[2]), fmaxf(s[1], s[3])};
+#pragma unroll
+          for (int off = 4; off <= 16; off <<= 1) {
+            mx[0] = fmaxf(mx[0], __shfl_xor_sync(0xffffffffu, mx[0], off));
+            mx[1] = fmaxf(mx[1], __shfl_xor_sync(0xffffffffu, mx[1], off));
+          }
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            if (mx[j] > m[nt][j] + (kLift + kRescaleLog2)) {  // always on the first
+              const float corr = exp2f(m[nt][j] - (mx[j] - kLift));
+              l[nt][j] *= corr;
+              z[nt][j] *= corr;
+              z[nt][j + 2] *= corr;
+#pragma unroll
+              for (int mt = 0; mt < 8; ++mt) {
+                o[mt][nt][j] *= corr;
+                o[mt][nt][j + 2] *= corr;
+              }
+              m[nt][j] = mx[j] - kLift;
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) sr[nt][i] = s[i] - m[nt][i & 1];
+          if (!v0) sr[nt][0] = sr[nt][1] = -INFINITY;
+          if (!v1) sr[nt][2] = sr[nt][3] = -INFINITY;
+        }
+      }
+      uint32_t pb[NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const float p0 = ex2(sr[nt][0]), p1 = ex2(sr[nt][1]);
+        const float p2 = ex2(sr[nt][2]), p3 = ex2(sr[nt][3]);
+        l[nt][0] += p0 + p2;
+        l[nt][1] += p1 + p3;
+        // (token, heads) pairs to the B operand's (tokens, head) pairs
+        pb[nt][0] = transpose8(pack_f16x2(p0, p1));
+        pb[nt][1] = transpose8(pack_f16x2(p2, p3));
+      }
+      // ---- sum p m (and p s): the rows' (s, m) pairs as a matrix
+      {
+        uint32_t r[4];
+        ldsm_x4_trans(kbase + kTensorBytes + meta_frag, r);
+        const uint32_t am[4] = {r[0], 0u, r[1], 0u};
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) mma_f16_16816(z[nt], am, pb[nt][0], pb[nt][1]);
+      }
+      // ---- O^T += (s c)^T . P^T
+      uint32_t sv[2][4], sn[2][4];  // (s, s') and -64 (s, s') of tokens 2tq, 2tq + 1 (+ 8)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const uint4 x = lds128(kbase + v_meta + 8 * i * kRow);
+        const uint4 y = lds128(kbase + v_meta + (8 * i + 1) * kRow);
+        sv[i][0] = __byte_perm(x.x, y.x, 0x5410u);
+        sv[i][1] = __byte_perm(x.y, y.y, 0x5410u);
+        sv[i][2] = __byte_perm(x.z, y.z, 0x5410u);
+        sv[i][3] = __byte_perm(x.w, y.w, 0x5410u);
+#pragma unroll
+        for (int v = 0; v < 4; ++v) sn[i][v] = hmul2(sv[i][v], 0xD400D400u);  // -64
+      }
+#pragma unroll
+      for (int u2 = 0; u2 < 4; u2 += 2) {
+        uint32_t r[4];  // (tokens 2tq, u2), (tokens 2tq + 8, u2), the same of u2 + 1
+        ldsm_x4_trans(vaddr + 16 * u2, r);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int v = u2 + i;
+          uint32_t x[2][4];  // s c of tokens 2tq.. (+8), element 32v + 4gq + k
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const uint32_t w = r[2 * i + j];
+            x[j][0] = hfma2(((w << 4) & 0x00F000F0u) | 0x54005400u, sv[j][v], sn[j][v]);
+            x[j][1] = hfma2((w & 0x00F000F0u) | 0x54005400u, sv[j][v], sn[j][v]);
+            x[j][2] = hfma2(((w >> 4) & 0x00F000F0u) | 0x54005400u, sv[j][v], sn[j][v]);
+            x[j][3] = hfma2(((w >> 8) & 0x00F000F0u) | 0x54005400u, sv[j][v], sn[j][v]);
+          }
+#pragma unroll
+          for (int hh = 0; hh < 2; ++hh) {
+            const uint32_t av[4] = {x[0][2 * hh], x[0][2 * hh + 1], x[1][2 * hh],
+                                    x[1][2 * hh + 1]};
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+              mma_f16_16816(o[2 * v + hh][nt], av, pb[nt][0], pb[nt][1]);
+          }
+        }
+      }
+    };
+
+    for (int tok = pc.tok_begin; ok && tok < pc.tok_end; tok += kTile) {
+      const bool w_ok = mbar_wait_bounded(&full[stage], phase, abort_flag);
       if (!__all_sync(0xffffffffu, w_ok)) {
         ok = false;
         break;
       }
       const uint32_t mask32 = tile_mask[4 * stage + warp];
-      uint8_t* st_k = smem + stage * L_::kStageBytes;
-      uint8_t* st_v = st_k + kTensorBytes;
-      if (mask32 != 0xFFFFFFFFu) {
+      const uint32_t st = smem_base + stage * L_::kStageBytes;
+      if (mask32 == 0xFFFFFFFFu) {
+        slice(std::true_type{}, 0, tok, st, mask32);
+        slice(std::true_type{}, 1, tok, st, mask32);
+      } else {
         // rows without a token: s = m = 0 makes their values 0 (the ring's
         // leftovers could be NaN, and 0 x NaN would poison the sums)
         if (!((mask32 >> lane) & 1u))
-          *reinterpret_cast<uint4*>(st_v + (32 * warp + lane) * kRow + 64) =
-              make_uint4(0u, 0u, 0u, 0u);
+          *reinterpret_cast<uint4*>(smem + stage * L_::kStageBytes + kTensorBytes +
+                                    (32 * warp + lane) * kRow + 64) = make_uint4(0u, 0u, 0u, 0u);
         __syncwarp();
-      }
 #pragma unroll 1
-      for (int sl = 0; sl < 2; ++sl) {
-        const uint32_t mask16 = (mask32 >> (16 * sl)) & 0xFFFFu;
-        const int r0 = 32 * warp + 16 * sl;
-        if (mask16 == 0u) {  // no token of the slice is there
-          if constexpr (kScored) {
-            const float none[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-              store_scores(p, pc.b, g, G, tok + r0, gq, pc.tok_end - tok - r0, nt * 8 + 2 * tq,
-                           none);
-          }
-          continue;
-        }
-        const uint32_t kbase = smem_base + stage * L_::kStageBytes + sl * 16 * kRow;
-        const uint32_t kaddr = kbase + frag;
-        const uint32_t vaddr = kaddr + kTensorBytes;
-        // ---- S_u = codes . q, and the minima's sum
-        float su[NT][4][4], zk[NT][4];
-#pragma unroll
-        for (int u2 = 0; u2 < 4; u2 += 2) {
-          uint32_t r[4];  // (row gq, u2), (row gq + 8, u2), (row gq, u2 + 1), (row gq + 8, u2 + 1)
-          ldsm_x4(kaddr + 16 * u2, r);
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const uint32_t lo = r[2 * i], hi = r[2 * i + 1];
-            const uint32_t lo8 = lo >> 8, hi8 = hi >> 8;
-            const uint32_t a0[4] = {lo & 0x000F000Fu, hi & 0x000F000Fu, lo & 0x00F000F0u,
-                                    hi & 0x00F000F0u};
-            const uint32_t a1[4] = {lo8 & 0x000F000Fu, hi8 & 0x000F000Fu, lo8 & 0x00F000F0u,
-                                    hi8 & 0x00F000F0u};
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              mma_f16_first(su[nt][u2 + i], a0, qb[nt][u2 + i][0], qb[nt][u2 + i][1]);
-              mma_f16_16816(su[nt][u2 + i], a1, qb[nt][u2 + i][2], qb[nt][u2 + i][3]);
-            }
-          }
-        }
-        {
-          uint32_t r[4];  // (s, m) of group tq, rows gq and gq + 8
-          ldsm_x4(kbase + meta_frag, r);
-          const uint32_t a[4] = {r[0], r[1], r[0], r[1]};
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) mma_f16_first(zk[nt], a, qz[nt][0], qz[nt][1]);
-        }
-        float ss[2][4];  // s_u of rows gq, gq + 8
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const uint4 w = *reinterpret_cast<const uint4*>(st_k + (r0 + gq + 8 * i) * kRow + 64);
-          ss[i][0] = low_f32(w.x);
-          ss[i][1] = low_f32(w.y);
-          ss[i][2] = low_f32(w.z);
-          ss[i][3] = low_f32(w.w);
-        }
-        const bool v0 = (mask16 >> gq) & 1u;        // token r0 + gq
-        const bool v1 = (mask16 >> (gq + 8)) & 1u;  // token r0 + gq + 8
-        // ---- scores relative to the running maximum (first: to -inf, so +inf)
-        float a[NT][4], sr[NT][4];
-        bool high = false;
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            a[nt][i] = ss[i >> 1][0] * su[nt][0][i];
-#pragma unroll
-            for (int v = 1; v < 4; ++v) a[nt][i] = fmaf(ss[i >> 1][v], su[nt][v][i], a[nt][i]);
-            sr[nt][i] = fmaf(a[nt][i], sscale[nt][i & 1],
-                             fmaf(zk[nt][i], zscale[nt][i & 1], -m[nt][i & 1]));
-          }
-          if (mask16 != 0xFFFFu) {
-            if (!v0) sr[nt][0] = sr[nt][1] = -INFINITY;
-            if (!v1) sr[nt][2] = sr[nt][3] = -INFINITY;
-          }
-          high |= fmaxf(fmaxf(sr[nt][0], sr[nt][1]), fmaxf(sr[nt][2], sr[nt][3])) >
-                  kLift + kRescaleLog2;
-        }
-        if (kScored || __any_sync(0xffffffffu, high)) {
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            float s[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              s[i] = fmaf(a[nt][i], sscale[nt][i & 1], zk[nt][i] * zscale[nt][i & 1]);
-            if (!v0) s[0] = s[1] = -INFINITY;
-            if (!v1) s[2] = s[3] = -INFINITY;
-            if constexpr (kScored)
-              store_scores(p, pc.b, g, G, tok + r0, gq, pc.tok_end - tok - r0, nt * 8 + 2 * tq, s);
-            if (kScored && !__any_sync(0xffffffffu, high)) continue;
-            float mx[2] = {fmaxf(s[0], s[2]), fmaxf(s[1], s[3])};
-#pragma unroll
-            for (int off = 4; off <= 16; off <<= 1) {
-              mx[0] = fmaxf(mx[0], __shfl_xor_sync(0xffffffffu, mx[0], off));
-              mx[1] = fmaxf(mx[1], __shfl_xor_sync(0xffffffffu, mx[1], off));
-            }
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              if (mx[j] > m[nt][j] + (kLift + kRescaleLog2)) {  // always on the first
-                const float corr = exp2f(m[nt][j] - (mx[j] - kLift));
-                l[nt][j] *= corr;
-                z[nt][j] *= corr;
-                z[nt][j + 2] *= corr;
-#pragma unroll
-                for (int mt = 0; mt < 8; ++mt) {
-                  o[mt][nt][j] *= corr;
-                  o[mt][nt][j + 2] *= corr;
-                }
-                m[nt][j] = mx[j] - kLift;
-              }
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) sr[nt][i] = s[i] - m[nt][i & 1];
-            if (!v0) sr[nt][0] = sr[nt][1] = -INFINITY;
-            if (!v1) sr[nt][2] = sr[nt][3] = -INFINITY;
-          }
-        }
-        uint32_t pb[NT][2];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          const float p0 = ex2(sr[nt][0]), p1 = ex2(sr[nt][1]);
-          const float p2 = ex2(sr[nt][2]), p3 = ex2(sr[nt][3]);
-          l[nt][0] += p0 + p2;
-          l[nt][1] += p1 + p3;
-          // (token, heads) pairs to the B operand's (tokens, head) pairs
-          pb[nt][0] = transpose8(pack_f16x2(p0, p1));
-          pb[nt][1] = transpose8(pack_f16x2(p2, p3));
-        }
-        // ---- sum p m (and p s): the rows' (s, m) pairs as a matrix
-        {
-          uint32_t r[4];
-          ldsm_x4_trans(kbase + kTensorBytes + meta_frag, r);
-          const uint32_t am[4] = {r[0], 0u, r[1], 0u};
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) mma_f16_16816(z[nt], am, pb[nt][0], pb[nt][1]);
-        }
-        // ---- O^T += (s c)^T . P^T
-        uint32_t sv[2][4], sn[2][4];  // (s, s') and -64 (s, s') of tokens 2tq, 2tq + 1 (+ 8)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const uint8_t* row = st_v + (r0 + 2 * tq + 8 * i) * kRow + 64;
-          const uint4 x = *reinterpret_cast<const uint4*>(row);
-          const uint4 y = *reinterpret_cast<const uint4*>(row + kRow);
-          sv[i][0] = __byte_perm(x.x, y.x, 0x5410u);
-          sv[i][1] = __byte_perm(x.y, y.y, 0x5410u);
-          sv[i][2] = __byte_perm(x.z, y.z, 0x5410u);
-          sv[i][3] = __byte_perm(x.w, y.w, 0x5410u);
-#pragma unroll
-          for (int v = 0; v < 4; ++v) sn[i][v] = hmul2(sv[i][v], 0xD400D400u);  // -64
-        }
-#pragma unroll
-        for (int u2 = 0; u2 < 4; u2 += 2) {
-          uint32_t r[4];  // (tokens 2tq, u2), (tokens 2tq + 8, u2), the same of u2 + 1
-          ldsm_x4_trans(vaddr + 16 * u2, r);
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int v = u2 + i;
-            uint32_t x[2][4];  // s c of tokens 2tq.. (+8), element 32v + 4gq + k
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              const uint32_t w = r[2 * i + j];
-              x[j][0] = hfma2(((w << 4) & 0x00F000F0u) | 0x54005400u, sv[j][v], sn[j][v]);
-              x[j][1] = hfma2((w & 0x00F000F0u) | 0x54005400u, sv[j][v], sn[j][v]);
-              x[j][2] = hfma2(((w >> 4) & 0x00F000F0u) | 0x54005400u, sv[j][v], sn[j][v]);
-              x[j][3] = hfma2(((w >> 8) & 0x00F000F0u) | 0x54005400u, sv[j][v], sn[j][v]);
-            }
-#pragma unroll
-            for (int hh = 0; hh < 2; ++hh) {
-              const uint32_t av[4] = {x[0][2 * hh], x[0][2 * hh + 1], x[1][2 * hh],
-                                      x[1][2 * hh + 1]};
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt)
-                mma_f16_16816(o[2 * v + hh][nt], av, pb[nt][0], pb[nt][1]);
-            }
-          }
-        }
+        for (int sl = 0; sl < 2; ++sl) slice(std::false_type{}, sl, tok, st, mask32);
+        fence_proxy_async_smem();  // stores before the next TMA
       }
-      if (mask32 != 0xFFFFFFFFu) fence_proxy_async_smem();  // stores before the next TMA
       __syncwarp();
       if (lane == 0) mbar_arrive(&empty[stage]);
+      if (++stage == kStages) {
+        stage = 0;
+        phase ^= 1u;
+      }
     }
     if (!ok && lane == 0) {
       *abort_flag = 1;
