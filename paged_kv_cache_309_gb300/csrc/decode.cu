@@ -743,22 +743,17 @@ bool make_kv_map_fp8(CUtensorMap* map, const void* base, int64_t rows, int32_t n
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// [rows, H_KV, 80] bytes of 4-bit rows; box = a whole row x 1 head x box_rows
-// rows, packed at 80 bytes.
-bool make_kv_map_q4(CUtensorMap* map, const void* base, int64_t rows, int32_t num_kv_heads,
-                    int32_t box_rows) {
+// [rows, row_bytes] bytes; box = box_bytes of a row x box_rows rows, packed.
+bool make_row_map(CUtensorMap* map, const void* base, int64_t rows, int32_t row_bytes,
+                  int32_t box_bytes, int32_t box_rows) {
   auto enc = encode_fn();
   if (enc == nullptr) return false;
-  constexpr int kQ4Row = kD / 2 + kD / 8;
-  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(kQ4Row),
-                              static_cast<cuuint64_t>(num_kv_heads),
-                              static_cast<cuuint64_t>(rows)};
-  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(kQ4Row),
-                                 static_cast<cuuint64_t>(kQ4Row) * num_kv_heads};
-  const cuuint32_t box[3] = {static_cast<cuuint32_t>(kQ4Row), 1u,
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(row_bytes), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(row_bytes)};
+  const cuuint32_t box[2] = {static_cast<cuuint32_t>(box_bytes),
                              static_cast<cuuint32_t>(box_rows)};
-  const cuuint32_t es[3] = {1u, 1u, 1u};
-  return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, es,
+  const cuuint32_t es[2] = {1u, 1u};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, es,
              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
              CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }

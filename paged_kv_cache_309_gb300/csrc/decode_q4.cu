@@ -21,7 +21,8 @@
 // 2^7 above the running maximum's scale, so that fp16 carries them down to 2^-31 of it.
 //
 // Rows of 80 bytes need no swizzle: eight consecutive rows start in eight
-// different groups of four banks (20 r mod 32).
+// different groups of four banks (20 r mod 32); the 160-byte rows of two kv
+// heads in four (two passes).
 //
 // What bounds it: at 160 bytes per token and kv head HBM leaves an SM 440
 // issue slots for 16 tokens, and the first form of this kernel needed 431 of
@@ -35,11 +36,15 @@
 //   once) is the units whose cost lies in [c, c + 1) total / C.  A chunk
 //   walks its pieces with the ring running on across them.  A sequence that
 //   lies in one chunk is written directly; the pieces of one that does not
-//   go to partial slots, and the last of them to finish merges them.
+//   go to partial slots, which a second launch merges with one CTA per query
+//   head (a single long sequence has 200 pieces: merged by the CTA that
+//   finished last, its 16 heads took 54 us at 9001 tokens and 8 heads per kv
+//   head; apart 9).  Its CTAs are launched while this kernel runs and wait for
+//   its end (programmatic dependent launch).
 //
 // Every mbarrier wait is bounded (2 s); after a timeout the error bit is
-// set, the remaining pieces end empty (so the counts complete), the copies in
-// flight are waited for, and the CTA exits.
+// set, the remaining pieces end empty, the copies in flight are waited for, and
+// the CTA exits.
 #include <atomic>
 #include <type_traits>
 
@@ -49,9 +54,9 @@ namespace pa_detail {
 namespace {
 
 constexpr int kUnit = 64;          // tokens per unit of the cut (boxes are up to 64 rows)
-constexpr int kTile = 128;         // tokens per stage, 32 per consumer warp
-constexpr int kRow = 80;           // bytes of a cached row
-constexpr int kTensorBytes = kTile * kRow;
+constexpr int kRow = 80;           // bytes of a cached row of one kv head
+constexpr int kStageRows = 128;    // head rows per stage, 32 per consumer warp
+constexpr int kTensorBytes = kStageRows * kRow;
 constexpr float kLift = 7.0f;      // weights are 2^kLift (score - running maximum)
 constexpr int kPieceCost = 1;      // units charged for a sequence's start
 constexpr int kConsumers = kConsumerWarps * 32;
@@ -60,7 +65,9 @@ struct Q4Params {
   DecodeParams d;
   int32_t num_seqs;
   int32_t slots;  // partial slots per kv head
+  int32_t* info;  // [H_KV / HP, B]: chunk of the first piece << 16 | pieces, 0 if not split
   bool whole;     // no partials: chunks begin at sequence starts
+  int32_t pair_tokens;  // 1: the maps' rows are pairs of tokens (one kv head)
 };
 
 template <int NT>
@@ -70,11 +77,11 @@ struct Lay {
   static constexpr int kStageBytes = 2 * kTensorBytes;  // K rows, then V rows
   static constexpr int kHeads = NT * 8;
   // the join of the four warps, 64 head elements at a time: [warp][h][64], then
-  // maxima and sums [warp][h], weights [warp][h], totals [h][2]
+  // maxima and sums [warp][h], weights [warp][h], totals [head, h][2]
   static constexpr int kRedOffset = kStages * kStageBytes;
   static constexpr int kRedFloats = kConsumerWarps * kHeads * 64;
   static constexpr int kStatOffset = kRedOffset + kRedFloats * 4;
-  static constexpr int kStatFloats = 3 * kConsumerWarps * kHeads + 2 * kHeads;
+  static constexpr int kStatFloats = 3 * kConsumerWarps * kHeads + 4 * kHeads;
   static constexpr int kBarOffset = kStatOffset + kStatFloats * 4;
   static constexpr int kMaskOffset = kBarOffset + 2 * kStages * 8;  // four words per stage
   static constexpr int kSchedOffset = kMaskOffset + kStages * 16;   // five 64-bit words
@@ -97,6 +104,12 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
 // the low half of an fp16 pair in fp32
 __device__ __forceinline__ float low_f32(uint32_t h) {
   return __half2float(__ushort_as_half(static_cast<uint16_t>(h)));
+}
+// (a & b) | c in one instruction (two constants in the expression make two)
+__device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t d;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+  return d;
 }
 __device__ __forceinline__ float ex2(float x) {
   float d;
@@ -247,55 +260,91 @@ __device__ __forceinline__ bool next_piece(const Q4Params& q, Walk& w, Piece& pc
   return false;
 }
 
-// Merge of one query head's n partials by one warp (the first in start_slot, the others
-// in slots first_slot, first_slot + 1, ...): weights 2^(lse - max).
-template <bool kScored>
-__device__ __forceinline__ void merge_pieces(const DecodeParams& p, int64_t bh, const float* lse,
-                                             const float* o, int G, int start_slot, int first_slot,
-                                             int n, int lane) {
-  auto slot = [&](int i) -> int64_t {
-    return static_cast<int64_t>(i == 0 ? start_slot : first_slot + i - 1) * G;
-  };
-  float M = -INFINITY;  // (a NaN lse is carried to the output)
-  for (int i = lane; i < n; i += 32) M = max_nan(M, __ldcg(lse + slot(i)));
+// Slot of a split sequence's first piece (the others go to slots c_first, c_first + 1, ...).
+__device__ __forceinline__ int start_slot_of(int chunks, int num_seqs, int b, int c_first) {
+  return chunks - 1 + (num_seqs <= chunks - 1 ? b : c_first);
+}
+
+// Merge of the split sequences' partials: one CTA per query head, for every
+// gridDim.y-th sequence; weights 2^(lse - max).  Warp w takes pieces w, w + 8, ...
+constexpr int kMergeWarps = 8;
+template <int HP, bool kScored>
+__global__ void __launch_bounds__(kMergeWarps * 32)
+    merge_pieces_kernel(const __grid_constant__ Q4Params qp, int G, int chunks) {
+  __shared__ float4 part[kMergeWarps][32];
+  __shared__ float part_w[kMergeWarps];
+  const DecodeParams& p = qp.d;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int hq = blockIdx.x, g = hq / G;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (kScored) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  for (int b = blockIdx.y; b < qp.num_seqs; b += gridDim.y) {
+    const int32_t info = __ldcg(qp.info + static_cast<int64_t>(g / HP) * qp.num_seqs + b);
+    if (info == 0) continue;
+    const int c_first = info >> 16, n = info & 0xFFFF;
+    const int start = start_slot_of(chunks, qp.num_seqs, b, c_first);
+    const int64_t at = static_cast<int64_t>(g) * qp.slots * G + hq % G;
+    const float* lse = p.ws_lse + at;
+    const float* o = p.ws_o + at * kD;
+    auto slot = [&](int i) -> int64_t {
+      return static_cast<int64_t>(i == 0 ? start : c_first + i - 1) * G;
+    };
+    float M = -INFINITY;  // (a NaN lse is carried to the output)
+    for (int i = lane; i < n; i += 32) M = max_nan(M, __ldcg(lse + slot(i)));
 #pragma unroll
-  for (int off = 16; off >= 1; off >>= 1) M = max_nan(M, __shfl_xor_sync(0xffffffffu, M, off));
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  float W = 0.f;
-  if (M != -INFINITY) {
-    for (int i0 = 0; i0 < n; i0 += 32) {
-      const float wl = i0 + lane < n ? exp2f(__ldcg(lse + slot(i0 + lane)) - M) : 0.f;
-      const int cnt = min(32, n - i0);
-      for (int k0 = 0; k0 < cnt; k0 += 8) {
+    for (int off = 16; off >= 1; off >>= 1) M = max_nan(M, __shfl_xor_sync(0xffffffffu, M, off));
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    float W = 0.f;
+    if (M != -INFINITY) {
+      for (int i0 = warp; i0 < n; i0 += 8 * kMergeWarps) {
         float4 v[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-          v[k] = k0 + k < cnt
-                     ? __ldcg(reinterpret_cast<const float4*>(o + slot(i0 + k0 + k) * kD) + lane)
-                     : make_float4(0.f, 0.f, 0.f, 0.f);
+        float w[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-          const float w = __shfl_sync(0xffffffffu, wl, (k0 + k) & 31);
-          if (k0 + k < cnt) {
-            W += w;
-            acc.x += w * v[k].x;
-            acc.y += w * v[k].y;
-            acc.z += w * v[k].z;
-            acc.w += w * v[k].w;
+          const int i = i0 + k * kMergeWarps;
+          if (i < n) {
+            v[k] = __ldcg(reinterpret_cast<const float4*>(o + slot(i) * kD) + lane);
+            w[k] = exp2f(__ldcg(lse + slot(i)) - M);
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          if (i0 + k * kMergeWarps < n) {
+            W += w[k];
+            acc.x += w[k] * v[k].x;
+            acc.y += w[k] * v[k].y;
+            acc.z += w[k] * v[k].z;
+            acc.w += w[k] * v[k].w;
           }
         }
       }
     }
+    part[warp][lane] = acc;
+    if (lane == 0) part_w[warp] = W;
+    __syncthreads();
+    if (warp == 0) {
+#pragma unroll
+      for (int w = 1; w < kMergeWarps; ++w) {
+        const float4 v = part[w][lane];
+        acc.x += v.x;
+        acc.y += v.y;
+        acc.z += v.z;
+        acc.w += v.w;
+        W += part_w[w];
+      }
+      const int64_t bh = static_cast<int64_t>(b) * p.num_q_heads + hq;
+      if (kScored && lane == 0) p.final_lse[bh] = W == 0.f ? -INFINITY : M + log2f(W);
+      const float inv = W == 0.f ? 0.f : 1.f / W;
+      *reinterpret_cast<uint2*>(p.out + bh * kD + lane * 4) =
+          make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+    }
+    __syncthreads();
   }
-  if (kScored && lane == 0) p.final_lse[bh] = W == 0.f ? -INFINITY : M + log2f(W);
-  const float inv = W == 0.f ? 0.f : 1.f / W;
-  *reinterpret_cast<uint2*>(p.out + bh * kD + lane * 4) =
-      make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
 }
 
-// NT: n-tiles of 8 query heads (G <= 8 -> 1, G = 16 -> 2); kScored: also
-// store the scores and each query head's log2-sum-exp.
-template <int NT, bool kScored>
+// NT: n-tiles of 8 query heads (G <= 8 -> 1, G = 16 -> 2); HP: kv heads per
+// CTA; kScored: also store the scores and each query head's log2-sum-exp.
+template <int NT, int HP, bool kScored>
 __global__ void __launch_bounds__(kThreads, Lay<NT>::kCtasPerSm)
     paged_decode_q4_kernel(const __grid_constant__ CUtensorMap tm_k,
                            const __grid_constant__ CUtensorMap tm_v,
@@ -303,6 +352,9 @@ __global__ void __launch_bounds__(kThreads, Lay<NT>::kCtasPerSm)
   using L_ = Lay<NT>;
   const DecodeParams& p = qp.d;
   constexpr int kStages = L_::kStages;
+  constexpr int kTile = kStageRows / HP;  // tokens per stage
+  constexpr int kPitch = kRow * HP;       // bytes of a token's rows in a stage
+  constexpr int kHeadWarps = kConsumerWarps / HP;
   extern __shared__ __align__(128) uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((128u - (smem_u32(smem_raw) & 127u)) & 127u);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + L_::kBarOffset);
@@ -310,17 +362,15 @@ __global__ void __launch_bounds__(kThreads, Lay<NT>::kCtasPerSm)
   uint32_t* tile_mask = reinterpret_cast<uint32_t*>(smem + L_::kMaskOffset);
   int64_t* sched = reinterpret_cast<int64_t*>(smem + L_::kSchedOffset);
   int* abort_ptr = reinterpret_cast<int*>(smem + L_::kFlagOffset);
-  int* last_flag = abort_ptr + 1;
 
   // kv heads fastest in launch order: the CTAs of one chunk read neighbouring
   // rows at the same time
-  const int g = blockIdx.x;
+  const int g0 = blockIdx.x * HP;  // the CTA's first kv head
   const int c = blockIdx.y;
   const int chunks = gridDim.y;
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const int bs = p.block_size;
-  const int hq0 = g * G;
 
   if (warp == 0) find_chunk(qp, c, chunks, lane, sched);
   if (threadIdx.x == 32) {
@@ -334,6 +384,8 @@ __global__ void __launch_bounds__(kThreads, Lay<NT>::kCtasPerSm)
   }
   __syncthreads();
   volatile int* abort_flag = abort_ptr;
+  // (the merging CTAs may take their places; they wait for this kernel's end)
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int64_t total = sched[0];
   const int parts = static_cast<int>(min(total, static_cast<int64_t>(chunks)));
 
@@ -386,14 +438,15 @@ __global__ void __launch_bounds__(kThreads, Lay<NT>::kCtasPerSm)
         if (lane == 0) {
           *reinterpret_cast<uint4*>(tile_mask + 4 * stage) =
               make_uint4(words[0], words[1], words[2], words[3]);
-          mbar_arrive_expect_tx(&full[stage], static_cast<uint32_t>(__popc(vb) * rpb * kRow * 2));
+          mbar_arrive_expect_tx(&full[stage], static_cast<uint32_t>(__popc(vb) * rpb * kPitch * 2));
         }
         __syncwarp();
         if (valid) {
-          const int32_t row = bid * bs + (first & (bs - 1));
-          uint8_t* st = smem + stage * L_::kStageBytes + lane * rpb * kRow;
-          tma_load_3d(st, &tm_k, 0, g, row, &full[stage], pol);
-          tma_load_3d(st + kTensorBytes, &tm_v, 0, g, row, &full[stage], pol);
+          // (a cache of one head: two tokens make one 160-byte row of the map)
+          const int32_t row = (bid * bs + (first & (bs - 1))) >> qp.pair_tokens;
+          uint8_t* st = smem + stage * L_::kStageBytes + lane * rpb * kPitch;
+          tma_load_2d(st, &tm_k, g0 * kRow, row, &full[stage], pol);
+          tma_load_2d(st + kTensorBytes, &tm_v, g0 * kRow, row, &full[stage], pol);
         }
       }
     }
@@ -413,24 +466,32 @@ __global__ void __launch_bounds__(kThreads, Lay<NT>::kCtasPerSm)
   // sequences without tokens: zero rows (chunk c takes b = c mod C)
   for (int b = c; b < qp.num_seqs; b += chunks) {
     if (units_of(p, b) == 0) {
-      for (int i = threadIdx.x; i < G * (kD / 8); i += kConsumers)
-        reinterpret_cast<uint4*>(p.out + (static_cast<int64_t>(b) * p.num_q_heads + hq0) * kD)[i] =
-            make_uint4(0u, 0u, 0u, 0u);
-      if (kScored && threadIdx.x < G)
-        p.final_lse[static_cast<int64_t>(b) * p.num_q_heads + hq0 + threadIdx.x] = -INFINITY;
+      const int64_t row = static_cast<int64_t>(b) * p.num_q_heads + g0 * G;
+      for (int i = threadIdx.x; i < HP * G * (kD / 8); i += kConsumers)
+        reinterpret_cast<uint4*>(p.out + row * kD)[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (kScored && threadIdx.x < HP * G) p.final_lse[row + threadIdx.x] = -INFINITY;
+      if (!qp.whole && threadIdx.x == 0)
+        qp.info[static_cast<int64_t>(blockIdx.x) * qp.num_seqs + b] = 0;
     }
   }
 
   const int gq = lane >> 2;  // mma groupID
   const int tq = lane & 3;   // thread in group
+  // this warp's head and tokens of a tile
+  const int g = g0 + warp / kHeadWarps;
+  const int hq0 = g * G;
+  const int t0 = 32 * (warp % kHeadWarps);
+  const uint32_t base = static_cast<uint32_t>(t0 * kPitch + warp / kHeadWarps * kRow);
   // ldmatrix rows and 16-byte columns of this lane (K and V alike): rows
   // (lane & 15), column u + (lane >> 4); the (s, m) pairs: rows (lane & 15)
-  const uint32_t frag = static_cast<uint32_t>((32 * warp + (lane & 15)) * kRow + 16 * (lane >> 4));
-  const uint32_t meta_frag = static_cast<uint32_t>((32 * warp + (lane & 15)) * kRow + 64);
+  const uint32_t frag = base + static_cast<uint32_t>((lane & 15) * kPitch + 16 * (lane >> 4));
+  const uint32_t meta_frag = base + static_cast<uint32_t>((lane & 15) * kPitch + 64);
   // (s, m) rows read directly: K row gq, V row 2tq
-  const uint32_t k_meta = static_cast<uint32_t>((32 * warp + gq) * kRow + 64);
-  const uint32_t v_meta = static_cast<uint32_t>(kTensorBytes + (32 * warp + 2 * tq) * kRow + 64);
+  const uint32_t k_meta = base + static_cast<uint32_t>(gq * kPitch + 64);
+  const uint32_t v_meta = base + static_cast<uint32_t>(kTensorBytes + 2 * tq * kPitch + 64);
   const uint32_t smem_base = smem_u32(smem);
+  uint32_t magic;  // fp16 pair (64, 64), kept in a register
+  asm volatile("mov.u32 %0, 0x54005400;" : "=r"(magic));
   Walk walk(sched);
   Piece pc;
   int stage = 0;  // of the next tile
@@ -513,7 +574,7 @@ __global__ void __launch_bounds__(kThreads, Lay<NT>::kCtasPerSm)
     auto slice = [&](auto full_tag, const int sl, const int tok, const uint32_t st,
                      const uint32_t mask32) {
       constexpr bool kFull = decltype(full_tag)::value;
-      const int r0 = 32 * warp + 16 * sl;
+      const int r0 = t0 + 16 * sl;  // of the tile's tokens
       const uint32_t mask16 = (mask32 >> (16 * sl)) & 0xFFFFu;
       if (!kFull && mask16 == 0u) {  // no token of the slice is there
         if constexpr (kScored) {
@@ -525,7 +586,7 @@ __global__ void __launch_bounds__(kThreads, Lay<NT>::kCtasPerSm)
         }
         return;
       }
-      const uint32_t kbase = st + sl * 16 * kRow;
+      const uint32_t kbase = st + sl * 16 * kPitch;
       const uint32_t kaddr = kbase + frag;
       const uint32_t vaddr = kaddr + kTensorBytes;
       // ---- S_u = codes . q, and the minima's sum
@@ -559,7 +620,7 @@ __global__ void __launch_bounds__(kThreads, Lay<NT>::kCtasPerSm)
       float ss[2][4];  // s_u of rows gq, gq + 8
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const uint4 w = lds128(kbase + k_meta + 8 * i * kRow);
+        const uint4 w = lds128(kbase + k_meta + 8 * i * kPitch);
         ss[i][0] = low_f32(w.x);
         ss[i][1] = low_f32(w.y);
         ss[i][2] = low_f32(w.z);
@@ -647,8 +708,8 @@ __global__ void __launch_bounds__(kThreads, Lay<NT>::kCtasPerSm)
       uint32_t sv[2][4], sn[2][4];  // (s, s') and -64 (s, s') of tokens 2tq, 2tq + 1 (+ 8)
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const uint4 x = lds128(kbase + v_meta + 8 * i * kRow);
-        const uint4 y = lds128(kbase + v_meta + (8 * i + 1) * kRow);
+        const uint4 x = lds128(kbase + v_meta + 8 * i * kPitch);
+        const uint4 y = lds128(kbase + v_meta + (8 * i + 1) * kPitch);
         sv[i][0] = __byte_perm(x.x, y.x, 0x5410u);
         sv[i][1] = __byte_perm(x.y, y.y, 0x5410u);
         sv[i][2] = __byte_perm(x.z, y.z, 0x5410u);
@@ -667,10 +728,10 @@ __global__ void __launch_bounds__(kThreads, Lay<NT>::kCtasPerSm)
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
             const uint32_t w = r[2 * i + j];
-            x[j][0] = hfma2(((w << 4) & 0x00F000F0u) | 0x54005400u, sv[j][v], sn[j][v]);
-            x[j][1] = hfma2((w & 0x00F000F0u) | 0x54005400u, sv[j][v], sn[j][v]);
-            x[j][2] = hfma2(((w >> 4) & 0x00F000F0u) | 0x54005400u, sv[j][v], sn[j][v]);
-            x[j][3] = hfma2(((w >> 8) & 0x00F000F0u) | 0x54005400u, sv[j][v], sn[j][v]);
+            x[j][0] = hfma2(and_or(w << 4, 0x00F000F0u, magic), sv[j][v], sn[j][v]);
+            x[j][1] = hfma2(and_or(w, 0x00F000F0u, magic), sv[j][v], sn[j][v]);
+            x[j][2] = hfma2(and_or(w >> 4, 0x00F000F0u, magic), sv[j][v], sn[j][v]);
+            x[j][3] = hfma2(and_or(w >> 8, 0x00F000F0u, magic), sv[j][v], sn[j][v]);
           }
 #pragma unroll
           for (int hh = 0; hh < 2; ++hh) {
@@ -690,7 +751,7 @@ __global__ void __launch_bounds__(kThreads, Lay<NT>::kCtasPerSm)
         ok = false;
         break;
       }
-      const uint32_t mask32 = tile_mask[4 * stage + warp];
+      const uint32_t mask32 = tile_mask[4 * stage + warp % kHeadWarps];
       const uint32_t st = smem_base + stage * L_::kStageBytes;
       if (mask32 == 0xFFFFFFFFu) {
         slice(std::true_type{}, 0, tok, st, mask32);
@@ -699,8 +760,8 @@ __global__ void __launch_bounds__(kThreads, Lay<NT>::kCtasPerSm)
         // rows without a token: s = m = 0 makes their values 0 (the ring's
         // leftovers could be NaN, and 0 x NaN would poison the sums)
         if (!((mask32 >> lane) & 1u))
-          *reinterpret_cast<uint4*>(smem + stage * L_::kStageBytes + kTensorBytes +
-                                    (32 * warp + lane) * kRow + 64) = make_uint4(0u, 0u, 0u, 0u);
+          *reinterpret_cast<uint4*>(smem + stage * L_::kStageBytes + kTensorBytes + base +
+                                    lane * kPitch + 64) = make_uint4(0u, 0u, 0u, 0u);
         __syncwarp();
 #pragma unroll 1
         for (int sl = 0; sl < 2; ++sl) slice(std::false_type{}, sl, tok, st, mask32);
@@ -729,8 +790,10 @@ __global__ void __launch_bounds__(kThreads, Lay<NT>::kCtasPerSm)
     const int c_last = qp.whole ? c : chunk_of(pc.last, pc.b, total, parts);
     // partial slot: c - 1 for a piece that goes on from chunk c - 1; for a
     // sequence's first piece one of its own behind those
-    const int start_slot = chunks - 1 + (qp.num_seqs <= chunks - 1 ? pc.b : c_first);
-    const int slot = c == c_first ? start_slot : c - 1;
+    const int slot = c == c_first ? start_slot_of(chunks, qp.num_seqs, pc.b, c_first) : c - 1;
+    if (!qp.whole && c == c_first && threadIdx.x == 0)
+      qp.info[static_cast<int64_t>(blockIdx.x) * qp.num_seqs + pc.b] =
+          c_first == c_last ? 0 : c_first << 16 | (c_last - c_first + 1);
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
       // (a barrier has passed since the last reads of this memory)
@@ -763,30 +826,31 @@ __global__ void __launch_bounds__(kThreads, Lay<NT>::kCtasPerSm)
       }
       consumer_barrier();
       if (half == 0) {
-        if (threadIdx.x < G) {
-          const int h = threadIdx.x;
+        if (threadIdx.x < HP * G) {
+          const int h = threadIdx.x % G, w0 = threadIdx.x / G * kHeadWarps;
           float M = -INFINITY;
 #pragma unroll
-          for (int w = 0; w < kConsumerWarps; ++w) M = fmaxf(M, red_m[w * GH + h]);
+          for (int w = w0; w < w0 + kHeadWarps; ++w) M = fmaxf(M, red_m[w * GH + h]);
           float Ls = 0.f;
 #pragma unroll
-          for (int w = 0; w < kConsumerWarps; ++w) {
+          for (int w = w0; w < w0 + kHeadWarps; ++w) {
             const float wt = (M == -INFINITY) ? 0.f : exp2f(red_m[w * GH + h] - M);
             red_w[w * GH + h] = wt;
             // (a warp of NaN scores only has no maximum: its sum is NaN all the same)
             Ls += red_l[w * GH + h] * (red_l[w * GH + h] != red_l[w * GH + h] ? 1.f : wt);
           }
-          fin[2 * h] = M;
-          fin[2 * h + 1] = Ls;
+          fin[2 * threadIdx.x] = M;
+          fin[2 * threadIdx.x + 1] = Ls;
         }
         consumer_barrier();
       }
-      for (int i = threadIdx.x; i < G * 16; i += kConsumers) {
-        const int h = i >> 4;
+      for (int i = threadIdx.x; i < HP * G * 16; i += kConsumers) {
+        const int hh = i >> 4;  // of the CTA's query heads
+        const int head = hh / G, h = hh % G;
         const int e0 = (i & 15) * 4;
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-        for (int w = 0; w < kConsumerWarps; ++w) {
+        for (int w = head * kHeadWarps; w < (head + 1) * kHeadWarps; ++w) {
           const float wt = red_w[w * GH + h];
           const float4 v = *reinterpret_cast<const float4*>(red + (w * GH + h) * 64 + e0);
           acc.x += wt * v.x;
@@ -794,77 +858,63 @@ __global__ void __launch_bounds__(kThreads, Lay<NT>::kCtasPerSm)
           acc.z += wt * v.z;
           acc.w += wt * v.w;
         }
-        const float Ls = fin[2 * h + 1];
+        const float Ls = fin[2 * hh + 1];
         const float inv = Ls == 0.f ? 0.f : 1.f / Ls;  // NaN stays NaN
         acc.x *= inv;
         acc.y *= inv;
         acc.z *= inv;
         acc.w *= inv;
-        const float lse = Ls == 0.f ? -INFINITY : fin[2 * h] + log2f(Ls);
+        const float lse = Ls == 0.f ? -INFINITY : fin[2 * hh] + log2f(Ls);
         const int e = 64 * half + e0;
         if (c_first == c_last) {
-          const int64_t row = static_cast<int64_t>(pc.b) * p.num_q_heads + hq0 + h;
+          const int64_t row = static_cast<int64_t>(pc.b) * p.num_q_heads + g0 * G + hh;
           *reinterpret_cast<uint2*>(p.out + row * kD + e) =
               make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
           if (kScored && e == 0) p.final_lse[row] = lse;
         } else {
-          const int64_t row = (static_cast<int64_t>(g) * qp.slots + slot) * G + h;
+          const int64_t row = (static_cast<int64_t>(g0 + head) * qp.slots + slot) * G + h;
           *reinterpret_cast<float4*>(p.ws_o + row * kD + e) = acc;
           if (e == 0) p.ws_lse[row] = lse;
         }
       }
       consumer_barrier();
     }
-    if (c_first != c_last) {
-      // the piece that completes the count merges the sequence's pieces and
-      // returns the counter to zero
-      if (threadIdx.x == 0) {
-        __threadfence();
-        unsigned* ctr = p.counters + static_cast<int64_t>(pc.b) * p.num_kv_heads + g;
-        const bool last = atomicAdd(ctr, 1u) + 1u == static_cast<unsigned>(c_last - c_first + 1);
-        if (last) {
-          atomicExch(ctr, 0u);
-          __threadfence();
-        }
-        *last_flag = last ? 1 : 0;
-      }
-      consumer_barrier();
-      if (*last_flag) {
-        const int64_t at = static_cast<int64_t>(g) * qp.slots * G;
-        for (int h = warp; h < G; h += kConsumerWarps)
-          merge_pieces<kScored>(p, static_cast<int64_t>(pc.b) * p.num_q_heads + hq0 + h,
-                                p.ws_lse + at + h, p.ws_o + (at + h) * kD, G, start_slot, c_first,
-                                c_last - c_first + 1, lane);
-      }
-    }
   }
 }
 
-template <int NT, bool kScored>
+template <int NT, int HP, bool kScored>
 pa_status launch_q4(const CUtensorMap& mk, const CUtensorMap& mv, Q4Params q, int G,
                     int num_splits, cudaStream_t stream) {
   static std::atomic<uint64_t> smem_raised{0};
-  auto kern = paged_decode_q4_kernel<NT, kScored>;
+  auto kern = paged_decode_q4_kernel<NT, HP, kScored>;
   if (!ensure_smem_limit(kern, Lay<NT>::kAlloc, smem_raised)) return PA_ERR_CUDA;
   // one wave of CTAs, as far as the workspace's partial rows (num_seqs * num_splits
-  // per query head) hold what the cut can leave: a piece behind every inner chunk
-  // boundary and a first piece for every sequence that crosses one
+  // per query head, some of them for `info`) hold what the cut can leave: a
+  // piece behind every inner chunk boundary and a first piece for every
+  // sequence that crosses one
   int sms = num_sms_current_device();
   if (sms <= 0) sms = 148;
-  int64_t chunks = static_cast<int64_t>(sms) * Lay<NT>::kCtasPerSm / q.d.num_kv_heads;
-  const int64_t seqs = q.num_seqs, rows = seqs * num_splits;
+  const int32_t heads = q.d.num_kv_heads;
+  int64_t chunks = static_cast<int64_t>(sms) * Lay<NT>::kCtasPerSm / (heads / HP);
+  const int64_t seqs = q.num_seqs, rows = seqs * num_splits - (seqs + kD - 1) / kD;
   q.whole = num_splits == 1;
   if (q.whole) {
     if (chunks > seqs) chunks = seqs;
   } else if (chunks - 1 + (seqs < chunks - 1 ? seqs : chunks - 1) > rows) {
     chunks = seqs < rows - seqs ? rows - seqs + 1 : rows / 2 + 1;
   }
-  if (chunks > 65535) chunks = 65535;
+  if (chunks > 32767) chunks = 32767;  // half of `info`'s word each
   if (chunks < 1) chunks = 1;
   q.slots = static_cast<int32_t>(chunks - 1 + (seqs < chunks - 1 ? seqs : chunks - 1));
-  const dim3 grid(static_cast<unsigned>(q.d.num_kv_heads), static_cast<unsigned>(chunks));
+  q.info = reinterpret_cast<int32_t*>(q.d.ws_o + static_cast<int64_t>(heads) * q.slots * G * kD);
+  const dim3 grid(static_cast<unsigned>(heads / HP), static_cast<unsigned>(chunks));
   kern<<<grid, kThreads, Lay<NT>::kAlloc, stream>>>(mk, mv, q, G);
-  return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+  if (cudaGetLastError() != cudaSuccess) return PA_ERR_CUDA;
+  if (q.whole || chunks == 1) return PA_OK;  // no sequence is split
+  const dim3 merge_grid(static_cast<unsigned>(heads * G),
+                        static_cast<unsigned>(seqs < 256 ? seqs : 256));
+  return launch_dependent(merge_pieces_kernel<HP, kScored>, merge_grid, kMergeWarps * 32, stream, q,
+                          G, static_cast<int>(chunks));
 }
 
 }  // namespace
@@ -873,21 +923,37 @@ pa_status launch_paged_decode_q4(const DecodeArgs& a, cudaStream_t stream) {
   if (a.num_seqs == 0) return PA_OK;
   if (a.num_seqs > 65535) return PA_ERR_UNSUPPORTED;
   const int32_t G = a.num_q_heads / a.num_kv_heads;
-  const int64_t rows = a.num_blocks * a.block_size;
-  const int32_t box_rows = a.block_size < kUnit ? a.block_size : kUnit;
+  // Two kv heads per CTA where their number is even: a token's rows of both
+  // are 160 contiguous bytes, and a copy's rate is per row, not per byte
+  // (rows of 80 bytes alone: 0.89 of the copy rate with nothing computed, 160: 0.98).
+  // A single kv head: two tokens' rows are one 160-byte row of the map.
+  const bool paired = a.num_kv_heads % 2 == 0, single = a.num_kv_heads == 1;
+  const int64_t rows = a.num_blocks * a.block_size >> (single ? 1 : 0);
+  const int32_t box_rows = (a.block_size < kUnit ? a.block_size : kUnit) >> (single ? 1 : 0);
+  const int32_t row_bytes = kRow * a.num_kv_heads * (single ? 2 : 1);
+  const int32_t box_bytes = kRow * (paired || single ? 2 : 1);
   CUtensorMap mk, mv;
-  if (!make_kv_map_q4(&mk, a.k_cache, rows, a.num_kv_heads, box_rows) ||
-      !make_kv_map_q4(&mv, a.v_cache, rows, a.num_kv_heads, box_rows))
+  if (!make_row_map(&mk, a.k_cache, rows, row_bytes, box_bytes, box_rows) ||
+      !make_row_map(&mv, a.v_cache, rows, row_bytes, box_bytes, box_rows))
     return PA_ERR_CUDA;
   Q4Params q{};
   q.d = make_decode_params(a);
   q.num_seqs = a.num_seqs;
+  q.pair_tokens = single ? 1 : 0;
   const int n = a.plan.num_splits;
-  if (a.scores != nullptr)
-    return G <= 8 ? launch_q4<1, true>(mk, mv, q, G, n, stream)
-                  : launch_q4<2, true>(mk, mv, q, G, n, stream);
-  return G <= 8 ? launch_q4<1, false>(mk, mv, q, G, n, stream)
-                : launch_q4<2, false>(mk, mv, q, G, n, stream);
+  const bool scored = a.scores != nullptr;
+  if (G <= 8) {
+    if (paired)
+      return scored ? launch_q4<1, 2, true>(mk, mv, q, G, n, stream)
+                    : launch_q4<1, 2, false>(mk, mv, q, G, n, stream);
+    return scored ? launch_q4<1, 1, true>(mk, mv, q, G, n, stream)
+                  : launch_q4<1, 1, false>(mk, mv, q, G, n, stream);
+  }
+  if (paired)
+    return scored ? launch_q4<2, 2, true>(mk, mv, q, G, n, stream)
+                  : launch_q4<2, 2, false>(mk, mv, q, G, n, stream);
+  return scored ? launch_q4<2, 1, true>(mk, mv, q, G, n, stream)
+                : launch_q4<2, 1, false>(mk, mv, q, G, n, stream);
 }
 
 }  // namespace pa_detail

@@ -26,6 +26,7 @@ template <int G>
 __global__ void __launch_bounds__(kSumThreads) add_weights_kernel(const DecodeParams p,
                                                                   const SumsParams w) {
   const int g = blockIdx.y, b = blockIdx.z;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the scores and sums of logs are there
   bool clipped;
   const int L = effective_len(p, b, &clipped);
   const int t = blockIdx.x * kSumThreads + threadIdx.x;
@@ -50,7 +51,7 @@ __global__ void __launch_bounds__(kSumThreads) add_weights_kernel(const DecodePa
   float weight = 0.f;
 #pragma unroll
   for (int h = 0; h < G; ++h) {
-    const float m = __ldg(lse + h);
+    const float m = __ldcg(lse + h);
     weight += m == -INFINITY ? 0.f : exp2f(v[h] - m);  // -inf: no token is there
   }
   const int64_t at = (static_cast<int64_t>(b) * p.num_kv_heads + g) * w.sums_len + t;
@@ -63,8 +64,7 @@ pa_status launch_add(const DecodeParams& p, const SumsParams& w, int32_t num_seq
                      cudaStream_t stream) {
   const dim3 grid(static_cast<unsigned>((tokens + kSumThreads - 1) / kSumThreads),
                   static_cast<unsigned>(p.num_kv_heads), static_cast<unsigned>(num_seqs));
-  add_weights_kernel<G><<<grid, kSumThreads, 0, stream>>>(p, w);
-  return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+  return launch_dependent(add_weights_kernel<G>, grid, kSumThreads, stream, p, w);
 }
 
 size_t align256(size_t x) { return (x + 255) / 256 * 256; }

@@ -537,6 +537,27 @@ inline bool ensure_smem_limit(Kernel kernel, int bytes, std::atomic<uint64_t>& r
 }
 
 
+// Launches a kernel whose CTAs may be placed while the one before it on the
+// stream still runs; it waits for that one's end itself (griddepcontrol.wait).
+template <typename... Params, typename... Args>
+inline pa_status launch_dependent(void (*kernel)(Params...), dim3 grid, int threads,
+                                  cudaStream_t stream, Args... args) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...) != cudaSuccess) {
+    cudaGetLastError();
+    return PA_ERR_CUDA;
+  }
+  return PA_OK;
+}
+
 int num_sms_current_device();  // cached per device; 0 if no device
 
 // TMA maps over a [rows, H_KV, 128] cache (rows = num_blocks * block_size):
@@ -546,9 +567,9 @@ bool make_kv_map_swizzled(CUtensorMap* map, const void* base, int64_t rows, int3
                           int32_t box_rows);
 bool make_kv_map_fp8(CUtensorMap* map, const void* base, int64_t rows, int32_t num_kv_heads,
                      int32_t box_rows);
-// The same over a [rows, H_KV, 80] 4-bit cache: whole 80-byte rows, no swizzle.
-bool make_kv_map_q4(CUtensorMap* map, const void* base, int64_t rows, int32_t num_kv_heads,
-                    int32_t box_rows);
+// TMA map over [rows, row_bytes] bytes, boxes of box_bytes x box_rows, not swizzled.
+bool make_row_map(CUtensorMap* map, const void* base, int64_t rows, int32_t row_bytes,
+                  int32_t box_bytes, int32_t box_rows);
 
 struct ReshapeArgs {
   const void* key;

@@ -14,13 +14,13 @@ import pytest
 
 
 def launch_chunks(slots_on_gpu, heads, seqs, num_splits):
-    chunks, rows = slots_on_gpu // heads, seqs * num_splits
+    chunks, rows = slots_on_gpu // heads, seqs * num_splits - -(-seqs // 128)
     whole = num_splits == 1
     if whole:
         chunks = min(chunks, seqs)
     elif chunks - 1 + min(seqs, chunks - 1) > rows:
         chunks = rows - seqs + 1 if seqs < rows - seqs else rows // 2 + 1
-    chunks = max(1, min(chunks, 65535))
+    chunks = max(1, min(chunks, 32767))
     return chunks, chunks - 1 + min(seqs, chunks - 1), whole
 
 
@@ -51,7 +51,7 @@ def pieces(lens, chunks, whole, kpc):
 def check(lens, slots_on_gpu, heads, num_splits, kpc=1):
     B = len(lens)
     chunks, slots, whole = launch_chunks(slots_on_gpu, heads, B, num_splits)
-    assert slots <= B * num_splits or whole
+    assert slots <= B * num_splits - -(-B // 128) or whole
     got, n, pre, total, parts = pieces(lens, chunks, whole, kpc)
     used, seen = set(), np.zeros(sum(n), int)
     count = {}
