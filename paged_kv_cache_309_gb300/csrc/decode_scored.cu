@@ -14,55 +14,109 @@ namespace pa_detail {
 namespace {
 
 constexpr int kSumThreads = 256;
+constexpr int kSumLoads = 8;  // 16-byte score loads in flight per thread
 
 struct SumsParams {
   float* out;
   const float* in;
   int32_t sums_len;
   int32_t num_new;
+  bool wide;  // rows of sums on 16-byte boundaries
 };
 
+// A 16-byte load holds 4 / G tokens' scores (G <= 4) or a quarter to a half of
+// one token's (G = 16, 8).  A CTA takes kSumThreads * kSumLoads loads' worth of
+// tokens of one (sequence, kv head): one token per thread, a CTA for every
+// 256 tokens, spent its time waiting for the lengths and sums of logs
+// (B = 8, 32K-128K, G = 4: 125 us; so: see kSumLoads).
 template <int G>
 __global__ void __launch_bounds__(kSumThreads) add_weights_kernel(const DecodeParams p,
                                                                   const SumsParams w) {
+  constexpr int kV = G < 4 ? 4 / G : 1;   // tokens per step of a thread
+  constexpr int kL = G < 4 ? 1 : G / 4;   // loads per step
+  constexpr int kSteps = kSumLoads / kL;
   const int g = blockIdx.y, b = blockIdx.z;
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the scores and sums of logs are there
   bool clipped;
   const int L = effective_len(p, b, &clipped);
-  const int t = blockIdx.x * kSumThreads + threadIdx.x;
-  if (t >= min(L, w.sums_len)) return;
-  const float* lse = p.final_lse + static_cast<int64_t>(b) * p.num_q_heads + g * G;
-  const float* s = p.scores +
-                   ((static_cast<int64_t>(b) * p.num_kv_heads + g) * p.score_len + t) * G;
-  float v[G];
-  if constexpr (G % 4 == 0) {
+  const int end = min(L, w.sums_len);
+  const int64_t row = static_cast<int64_t>(b) * p.num_kv_heads + g;
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * (kSumThreads * kSteps * kV);
+  if (first >= end) return;
+  const float* scores = p.scores + row * p.score_len * G;
+  const int t0 = static_cast<int>(first) + threadIdx.x * kV;
+  float4 v[kSteps][kL];
+  float old[kSteps][kV];
 #pragma unroll
-    for (int h = 0; h < G; h += 4) {
-      const float4 x = __ldcs(reinterpret_cast<const float4*>(s + h));
-      v[h] = x.x;
-      v[h + 1] = x.y;
-      v[h + 2] = x.z;
-      v[h + 3] = x.w;
+  for (int i = 0; i < kSteps; ++i) {
+    const int t = t0 + i * kSumThreads * kV;
+    if (t < end) {
+#pragma unroll
+      for (int k = 0; k < kL; ++k)  // (rows of scores are 64 tokens long at least)
+        v[i][k] = __ldcs(reinterpret_cast<const float4*>(scores + static_cast<int64_t>(t) * G) + k);
+      const float* in = w.in + row * w.sums_len + t;
+      if (kV > 1 && w.wide && t + kV <= end) {
+        if constexpr (kV == 4) {
+          const float4 x = *reinterpret_cast<const float4*>(in);
+          old[i][0] = x.x;
+          old[i][1] = x.y;
+          old[i][2] = x.z;
+          old[i][3] = x.w;
+        } else if constexpr (kV == 2) {
+          const float2 x = *reinterpret_cast<const float2*>(in);
+          old[i][0] = x.x;
+          old[i][1] = x.y;
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < kV; ++j) old[i][j] = t + j < end ? in[j] : 0.f;
+      }
     }
-  } else {
-#pragma unroll
-    for (int h = 0; h < G; ++h) v[h] = __ldcs(s + h);
   }
-  float weight = 0.f;
+  float lse[G];
 #pragma unroll
-  for (int h = 0; h < G; ++h) {
-    const float m = __ldcg(lse + h);
-    weight += m == -INFINITY ? 0.f : exp2f(v[h] - m);  // -inf: no token is there
+  for (int h = 0; h < G; ++h)
+    lse[h] = __ldcg(p.final_lse + static_cast<int64_t>(b) * p.num_q_heads + g * G + h);
+#pragma unroll
+  for (int i = 0; i < kSteps; ++i) {
+    const int t = t0 + i * kSumThreads * kV;
+    if (t >= end) break;
+    float s[4 * kL];
+#pragma unroll
+    for (int k = 0; k < kL; ++k) {
+      s[4 * k] = v[i][k].x;
+      s[4 * k + 1] = v[i][k].y;
+      s[4 * k + 2] = v[i][k].z;
+      s[4 * k + 3] = v[i][k].w;
+    }
+    float sum[kV];
+#pragma unroll
+    for (int j = 0; j < kV; ++j) {
+      float weight = 0.f;
+#pragma unroll
+      for (int h = 0; h < G; ++h)  // (a sum of logs of -inf: no token is there)
+        weight += lse[h] == -INFINITY ? 0.f : exp2f(s[j * G + h] - lse[h]);
+      sum[j] = (t + j >= L - w.num_new ? 0.f : old[i][j]) + weight;
+    }
+    float* out = w.out + row * w.sums_len + t;
+    if (kV > 1 && w.wide && t + kV <= end) {
+      if constexpr (kV == 4)
+        *reinterpret_cast<float4*>(out) = make_float4(sum[0], sum[1], sum[2], sum[3]);
+      else if constexpr (kV == 2)
+        *reinterpret_cast<float2*>(out) = make_float2(sum[0], sum[1]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < kV; ++j)
+        if (t + j < end) out[j] = sum[j];
+    }
   }
-  const int64_t at = (static_cast<int64_t>(b) * p.num_kv_heads + g) * w.sums_len + t;
-  const float old = t >= L - w.num_new ? 0.f : w.in[at];
-  w.out[at] = old + weight;
 }
 
 template <int G>
 pa_status launch_add(const DecodeParams& p, const SumsParams& w, int32_t num_seqs, int64_t tokens,
                      cudaStream_t stream) {
-  const dim3 grid(static_cast<unsigned>((tokens + kSumThreads - 1) / kSumThreads),
+  constexpr int64_t kPerCta = static_cast<int64_t>(kSumThreads) * kSumLoads * 4 / G;
+  const dim3 grid(static_cast<unsigned>((tokens + kPerCta - 1) / kPerCta),
                   static_cast<unsigned>(p.num_kv_heads), static_cast<unsigned>(num_seqs));
   return launch_dependent(add_weights_kernel<G>, grid, kSumThreads, stream, p, w);
 }
@@ -95,7 +149,9 @@ pa_status launch_paged_decode_scored(DecodeArgs a, float* sums_out, const float*
                                               : launch_paged_decode(a, stream);
   if (st != PA_OK) return st;
   const DecodeParams p = make_decode_params(a);
-  const SumsParams w{sums_out, sums_in, sums_len, num_new};
+  const bool wide = sums_len % 4 == 0 && ((reinterpret_cast<uintptr_t>(sums_out) |
+                                           reinterpret_cast<uintptr_t>(sums_in)) & 15u) == 0u;
+  const SumsParams w{sums_out, sums_in, sums_len, num_new, wide};
   const int64_t tokens = p.score_len < sums_len ? p.score_len : sums_len;
   switch (a.num_q_heads / a.num_kv_heads) {
     case 1: return launch_add<1>(p, w, a.num_seqs, tokens, stream);
