@@ -21,8 +21,10 @@
 // 2^7 above the running maximum's scale, so that fp16 carries them down to 2^-31 of it.
 //
 // Rows of 80 bytes need no swizzle: eight consecutive rows start in eight
-// different groups of four banks (20 r mod 32); the 160-byte rows of two kv
-// heads in four (two passes).
+// different groups of four banks (20 r mod 32).  The 160 bytes of two kv heads
+// would start in four, so their boxes are 176 bytes wide (44 r mod 32; the last
+// 16 bytes are the next head's or past the row, and unused): shared memory was
+// 66% busy with 160.
 //
 // What bounds it: at 160 bytes per token and kv head HBM leaves an SM 440
 // issue slots for 16 tokens, and the first form of this kernel needed 431 of
@@ -56,7 +58,6 @@ namespace {
 constexpr int kUnit = 64;          // tokens per unit of the cut (boxes are up to 64 rows)
 constexpr int kRow = 80;           // bytes of a cached row of one kv head
 constexpr int kStageRows = 128;    // head rows per stage, 32 per consumer warp
-constexpr int kTensorBytes = kStageRows * kRow;
 constexpr float kLift = 7.0f;      // weights are 2^kLift (score - running maximum)
 constexpr int kPieceCost = 1;      // units charged for a sequence's start
 constexpr int kConsumers = kConsumerWarps * 32;
@@ -70,16 +71,19 @@ struct Q4Params {
   int32_t pair_tokens;  // 1: the maps' rows are pairs of tokens (one kv head)
 };
 
-template <int NT>
+template <int NT, int HP>
 struct Lay {
   static constexpr int kStages = 3;
   static constexpr int kCtasPerSm = NT == 1 ? 3 : 2;
+  static constexpr int kTile = kStageRows / HP;        // tokens per stage
+  static constexpr int kPitch = HP == 2 ? 176 : kRow;  // bytes of a token in a stage
+  static constexpr int kTensorBytes = kTile * kPitch;
   static constexpr int kStageBytes = 2 * kTensorBytes;  // K rows, then V rows
   static constexpr int kHeads = NT * 8;
-  // the join of the four warps, 64 head elements at a time: [warp][h][64], then
+  // the join of the four warps, 32 head elements at a time: [warp][h][32], then
   // maxima and sums [warp][h], weights [warp][h], totals [head, h][2]
   static constexpr int kRedOffset = kStages * kStageBytes;
-  static constexpr int kRedFloats = kConsumerWarps * kHeads * 64;
+  static constexpr int kRedFloats = kConsumerWarps * kHeads * 32;
   static constexpr int kStatOffset = kRedOffset + kRedFloats * 4;
   static constexpr int kStatFloats = 3 * kConsumerWarps * kHeads + 4 * kHeads;
   static constexpr int kBarOffset = kStatOffset + kStatFloats * 4;
@@ -345,15 +349,16 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
 // NT: n-tiles of 8 query heads (G <= 8 -> 1, G = 16 -> 2); HP: kv heads per
 // CTA; kScored: also store the scores and each query head's log2-sum-exp.
 template <int NT, int HP, bool kScored>
-__global__ void __launch_bounds__(kThreads, Lay<NT>::kCtasPerSm)
+__global__ void __launch_bounds__(kThreads, Lay<NT, HP>::kCtasPerSm)
     paged_decode_q4_kernel(const __grid_constant__ CUtensorMap tm_k,
                            const __grid_constant__ CUtensorMap tm_v,
                            const __grid_constant__ Q4Params qp, int G) {
-  using L_ = Lay<NT>;
+  using L_ = Lay<NT, HP>;
   const DecodeParams& p = qp.d;
   constexpr int kStages = L_::kStages;
-  constexpr int kTile = kStageRows / HP;  // tokens per stage
-  constexpr int kPitch = kRow * HP;       // bytes of a token's rows in a stage
+  constexpr int kTile = L_::kTile;
+  constexpr int kPitch = L_::kPitch;
+  constexpr int kTensorBytes = L_::kTensorBytes;
   constexpr int kHeadWarps = kConsumerWarps / HP;
   extern __shared__ __align__(128) uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((128u - (smem_u32(smem_raw) & 127u)) & 127u);
@@ -488,7 +493,7 @@ __global__ void __launch_bounds__(kThreads, Lay<NT>::kCtasPerSm)
   const uint32_t meta_frag = base + static_cast<uint32_t>((lane & 15) * kPitch + 64);
   // (s, m) rows read directly: K row gq, V row 2tq
   const uint32_t k_meta = base + static_cast<uint32_t>(gq * kPitch + 64);
-  const uint32_t v_meta = base + static_cast<uint32_t>(kTensorBytes + 2 * tq * kPitch + 64);
+  const uint32_t v_meta = base + static_cast<uint32_t>(2 * tq * kPitch + 64);
   const uint32_t smem_base = smem_u32(smem);
   uint32_t magic;  // fp16 pair (64, 64), kept in a register
   asm volatile("mov.u32 %0, 0x54005400;" : "=r"(magic));
@@ -570,104 +575,91 @@ __global__ void __launch_bounds__(kThreads, Lay<NT>::kCtasPerSm)
       }
     }
 
-    // One 16-token slice of a tile (sl 0 or 1).  kFull: every row is a token.
-    auto slice = [&](auto full_tag, const int sl, const int tok, const uint32_t st,
-                     const uint32_t mask32) {
+    // The warp's 32 tokens of a tile, two slices of 16.  kFull: every row is a token.
+    auto tile = [&](auto full_tag, const int tok, const uint32_t st, const uint32_t mask32) {
       constexpr bool kFull = decltype(full_tag)::value;
-      const int r0 = t0 + 16 * sl;  // of the tile's tokens
-      const uint32_t mask16 = (mask32 >> (16 * sl)) & 0xFFFFu;
-      if (!kFull && mask16 == 0u) {  // no token of the slice is there
-        if constexpr (kScored) {
-          const float none[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-            store_scores(p, pc.b, g, G, tok + r0, gq, pc.tok_end - tok - r0, nt * 8 + 2 * tq,
-                         none);
-        }
-        return;
-      }
-      const uint32_t kbase = st + sl * 16 * kPitch;
-      const uint32_t kaddr = kbase + frag;
-      const uint32_t vaddr = kaddr + kTensorBytes;
-      // ---- S_u = codes . q, and the minima's sum
-      float su[NT][4][4], zk[NT][4];
-#pragma unroll
-      for (int u2 = 0; u2 < 4; u2 += 2) {
-        uint32_t r[4];  // (row gq, u2), (row gq + 8, u2), (row gq, u2 + 1), (row gq + 8, u2 + 1)
-        ldsm_x4(kaddr + 16 * u2, r);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const uint32_t lo = r[2 * i], hi = r[2 * i + 1];
-          const uint32_t lo8 = lo >> 8, hi8 = hi >> 8;
-          const uint32_t a0[4] = {lo & 0x000F000Fu, hi & 0x000F000Fu, lo & 0x00F000F0u,
-                                  hi & 0x00F000F0u};
-          const uint32_t a1[4] = {lo8 & 0x000F000Fu, hi8 & 0x000F000Fu, lo8 & 0x00F000F0u,
-                                  hi8 & 0x00F000F0u};
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            mma_f16_first(su[nt][u2 + i], a0, qb[nt][u2 + i][0], qb[nt][u2 + i][1]);
-            mma_f16_16816(su[nt][u2 + i], a1, qb[nt][u2 + i][2], qb[nt][u2 + i][3]);
-          }
-        }
-      }
-      {
-        uint32_t r[4];  // (s, m) of group tq, rows gq and gq + 8
-        ldsm_x4(kbase + meta_frag, r);
-        const uint32_t a[4] = {r[0], r[1], r[0], r[1]};
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) mma_f16_first(zk[nt], a, qz[nt][0], qz[nt][1]);
-      }
-      float ss[2][4];  // s_u of rows gq, gq + 8
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const uint4 w = lds128(kbase + k_meta + 8 * i * kPitch);
-        ss[i][0] = low_f32(w.x);
-        ss[i][1] = low_f32(w.y);
-        ss[i][2] = low_f32(w.z);
-        ss[i][3] = low_f32(w.w);
-      }
-      const bool v0 = kFull || ((mask16 >> gq) & 1u);        // token r0 + gq
-      const bool v1 = kFull || ((mask16 >> (gq + 8)) & 1u);  // token r0 + gq + 8
-      // ---- scores relative to the running maximum (first: to -inf, so +inf)
-      float a[NT][4], sr[NT][4];
+      float s[2][NT][4];  // scores of rows gq (0, 1) and gq + 8 (2, 3), heads 2tq, 2tq + 1
       bool high = false;
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
+      for (int sl = 0; sl < 2; ++sl) {
+        const uint32_t kbase = st + sl * 16 * kPitch;
+        // ---- S_u = codes . q, and the minima's sum
+        float su[NT][4][4], zk[NT][4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          a[nt][i] = ss[i >> 1][0] * su[nt][0][i];
+        for (int u2 = 0; u2 < 4; u2 += 2) {
+          uint32_t r[4];  // (row gq, u2), (row gq + 8, u2), (row gq, u2 + 1), (row gq + 8, u2 + 1)
+          ldsm_x4(kbase + frag + 16 * u2, r);
 #pragma unroll
-          for (int v = 1; v < 4; ++v) a[nt][i] = fmaf(ss[i >> 1][v], su[nt][v][i], a[nt][i]);
-          sr[nt][i] = fmaf(a[nt][i], sscale[nt][i & 1],
-                           fmaf(zk[nt][i], zscale[nt][i & 1], -m[nt][i & 1]));
+          for (int i = 0; i < 2; ++i) {
+            const uint32_t lo = r[2 * i], hi = r[2 * i + 1];
+            const uint32_t lo8 = lo >> 8, hi8 = hi >> 8;
+            const uint32_t a0[4] = {lo & 0x000F000Fu, hi & 0x000F000Fu, lo & 0x00F000F0u,
+                                    hi & 0x00F000F0u};
+            const uint32_t a1[4] = {lo8 & 0x000F000Fu, hi8 & 0x000F000Fu, lo8 & 0x00F000F0u,
+                                    hi8 & 0x00F000F0u};
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              mma_f16_first(su[nt][u2 + i], a0, qb[nt][u2 + i][0], qb[nt][u2 + i][1]);
+              mma_f16_16816(su[nt][u2 + i], a1, qb[nt][u2 + i][2], qb[nt][u2 + i][3]);
+            }
+          }
         }
-        if (!v0) sr[nt][0] = sr[nt][1] = -INFINITY;
-        if (!v1) sr[nt][2] = sr[nt][3] = -INFINITY;
-        high |= fmaxf(fmaxf(sr[nt][0], sr[nt][1]), fmaxf(sr[nt][2], sr[nt][3])) >
-                kLift + kRescaleLog2;
-      }
-      if (kScored || __any_sync(0xffffffffu, high)) {
+        {
+          uint32_t r[4];  // (s, m) of group tq, rows gq and gq + 8
+          ldsm_x4(kbase + meta_frag, r);
+          const uint32_t a[4] = {r[0], r[1], r[0], r[1]};
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) mma_f16_first(zk[nt], a, qz[nt][0], qz[nt][1]);
+        }
+        float ss[2][4];  // s_u of rows gq, gq + 8
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint4 w = lds128(kbase + k_meta + 8 * i * kPitch);
+          ss[i][0] = low_f32(w.x);
+          ss[i][1] = low_f32(w.y);
+          ss[i][2] = low_f32(w.z);
+          ss[i][3] = low_f32(w.w);
+        }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          float s[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            s[i] = fmaf(a[nt][i], sscale[nt][i & 1], zk[nt][i] * zscale[nt][i & 1]);
-          if (!v0) s[0] = s[1] = -INFINITY;
-          if (!v1) s[2] = s[3] = -INFINITY;
-          if constexpr (kScored)
-            store_scores(p, pc.b, g, G, tok + r0, gq, pc.tok_end - tok - r0, nt * 8 + 2 * tq, s);
-          if (kScored && !__any_sync(0xffffffffu, high)) continue;
-          float mx[2] = {fmaxf(s[0], s[2]), fmaxf(s[1], s[3])};
+          for (int i = 0; i < 4; ++i) {
+            float a = ss[i >> 1][0] * su[nt][0][i];
 #pragma unroll
-          for (int off = 4; off <= 16; off <<= 1) {
-            mx[0] = fmaxf(mx[0], __shfl_xor_sync(0xffffffffu, mx[0], off));
-            mx[1] = fmaxf(mx[1], __shfl_xor_sync(0xffffffffu, mx[1], off));
+            for (int v = 1; v < 4; ++v) a = fmaf(ss[i >> 1][v], su[nt][v][i], a);
+            s[sl][nt][i] = fmaf(a, sscale[nt][i & 1], zk[nt][i] * zscale[nt][i & 1]);
           }
+          if (!kFull) {
+            const uint32_t mask16 = mask32 >> (16 * sl);
+            if (!((mask16 >> gq) & 1u)) s[sl][nt][0] = s[sl][nt][1] = -INFINITY;
+            if (!((mask16 >> (gq + 8)) & 1u)) s[sl][nt][2] = s[sl][nt][3] = -INFINITY;
+          }
+          if constexpr (kScored)
+            store_scores(p, pc.b, g, G, tok + t0 + 16 * sl, gq,
+                         pc.tok_end - tok - t0 - 16 * sl, nt * 8 + 2 * tq, s[sl][nt]);
+        }
+      }
+      // ---- running maximum: moved when a score beats it by 2^kRescaleLog2 (always on
+      // the first); whether any does is one vote
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          high |= fmaxf(fmaxf(s[0][nt][j], s[0][nt][j + 2]),
+                        fmaxf(s[1][nt][j], s[1][nt][j + 2])) >
+                  m[nt][j] + (kLift + kRescaleLog2);
+      if (__any_sync(0xffffffffu, high)) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            if (mx[j] > m[nt][j] + (kLift + kRescaleLog2)) {  // always on the first
-              const float corr = exp2f(m[nt][j] - (mx[j] - kLift));
+            float mx = fmaxf(fmaxf(s[0][nt][j], s[0][nt][j + 2]),
+                             fmaxf(s[1][nt][j], s[1][nt][j + 2]));
+#pragma unroll
+            for (int off = 4; off <= 16; off <<= 1)
+              mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+            if (mx > m[nt][j] + (kLift + kRescaleLog2)) {
+              const float corr = exp2f(m[nt][j] - (mx - kLift));
               l[nt][j] *= corr;
               z[nt][j] *= corr;
               z[nt][j + 2] *= corr;
@@ -676,70 +668,76 @@ __global__ void __launch_bounds__(kThreads, Lay<NT>::kCtasPerSm)
                 o[mt][nt][j] *= corr;
                 o[mt][nt][j + 2] *= corr;
               }
-              m[nt][j] = mx[j] - kLift;
+              m[nt][j] = mx - kLift;
             }
           }
-#pragma unroll
-          for (int i = 0; i < 4; ++i) sr[nt][i] = s[i] - m[nt][i & 1];
-          if (!v0) sr[nt][0] = sr[nt][1] = -INFINITY;
-          if (!v1) sr[nt][2] = sr[nt][3] = -INFINITY;
         }
       }
-      uint32_t pb[NT][2];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        const float p0 = ex2(sr[nt][0]), p1 = ex2(sr[nt][1]);
-        const float p2 = ex2(sr[nt][2]), p3 = ex2(sr[nt][3]);
-        l[nt][0] += p0 + p2;
-        l[nt][1] += p1 + p3;
-        // (token, heads) pairs to the B operand's (tokens, head) pairs
-        pb[nt][0] = transpose8(pack_f16x2(p0, p1));
-        pb[nt][1] = transpose8(pack_f16x2(p2, p3));
-      }
-      // ---- sum p m (and p s): the rows' (s, m) pairs as a matrix
-      {
-        uint32_t r[4];
-        ldsm_x4_trans(kbase + kTensorBytes + meta_frag, r);
-        const uint32_t am[4] = {r[0], 0u, r[1], 0u};
+      for (int sl = 0; sl < 2; ++sl) {
+        const uint32_t vbase = st + kTensorBytes + sl * 16 * kPitch;
+        uint32_t pb[NT][2];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) mma_f16_16816(z[nt], am, pb[nt][0], pb[nt][1]);
-      }
-      // ---- O^T += (s c)^T . P^T
-      uint32_t sv[2][4], sn[2][4];  // (s, s') and -64 (s, s') of tokens 2tq, 2tq + 1 (+ 8)
+        for (int nt = 0; nt < NT; ++nt) {
+          float e[4];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const uint4 x = lds128(kbase + v_meta + 8 * i * kPitch);
-        const uint4 y = lds128(kbase + v_meta + (8 * i + 1) * kPitch);
-        sv[i][0] = __byte_perm(x.x, y.x, 0x5410u);
-        sv[i][1] = __byte_perm(x.y, y.y, 0x5410u);
-        sv[i][2] = __byte_perm(x.z, y.z, 0x5410u);
-        sv[i][3] = __byte_perm(x.w, y.w, 0x5410u);
+          for (int i = 0; i < 4; ++i) e[i] = ex2(s[sl][nt][i] - m[nt][i & 1]);
+          if (!kFull) {  // (a head without a maximum yet: -inf - -inf)
+            const uint32_t mask16 = mask32 >> (16 * sl);
+            if (!((mask16 >> gq) & 1u)) e[0] = e[1] = 0.f;
+            if (!((mask16 >> (gq + 8)) & 1u)) e[2] = e[3] = 0.f;
+          }
+          l[nt][0] += e[0] + e[2];
+          l[nt][1] += e[1] + e[3];
+          // (token, heads) pairs to the B operand's (tokens, head) pairs
+          pb[nt][0] = transpose8(pack_f16x2(e[0], e[1]));
+          pb[nt][1] = transpose8(pack_f16x2(e[2], e[3]));
+        }
+        // ---- sum p m (and p s): the rows' (s, m) pairs as a matrix
+        {
+          uint32_t r[4];
+          ldsm_x4_trans(vbase + meta_frag, r);
+          const uint32_t am[4] = {r[0], 0u, r[1], 0u};
 #pragma unroll
-        for (int v = 0; v < 4; ++v) sn[i][v] = hmul2(sv[i][v], 0xD400D400u);  // -64
-      }
-#pragma unroll
-      for (int u2 = 0; u2 < 4; u2 += 2) {
-        uint32_t r[4];  // (tokens 2tq, u2), (tokens 2tq + 8, u2), the same of u2 + 1
-        ldsm_x4_trans(vaddr + 16 * u2, r);
+          for (int nt = 0; nt < NT; ++nt) mma_f16_16816(z[nt], am, pb[nt][0], pb[nt][1]);
+        }
+        // ---- O^T += (s c)^T . P^T
+        uint32_t sv[2][4], sn[2][4];  // (s, s') and -64 (s, s') of tokens 2tq, 2tq + 1 (+ 8)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const int v = u2 + i;
-          uint32_t x[2][4];  // s c of tokens 2tq.. (+8), element 32v + 4gq + k
+          const uint4 x = lds128(vbase + v_meta + 8 * i * kPitch);
+          const uint4 y = lds128(vbase + v_meta + (8 * i + 1) * kPitch);
+          sv[i][0] = __byte_perm(x.x, y.x, 0x5410u);
+          sv[i][1] = __byte_perm(x.y, y.y, 0x5410u);
+          sv[i][2] = __byte_perm(x.z, y.z, 0x5410u);
+          sv[i][3] = __byte_perm(x.w, y.w, 0x5410u);
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const uint32_t w = r[2 * i + j];
-            x[j][0] = hfma2(and_or(w << 4, 0x00F000F0u, magic), sv[j][v], sn[j][v]);
-            x[j][1] = hfma2(and_or(w, 0x00F000F0u, magic), sv[j][v], sn[j][v]);
-            x[j][2] = hfma2(and_or(w >> 4, 0x00F000F0u, magic), sv[j][v], sn[j][v]);
-            x[j][3] = hfma2(and_or(w >> 8, 0x00F000F0u, magic), sv[j][v], sn[j][v]);
-          }
+          for (int v = 0; v < 4; ++v) sn[i][v] = hmul2(sv[i][v], 0xD400D400u);  // -64
+        }
 #pragma unroll
-          for (int hh = 0; hh < 2; ++hh) {
-            const uint32_t av[4] = {x[0][2 * hh], x[0][2 * hh + 1], x[1][2 * hh],
-                                    x[1][2 * hh + 1]};
+        for (int u2 = 0; u2 < 4; u2 += 2) {
+          uint32_t r[4];  // (tokens 2tq, u2), (tokens 2tq + 8, u2), the same of u2 + 1
+          ldsm_x4_trans(vbase + frag + 16 * u2, r);
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-              mma_f16_16816(o[2 * v + hh][nt], av, pb[nt][0], pb[nt][1]);
+          for (int i = 0; i < 2; ++i) {
+            const int v = u2 + i;
+            uint32_t x[2][4];  // s c of tokens 2tq.. (+8), element 32v + 4gq + k
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const uint32_t w = r[2 * i + j];
+              x[j][0] = hfma2(and_or(w << 4, 0x00F000F0u, magic), sv[j][v], sn[j][v]);
+              x[j][1] = hfma2(and_or(w, 0x00F000F0u, magic), sv[j][v], sn[j][v]);
+              x[j][2] = hfma2(and_or(w >> 4, 0x00F000F0u, magic), sv[j][v], sn[j][v]);
+              x[j][3] = hfma2(and_or(w >> 8, 0x00F000F0u, magic), sv[j][v], sn[j][v]);
+            }
+#pragma unroll
+            for (int hh = 0; hh < 2; ++hh) {
+              const uint32_t av[4] = {x[0][2 * hh], x[0][2 * hh + 1], x[1][2 * hh],
+                                      x[1][2 * hh + 1]};
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+                mma_f16_16816(o[2 * v + hh][nt], av, pb[nt][0], pb[nt][1]);
+            }
           }
         }
       }
@@ -754,8 +752,17 @@ __global__ void __launch_bounds__(kThreads, Lay<NT>::kCtasPerSm)
       const uint32_t mask32 = tile_mask[4 * stage + warp % kHeadWarps];
       const uint32_t st = smem_base + stage * L_::kStageBytes;
       if (mask32 == 0xFFFFFFFFu) {
-        slice(std::true_type{}, 0, tok, st, mask32);
-        slice(std::true_type{}, 1, tok, st, mask32);
+        tile(std::true_type{}, tok, st, mask32);
+      } else if (mask32 == 0u) {  // no token of the warp's is there
+        if constexpr (kScored) {
+          const float none[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int sl = 0; sl < 2; ++sl)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+              store_scores(p, pc.b, g, G, tok + t0 + 16 * sl, gq,
+                           pc.tok_end - tok - t0 - 16 * sl, nt * 8 + 2 * tq, none);
+        }
       } else {
         // rows without a token: s = m = 0 makes their values 0 (the ring's
         // leftovers could be NaN, and 0 x NaN would poison the sums)
@@ -763,8 +770,7 @@ __global__ void __launch_bounds__(kThreads, Lay<NT>::kCtasPerSm)
           *reinterpret_cast<uint4*>(smem + stage * L_::kStageBytes + kTensorBytes + base +
                                     lane * kPitch + 64) = make_uint4(0u, 0u, 0u, 0u);
         __syncwarp();
-#pragma unroll 1
-        for (int sl = 0; sl < 2; ++sl) slice(std::false_type{}, sl, tok, st, mask32);
+        tile(std::false_type{}, tok, st, mask32);
         fence_proxy_async_smem();  // stores before the next TMA
       }
       __syncwarp();
@@ -781,7 +787,7 @@ __global__ void __launch_bounds__(kThreads, Lay<NT>::kCtasPerSm)
 
     // ---- the four warps' (maximum, sum, accumulator) joined in shared memory
     constexpr int GH = L_::kHeads;
-    float* red = reinterpret_cast<float*>(smem + L_::kRedOffset);  // [warp][h][64]
+    float* red = reinterpret_cast<float*>(smem + L_::kRedOffset);  // [warp][h][32]
     float* red_m = reinterpret_cast<float*>(smem + L_::kStatOffset);
     float* red_l = red_m + kConsumerWarps * GH;
     float* red_w = red_l + kConsumerWarps * GH;
@@ -795,14 +801,14 @@ __global__ void __launch_bounds__(kThreads, Lay<NT>::kCtasPerSm)
       qp.info[static_cast<int64_t>(blockIdx.x) * qp.num_seqs + pc.b] =
           c_first == c_last ? 0 : c_first << 16 | (c_last - c_first + 1);
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
+    for (int v = 0; v < 4; ++v) {
       // (a barrier has passed since the last reads of this memory)
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           const int h = nt * 8 + 2 * tq + j;
-          if (half == 0) {
+          if (v == 0) {
             float lv = l[nt][j];
             lv += __shfl_xor_sync(0xffffffffu, lv, 4);
             lv += __shfl_xor_sync(0xffffffffu, lv, 8);
@@ -812,20 +818,14 @@ __global__ void __launch_bounds__(kThreads, Lay<NT>::kCtasPerSm)
               red_l[warp * GH + h] = lv;
             }
           }
-#pragma unroll
-          for (int v = 2 * half; v < 2 * half + 2; ++v) {
-            const float zu = __shfl_sync(0xffffffffu, z[nt][j], 4 * (2 * v + 1) + tq);
-#pragma unroll
-            for (int hh = 0; hh < 2; ++hh) {
-              float* dst = red + (warp * GH + h) * 64 + 32 * (v & 1) + 4 * gq + 2 * hh;
-              *reinterpret_cast<float2*>(dst) =
-                  make_float2(o[2 * v + hh][nt][j] + zu, o[2 * v + hh][nt][j + 2] + zu);
-            }
-          }
+          const float zu = __shfl_sync(0xffffffffu, z[nt][j], 4 * (2 * v + 1) + tq);
+          *reinterpret_cast<float4*>(red + (warp * GH + h) * 32 + 4 * gq) =
+              make_float4(o[2 * v][nt][j] + zu, o[2 * v][nt][j + 2] + zu,
+                          o[2 * v + 1][nt][j] + zu, o[2 * v + 1][nt][j + 2] + zu);
         }
       }
       consumer_barrier();
-      if (half == 0) {
+      if (v == 0) {
         if (threadIdx.x < HP * G) {
           const int h = threadIdx.x % G, w0 = threadIdx.x / G * kHeadWarps;
           float M = -INFINITY;
@@ -844,19 +844,19 @@ __global__ void __launch_bounds__(kThreads, Lay<NT>::kCtasPerSm)
         }
         consumer_barrier();
       }
-      for (int i = threadIdx.x; i < HP * G * 16; i += kConsumers) {
-        const int hh = i >> 4;  // of the CTA's query heads
+      for (int i = threadIdx.x; i < HP * G * 8; i += kConsumers) {
+        const int hh = i >> 3;  // of the CTA's query heads
         const int head = hh / G, h = hh % G;
-        const int e0 = (i & 15) * 4;
+        const int e0 = (i & 7) * 4;
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int w = head * kHeadWarps; w < (head + 1) * kHeadWarps; ++w) {
           const float wt = red_w[w * GH + h];
-          const float4 v = *reinterpret_cast<const float4*>(red + (w * GH + h) * 64 + e0);
-          acc.x += wt * v.x;
-          acc.y += wt * v.y;
-          acc.z += wt * v.z;
-          acc.w += wt * v.w;
+          const float4 x = *reinterpret_cast<const float4*>(red + (w * GH + h) * 32 + e0);
+          acc.x += wt * x.x;
+          acc.y += wt * x.y;
+          acc.z += wt * x.z;
+          acc.w += wt * x.w;
         }
         const float Ls = fin[2 * hh + 1];
         const float inv = Ls == 0.f ? 0.f : 1.f / Ls;  // NaN stays NaN
@@ -865,7 +865,7 @@ __global__ void __launch_bounds__(kThreads, Lay<NT>::kCtasPerSm)
         acc.z *= inv;
         acc.w *= inv;
         const float lse = Ls == 0.f ? -INFINITY : fin[2 * hh] + log2f(Ls);
-        const int e = 64 * half + e0;
+        const int e = 32 * v + e0;
         if (c_first == c_last) {
           const int64_t row = static_cast<int64_t>(pc.b) * p.num_q_heads + g0 * G + hh;
           *reinterpret_cast<uint2*>(p.out + row * kD + e) =
@@ -887,7 +887,7 @@ pa_status launch_q4(const CUtensorMap& mk, const CUtensorMap& mv, Q4Params q, in
                     int num_splits, cudaStream_t stream) {
   static std::atomic<uint64_t> smem_raised{0};
   auto kern = paged_decode_q4_kernel<NT, HP, kScored>;
-  if (!ensure_smem_limit(kern, Lay<NT>::kAlloc, smem_raised)) return PA_ERR_CUDA;
+  if (!ensure_smem_limit(kern, Lay<NT, HP>::kAlloc, smem_raised)) return PA_ERR_CUDA;
   // one wave of CTAs, as far as the workspace's partial rows (num_seqs * num_splits
   // per query head, some of them for `info`) hold what the cut can leave: a
   // piece behind every inner chunk boundary and a first piece for every
@@ -895,7 +895,7 @@ pa_status launch_q4(const CUtensorMap& mk, const CUtensorMap& mv, Q4Params q, in
   int sms = num_sms_current_device();
   if (sms <= 0) sms = 148;
   const int32_t heads = q.d.num_kv_heads;
-  int64_t chunks = static_cast<int64_t>(sms) * Lay<NT>::kCtasPerSm / (heads / HP);
+  int64_t chunks = static_cast<int64_t>(sms) * Lay<NT, HP>::kCtasPerSm / (heads / HP);
   const int64_t seqs = q.num_seqs, rows = seqs * num_splits - (seqs + kD - 1) / kD;
   q.whole = num_splits == 1;
   if (q.whole) {
@@ -908,7 +908,7 @@ pa_status launch_q4(const CUtensorMap& mk, const CUtensorMap& mv, Q4Params q, in
   q.slots = static_cast<int32_t>(chunks - 1 + (seqs < chunks - 1 ? seqs : chunks - 1));
   q.info = reinterpret_cast<int32_t*>(q.d.ws_o + static_cast<int64_t>(heads) * q.slots * G * kD);
   const dim3 grid(static_cast<unsigned>(heads / HP), static_cast<unsigned>(chunks));
-  kern<<<grid, kThreads, Lay<NT>::kAlloc, stream>>>(mk, mv, q, G);
+  kern<<<grid, kThreads, Lay<NT, HP>::kAlloc, stream>>>(mk, mv, q, G);
   if (cudaGetLastError() != cudaSuccess) return PA_ERR_CUDA;
   if (q.whole || chunks == 1) return PA_OK;  // no sequence is split
   const dim3 merge_grid(static_cast<unsigned>(heads * G),
@@ -931,7 +931,7 @@ pa_status launch_paged_decode_q4(const DecodeArgs& a, cudaStream_t stream) {
   const int64_t rows = a.num_blocks * a.block_size >> (single ? 1 : 0);
   const int32_t box_rows = (a.block_size < kUnit ? a.block_size : kUnit) >> (single ? 1 : 0);
   const int32_t row_bytes = kRow * a.num_kv_heads * (single ? 2 : 1);
-  const int32_t box_bytes = kRow * (paired || single ? 2 : 1);
+  const int32_t box_bytes = paired ? Lay<1, 2>::kPitch : kRow * (single ? 2 : 1);
   CUtensorMap mk, mv;
   if (!make_row_map(&mk, a.k_cache, rows, row_bytes, box_bytes, box_rows) ||
       !make_row_map(&mv, a.v_cache, rows, row_bytes, box_bytes, box_rows))
