@@ -59,7 +59,7 @@ constexpr int kUnit = 64;          // tokens per unit of the cut (boxes are up t
 constexpr int kRow = 80;           // bytes of a cached row of one kv head
 constexpr int kStageRows = 128;    // head rows per stage, 32 per consumer warp
 constexpr float kLift = 7.0f;      // weights are 2^kLift (score - running maximum)
-constexpr int kPieceCost = 1;      // units charged for a sequence's start
+constexpr int kPieceCost = 2;      // units charged for a sequence's start
 constexpr int kConsumers = kConsumerWarps * 32;
 
 struct Q4Params {
@@ -68,6 +68,7 @@ struct Q4Params {
   int32_t slots;  // partial slots per kv head
   int32_t* info;  // [H_KV / HP, B]: chunk of the first piece << 16 | pieces, 0 if not split
   bool whole;     // no partials: chunks begin at sequence starts
+  int32_t log2_g;       // of the query heads per kv head
   int32_t pair_tokens;  // 1: the maps' rows are pairs of tokens (one kv head)
 };
 
@@ -80,12 +81,12 @@ struct Lay {
   static constexpr int kTensorBytes = kTile * kPitch;
   static constexpr int kStageBytes = 2 * kTensorBytes;  // K rows, then V rows
   static constexpr int kHeads = NT * 8;
-  // the join of the four warps, 32 head elements at a time: [warp][h][32], then
-  // maxima and sums [warp][h], weights [warp][h], totals [head, h][2]
+  // the join of a head's warps: 32 elements of every head of a warp at a time (more
+  // where G is less than kHeads), then maxima and sums [warp][h]
   static constexpr int kRedOffset = kStages * kStageBytes;
   static constexpr int kRedFloats = kConsumerWarps * kHeads * 32;
   static constexpr int kStatOffset = kRedOffset + kRedFloats * 4;
-  static constexpr int kStatFloats = 3 * kConsumerWarps * kHeads + 4 * kHeads;
+  static constexpr int kStatFloats = 2 * kConsumerWarps * kHeads;
   static constexpr int kBarOffset = kStatOffset + kStatFloats * 4;
   static constexpr int kMaskOffset = kBarOffset + 2 * kStages * 8;  // four words per stage
   static constexpr int kSchedOffset = kMaskOffset + kStages * 16;   // five 64-bit words
@@ -169,7 +170,19 @@ __device__ __forceinline__ void find_chunk(const Q4Params& q, int c, int chunks,
   const DecodeParams& p = q.d;
   int64_t units = 0;
   bool any_clipped = false;
-  for (int b = lane; b < q.num_seqs; b += 32) {
+  int held[4];  // units of sequences lane, lane + 32, ...: the lengths are read in one round
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int b = lane + 32 * k;
+    held[k] = 0;
+    if (b < q.num_seqs) {
+      bool clipped;
+      held[k] = (effective_len(p, b, &clipped) + kUnit - 1) / kUnit;
+      any_clipped |= clipped;
+    }
+    units += held[k];
+  }
+  for (int b = lane + 128; b < q.num_seqs; b += 32) {
     bool clipped;
     units += (effective_len(p, b, &clipped) + kUnit - 1) / kUnit;
     any_clipped |= clipped;
@@ -188,7 +201,12 @@ __device__ __forceinline__ void find_chunk(const Q4Params& q, int c, int chunks,
   int64_t base = 0;
   for (int first = 0; first < q.num_seqs && !(found0 && found1); first += 32) {
     const int b = first + lane;
-    const int n = b < q.num_seqs ? units_of(p, b) : 0;
+    const int n = first == 0    ? held[0]
+                  : first == 32 ? held[1]
+                  : first == 64 ? held[2]
+                  : first == 96 ? held[3]
+                  : b < q.num_seqs ? units_of(p, b)
+                                   : 0;
     int64_t incl = n;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
@@ -785,13 +803,14 @@ __global__ void __launch_bounds__(kThreads, Lay<NT, HP>::kCtasPerSm)
       atomicOr(p.err, PA_DEVERR_WAIT_TIMEOUT);
     }
 
-    // ---- the four warps' (maximum, sum, accumulator) joined in shared memory
+    // ---- the accumulators of a head's warps joined in shared memory, as many
+    // groups of 32 head elements at a time as the G heads leave room for
     constexpr int GH = L_::kHeads;
-    float* red = reinterpret_cast<float*>(smem + L_::kRedOffset);  // [warp][h][32]
+    float* red = reinterpret_cast<float*>(smem + L_::kRedOffset);  // [warp][G][32 vs]
     float* red_m = reinterpret_cast<float*>(smem + L_::kStatOffset);
     float* red_l = red_m + kConsumerWarps * GH;
-    float* red_w = red_l + kConsumerWarps * GH;
-    float* fin = red_w + kConsumerWarps * GH;
+    const int vs = min(4, GH >> qp.log2_g);  // groups per round
+    const int lv = vs == 4 ? 2 : vs - 1;     // log2(vs)
     const int c_first = qp.whole ? c : chunk_of(pc.first, pc.b, total, parts);
     const int c_last = qp.whole ? c : chunk_of(pc.last, pc.b, total, parts);
     // partial slot: c - 1 for a piece that goes on from chunk c - 1; for a
@@ -801,6 +820,20 @@ __global__ void __launch_bounds__(kThreads, Lay<NT, HP>::kCtasPerSm)
       qp.info[static_cast<int64_t>(blockIdx.x) * qp.num_seqs + pc.b] =
           c_first == c_last ? 0 : c_first << 16 | (c_last - c_first + 1);
 #pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        float x = l[nt][j];
+        x += __shfl_xor_sync(0xffffffffu, x, 4);
+        x += __shfl_xor_sync(0xffffffffu, x, 8);
+        x += __shfl_xor_sync(0xffffffffu, x, 16);
+        if (gq == 0) {
+          red_m[warp * GH + nt * 8 + 2 * tq + j] = m[nt][j];
+          red_l[warp * GH + nt * 8 + 2 * tq + j] = x;
+        }
+      }
+    }
+#pragma unroll
     for (int v = 0; v < 4; ++v) {
       // (a barrier has passed since the last reads of this memory)
 #pragma unroll
@@ -808,73 +841,55 @@ __global__ void __launch_bounds__(kThreads, Lay<NT, HP>::kCtasPerSm)
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           const int h = nt * 8 + 2 * tq + j;
-          if (v == 0) {
-            float lv = l[nt][j];
-            lv += __shfl_xor_sync(0xffffffffu, lv, 4);
-            lv += __shfl_xor_sync(0xffffffffu, lv, 8);
-            lv += __shfl_xor_sync(0xffffffffu, lv, 16);
-            if (gq == 0) {
-              red_m[warp * GH + h] = m[nt][j];
-              red_l[warp * GH + h] = lv;
-            }
-          }
           const float zu = __shfl_sync(0xffffffffu, z[nt][j], 4 * (2 * v + 1) + tq);
-          *reinterpret_cast<float4*>(red + (warp * GH + h) * 32 + 4 * gq) =
-              make_float4(o[2 * v][nt][j] + zu, o[2 * v][nt][j + 2] + zu,
-                          o[2 * v + 1][nt][j] + zu, o[2 * v + 1][nt][j + 2] + zu);
+          if (h < G)
+            *reinterpret_cast<float4*>(red + ((warp << qp.log2_g) + h) * (32 << lv) +
+                                       32 * (v & (vs - 1)) + 4 * gq) =
+                make_float4(o[2 * v][nt][j] + zu, o[2 * v][nt][j + 2] + zu,
+                            o[2 * v + 1][nt][j] + zu, o[2 * v + 1][nt][j + 2] + zu);
         }
       }
+      if ((v + 1) & (vs - 1)) continue;  // more groups in this round
       consumer_barrier();
-      if (v == 0) {
-        if (threadIdx.x < HP * G) {
-          const int h = threadIdx.x % G, w0 = threadIdx.x / G * kHeadWarps;
-          float M = -INFINITY;
+      for (int i = threadIdx.x; i < (HP * 8 << lv) << qp.log2_g; i += kConsumers) {
+        const int hh = i >> (3 + lv);  // of the CTA's query heads
+        const int head = hh >> qp.log2_g, h = hh & (G - 1);
+        const int e0 = (i & ((8 << lv) - 1)) * 4;
+        float M = -INFINITY;
 #pragma unroll
-          for (int w = w0; w < w0 + kHeadWarps; ++w) M = fmaxf(M, red_m[w * GH + h]);
-          float Ls = 0.f;
-#pragma unroll
-          for (int w = w0; w < w0 + kHeadWarps; ++w) {
-            const float wt = (M == -INFINITY) ? 0.f : exp2f(red_m[w * GH + h] - M);
-            red_w[w * GH + h] = wt;
-            // (a warp of NaN scores only has no maximum: its sum is NaN all the same)
-            Ls += red_l[w * GH + h] * (red_l[w * GH + h] != red_l[w * GH + h] ? 1.f : wt);
-          }
-          fin[2 * threadIdx.x] = M;
-          fin[2 * threadIdx.x + 1] = Ls;
-        }
-        consumer_barrier();
-      }
-      for (int i = threadIdx.x; i < HP * G * 8; i += kConsumers) {
-        const int hh = i >> 3;  // of the CTA's query heads
-        const int head = hh / G, h = hh % G;
-        const int e0 = (i & 7) * 4;
+        for (int w = 0; w < kHeadWarps; ++w)
+          M = fmaxf(M, red_m[(head * kHeadWarps + w) * GH + h]);
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        float Ls = 0.f;
 #pragma unroll
-        for (int w = head * kHeadWarps; w < (head + 1) * kHeadWarps; ++w) {
-          const float wt = red_w[w * GH + h];
-          const float4 x = *reinterpret_cast<const float4*>(red + (w * GH + h) * 32 + e0);
+        for (int w = 0; w < kHeadWarps; ++w) {
+          const int wi = head * kHeadWarps + w;
+          const float wt = M == -INFINITY ? 0.f : exp2f(red_m[wi * GH + h] - M);
+          const float lw = red_l[wi * GH + h];
+          // (a warp of NaN scores only has no maximum: its sum is NaN all the same)
+          Ls += lw * (lw != lw ? 1.f : wt);
+          const float4 x =
+              *reinterpret_cast<const float4*>(red + ((wi << qp.log2_g) + h) * (32 << lv) + e0);
           acc.x += wt * x.x;
           acc.y += wt * x.y;
           acc.z += wt * x.z;
           acc.w += wt * x.w;
         }
-        const float Ls = fin[2 * hh + 1];
         const float inv = Ls == 0.f ? 0.f : 1.f / Ls;  // NaN stays NaN
         acc.x *= inv;
         acc.y *= inv;
         acc.z *= inv;
         acc.w *= inv;
-        const float lse = Ls == 0.f ? -INFINITY : fin[2 * hh] + log2f(Ls);
-        const int e = 32 * v + e0;
+        const int e = 32 * (v & ~(vs - 1)) + e0;
         if (c_first == c_last) {
           const int64_t row = static_cast<int64_t>(pc.b) * p.num_q_heads + g0 * G + hh;
           *reinterpret_cast<uint2*>(p.out + row * kD + e) =
               make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
-          if (kScored && e == 0) p.final_lse[row] = lse;
+          if (kScored && e == 0) p.final_lse[row] = Ls == 0.f ? -INFINITY : M + log2f(Ls);
         } else {
           const int64_t row = (static_cast<int64_t>(g0 + head) * qp.slots + slot) * G + h;
           *reinterpret_cast<float4*>(p.ws_o + row * kD + e) = acc;
-          if (e == 0) p.ws_lse[row] = lse;
+          if (e == 0) p.ws_lse[row] = Ls == 0.f ? -INFINITY : M + log2f(Ls);
         }
       }
       consumer_barrier();
@@ -940,6 +955,7 @@ pa_status launch_paged_decode_q4(const DecodeArgs& a, cudaStream_t stream) {
   q.d = make_decode_params(a);
   q.num_seqs = a.num_seqs;
   q.pair_tokens = single ? 1 : 0;
+  while ((1 << q.log2_g) < G) ++q.log2_g;
   const int n = a.plan.num_splits;
   const bool scored = a.scores != nullptr;
   if (G <= 8) {

@@ -48,7 +48,7 @@ def pieces(lens, chunks, whole, kpc):
     return out, n, pre, total, parts
 
 
-def check(lens, slots_on_gpu, heads, num_splits, kpc=1):
+def check(lens, slots_on_gpu, heads, num_splits, kpc=2):
     B = len(lens)
     chunks, slots, whole = launch_chunks(slots_on_gpu, heads, B, num_splits)
     assert slots <= B * num_splits - -(-B // 128) or whole
