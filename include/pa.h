@@ -612,7 +612,8 @@ pa_status pa_evict_select(int32_t *keep, int32_t *new_lens, float *sums_out,
  *   e4m3, 80 PA_Q4 at head_size 128; 1152 an MLA latent row, one head).
  * keep: [num_seqs, num_kv_heads, keep_len] int32, contiguous; keep_lens
  *   [num_seqs] int32.  block_size >= 1.  Tables [num_seqs, src/dst_max_blocks]
- *   int32.  num_seqs or num_kv_heads above 65535: PA_ERR_UNSUPPORTED.
+ *   int32.  num_seqs or num_kv_heads above 65535, or 2^31 slots or more:
+ *   PA_ERR_UNSUPPORTED.
  * Alignment: caches 16 bytes.
  * ---------------------------------------------------------------------- */
 pa_status pa_cache_compact(void *k_cache, void *v_cache, int32_t row_bytes, const int32_t *keep,

@@ -2,15 +2,23 @@
 // tokens each (sequence, kv head) keeps, and the moving of their rows.
 //
 // Choice.  A sum becomes an unsigned key of the same order (NaN lowest,
-// protected tokens highest); a radix search of four 8-bit digits finds the
-// key of rank `budget`, and one ordered pass writes the indices of every key
-// above it and of the first ties, ascending, with the sums beside them.
+// protected tokens highest); a radix search finds the key of rank `budget`,
+// and one ordered pass writes the indices of every key above it and of the
+// first ties, ascending, with the sums beside them.  A row is read once: the
+// CTAs of a cluster hold a part of it each in shared memory, and join their
+// digit counts through distributed shared memory.  (One CTA re-reading its row
+// for every digit: 222 us for 64 rows of 32K-128K, 27 us for 128 rows of 2.3K.)
 //
-// Moving.  Row j of the kept list comes from token keep[j].  Into other
-// blocks every row is independent.  In place (keep[j] >= j, ascending) one
-// CTA walks a (sequence, kv head, column range) in chunks and stores a chunk
-// only after every load of the chunks up to it: what a store overwrites,
-// position j, can be the source of rows <= j only.
+// Moving.  Row j of the kept list comes from token keep[j].  The places of a
+// chunk of rows are looked up once, a thread per row; then 16-byte units move,
+// eight of K and eight of V in flight per thread (looked up per unit, the
+// integer work alone took 136 us of a 284 us move of 1.07 GB).
+// Into other blocks every row is independent.  In place (keep[j] >= j,
+// ascending) one CTA walks a column range of a (sequence, kv head) in chunks
+// and stores a chunk only after every load of the chunks up to it: what a
+// store overwrites, position j, can be the source of rows <= j only.
+#include <atomic>
+
 #include "pa_internal.cuh"
 
 namespace pa_detail {
@@ -19,6 +27,10 @@ namespace {
 using namespace pa;
 
 constexpr int kSelThreads = 1024;
+constexpr int kSegment = 16384;     // sums per CTA that a cluster is sized for
+constexpr int kMaxSegment = 49152;  // and that shared memory holds at most (192 KB)
+constexpr int kMaxCluster = 8;
+constexpr int kBins = 2048;         // digits of 11, 11 and 10 bits
 
 __device__ __forceinline__ uint32_t order_key(float x) {
   if (x != x) return 0u;
@@ -56,7 +68,8 @@ __device__ __forceinline__ uint32_t block_scan(uint32_t x, uint32_t* warp_sums, 
   return before;
 }
 
-__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const SelectArgs a) {
+// Rows longer than a cluster holds: one CTA per row, re-read for every digit.
+__global__ void __launch_bounds__(kSelThreads) evict_select_long_kernel(const SelectArgs a) {
   __shared__ uint32_t hist[256];
   __shared__ uint32_t warp_sums[33];
   __shared__ uint32_t found[2];  // digit, rank within it
@@ -128,69 +141,251 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const SelectA
   }
 }
 
+// ------------------------------------------------- a row held by a cluster --
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
+                   : "memory");
+}
+// a 32-bit word of another CTA of the cluster, at the address `local` has here
+__device__ __forceinline__ uint32_t cluster_load(const uint32_t* local, int rank) {
+  uint32_t addr, v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(addr) : "r"(smem_u32(local)), "r"(rank));
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const SelectArgs a, int ranks) {
+  extern __shared__ float vals[];  // this CTA's part of the row
+  __shared__ uint32_t hist[kBins];
+  __shared__ uint32_t warp_sums[33];
+  __shared__ uint32_t warp_above[kSelThreads / 32], warp_equal[kSelThreads / 32];
+  __shared__ uint32_t found[2];   // digit, rank within it
+  __shared__ uint32_t counts[2];  // of this CTA: above, equal
+  const int row = blockIdx.x / ranks, rank_id = blockIdx.x - row * ranks;
+  const int b = row / a.num_kv_heads;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int L = min(max(__ldg(a.context_lens + b), 0), a.sums_len);
+  const int n = min(L, a.budget);
+  if (row == b * a.num_kv_heads && rank_id == 0 && tid == 0) a.new_lens[b] = n;
+  int32_t* keep = a.keep + static_cast<int64_t>(row) * a.budget;
+  const float* in = a.sums_in + static_cast<int64_t>(row) * a.sums_len;
+  float* out = a.sums_out == nullptr ? nullptr : a.sums_out + static_cast<int64_t>(row) * a.sums_len;
+  const int step = ranks * kSelThreads, me = rank_id * kSelThreads + tid;
+  for (int64_t j = static_cast<int64_t>(n) + me; j < a.budget; j += step) keep[j] = -1;
+  if (L <= a.budget) {  // (every CTA of the cluster: no barrier is missed)
+    for (int j = me; j < n; j += step) {
+      keep[j] = j;
+      if (out != nullptr && out != in) out[j] = in[j];
+    }
+    return;
+  }
+  const int seg = ((L + ranks - 1) / ranks + 31) & ~31;  // <= the shared memory's
+  const int t0 = min(rank_id * seg, L), size = min(seg, L - t0);
+  for (int i0 = tid; i0 < size; i0 += 8 * kSelThreads) {
+    float x[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (i0 + k * kSelThreads < size) x[k] = in[t0 + i0 + k * kSelThreads];
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (i0 + k * kSelThreads < size) vals[i0 + k * kSelThreads] = x[k];
+  }
+  auto key_of = [&](int i) -> uint32_t {
+    const int t = t0 + i;
+    return t < a.num_sink || t >= L - a.num_recent ? 0xFFFFFFFFu : order_key(vals[i]);
+  };
+  uint32_t prefix = 0u;
+  uint32_t rank = static_cast<uint32_t>(n);  // of the kept, the lowest key's rank from the top
+#pragma unroll
+  for (int pass = 0; pass < 3; ++pass) {
+    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
+    const uint32_t mask = pass == 2 ? 1023u : 2047u;
+    const int above = pass == 0 ? 32 : pass == 1 ? 21 : 10;  // bits found so far start here
+    hist[tid] = 0u;
+    hist[tid + kSelThreads] = 0u;
+    __syncthreads();
+    for (int i = tid; i < size; i += kSelThreads) {
+      const uint32_t k = key_of(i);
+      if (pass == 0 || (k >> above) == (prefix >> above)) atomicAdd(&hist[(k >> shift) & mask], 1u);
+    }
+    // the digits' counts over the cluster, the largest digit first
+    if (ranks > 1) cluster_sync();
+    else __syncthreads();
+    const int d = kBins - 1 - 2 * tid;
+    uint32_t c0 = 0u, c1 = 0u;
+    if (ranks == 1) {
+      c0 = hist[d];
+      c1 = hist[d - 1];
+    } else {
+      for (int r = 0; r < ranks; ++r) {
+        c0 += cluster_load(hist + d, r);
+        c1 += cluster_load(hist + d - 1, r);
+      }
+    }
+    uint32_t total;
+    const uint32_t before = block_scan(c0 + c1, warp_sums, total);
+    if (before < rank && rank <= before + c0 + c1) {
+      const bool first = rank <= before + c0;
+      found[0] = static_cast<uint32_t>(first ? d : d - 1);
+      found[1] = rank - before - (first ? 0u : c0);
+    }
+    // (after this the counts may be cleared: every CTA has read them)
+    if (ranks > 1) cluster_sync();
+    else __syncthreads();
+    prefix |= found[0] << shift;
+    rank = found[1];
+  }
+  // keys above `prefix` are kept, and the first `rank` equal to it: each warp
+  // counts its consecutive part, then writes at its place
+  const int per = ((size + 31) / 32 + 31) & ~31;
+  const int w0 = min(warp * per, size), w1 = min(w0 + per, size);
+  uint32_t above = 0u, equal = 0u;
+  for (int i = w0 + lane; i < w1; i += 32) {
+    const uint32_t k = key_of(i);
+    above += k > prefix;
+    equal += k == prefix;
+  }
+  above = __reduce_add_sync(0xffffffffu, above);
+  equal = __reduce_add_sync(0xffffffffu, equal);
+  if (lane == 0) {
+    warp_above[warp] = above;
+    warp_equal[warp] = equal;
+  }
+  __syncthreads();
+  if (warp == 0) {
+    uint32_t x = warp_above[lane], y = warp_equal[lane];
+    const uint32_t x0 = x, y0 = y;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const uint32_t p = __shfl_up_sync(0xffffffffu, x, off), q = __shfl_up_sync(0xffffffffu, y, off);
+      if (lane >= off) {
+        x += p;
+        y += q;
+      }
+    }
+    warp_above[lane] = x - x0;
+    warp_equal[lane] = y - y0;
+    if (lane == 31) {
+      counts[0] = x;
+      counts[1] = y;
+    }
+  }
+  __syncthreads();
+  above = warp_above[warp];
+  equal = warp_equal[warp];
+  if (ranks > 1) {
+    cluster_sync();
+    for (int r = 0; r < rank_id; ++r) {
+      above += cluster_load(counts, r);
+      equal += cluster_load(counts + 1, r);
+    }
+    cluster_sync();  // no CTA leaves while its counts are read
+  }
+  for (int i0 = w0; i0 < w1; i0 += 32) {
+    const int i = i0 + lane;
+    const uint32_t k = i < w1 ? key_of(i) : 0u;
+    const bool is_above = i < w1 && k > prefix, is_equal = i < w1 && k == prefix;
+    const uint32_t ma = __ballot_sync(0xffffffffu, is_above);
+    const uint32_t me_ = __ballot_sync(0xffffffffu, is_equal);
+    const uint32_t low = (1u << lane) - 1u;
+    const uint32_t na = above + __popc(ma & low), ne = equal + __popc(me_ & low);
+    if (is_above || (is_equal && ne < rank)) {
+      const uint32_t j = na + min(ne, rank);
+      keep[j] = t0 + i;
+      if (out != nullptr) out[j] = vals[i];  // (in place: the whole row was read above)
+    }
+    above += __popc(ma);
+    equal += __popc(me_);
+  }
+}
+
 // ----------------------------------------------------------------- moving --
 constexpr int kMoveThreads = 256;
-constexpr int kMoveUnits = 8;  // 16-byte units in flight per thread
+constexpr int kMoveUnits = 4;         // 16-byte units of a tensor in flight per thread, of both
+constexpr int kMoveUnitsInPlace = 8;  // of one tensor
 
-// Units are 16 bytes; a CTA moves columns [u0, u0 + U) of rows [j0, j1) of one
-// tensor, in chunks of kMoveThreads * kMoveUnits / U rows.
+// Units are 16 bytes; a CTA moves columns [u0, u0 + U) of rows [j0, j1) in chunks of
+// kChunk / U rows.  kInPlace: of one tensor (K or V); else of both.
 template <bool kInPlace>
-__global__ void __launch_bounds__(kMoveThreads) cache_compact_kernel(const CompactArgs a) {
+__global__ void __launch_bounds__(kMoveThreads, kInPlace ? 3 : 4)
+    cache_compact_kernel(const CompactArgs a) {
+  constexpr int kUnits = kInPlace ? kMoveUnitsInPlace : kMoveUnits;
+  constexpr int kChunk = kMoveThreads * kUnits;
+  // slots (block * block_size + offset) of a chunk's rows, -1: not moved
+  __shared__ int2 places[kInPlace ? 2 : 1][kChunk];
   const int g = blockIdx.y, b = blockIdx.z;
   const int n = min(max(__ldg(a.keep_lens + b), 0), a.keep_len);
-  const int row_units = a.row_units;
-  int x = blockIdx.x;
-  const int tensor = a.v_cache == nullptr ? 0 : x & 1;
-  if (a.v_cache != nullptr) x >>= 1;
-  uint4* cache = static_cast<uint4*>(tensor ? a.v_cache : a.k_cache);
-  int u0 = 0, U = row_units, j0 = 0, j1 = n;
-  if (kInPlace) {
-    u0 = x * a.units_per_cta;
-    U = min(a.units_per_cta, row_units - u0);
-  } else {
-    j0 = x * a.rows_per_cta;
-    j1 = min(j0 + a.rows_per_cta, n);
-  }
+  const int tensors = kInPlace && a.v_cache != nullptr ? 2 : 1;
+  const int tensor = kInPlace ? blockIdx.x % tensors : 0;
+  const int x = kInPlace ? blockIdx.x / tensors : blockIdx.x;
+  const int part = x % a.parts;
+  const int u0 = part * a.units_per_cta;
+  const int U = min(a.units_per_cta, a.row_units - u0);
+  const int rows = kChunk / a.units_per_cta;  // of a chunk
+  const int j0 = kInPlace ? 0 : x / a.parts * rows;
+  const int j1 = kInPlace ? n : min(j0 + rows, n);
   if (j0 >= j1) return;
   const int32_t* keep = a.keep + (static_cast<int64_t>(b) * a.num_kv_heads + g) * a.keep_len;
   const int32_t* src_table = a.src_table + static_cast<int64_t>(b) * a.src_max_blocks;
   const int32_t* dst_table = a.dst_table + static_cast<int64_t>(b) * a.dst_max_blocks;
-  // unit offset of logical row t of this head, or -1
-  auto place = [&](const int32_t* table, int max_blocks, int t) -> int64_t {
+  uint4* k_cache = static_cast<uint4*>(kInPlace && tensor ? a.v_cache : a.k_cache);
+  uint4* v_cache = kInPlace ? nullptr : static_cast<uint4*>(a.v_cache);
+  // at / U for at < kChunk
+  const uint32_t magic = U > 1 ? 0xFFFFFFFFu / static_cast<uint32_t>(U) + 1u : 0u;
+  auto place = [&](const int32_t* table, int max_blocks, int t) -> int {
     if (t < 0) return -1;
-    const int blk = t / a.block_size;
+    const int blk = (a.block_size & (a.block_size - 1)) == 0 ? t >> (31 - __clz(a.block_size))
+                                                             : t / a.block_size;
     if (blk >= max_blocks) return -1;
     const int id = __ldg(table + blk);
     if (id < 0 || id >= a.num_blocks) return -1;
-    return ((static_cast<int64_t>(id) * a.block_size + (t - blk * a.block_size)) * a.num_kv_heads +
-            g) * row_units + u0;
+    return id * a.block_size + (t - blk * a.block_size);
   };
-  const int chunk = max(1, kMoveThreads * kMoveUnits / U);  // rows
-  for (int c0 = j0; c0 < j1; c0 += chunk) {
-    uint4 v[kMoveUnits];
-    int64_t to[kMoveUnits];
-    const int units = min(chunk, j1 - c0) * U;
-    for (int base = 0; base < units; base += kMoveThreads * kMoveUnits) {
+  auto look_up = [&](int c0, int2* to) {
+    for (int r = threadIdx.x; r < rows && c0 + r < j1; r += kMoveThreads) {
+      int2 p;
+      p.x = place(src_table, a.src_max_blocks, __ldg(keep + c0 + r));
+      p.y = place(dst_table, a.dst_max_blocks, c0 + r);
+      if (p.x < 0 || p.y < 0 || p.x == p.y) p.y = -1;
+      to[r] = p;
+    }
+  };
+  auto unit = [&](int slot, int u) -> int64_t {
+    return (static_cast<int64_t>(slot) * a.num_kv_heads + g) * a.row_units + u0 + u;
+  };
+  look_up(j0, places[0]);
+  __syncthreads();
+  int buf = 0;
+  for (int c0 = j0; c0 < j1; c0 += rows, buf ^= kInPlace ? 1 : 0) {
+    uint4 k[kUnits], v[kInPlace ? 1 : kUnits];
+    int64_t to[kUnits];
+    const int units = min(rows, j1 - c0) * U;
 #pragma unroll
-      for (int i = 0; i < kMoveUnits; ++i) {
-        const int at = base + threadIdx.x + kMoveThreads * i;
-        to[i] = -1;
-        if (at < units) {
-          const int r = at / U, u = at - r * U;
-          const int j = c0 + r, t = __ldg(keep + j);
-          const int64_t from = place(src_table, a.src_max_blocks, t);
-          const int64_t dst = place(dst_table, a.dst_max_blocks, j);
-          if (from >= 0 && dst >= 0 && from != dst) {
-            v[i] = cache[from + u];
-            to[i] = dst + u;
-          }
+    for (int i = 0; i < kUnits; ++i) {
+      const int at = threadIdx.x + kMoveThreads * i;
+      to[i] = -1;
+      if (at < units) {
+        const int r = U > 1 ? static_cast<int>(__umulhi(static_cast<uint32_t>(at), magic)) : at;
+        const int u = at - r * U;
+        const int2 p = places[buf][r];
+        if (p.y >= 0) {
+          to[i] = unit(p.y, u);
+          const int64_t from = unit(p.x, u);
+          k[i] = k_cache[from];
+          if (!kInPlace && v_cache != nullptr) v[i] = v_cache[from];
         }
       }
-      if (kInPlace) __syncthreads();  // every load of the chunk, then its stores
+    }
+    if (kInPlace) {
+      if (c0 + rows < j1) look_up(c0 + rows, places[buf ^ 1]);
+      __syncthreads();  // every load of the chunk, then its stores
+    }
 #pragma unroll
-      for (int i = 0; i < kMoveUnits; ++i)
-        if (to[i] >= 0) cache[to[i]] = v[i];
-      if (kInPlace) __syncthreads();
+    for (int i = 0; i < kUnits; ++i) {
+      if (to[i] >= 0) {
+        k_cache[to[i]] = k[i];
+        if (!kInPlace && v_cache != nullptr) v_cache[to[i]] = v[i];
+      }
     }
   }
 }
@@ -198,27 +393,53 @@ __global__ void __launch_bounds__(kMoveThreads) cache_compact_kernel(const Compa
 }  // namespace
 
 pa_status launch_evict_select(const SelectArgs& a, cudaStream_t stream) {
-  const int64_t rows = static_cast<int64_t>(a.num_seqs) * a.num_kv_heads;
-  evict_select_kernel<<<static_cast<unsigned>(rows), kSelThreads, 0, stream>>>(a);
-  return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+  const unsigned rows = static_cast<unsigned>(a.num_seqs) * static_cast<unsigned>(a.num_kv_heads);
+  // as many CTAs per row as keep each part near kSegment sums
+  int ranks = 1;
+  while (ranks < kMaxCluster && static_cast<int64_t>(ranks) * kSegment < a.sums_len) ranks *= 2;
+  if (static_cast<int64_t>(ranks) * kMaxSegment < a.sums_len) {
+    evict_select_long_kernel<<<rows, kSelThreads, 0, stream>>>(a);
+    return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+  }
+  static std::atomic<uint64_t> smem_raised{0};
+  if (!ensure_smem_limit(evict_select_kernel, kMaxSegment * 4, smem_raised)) return PA_ERR_CUDA;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(ranks);
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(rows * static_cast<unsigned>(ranks));
+  cfg.blockDim = dim3(kSelThreads);
+  cfg.dynamicSmemBytes = (((a.sums_len + ranks - 1) / ranks + 31) & ~31) * sizeof(float);
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, evict_select_kernel, a, ranks) != cudaSuccess) {
+    cudaGetLastError();
+    return PA_ERR_CUDA;
+  }
+  return PA_OK;
 }
 
 pa_status launch_cache_compact(CompactArgs a, bool in_place, cudaStream_t stream) {
-  const unsigned tensors = a.v_cache == nullptr ? 1u : 2u;
-  dim3 grid(1, static_cast<unsigned>(a.num_kv_heads), static_cast<unsigned>(a.num_seqs));
-  if (in_place) {
-    a.units_per_cta = a.row_units < 4 ? a.row_units : 4;
-    grid.x = tensors * static_cast<unsigned>((a.row_units + a.units_per_cta - 1) / a.units_per_cta);
+  const int tensors = in_place && a.v_cache != nullptr ? 2 : 1;
+  // columns per CTA: whole rows, as far as a chunk holds a row; in place 64 bytes, for
+  // the only other parallelism there is (sequences x kv heads)
+  const int chunk = kMoveThreads * (in_place ? kMoveUnitsInPlace : kMoveUnits);
+  const int most = in_place ? 4 : chunk;
+  a.units_per_cta = a.row_units < most ? a.row_units : most;
+  a.parts = (a.row_units + a.units_per_cta - 1) / a.units_per_cta;
+  const int rows = chunk / a.units_per_cta;
+  const int64_t blocks = in_place ? static_cast<int64_t>(tensors) * a.parts
+                                  : (static_cast<int64_t>(a.keep_len) + rows - 1) / rows * a.parts;
+  if (blocks > 0x7FFFFFFFll) return PA_ERR_UNSUPPORTED;
+  const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>(a.num_kv_heads),
+                  static_cast<unsigned>(a.num_seqs));
+  if (in_place)
     cache_compact_kernel<true><<<grid, kMoveThreads, 0, stream>>>(a);
-  } else {
-    const int32_t rows = kMoveThreads * kMoveUnits / a.row_units;
-    a.rows_per_cta = rows < 1 ? 1 : rows;
-    const int64_t blocks =
-        tensors * ((static_cast<int64_t>(a.keep_len) + a.rows_per_cta - 1) / a.rows_per_cta);
-    if (blocks > 0x7FFFFFFFll) return PA_ERR_UNSUPPORTED;
-    grid.x = static_cast<unsigned>(blocks);
+  else
     cache_compact_kernel<false><<<grid, kMoveThreads, 0, stream>>>(a);
-  }
   return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 

@@ -701,7 +701,8 @@ pa_status pa_cache_compact(void* k_cache, void* v_cache, int32_t row_bytes, cons
     return PA_ERR_INVALID;
   const bool in_place = src_block_tables == dst_block_tables;
   if (in_place && src_max_blocks != dst_max_blocks) return PA_ERR_INVALID;
-  if (num_seqs > 65535 || num_kv_heads > 65535) return PA_ERR_UNSUPPORTED;
+  if (num_seqs > 65535 || num_kv_heads > 65535 || num_blocks >= (1ll << 31) / block_size)
+    return PA_ERR_UNSUPPORTED;
   if (row_bytes % 16 != 0 || !aligned(k_cache, 16) || !aligned(v_cache, 16) ||
       !aligned(keep, 4) || !aligned(keep_lens, 4) || !aligned(src_block_tables, 4) ||
       !aligned(dst_block_tables, 4))

@@ -696,7 +696,7 @@ struct CompactArgs {  // evict.cu
   int32_t keep_len, src_max_blocks, dst_max_blocks, num_seqs, num_kv_heads, block_size;
   int32_t row_units;  // 16-byte units of a row
   int64_t num_blocks;
-  int32_t rows_per_cta, units_per_cta;  // set by the launcher
+  int32_t units_per_cta, parts;  // columns of a CTA, CTAs per row (set by the launcher)
 };
 pa_status launch_cache_compact(CompactArgs a, bool in_place, cudaStream_t stream);
 

@@ -341,3 +341,12 @@ def test_sequential_prefix_feeds_prefill():
         # elements, |dk . q| scale < 2^-8 |k| |q| scale < 0.06 at most and far less on average;
         # the norm of the outputs is within a percent
         assert np.linalg.norm(got - ref) <= 1e-2 * np.linalg.norm(ref)
+
+
+@pytest.mark.parametrize("T", [16384, 16385, 65537, 393216, 393217])
+def test_select_at_the_cluster_sizes(T):
+    """Row lengths where the number of CTAs per row changes, and beyond what a cluster holds."""
+    sums = random_sums((2, 1, T), T, "weights")
+    sums[:, :, ::3] = 0.5  # many ties
+    check_select(sums, [T, T - 5000], T // 2 + 3, 7, 100, "same")
+    check_select(sums, [T - 1, 40], 64, 4, 8)
