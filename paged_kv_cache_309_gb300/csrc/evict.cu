@@ -27,10 +27,11 @@ namespace {
 using namespace pa;
 
 constexpr int kSelThreads = 1024;
-constexpr int kSegment = 16384;     // sums per CTA that a cluster is sized for
 constexpr int kMaxSegment = 49152;  // and that shared memory holds at most (192 KB)
 constexpr int kMaxCluster = 8;
 constexpr int kBins = 2048;         // digits of 11, 11 and 10 bits
+static_assert(kBins == 2 * kSelThreads, "a thread looks at two digits");
+constexpr int kCandidates = 4096;   // keys of one first digit that every CTA of a cluster holds
 
 __device__ __forceinline__ uint32_t order_key(float x) {
   if (x != x) return 0u;
@@ -146,21 +147,30 @@ __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
                    : "memory");
 }
-// a 32-bit word of another CTA of the cluster, at the address `local` has here
-__device__ __forceinline__ uint32_t cluster_load(const uint32_t* local, int rank) {
-  uint32_t addr, v;
+// two 32-bit words of another CTA of the cluster, at the address `local` has here
+// (the barriers around the loads order them; no clobber, so that they overlap)
+__device__ __forceinline__ uint2 cluster_load(const uint32_t* local, int rank) {
+  uint32_t addr;
+  uint2 v;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(addr) : "r"(smem_u32(local)), "r"(rank));
-  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  asm volatile("ld.shared::cluster.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr));
   return v;
+}
+__device__ __forceinline__ void cluster_store(const uint32_t* local, int rank, uint32_t x) {
+  uint32_t addr;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(addr) : "r"(smem_u32(local)), "r"(rank));
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(x) : "memory");
 }
 
 __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const SelectArgs a, int ranks) {
   extern __shared__ float vals[];  // this CTA's part of the row
-  __shared__ uint32_t hist[kBins];
+  __shared__ __align__(8) uint32_t hist[kBins];
+  __shared__ uint32_t candidates[kCandidates];
   __shared__ uint32_t warp_sums[33];
   __shared__ uint32_t warp_above[kSelThreads / 32], warp_equal[kSelThreads / 32];
-  __shared__ uint32_t found[2];   // digit, rank within it
-  __shared__ uint32_t counts[2];  // of this CTA: above, equal
+  __shared__ uint32_t found[4];  // digit, rank within it, its keys in the cluster, in lower CTAs
+  __shared__ uint32_t appended;
+  __shared__ __align__(8) uint32_t counts[2];  // of this CTA: above, equal
   const int row = blockIdx.x / ranks, rank_id = blockIdx.x - row * ranks;
   const int b = row / a.num_kv_heads;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -181,67 +191,132 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const SelectA
   }
   const int seg = ((L + ranks - 1) / ranks + 31) & ~31;  // <= the shared memory's
   const int t0 = min(rank_id * seg, L), size = min(seg, L - t0);
+  auto key = [&](int i, float x) -> uint32_t {
+    const int t = t0 + i;
+    return t < a.num_sink || t >= L - a.num_recent ? 0xFFFFFFFFu : order_key(x);
+  };
+  auto clear_hist = [&]() { reinterpret_cast<uint2*>(hist)[tid] = make_uint2(0u, 0u); };
+  // The digit that holds the key of rank `rank` (counted from the largest), from every
+  // digit's count: this thread's are those of digits d + 1 (c.y) and d (c.x), lower.y
+  // and lower.x of them in CTAs before this one.
+  const int d = kBins - 2 - 2 * tid;
+  auto find_digit = [&](uint2 c, uint2 lower, uint32_t rank) {
+    uint32_t total;
+    const uint32_t before = block_scan(c.x + c.y, warp_sums, total);
+    if (before < rank && rank <= before + c.x + c.y) {
+      const bool first = rank <= before + c.y;
+      found[0] = static_cast<uint32_t>(first ? d + 1 : d);
+      found[1] = rank - before - (first ? 0u : c.y);
+      found[2] = first ? c.y : c.x;
+      found[3] = first ? lower.y : lower.x;
+    }
+  };
+  auto cluster_digits = [&](uint32_t rank) {
+    uint2 c = make_uint2(0u, 0u), lower = c;
+    if (ranks == 1) {
+      c = *reinterpret_cast<const uint2*>(hist + d);
+    } else {
+      uint2 v[kMaxCluster];
+#pragma unroll
+      for (int r = 0; r < kMaxCluster; ++r)
+        v[r] = r < ranks ? cluster_load(hist + d, r) : make_uint2(0u, 0u);
+#pragma unroll
+      for (int r = 0; r < kMaxCluster; ++r) {
+        if (r == rank_id) lower = c;
+        c.x += v[r].x;
+        c.y += v[r].y;
+      }
+    }
+    find_digit(c, lower, rank);
+  };
+  auto all_sync = [&]() {
+    if (ranks > 1) cluster_sync();
+    else __syncthreads();
+  };
+
+  // ---- first digit (11 bits), counted as the row is read
+  clear_hist();
+  if (tid == 0) appended = 0u;
+  __syncthreads();
   for (int i0 = tid; i0 < size; i0 += 8 * kSelThreads) {
     float x[8];
 #pragma unroll
     for (int k = 0; k < 8; ++k)
       if (i0 + k * kSelThreads < size) x[k] = in[t0 + i0 + k * kSelThreads];
 #pragma unroll
-    for (int k = 0; k < 8; ++k)
-      if (i0 + k * kSelThreads < size) vals[i0 + k * kSelThreads] = x[k];
-  }
-  auto key_of = [&](int i) -> uint32_t {
-    const int t = t0 + i;
-    return t < a.num_sink || t >= L - a.num_recent ? 0xFFFFFFFFu : order_key(vals[i]);
-  };
-  uint32_t prefix = 0u;
-  uint32_t rank = static_cast<uint32_t>(n);  // of the kept, the lowest key's rank from the top
-#pragma unroll
-  for (int pass = 0; pass < 3; ++pass) {
-    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
-    const uint32_t mask = pass == 2 ? 1023u : 2047u;
-    const int above = pass == 0 ? 32 : pass == 1 ? 21 : 10;  // bits found so far start here
-    hist[tid] = 0u;
-    hist[tid + kSelThreads] = 0u;
-    __syncthreads();
-    for (int i = tid; i < size; i += kSelThreads) {
-      const uint32_t k = key_of(i);
-      if (pass == 0 || (k >> above) == (prefix >> above)) atomicAdd(&hist[(k >> shift) & mask], 1u);
-    }
-    // the digits' counts over the cluster, the largest digit first
-    if (ranks > 1) cluster_sync();
-    else __syncthreads();
-    const int d = kBins - 1 - 2 * tid;
-    uint32_t c0 = 0u, c1 = 0u;
-    if (ranks == 1) {
-      c0 = hist[d];
-      c1 = hist[d - 1];
-    } else {
-      for (int r = 0; r < ranks; ++r) {
-        c0 += cluster_load(hist + d, r);
-        c1 += cluster_load(hist + d - 1, r);
+    for (int k = 0; k < 8; ++k) {
+      const int i = i0 + k * kSelThreads;
+      if (i < size) {
+        vals[i] = x[k];
+        atomicAdd(&hist[key(i, x[k]) >> 21], 1u);
       }
     }
-    uint32_t total;
-    const uint32_t before = block_scan(c0 + c1, warp_sums, total);
-    if (before < rank && rank <= before + c0 + c1) {
-      const bool first = rank <= before + c0;
-      found[0] = static_cast<uint32_t>(first ? d : d - 1);
-      found[1] = rank - before - (first ? 0u : c0);
-    }
-    // (after this the counts may be cleared: every CTA has read them)
-    if (ranks > 1) cluster_sync();
-    else __syncthreads();
-    prefix |= found[0] << shift;
-    rank = found[1];
   }
-  // keys above `prefix` are kept, and the first `rank` equal to it: each warp
-  // counts its consecutive part, then writes at its place
-  const int per = ((size + 31) / 32 + 31) & ~31;
+  all_sync();
+  cluster_digits(static_cast<uint32_t>(n));
+  __syncthreads();
+  uint32_t prefix = found[0] << 21, rank = found[1];
+  const uint32_t num = found[2], lower = found[3];
+  if (num <= kCandidates) {
+    // the keys with that digit, given to every CTA, which find the rest of
+    // the key by themselves
+    for (int i = tid; i < size; i += kSelThreads) {
+      const uint32_t k = key(i, vals[i]);
+      if (k >> 21 == prefix >> 21) {
+        const uint32_t at = lower + atomicAdd(&appended, 1u);
+        if (ranks == 1) {
+          candidates[at] = k;
+        } else {
+          for (int r = 0; r < ranks; ++r) cluster_store(candidates + at, r, k);
+        }
+      }
+    }
+    all_sync();
+#pragma unroll
+    for (int pass = 1; pass < 3; ++pass) {
+      const int shift = pass == 1 ? 10 : 0, known = pass == 1 ? 21 : 10;
+      clear_hist();
+      __syncthreads();
+      for (uint32_t i = tid; i < num; i += kSelThreads) {
+        const uint32_t k = candidates[i];
+        if (k >> known == prefix >> known)
+          atomicAdd(&hist[(k >> shift) & (pass == 1 ? 2047u : 1023u)], 1u);
+      }
+      __syncthreads();
+      find_digit(*reinterpret_cast<const uint2*>(hist + d), make_uint2(0u, 0u), rank);
+      __syncthreads();
+      prefix |= found[0] << shift;
+      rank = found[1];
+      __syncthreads();
+    }
+  } else {
+    // many keys with that digit (ties): the other digits over the whole row too
+#pragma unroll
+    for (int pass = 1; pass < 3; ++pass) {
+      const int shift = pass == 1 ? 10 : 0, known = pass == 1 ? 21 : 10;
+      all_sync();  // every CTA has read the counts
+      clear_hist();
+      __syncthreads();
+      for (int i = tid; i < size; i += kSelThreads) {
+        const uint32_t k = key(i, vals[i]);
+        if (k >> known == prefix >> known)
+          atomicAdd(&hist[(k >> shift) & (pass == 1 ? 2047u : 1023u)], 1u);
+      }
+      all_sync();
+      cluster_digits(rank);
+      __syncthreads();
+      prefix |= found[0] << shift;
+      rank = found[1];
+    }
+  }
+  // ---- keys above `prefix` are kept, and the first `rank` equal to it: each
+  // warp counts its consecutive part, then writes at its place
+  constexpr int kWarps = kSelThreads / 32;
+  const int per = ((size + kWarps - 1) / kWarps + 31) & ~31;
   const int w0 = min(warp * per, size), w1 = min(w0 + per, size);
   uint32_t above = 0u, equal = 0u;
   for (int i = w0 + lane; i < w1; i += 32) {
-    const uint32_t k = key_of(i);
+    const uint32_t k = key(i, vals[i]);
     above += k > prefix;
     equal += k == prefix;
   }
@@ -270,32 +345,37 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const SelectA
       counts[1] = y;
     }
   }
-  __syncthreads();
+  all_sync();
   above = warp_above[warp];
   equal = warp_equal[warp];
   if (ranks > 1) {
-    cluster_sync();
-    for (int r = 0; r < rank_id; ++r) {
-      above += cluster_load(counts, r);
-      equal += cluster_load(counts + 1, r);
+#pragma unroll
+    for (int r = 0; r < kMaxCluster; ++r) {
+      if (r < rank_id) {
+        const uint2 c = cluster_load(counts, r);
+        above += c.x;
+        equal += c.y;
+      }
     }
     cluster_sync();  // no CTA leaves while its counts are read
   }
+#pragma unroll 4
   for (int i0 = w0; i0 < w1; i0 += 32) {
     const int i = i0 + lane;
-    const uint32_t k = i < w1 ? key_of(i) : 0u;
+    const float x = i < w1 ? vals[i] : 0.f;
+    const uint32_t k = i < w1 ? key(i, x) : 0u;
     const bool is_above = i < w1 && k > prefix, is_equal = i < w1 && k == prefix;
     const uint32_t ma = __ballot_sync(0xffffffffu, is_above);
-    const uint32_t me_ = __ballot_sync(0xffffffffu, is_equal);
+    const uint32_t mq = __ballot_sync(0xffffffffu, is_equal);
     const uint32_t low = (1u << lane) - 1u;
-    const uint32_t na = above + __popc(ma & low), ne = equal + __popc(me_ & low);
+    const uint32_t na = above + __popc(ma & low), ne = equal + __popc(mq & low);
     if (is_above || (is_equal && ne < rank)) {
       const uint32_t j = na + min(ne, rank);
       keep[j] = t0 + i;
-      if (out != nullptr) out[j] = vals[i];  // (in place: the whole row was read above)
+      if (out != nullptr) out[j] = x;  // (in place: the whole row was read above)
     }
     above += __popc(ma);
-    equal += __popc(me_);
+    equal += __popc(mq);
   }
 }
 
@@ -394,9 +474,18 @@ __global__ void __launch_bounds__(kMoveThreads, kInPlace ? 3 : 4)
 
 pa_status launch_evict_select(const SelectArgs& a, cudaStream_t stream) {
   const unsigned rows = static_cast<unsigned>(a.num_seqs) * static_cast<unsigned>(a.num_kv_heads);
-  // as many CTAs per row as keep each part near kSegment sums
-  int ranks = 1;
-  while (ranks < kMaxCluster && static_cast<int64_t>(ranks) * kSegment < a.sums_len) ranks *= 2;
+  // CTAs per row: parts of 16K sums are the fastest for a row (131072 sums: 25 us, parts of
+  // 32K: 33), but only some 16 clusters of eight run at a time, so where the rows
+  // fill the GPU parts of 32K give more (64 rows: 50 us instead of 75)
+  int sms = num_sms_current_device();
+  if (sms <= 0) sms = 148;
+  auto ranks_for = [&](int64_t part) {
+    int r = 1;
+    while (r < kMaxCluster && r * part < a.sums_len) r *= 2;
+    return r;
+  };
+  int ranks = ranks_for(16384);
+  if (static_cast<int64_t>(rows) * ranks > sms) ranks = ranks_for(32768);
   if (static_cast<int64_t>(ranks) * kMaxSegment < a.sums_len) {
     evict_select_long_kernel<<<rows, kSelThreads, 0, stream>>>(a);
     return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
