@@ -433,12 +433,9 @@ __global__ void __launch_bounds__(kMoveThreads, kInPlace ? 3 : 4)
   auto unit = [&](int slot, int u) -> int64_t {
     return (static_cast<int64_t>(slot) * a.num_kv_heads + g) * a.row_units + u0 + u;
   };
-  look_up(j0, places[0]);
-  __syncthreads();
-  int buf = 0;
-  for (int c0 = j0; c0 < j1; c0 += rows, buf ^= kInPlace ? 1 : 0) {
-    uint4 k[kUnits], v[kInPlace ? 1 : kUnits];
-    int64_t to[kUnits];
+  // Loads of the chunk at c0 (its places in `from`), and their stores
+  auto load = [&](int c0, const int2* places_of, uint4 (&k)[kUnits], uint4* v,
+                  int64_t (&to)[kUnits]) {
     const int units = min(rows, j1 - c0) * U;
 #pragma unroll
     for (int i = 0; i < kUnits; ++i) {
@@ -447,7 +444,7 @@ __global__ void __launch_bounds__(kMoveThreads, kInPlace ? 3 : 4)
       if (at < units) {
         const int r = U > 1 ? static_cast<int>(__umulhi(static_cast<uint32_t>(at), magic)) : at;
         const int u = at - r * U;
-        const int2 p = places[buf][r];
+        const int2 p = places_of[r];
         if (p.y >= 0) {
           to[i] = unit(p.y, u);
           const int64_t from = unit(p.x, u);
@@ -456,16 +453,33 @@ __global__ void __launch_bounds__(kMoveThreads, kInPlace ? 3 : 4)
         }
       }
     }
-    if (kInPlace) {
-      if (c0 + rows < j1) look_up(c0 + rows, places[buf ^ 1]);
-      __syncthreads();  // every load of the chunk, then its stores
-    }
+  };
+  auto store = [&](const uint4 (&k)[kUnits], const uint4* v, const int64_t (&to)[kUnits]) {
 #pragma unroll
     for (int i = 0; i < kUnits; ++i) {
       if (to[i] >= 0) {
         k_cache[to[i]] = k[i];
         if (!kInPlace && v_cache != nullptr) v_cache[to[i]] = v[i];
       }
+    }
+  };
+  look_up(j0, places[0]);
+  __syncthreads();
+  uint4 k0[kUnits];
+  int64_t to0[kUnits];
+  if constexpr (!kInPlace) {
+    uint4 v0[kUnits];
+    load(j0, places[0], k0, v0, to0);
+    store(k0, v0, to0);
+  } else {
+    // (the next chunk's loads ahead of this one's stores, in a second set of
+    // registers, made it slower: 223 -> 403 us for 1.07 GB)
+    int buf = 0;
+    for (int c0 = j0; c0 < j1; c0 += rows, buf ^= 1) {
+      load(c0, places[buf], k0, nullptr, to0);
+      if (c0 + rows < j1) look_up(c0 + rows, places[buf ^ 1]);
+      __syncthreads();  // every load of the chunk, then its stores
+      store(k0, nullptr, to0);
     }
   }
 }
@@ -513,10 +527,16 @@ pa_status launch_evict_select(const SelectArgs& a, cudaStream_t stream) {
 
 pa_status launch_cache_compact(CompactArgs a, bool in_place, cudaStream_t stream) {
   const int tensors = in_place && a.v_cache != nullptr ? 2 : 1;
-  // columns per CTA: whole rows, as far as a chunk holds a row; in place 64 bytes, for
-  // the only other parallelism there is (sequences x kv heads)
+  // columns per CTA: whole rows, as far as a chunk holds a row.  In place the columns
+  // are the only parallelism beside sequences and kv heads: 128 bytes where those fill
+  // the GPU (1.07 GB, 128 rows and tensors: 223 us, 64 bytes 273, whole rows 321), down to 32 where
+  // they do not (16 of them: 97 us, 64 bytes 111, 128 bytes 156)
   const int chunk = kMoveThreads * (in_place ? kMoveUnitsInPlace : kMoveUnits);
-  const int most = in_place ? 4 : chunk;
+  int sms = num_sms_current_device();
+  if (sms <= 0) sms = 148;
+  int most = in_place ? 8 : chunk;
+  const int64_t lists = static_cast<int64_t>(a.num_seqs) * a.num_kv_heads * tensors;
+  while (in_place && most > 2 && lists * ((a.row_units + most - 1) / most) * 2 < 3 * sms) most /= 2;
   a.units_per_cta = a.row_units < most ? a.row_units : most;
   a.parts = (a.row_units + a.units_per_cta - 1) / a.units_per_cta;
   const int rows = chunk / a.units_per_cta;
