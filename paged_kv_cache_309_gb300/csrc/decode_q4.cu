@@ -168,6 +168,19 @@ __device__ __forceinline__ int units_of(const DecodeParams& p, int b) {
 __device__ __forceinline__ void find_chunk(const Q4Params& q, int c, int chunks, int lane,
                                            int64_t* sched) {
   const DecodeParams& p = q.d;
+  if (q.whole && chunks == q.num_seqs) {  // one sequence per chunk: nothing to cut
+    bool clipped;
+    const int n = (effective_len(p, c, &clipped) + kUnit - 1) / kUnit;
+    if (clipped && blockIdx.x == 0 && lane == 0) atomicOr(p.err, PA_DEVERR_CONTEXT_CLIPPED);
+    if (lane == 0) {
+      sched[0] = 1;
+      sched[1] = 0;
+      sched[2] = n;
+      sched[3] = c;
+      sched[4] = 0;
+    }
+    return;
+  }
   int64_t units = 0;
   bool any_clipped = false;
   int held[4];  // units of sequences lane, lane + 32, ...: the lengths are read in one round

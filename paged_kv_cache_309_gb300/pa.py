@@ -140,11 +140,14 @@ def _on_device(**tensors):
             continue
         if not isinstance(t, torch.Tensor):
             raise ValueError(f"{name} must be a torch tensor")
+        device = t.get_device()  # -1 on the host
+        if device == cur:
+            continue
         if not t.is_cuda:
             raise ValueError(f"{name} must be a CUDA tensor (it is on {t.device})")
         if cur is None:
             cur = torch.cuda.current_device()
-        if t.device.index != cur:
+        if device != cur:
             raise ValueError(f"{name} is on {t.device}, but the current device is cuda:{cur}")
 
 
@@ -178,14 +181,15 @@ def _workspace(t):
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _stream(stream):
-    s = torch.cuda.current_stream() if stream is None else stream
-    if stream is not None and s.device.index != torch.cuda.current_device():
-        raise ValueError(f"stream belongs to {s.device}, not the current device")
-    return ctypes.c_void_p(s.cuda_stream)
+    if stream is None:  # (the raw handle: a Stream object costs 3 us)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    if stream.device.index != torch.cuda.current_device():
+        raise ValueError(f"stream belongs to {stream.device}, not the current device")
+    return stream.cuda_stream
 
 
 def _dtype(t):
@@ -606,23 +610,27 @@ def pa_gather_cache_q4(key, value, key_cache, value_cache, slot_mapping, stream=
 def _decode_shapes(out, q, k_cache, v_cache, block_tables, context_lens, workspace):
     """Checks shared by the calls below: (B, H_Q, H_KV, d, block_size, num_blocks)."""
     _on_device(out=out, q=q, k_cache=k_cache, v_cache=v_cache, block_tables=block_tables,
-               context_lens=context_lens)
-    _workspace(workspace)
+               context_lens=context_lens, workspace=workspace)
     B, HQ, d = q.shape
-    nb, bs, HKV, row = k_cache.shape
-    for t, name in ((q, "q"), (out, "out"), (k_cache, "k_cache"), (v_cache, "v_cache"),
-                    (block_tables, "block_tables"), (context_lens, "context_lens")):
-        _need(t.is_contiguous(), f"{name} must be contiguous")
-    _need(out.shape == q.shape and q.dtype == torch.bfloat16 and out.dtype == torch.bfloat16,
-          "q and out must be bf16 [B, H_Q, d]")
-    _need(v_cache.shape == k_cache.shape and v_cache.dtype == k_cache.dtype,
-          "v_cache must match k_cache")
-    _need(row == (q4_row_bytes(d) if k_cache.dtype == torch.uint8 else d),
-          "cache rows must be d elements, or 5 * d / 8 bytes of a 4-bit cache (uint8)")
-    _need(block_tables.dtype == torch.int32 and context_lens.dtype == torch.int32,
-          "block_tables and context_lens must be int32")
-    _need(block_tables.dim() == 2 and block_tables.shape[0] == B and context_lens.numel() == B,
-          "block_tables must be [B, max_blocks_per_seq], context_lens [B]")
+    shape = k_cache.shape
+    nb, bs, HKV, row = shape
+    kind = k_cache.dtype
+    if not (q.is_contiguous() and out.is_contiguous() and k_cache.is_contiguous()
+            and v_cache.is_contiguous() and block_tables.is_contiguous()
+            and context_lens.is_contiguous() and workspace.is_contiguous()):
+        raise ValueError("out, q, caches, block_tables, context_lens and workspace must be "
+                         "contiguous")
+    if q.dtype != torch.bfloat16 or out.dtype != torch.bfloat16 or out.shape != q.shape:
+        raise ValueError("q and out must be bf16 [B, H_Q, d]")
+    if v_cache.dtype != kind or v_cache.shape != shape:
+        raise ValueError("v_cache must match k_cache")
+    if row != (q4_row_bytes(d) if kind == torch.uint8 else d):
+        raise ValueError("cache rows must be d elements, or 5 * d / 8 bytes of a 4-bit cache "
+                         "(uint8)")
+    if block_tables.dtype != torch.int32 or context_lens.dtype != torch.int32:
+        raise ValueError("block_tables and context_lens must be int32")
+    if block_tables.dim() != 2 or block_tables.shape[0] != B or context_lens.numel() != B:
+        raise ValueError("block_tables must be [B, max_blocks_per_seq], context_lens [B]")
     return B, HQ, HKV, d, bs, nb
 
 
