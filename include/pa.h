@@ -549,7 +549,9 @@ pa_status pa_paged_decode_attention_q4(void *out, const void *q, const void *k_c
  * cache_dtype: PA_BF16 (k_scale, v_scale NULL), PA_FP8_E4M3 (scales as in
  *   pa_paged_decode_attention_fp8) or PA_Q4 (scales NULL; caches as in
  *   pa_paged_decode_attention_q4).  out is what the decode call of that
- *   cache gives.
+ *   cache gives (over bf16 and e4m3 the context is split in longer ranges,
+ *   so the last bit may differ).  A length above the decode call's plan is
+ *   clipped and flagged as there, so lengths within max_context_len never are.
  * workspace: at least pa_paged_decode_scored_workspace_size(...) bytes (the
  *   decode workspace, then one fp32 score for each query head and token and
  *   a log-sum-exp for each query head); otherwise as for

@@ -794,12 +794,13 @@ pa_status static_decode_scratch_address(void** ptr) {
 }
 
 DecodePlan make_decode_plan(int32_t num_seqs, int32_t num_kv_heads, int32_t max_context_len,
-                            int32_t num_sms) {
+                            int32_t num_sms, int32_t ctas_per_sm) {
   if (num_sms <= 0) num_sms = 148;
   if (max_context_len <= 0 || num_seqs <= 0 || num_kv_heads <= 0) return {1, kTile};
   const int64_t tiles_max = (static_cast<int64_t>(max_context_len) + kTile - 1) / kTile;
   const int64_t work = static_cast<int64_t>(num_seqs) * num_kv_heads;  // CTAs per split index
-  const int64_t target = 32ll * num_sms;  // aim for ~32 CTAs per SM over the whole grid
+  // aim for so many CTAs per SM over the whole grid
+  const int64_t target = static_cast<int64_t>(ctas_per_sm) * num_sms;
   int64_t splits = (target + work - 1) / work;
   if (splits < 1) splits = 1;
   if (splits > tiles_max) splits = tiles_max;

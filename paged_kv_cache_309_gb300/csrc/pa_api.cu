@@ -612,9 +612,15 @@ size_t pa_paged_decode_scored_workspace_size(int32_t num_seqs, int32_t num_q_hea
   if (num_seqs < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || head_size <= 0 ||
       max_context_len < 0 || max_context_len > (1 << 30))
     return 0;
-  const pa_detail::DecodePlan plan = pa_detail::make_decode_plan(
-      num_seqs, num_kv_heads, max_context_len, pa_detail::num_sms_current_device());
-  return pa_detail::scored_workspace_bytes(num_seqs, num_q_heads, num_kv_heads, head_size, plan);
+  // the call over a 4-bit cache and the one over the others have different plans
+  const int sms = pa_detail::num_sms_current_device();
+  const size_t q4 = pa_detail::scored_workspace_bytes(
+      num_seqs, num_q_heads, num_kv_heads, head_size,
+      pa_detail::make_decode_plan(num_seqs, num_kv_heads, max_context_len, sms));
+  const size_t other = pa_detail::scored_workspace_bytes(
+      num_seqs, num_q_heads, num_kv_heads, head_size,
+      pa_detail::make_scored_plan(num_seqs, num_kv_heads, max_context_len, sms));
+  return q4 > other ? q4 : other;
 }
 
 pa_status pa_paged_decode_attention_scored(
@@ -640,8 +646,11 @@ pa_status pa_paged_decode_attention_scored(
   if (partly_overlap(sums_out, sums_in,
                      static_cast<uintptr_t>(num_seqs) * num_kv_heads * sums_len * 4))
     return PA_ERR_INVALID;
-  const size_t need =
-      pa_detail::scored_workspace_bytes(num_seqs, num_q_heads, num_kv_heads, head_size, a.plan);
+  if (cache_dtype != PA_Q4)
+    a.plan = pa_detail::make_scored_plan(num_seqs, num_kv_heads, max_context_len,
+                                         pa_detail::num_sms_current_device());
+  const size_t need = pa_paged_decode_scored_workspace_size(num_seqs, num_q_heads, num_kv_heads,
+                                                            head_size, max_context_len);
   if (workspace == nullptr || workspace_bytes < need) return PA_ERR_WORKSPACE;
   if (!aligned(workspace, 256)) return PA_ERR_ALIGN;
   a.workspace = workspace;

@@ -642,7 +642,14 @@ struct DecodePlan {
   int32_t tokens_per_split;
 };
 DecodePlan make_decode_plan(int32_t num_seqs, int32_t num_kv_heads, int32_t max_context_len,
-                            int32_t num_sms);
+                            int32_t num_sms, int32_t ctas_per_sm = 32);
+// The plan of the scored call over bf16 and e4m3 caches: a CTA there costs more
+// (its scores, the sums of logs), so ranges are longer (B = 64, 512-4096, e4m3: 78 -> 71 us
+// with 8 CTAs per SM, bf16 119 -> 108; B = 8, 32K-128K, bf16: 460 -> 452).
+inline DecodePlan make_scored_plan(int32_t num_seqs, int32_t num_kv_heads,
+                                   int32_t max_context_len, int32_t num_sms) {
+  return make_decode_plan(num_seqs, num_kv_heads, max_context_len, num_sms, 8);
+}
 size_t decode_workspace_bytes(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads,
                               int32_t head_size, const DecodePlan& plan);
 

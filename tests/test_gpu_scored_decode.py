@@ -1,7 +1,7 @@
 """GPU parity of the decode attention that adds up attention weights.
 
-The outputs are those of the cache's own decode call (compared bit for bit
-with it, which its own tests check against the oracle).  Weights against the
+The outputs are those of the cache's own decode call (compared with it, bit
+for bit over 4 bits; its own tests check it against the oracle).  Weights against the
 oracle in double: a score (base 2) is an fp32 sum of 128 exact products (or 4
 groups' sums) with at most 24 roundings in a chain, each 2^-23 of a partial sum
 below 2^5.1 (normal data: sum |q k| scale log2 e, or its 4-bit form with codes
@@ -68,8 +68,16 @@ def run(w, num_new, T=None, sums=None, max_len=None, ws=None, in_place=False):
         pa.pa_paged_decode_attention(plain, q, w["kd"], w["vd"], table, lens, w["scale"], mcl, dws,
                                      k_scale=w["ks"], v_scale=w["vs"])
     torch.cuda.synchronize()
-    same = out.view(torch.int16) == plain.view(torch.int16)
-    assert (same | (out.isnan() & plain.isnan())).all()
+    if w["kd"].dtype == torch.uint8:
+        same = out.view(torch.int16) == plain.view(torch.int16)
+        assert (same | (out.isnan() & plain.isnan())).all()
+    elif not pa.read_device_error(dws):
+        # other ranges, the same values: each rounded to bf16 once (2^-7 of the smaller apart
+        # at most), fp32 sums in another order
+        a, b = out.float(), plain.float()
+        assert (a.isnan() == b.isnan()).all()
+        a, b = a.nan_to_num(), b.nan_to_num()
+        assert ((a - b).abs() <= 2.0 ** -7 * b.abs() + 2e-4 * b.abs().amax().clamp(min=1.0)).all()
     return dst.cpu().numpy().astype(np.float64), before, pa.read_device_error(ws), out
 
 
@@ -167,8 +175,7 @@ def test_clipped_lengths():
     w = batch("bf16", [500, 20], 2, 4, 16, seed=12)
     got, before, err, _ = run(w, 1, max_len=128)
     assert err & pa.PA_DEVERR_CONTEXT_CLIPPED
-    splits, per = pa.pa_paged_decode_plan(2, 2, 128)
-    check(w, got, before, 1, "bf16", limit=splits * per)
+    check(w, got, before, 1, "bf16", limit=128)  # ranges of whole 64s
 
 
 @pytest.mark.parametrize("cache", CACHES)
