@@ -549,22 +549,24 @@ def q4_row_bytes(head_size):
 
 def _q4_shapes(key, value, key_cache, value_cache, slot_mapping):
     """Checks shared by the 4-bit write and gather: (N, H, d, num_blocks, bs)."""
-    N, H, d = key.shape
-    for t, name in ((key, "key"), (value, "value")):
-        if t is not None and (t.shape != key.shape or t.dtype != key.dtype or t.stride(2) != 1
-                              or t.stride(1) != d):
-            raise ValueError(f"{name}: [N, H, d] with heads and elements contiguous expected")
+    shape = key.shape
+    N, H, d = shape
+    if key.stride(2) != 1 or key.stride(1) != d:
+        raise ValueError("key: [N, H, d] with heads and elements contiguous expected")
     if (value is None) != (value_cache is None):
         raise ValueError("give both value and value_cache, or neither")
+    if value is not None and (value.shape != shape or value.dtype != key.dtype
+                              or value.stride(2) != 1 or value.stride(1) != d):
+        raise ValueError("value must match key, heads and elements contiguous")
     nb, bs, Hc, rb = key_cache.shape
-    if key_cache.dtype != torch.uint8 or (Hc, rb) != (H, q4_row_bytes(d)) \
-            or key_cache.stride(3) != 1 or key_cache.stride(2) != rb \
-            or key_cache.stride(1) != H * rb:
+    strides = key_cache.stride()
+    if key_cache.dtype != torch.uint8 or Hc != H or rb != q4_row_bytes(d) \
+            or strides[1:] != (H * rb, rb, 1):
         raise ValueError("key_cache must be uint8 [num_blocks, bs, H, 5 * d / 8], contiguous "
                          "inside a block")
     if value_cache is not None and (value_cache.shape != key_cache.shape
-                                    or value_cache.stride() != key_cache.stride()
-                                    or value_cache.dtype != key_cache.dtype):
+                                    or value_cache.stride() != strides
+                                    or value_cache.dtype != torch.uint8):
         raise ValueError("value_cache must match key_cache")
     if slot_mapping.dtype != torch.int64 or slot_mapping.numel() != N \
             or not slot_mapping.is_contiguous():
@@ -641,7 +643,8 @@ def pa_paged_decode_attention_q4(out, q, k_cache, v_cache, block_tables, context
     int32; workspace from decode_workspace."""
     B, HQ, HKV, d, bs, nb = _decode_shapes(out, q, k_cache, v_cache, block_tables, context_lens,
                                            workspace)
-    _need(k_cache.dtype == torch.uint8, "a 4-bit cache (uint8 rows) is expected")
+    if k_cache.dtype != torch.uint8:
+        raise ValueError("a 4-bit cache (uint8 rows) is expected")
     st = _load().pa_paged_decode_attention_q4(
         _ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables), _ptr(context_lens),
         B, HQ, HKV, d, bs, block_tables.shape[1], nb, float(scale), int(max_context_len),
@@ -664,10 +667,17 @@ def decode_scored_workspace(num_seqs, num_q_heads, num_kv_heads, head_size, max_
     return torch.zeros(max(n, 256), dtype=torch.uint8, device=device or "cuda")
 
 
-def _sums(t, name, B, H):
-    _on_device(**{name: t})
-    _need(t.dtype == torch.float32 and t.dim() == 3 and t.shape[:2] == (B, H) and t.is_contiguous(),
-          f"{name} must be float32 [B, H_KV, tokens], contiguous")
+def _sums(sums, sums_out, B, H):
+    """Checks of the accumulated weights (their device apart): tokens per row."""
+    shape = sums.shape
+    if len(shape) != 3 or shape[0] != B or shape[1] != H or sums.dtype != torch.float32 \
+            or not sums.is_contiguous():
+        raise ValueError("sums must be float32 [B, H_KV, tokens], contiguous")
+    if sums_out is not None and sums_out is not sums and (
+            sums_out.shape != shape or sums_out.dtype != torch.float32
+            or not sums_out.is_contiguous()):
+        raise ValueError("sums_out must match sums")
+    return shape[2]
 
 
 def pa_paged_decode_attention_scored(out, sums_out, sums, num_new, q, k_cache, v_cache,
@@ -680,16 +690,19 @@ def pa_paged_decode_attention_scored(out, sums_out, sums, num_new, q, k_cache, v
     workspace from decode_scored_workspace."""
     B, HQ, HKV, d, bs, nb = _decode_shapes(out, q, k_cache, v_cache, block_tables, context_lens,
                                            workspace)
-    _scales(k_scale, v_scale)
-    _sums(sums, "sums", B, HKV)
-    _sums(sums_out, "sums_out", B, HKV)
-    _need(sums.shape == sums_out.shape, "sums_out must match sums")
-    _need(0 <= num_new, "num_new must not be negative")
-    _need(k_scale is None or k_cache.dtype == torch.float8_e4m3fn,
-          "k_scale/v_scale apply to an e4m3 cache")
+    _on_device(sums=sums, sums_out=sums_out)
+    if sums_out is None:
+        raise ValueError("sums_out is required")
+    tokens = _sums(sums, sums_out, B, HKV)
+    if k_scale is not None or v_scale is not None:
+        _scales(k_scale, v_scale)
+        if k_cache.dtype != torch.float8_e4m3fn:
+            raise ValueError("k_scale/v_scale apply to an e4m3 cache")
+    if num_new < 0:
+        raise ValueError("num_new must not be negative")
     dtype = PA_Q4 if k_cache.dtype == torch.uint8 else _dtype(k_cache)
     st = _load().pa_paged_decode_attention_scored(
-        _ptr(out), _ptr(sums_out), _ptr(sums), sums.shape[2], min(int(num_new), 2 ** 31 - 1),
+        _ptr(out), _ptr(sums_out), _ptr(sums), tokens, min(int(num_new), 2 ** 31 - 1),
         _ptr(q), _ptr(k_cache), _ptr(v_cache), dtype, _ptr(k_scale), _ptr(v_scale),
         _ptr(block_tables), _ptr(context_lens), B, HQ, HKV, d, bs, block_tables.shape[1], nb,
         float(scale), int(max_context_len), _ptr(workspace),
@@ -703,20 +716,19 @@ def pa_evict_select(keep, new_lens, sums_out, sums, context_lens, budget, num_si
     -1 behind them: the first num_sink and last num_recent, then the largest
     sums [B, H_KV, T] float32 (ties to the lowest token); new_lens [B] int32 <-
     their number; sums_out (None, sums itself or another like it) <- their sums."""
-    _on_device(keep=keep, new_lens=new_lens, context_lens=context_lens)
-    _need(keep.dtype == torch.int32 and keep.dim() == 3 and keep.is_contiguous(),
-          "keep must be int32 [B, H_KV, budget], contiguous")
-    B, H, budget_dim = keep.shape
-    _need(budget_dim == budget, "keep must be [B, H_KV, budget]")
-    _sums(sums, "sums", B, H)
-    if sums_out is not None:
-        _sums(sums_out, "sums_out", B, H)
-        _need(sums_out.shape == sums.shape, "sums_out must match sums")
+    _on_device(keep=keep, new_lens=new_lens, sums=sums, sums_out=sums_out,
+               context_lens=context_lens)
+    if keep.dtype != torch.int32 or keep.dim() != 3 or not keep.is_contiguous():
+        raise ValueError("keep must be int32 [B, H_KV, budget], contiguous")
+    B, H, width = keep.shape
+    if width != budget:
+        raise ValueError("keep must be [B, H_KV, budget]")
+    tokens = _sums(sums, sums_out, B, H)
     for t, name in ((new_lens, "new_lens"), (context_lens, "context_lens")):
-        _need(t.dtype == torch.int32 and t.numel() == B and t.is_contiguous(),
-              f"{name} must be int32 [B]")
+        if t.dtype != torch.int32 or t.numel() != B or not t.is_contiguous():
+            raise ValueError(f"{name} must be int32 [B]")
     _check(_load().pa_evict_select(_ptr(keep), _ptr(new_lens), _ptr(sums_out), _ptr(sums),
-                                   _ptr(context_lens), B, H, sums.shape[2], budget, num_sink,
+                                   _ptr(context_lens), B, H, tokens, budget, num_sink,
                                    num_recent, _stream(stream)), "pa_evict_select")
 
 
@@ -729,19 +741,21 @@ def pa_cache_compact(k_cache, v_cache, keep, keep_lens, src_block_tables, dst_bl
     ascending)."""
     _on_device(k_cache=k_cache, v_cache=v_cache, keep=keep, keep_lens=keep_lens,
                src_block_tables=src_block_tables, dst_block_tables=dst_block_tables)
-    _need(k_cache.dim() == 4 and k_cache.is_contiguous(),
-          "k_cache must be [num_blocks, bs, H_KV, row], contiguous")
-    _need(v_cache is None or (v_cache.shape == k_cache.shape and v_cache.dtype == k_cache.dtype
-                              and v_cache.is_contiguous()), "v_cache must match k_cache")
+    if k_cache.dim() != 4 or not k_cache.is_contiguous():
+        raise ValueError("k_cache must be [num_blocks, bs, H_KV, row], contiguous")
+    if v_cache is not None and (v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype
+                                or not v_cache.is_contiguous()):
+        raise ValueError("v_cache must match k_cache")
     nb, bs, H, row = k_cache.shape
-    _need(keep.dtype == torch.int32 and keep.dim() == 3 and keep.shape[1] == H
-          and keep.is_contiguous(), "keep must be int32 [B, H_KV, n], contiguous")
+    if keep.dtype != torch.int32 or keep.dim() != 3 or keep.shape[1] != H \
+            or not keep.is_contiguous():
+        raise ValueError("keep must be int32 [B, H_KV, n], contiguous")
     B = keep.shape[0]
-    _need(keep_lens.dtype == torch.int32 and keep_lens.numel() == B and keep_lens.is_contiguous(),
-          "keep_lens must be int32 [B]")
+    if keep_lens.dtype != torch.int32 or keep_lens.numel() != B or not keep_lens.is_contiguous():
+        raise ValueError("keep_lens must be int32 [B]")
     for t, name in ((src_block_tables, "src_block_tables"), (dst_block_tables, "dst_block_tables")):
-        _need(t.dtype == torch.int32 and t.dim() == 2 and t.shape[0] == B and t.is_contiguous(),
-              f"{name} must be int32 [B, blocks], contiguous")
+        if t.dtype != torch.int32 or t.dim() != 2 or t.shape[0] != B or not t.is_contiguous():
+            raise ValueError(f"{name} must be int32 [B, blocks], contiguous")
     _check(_load().pa_cache_compact(
         _ptr(k_cache), _ptr(v_cache), row * k_cache.element_size(), _ptr(keep), _ptr(keep_lens),
         keep.shape[2], _ptr(src_block_tables), src_block_tables.shape[1], _ptr(dst_block_tables),
