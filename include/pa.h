@@ -466,7 +466,8 @@ pa_status pa_mla_project_out(void *out, const void *out_latent, const void *w_uv
 /* ------------------------------------------------------------------------
  * pa_reshape_and_cache_q4 -- pa_reshape_and_cache into a 4-bit cache.
  *
- * Slots, the SWA table and skips as in pa_reshape_and_cache.
+ * Slots, the SWA table and skips as in pa_reshape_and_cache (of two tokens
+ * that resolve to one slot, the row may hold parts of both).
  * key, value: [num_tokens, num_heads, head_size] of src_dtype (PA_BF16,
  *   PA_FP16 or PA_FP32), key_stride/value_stride elements between tokens;
  *   value and value_cache may both be NULL (K-only).
@@ -517,10 +518,11 @@ pa_status pa_gather_cache_q4(void *key, void *value, pa_dtype dst_dtype, int64_t
  * the 4-bit rows stand for.  k_cache, v_cache: [num_blocks, block_size,
  * num_kv_heads, 80] bytes, contiguous, 16-byte aligned.  Other arguments,
  * limits, the workspace (pa_paged_decode_workspace_size) and the error word
- * as for pa_paged_decode_attention.  q values must be finite.  A token whose
+ * as for pa_paged_decode_attention; one launch, or two where a sequence may be
+ * split over CTAs.  q values must be finite and below 2^100.  A token whose
  * row stands for NaN makes the outputs of its heads NaN.
  * Numerics: scores in fp32 from exact products of the codes with q (q in
- * fp16 after a power-of-two prescale: exact, but for elements below 2^-24
+ * fp16 after a power-of-two prescale: exact, but for elements below 2^-25
  * of a head's largest); fp32 softmax; the weights and s * code enter the
  * weighted sum rounded to fp16, the sum is fp32.
  * ---------------------------------------------------------------------- */
@@ -555,7 +557,9 @@ pa_status pa_paged_decode_attention_q4(void *out, const void *q, const void *k_c
  * workspace: at least pa_paged_decode_scored_workspace_size(...) bytes (the
  *   decode workspace, then one fp32 score for each query head and token and
  *   a log-sum-exp for each query head); otherwise as for
- *   pa_paged_decode_attention.  Two launches on `stream`.
+ *   pa_paged_decode_attention (calls that share one agree on num_seqs and
+ *   num_kv_heads, for the place of the split counters).  Two launches on
+ *   `stream` (three over a 4-bit cache).  sums_len above 2^30: PA_ERR_UNSUPPORTED.
  * ---------------------------------------------------------------------- */
 size_t pa_paged_decode_scored_workspace_size(int32_t num_seqs, int32_t num_q_heads,
                                              int32_t num_kv_heads, int32_t head_size,
@@ -587,8 +591,8 @@ pa_status pa_paged_decode_attention_scored(
  * keep [num_seqs, num_kv_heads, budget] int32 contiguous; new_lens
  *   [num_seqs] int32, not context_lens itself (PA_ERR_INVALID).
  * budget >= 1; num_sink, num_recent >= 0, num_sink + num_recent <= budget
- *   (else PA_ERR_INVALID).  num_seqs * num_kv_heads of 2^27 or more:
- *   PA_ERR_UNSUPPORTED.
+ *   (else PA_ERR_INVALID).  num_seqs * num_kv_heads of 2^27 or more, sums_len
+ *   or budget above 2^30: PA_ERR_UNSUPPORTED.
  * ---------------------------------------------------------------------- */
 pa_status pa_evict_select(int32_t *keep, int32_t *new_lens, float *sums_out,
                           const float *sums_in, const int32_t *context_lens, int32_t num_seqs,
@@ -614,8 +618,8 @@ pa_status pa_evict_select(int32_t *keep, int32_t *new_lens, float *sums_out,
  *   e4m3, 80 PA_Q4 at head_size 128; 1152 an MLA latent row, one head).
  * keep: [num_seqs, num_kv_heads, keep_len] int32, contiguous; keep_lens
  *   [num_seqs] int32.  block_size >= 1.  Tables [num_seqs, src/dst_max_blocks]
- *   int32.  num_seqs or num_kv_heads above 65535, or 2^31 slots or more:
- *   PA_ERR_UNSUPPORTED.
+ *   int32.  num_seqs or num_kv_heads above 65535, 2^31 slots or more, or
+ *   keep_len above 2^30: PA_ERR_UNSUPPORTED.
  * Alignment: caches 16 bytes.
  * ---------------------------------------------------------------------- */
 pa_status pa_cache_compact(void *k_cache, void *v_cache, int32_t row_bytes, const int32_t *keep,

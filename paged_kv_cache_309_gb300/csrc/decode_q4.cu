@@ -39,10 +39,10 @@
 //   walks its pieces with the ring running on across them.  A sequence that
 //   lies in one chunk is written directly; the pieces of one that does not
 //   go to partial slots, which a second launch merges with one CTA per query
-//   head (a single long sequence has 200 pieces: merged by the CTA that
-//   finished last, its 16 heads took 54 us at 9001 tokens and 8 heads per kv
-//   head; apart 9).  Its CTAs are launched while this kernel runs and wait for
-//   its end (programmatic dependent launch).
+//   head (a single long sequence has up to 200 pieces; with the CTA that finished
+//   last merging all its 16 query heads a scored call over 9001 tokens took 54
+//   us, so 19).  Its CTAs are launched while this kernel runs and wait for its
+//   end (programmatic dependent launch).
 //
 // Every mbarrier wait is bounded (2 s); after a timeout the error bit is
 // set, the remaining pieces end empty, the copies in flight are waited for, and

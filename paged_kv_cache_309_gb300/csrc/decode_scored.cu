@@ -123,6 +123,18 @@ pa_status launch_add(const DecodeParams& p, const SumsParams& w, int32_t num_seq
 
 size_t align256(size_t x) { return (x + 255) / 256 * 256; }
 
+// The decode workspace, with room for its split counters even where the plan has
+// one range and no counters: they have to be zero when a later call with a
+// longer max_context_len (or a decode call with another plan) finds them.
+size_t decode_part_bytes(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads,
+                         int32_t head_size, const DecodePlan& plan) {
+  const size_t bytes =
+      decode_workspace_bytes(num_seqs, num_q_heads, num_kv_heads, head_size, plan);
+  const size_t counters =
+      kWorkspaceHeader + static_cast<size_t>(num_seqs) * num_kv_heads * sizeof(unsigned);
+  return align256(bytes > counters ? bytes : counters);
+}
+
 }  // namespace
 
 // Workspace: [decode workspace, padded] [log2-sum-exp: B*H_Q f32, padded]
@@ -130,7 +142,7 @@ size_t align256(size_t x) { return (x + 255) / 256 * 256; }
 size_t scored_workspace_bytes(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads,
                               int32_t head_size, const DecodePlan& plan) {
   const size_t rows = static_cast<size_t>(num_seqs) * num_q_heads;
-  return align256(decode_workspace_bytes(num_seqs, num_q_heads, num_kv_heads, head_size, plan)) +
+  return decode_part_bytes(num_seqs, num_q_heads, num_kv_heads, head_size, plan) +
          align256(rows * sizeof(float)) +
          rows * plan.num_splits * static_cast<size_t>(plan.tokens_per_split) * sizeof(float);
 }
@@ -140,8 +152,7 @@ pa_status launch_paged_decode_scored(DecodeArgs a, float* sums_out, const float*
   if (a.num_seqs == 0) return PA_OK;
   if (a.num_kv_heads > 65535 || a.num_seqs > 65535) return PA_ERR_UNSUPPORTED;
   uint8_t* at = static_cast<uint8_t*>(a.workspace) +
-                align256(decode_workspace_bytes(a.num_seqs, a.num_q_heads, a.num_kv_heads,
-                                                a.head_size, a.plan));
+                decode_part_bytes(a.num_seqs, a.num_q_heads, a.num_kv_heads, a.head_size, a.plan);
   a.final_lse = reinterpret_cast<float*>(at);
   a.scores = reinterpret_cast<float*>(
       at + align256(static_cast<size_t>(a.num_seqs) * a.num_q_heads * sizeof(float)));

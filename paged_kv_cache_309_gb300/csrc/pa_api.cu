@@ -641,6 +641,7 @@ pa_status pa_paged_decode_attention_scored(
                                     block_size, max_blocks_per_seq, num_blocks, scale,
                                     max_context_len, &a, /*allow_q4=*/true);
   if (st != PA_OK) return st;
+  if (sums_len > (1 << 30)) return PA_ERR_UNSUPPORTED;
   if (!aligned(sums_out, 4) || !aligned(sums_in, 4)) return PA_ERR_ALIGN;
   // in place or apart: a partial overlap would read sums already written
   if (partly_overlap(sums_out, sums_in,
@@ -673,7 +674,8 @@ pa_status pa_evict_select(int32_t* keep, int32_t* new_lens, float* sums_out,
       new_lens == context_lens)
     return PA_ERR_INVALID;
   const int64_t rows = static_cast<int64_t>(num_seqs) * num_kv_heads;
-  if (rows >= (1ll << 27)) return PA_ERR_UNSUPPORTED;
+  if (rows >= (1ll << 27) || sums_len > (1 << 30) || budget > (1 << 30))
+    return PA_ERR_UNSUPPORTED;
   if (!aligned(keep, 4) || !aligned(new_lens, 4) || !aligned(sums_in, 4) ||
       !aligned(sums_out, 4) || !aligned(context_lens, 4))
     return PA_ERR_ALIGN;
@@ -710,7 +712,8 @@ pa_status pa_cache_compact(void* k_cache, void* v_cache, int32_t row_bytes, cons
     return PA_ERR_INVALID;
   const bool in_place = src_block_tables == dst_block_tables;
   if (in_place && src_max_blocks != dst_max_blocks) return PA_ERR_INVALID;
-  if (num_seqs > 65535 || num_kv_heads > 65535 || num_blocks >= (1ll << 31) / block_size)
+  if (num_seqs > 65535 || num_kv_heads > 65535 || num_blocks >= (1ll << 31) / block_size ||
+      keep_len > (1 << 30))
     return PA_ERR_UNSUPPORTED;
   if (row_bytes % 16 != 0 || !aligned(k_cache, 16) || !aligned(v_cache, 16) ||
       !aligned(keep, 4) || !aligned(keep_lens, 4) || !aligned(src_block_tables, 4) ||

@@ -204,7 +204,7 @@ def test_scored_rejects(lib):
                 dict(HQ=12), dict(so=P(0x100000 + 64)), dict(si=P(0x100000 + 4 * 8 * 128 * 4 - 4))):
         assert _scored(lib, **bad) == pa.PA_ERR_INVALID, bad
     for bad in (dict(cd=pa.PA_FP16), dict(cd=pa.PA_FP32), dict(cd=9), dict(d=64), dict(bs=12),
-                dict(HQ=24), dict(B=65536, wsb=1 << 50)):
+                dict(HQ=24), dict(B=65536, wsb=1 << 50), dict(T=(1 << 30) + 1)):
         assert _scored(lib, **bad) == pa.PA_ERR_UNSUPPORTED, bad
     for bad in (dict(so=P(0x100002), si=P(0x100002)), dict(out=FAKE_MIS), dict(ws=P(0x100010))):
         assert _scored(lib, **bad) == pa.PA_ERR_ALIGN, bad
@@ -261,7 +261,8 @@ def test_select_rejects(lib):
                 dict(sink=60), dict(sink=2 ** 31 - 1, recent=2 ** 31 - 1),
                 dict(so=P(0x300000 + 4)), dict(so=P(0x300000 - 4))):
         assert _select(lib, **bad) == pa.PA_ERR_INVALID, bad
-    assert _select(lib, B=1 << 24) == pa.PA_ERR_UNSUPPORTED
+    for bad in (dict(B=1 << 24), dict(T=(1 << 30) + 1), dict(budget=(1 << 30) + 1)):
+        assert _select(lib, **bad) == pa.PA_ERR_UNSUPPORTED, bad
     for n in ("keep", "new", "so", "si", "cl"):
         assert _select(lib, **{n: P(0x100002)}) == pa.PA_ERR_ALIGN, n
 
@@ -281,7 +282,7 @@ def test_compact_rejects(lib):
                 dict(row=0), dict(n=-1), dict(sm=0), dict(dm=0), dict(B=-1), dict(H=0), dict(bs=0),
                 dict(nb=-1), dict(src=FAKE, dst=FAKE)):
         assert _compact(lib, **bad) == pa.PA_ERR_INVALID, bad
-    for bad in (dict(B=65536), dict(H=65536)):
+    for bad in (dict(B=65536), dict(H=65536), dict(nb=1 << 27), dict(n=(1 << 30) + 1)):
         assert _compact(lib, **bad) == pa.PA_ERR_UNSUPPORTED, bad
     for bad in (dict(row=72), dict(k=FAKE_MIS), dict(v=FAKE_MIS), dict(keep=P(0x100002)),
                 dict(src=P(0x100002))):
