@@ -26,7 +26,8 @@ namespace {
 
 using namespace pa;
 
-constexpr int kWarps = 8;
+constexpr int kWarps = 8;        // per CTA of the write
+constexpr int kGatherWarps = 4;  // of the gather
 
 __device__ __forceinline__ float2 add2_rn(float2 a, float2 b) {
   float2 d;
@@ -263,10 +264,11 @@ __device__ __forceinline__ int64_t row_of(const Q4CacheArgs& a, int64_t s) {
 template <typename S>
 __global__ void __launch_bounds__(kWarps * 32, sizeof(S) == 2 ? 8 : 4) reshape_and_cache_q4_kernel(Q4CacheArgs a) {
   const int lane = threadIdx.x & 31;
-  const int64_t wid = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-  const int64_t t = a.groups == 1 ? wid : wid / a.groups;
+  // a CTA takes 32 units of kWarps tokens; the row's groups of 32 are the grid's y axis
+  // (a warp's number divided by the groups took a sixth of the instructions)
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
   if (t >= a.num_tokens) return;
-  const int c = static_cast<int>(wid - t * a.groups) * 32 + lane;
+  const int c = static_cast<int>(blockIdx.y) * 32 + lane;
   const int64_t s = slot_of(a, t);  // the same slot in every lane
   if (s < 0) return;
   const bool mine = c < a.row_units, has_v = a.value != nullptr;
@@ -302,10 +304,16 @@ template <typename D>
 __device__ __forceinline__ Vec8<D> restore(uint32_t w, float2 s2, float2 m2) {
   float f[8];
   const float2 back = make_float2(-8388608.f, -8388608.f);
+  uint32_t magic;  // 2^23, kept in a register: (x & 15) | magic is one instruction
+  asm("mov.u32 %0, 0x4B000000;" : "=r"(magic));
+  auto code = [&](uint32_t x) -> float {
+    uint32_t d;
+    asm("lop3.b32 %0, %1, 15, %2, 0xEA;" : "=r"(d) : "r"(x), "r"(magic));
+    return __uint_as_float(d);
+  };
 #pragma unroll
   for (int e = 0; e < 8; e += 2) {
-    const float2 c = make_float2(__uint_as_float(((w >> (4 * e)) & 15u) | 0x4B000000u),
-                                 __uint_as_float(((w >> (4 * e + 4)) & 15u) | 0x4B000000u));
+    const float2 c = make_float2(code(w >> (4 * e)), code(w >> (4 * e + 4)));
     const float2 y = fma2_rn(add2_rn(c, back), s2, m2);
     f[e] = y.x;
     f[e + 1] = y.y;
@@ -314,12 +322,14 @@ __device__ __forceinline__ Vec8<D> restore(uint32_t w, float2 s2, float2 m2) {
 }
 
 template <typename D>
-__global__ void __launch_bounds__(kWarps * 32) gather_cache_q4_kernel(Q4CacheArgs a) {
+__global__ void __launch_bounds__(kGatherWarps * 32) gather_cache_q4_kernel(Q4CacheArgs a) {
   const int lane = threadIdx.x & 31;
-  const int64_t wid = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-  const int64_t t = a.groups == 1 ? wid : wid / a.groups;
+  // a CTA takes 32 units of kGatherWarps tokens, the next CTA the next 32 of the same
+  // tokens (the groups on the grid's y axis, far apart in time: 63.5 us for 65K tokens, so 59.5)
+  const uint32_t block = a.groups == 1 ? blockIdx.x : blockIdx.x / a.groups;
+  const int64_t t = static_cast<int64_t>(block) * kGatherWarps + (threadIdx.x >> 5);
   if (t >= a.num_tokens) return;
-  const int c = static_cast<int>(wid - t * a.groups) * 32 + lane;
+  const int c = static_cast<int>(blockIdx.x - block * a.groups) * 32 + lane;
   const int64_t s = slot_of(a, t);
   if (s < 0 || c >= a.row_units) return;
   const RowPlace p = row_place(c, a.units_per_head);
@@ -351,8 +361,9 @@ __global__ void __launch_bounds__(kWarps * 32) gather_cache_q4_kernel(Q4CacheArg
   }
 }
 
-pa_status grid_of(Q4CacheArgs& a, int64_t elem_bytes, unsigned* grid) {
-  a.groups = (a.row_units + 31) / 32;
+// What both launchers derive from the arguments.
+void derive(Q4CacheArgs& a, int64_t elem_bytes) {
+  a.groups = static_cast<uint32_t>((a.row_units + 31) / 32);
   // 8-byte accesses to the codes: head rows (10 * units bytes) and blocks on multiples of 8
   a.wide = a.units_per_head % 4 == 0 && a.block_stride % 8 == 0;
   // 32-byte accesses to the rows
@@ -360,18 +371,15 @@ pa_status grid_of(Q4CacheArgs& a, int64_t elem_bytes, unsigned* grid) {
   a.whole32 = ((reinterpret_cast<uintptr_t>(a.key) | reinterpret_cast<uintptr_t>(a.value) |
                 static_cast<uintptr_t>(key_step) | static_cast<uintptr_t>(value_step)) &
                31u) == 0u;
-  const int64_t blocks = (a.num_tokens * a.groups + kWarps - 1) / kWarps;
-  if (blocks > 0x7FFFFFFFll) return PA_ERR_UNSUPPORTED;
-  *grid = static_cast<unsigned>(blocks);
-  return PA_OK;
 }
 
 }  // namespace
 
 pa_status launch_reshape_and_cache_q4(Q4CacheArgs a, pa_dtype src, cudaStream_t stream) {
-  unsigned grid = 0;
-  const pa_status st = grid_of(a, src == PA_FP32 ? 4 : 2, &grid);
-  if (st != PA_OK) return st;
+  derive(a, src == PA_FP32 ? 4 : 2);
+  const int64_t blocks = (a.num_tokens + kWarps - 1) / kWarps;
+  if (blocks > 0x7FFFFFFFll || a.groups > 65535u) return PA_ERR_UNSUPPORTED;
+  const dim3 grid(static_cast<unsigned>(blocks), a.groups);
   switch (src) {
     case PA_BF16: reshape_and_cache_q4_kernel<bf16><<<grid, kWarps * 32, 0, stream>>>(a); break;
     case PA_FP16: reshape_and_cache_q4_kernel<f16><<<grid, kWarps * 32, 0, stream>>>(a); break;
@@ -382,13 +390,14 @@ pa_status launch_reshape_and_cache_q4(Q4CacheArgs a, pa_dtype src, cudaStream_t 
 }
 
 pa_status launch_gather_cache_q4(Q4CacheArgs a, pa_dtype dst, cudaStream_t stream) {
-  unsigned grid = 0;
-  const pa_status st = grid_of(a, dst == PA_FP32 ? 4 : 2, &grid);
-  if (st != PA_OK) return st;
+  derive(a, dst == PA_FP32 ? 4 : 2);
+  const int64_t blocks = (a.num_tokens + kGatherWarps - 1) / kGatherWarps;
+  if (blocks > 0x7FFFFFFFll / a.groups) return PA_ERR_UNSUPPORTED;
+  const unsigned grid = static_cast<unsigned>(blocks * a.groups);
   switch (dst) {
-    case PA_BF16: gather_cache_q4_kernel<bf16><<<grid, kWarps * 32, 0, stream>>>(a); break;
-    case PA_FP16: gather_cache_q4_kernel<f16><<<grid, kWarps * 32, 0, stream>>>(a); break;
-    case PA_FP32: gather_cache_q4_kernel<float><<<grid, kWarps * 32, 0, stream>>>(a); break;
+    case PA_BF16: gather_cache_q4_kernel<bf16><<<grid, kGatherWarps * 32, 0, stream>>>(a); break;
+    case PA_FP16: gather_cache_q4_kernel<f16><<<grid, kGatherWarps * 32, 0, stream>>>(a); break;
+    case PA_FP32: gather_cache_q4_kernel<float><<<grid, kGatherWarps * 32, 0, stream>>>(a); break;
     default: return PA_ERR_UNSUPPORTED;
   }
   return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;

@@ -616,9 +616,9 @@ struct Q4CacheArgs {
   int32_t row_units;       // (num_heads * head_size) / 16
   int32_t units_per_head;  // head_size / 16
   int32_t block_size;
-  // set by the launcher: warps per token; whether codes can be accessed by 8
-  // bytes and the rows of key/value by 32
-  int32_t groups;
+  // set by the launcher: groups of 32 units per token; whether codes can be
+  // accessed by 8 bytes and the rows of key/value by 32
+  uint32_t groups;
   bool wide, whole32;
 };
 pa_status launch_reshape_and_cache_q4(Q4CacheArgs a, pa_dtype src, cudaStream_t stream);
