@@ -29,10 +29,13 @@
 // What bounds it: at 160 bytes per token and kv head HBM leaves an SM 440
 // issue slots for 16 tokens, and the first form of this kernel needed 431 of
 // them (0.54 of the copy rate at B = 8, 32K-128K).  So the element work is
-// the forms above, a new running maximum is looked for by a vote (the
+// the forms above, 32 tokens share one vote on a new running maximum (the
 // shuffles run only when a score beats the old one by 2^8), and the prologue
-// and epilogue, which cost as much as 40 tokens, run once per piece of a
-// balanced cut instead of once per short token range:
+// and epilogue run once per piece of a balanced cut instead of once per short
+// token range.  With 296 instructions for 16 tokens the copies alone take 137
+// us there, the computation alone 137 and both together 143 (0.87 of the
+// copy rate; B = 64, 512-4096: 41, 43 and 45; there a CTA spends 2 us on the
+// cut and some 1.6 on the end of each piece).  The cut:
 //   the sequences' units of 64 tokens lie end to end, every sequence start
 //   charged kPieceCost units more; chunk c of C (C x H_KV CTAs fill the GPU
 //   once) is the units whose cost lies in [c, c + 1) total / C.  A chunk
@@ -862,7 +865,7 @@ __global__ void __launch_bounds__(kThreads, Lay<NT, HP>::kCtasPerSm)
                             o[2 * v + 1][nt][j] + zu, o[2 * v + 1][nt][j + 2] + zu);
         }
       }
-      if ((v + 1) & (vs - 1)) continue;  // more groups in this round
+      if ((v + 1) & (vs - 1)) continue;  // more groups to load first
       consumer_barrier();
       for (int i = threadIdx.x; i < (HP * 8 << lv) << qp.log2_g; i += kConsumers) {
         const int hh = i >> (3 + lv);  // of the CTA's query heads
