@@ -538,6 +538,13 @@ def pa_mla_project_out(out, out_latent, w_uv, stream=None):
                                       _stream(stream)), "pa_mla_project_out")
 
 
+def _i32(name, value):
+    """value as a C int32; ctypes would keep its low 32 bits without a word."""
+    if not -2 ** 31 <= value < 2 ** 31:
+        raise ValueError(f"{name} does not fit 32 bits")
+    return int(value)
+
+
 # ------------------------------------------------------------ 4-bit cache --
 def q4_row_bytes(head_size):
     """Bytes of a kv head's row in a 4-bit cache: head_size / 2 of codes, then
@@ -645,9 +652,11 @@ def pa_paged_decode_attention_q4(out, q, k_cache, v_cache, block_tables, context
                                            workspace)
     if k_cache.dtype != torch.uint8:
         raise ValueError("a 4-bit cache (uint8 rows) is expected")
+    max_context_len = _i32("max_context_len", max_context_len)
     st = _load().pa_paged_decode_attention_q4(
         _ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables), _ptr(context_lens),
-        B, HQ, HKV, d, bs, block_tables.shape[1], nb, float(scale), int(max_context_len),
+        B, HQ, HKV, d, bs, block_tables.shape[1], nb, float(scale),
+        max_context_len,
         _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream))
     _check(st, "pa_paged_decode_attention_q4")
 
@@ -655,6 +664,7 @@ def pa_paged_decode_attention_q4(out, q, k_cache, v_cache, block_tables, context
 # ------------------------------------------------ attention weights, eviction --
 def pa_paged_decode_scored_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_size,
                                           max_context_len):
+    max_context_len = _i32("max_context_len", max_context_len)
     return int(_load().pa_paged_decode_scored_workspace_size(num_seqs, num_q_heads, num_kv_heads,
                                                              head_size, max_context_len))
 
@@ -700,12 +710,13 @@ def pa_paged_decode_attention_scored(out, sums_out, sums, num_new, q, k_cache, v
             raise ValueError("k_scale/v_scale apply to an e4m3 cache")
     if num_new < 0:
         raise ValueError("num_new must not be negative")
+    max_context_len = _i32("max_context_len", max_context_len)
     dtype = PA_Q4 if k_cache.dtype == torch.uint8 else _dtype(k_cache)
     st = _load().pa_paged_decode_attention_scored(
         _ptr(out), _ptr(sums_out), _ptr(sums), tokens, min(int(num_new), 2 ** 31 - 1),
         _ptr(q), _ptr(k_cache), _ptr(v_cache), dtype, _ptr(k_scale), _ptr(v_scale),
         _ptr(block_tables), _ptr(context_lens), B, HQ, HKV, d, bs, block_tables.shape[1], nb,
-        float(scale), int(max_context_len), _ptr(workspace),
+        float(scale), max_context_len, _ptr(workspace),
         workspace.numel() * workspace.element_size(), _stream(stream))
     _check(st, "pa_paged_decode_attention_scored")
 
@@ -727,6 +738,7 @@ def pa_evict_select(keep, new_lens, sums_out, sums, context_lens, budget, num_si
     for t, name in ((new_lens, "new_lens"), (context_lens, "context_lens")):
         if t.dtype != torch.int32 or t.numel() != B or not t.is_contiguous():
             raise ValueError(f"{name} must be int32 [B]")
+    num_sink, num_recent = _i32("num_sink", num_sink), _i32("num_recent", num_recent)
     _check(_load().pa_evict_select(_ptr(keep), _ptr(new_lens), _ptr(sums_out), _ptr(sums),
                                    _ptr(context_lens), B, H, tokens, budget, num_sink,
                                    num_recent, _stream(stream)), "pa_evict_select")

@@ -315,3 +315,25 @@ def test_eviction_binding_refusals(monkeypatch):
                 dict(src_block_tables=i32(3, 2).T), dict(keep_lens=i32(2).long())):
         with pytest.raises(ValueError):
             pa.pa_cache_compact(**{**com, **bad})
+
+
+# ------------------------------------------- integers past 32 bits do not wrap --
+@pytest.mark.parametrize("value", [2 ** 31, 2 ** 32, 2 ** 32 + 64, -2 ** 31 - 1])
+def test_binding_refuses_integers_past_32_bits(monkeypatch, value):
+    monkeypatch.setattr(pa, "_on_device", lambda **kw: None)
+    monkeypatch.setattr(pa, "_load", lambda: pytest.fail("reached the library"))
+    i32 = lambda *s: torch.zeros(*s, dtype=torch.int32)
+    sums = torch.zeros(2, 4, 30)
+    sel = dict(keep=i32(2, 4, 10), new_lens=i32(2), sums_out=None, sums=sums,
+               context_lens=i32(2), budget=10, num_sink=1, num_recent=2)
+    for name in ("num_sink", "num_recent"):
+        with pytest.raises(ValueError, match=name):
+            pa.pa_evict_select(**{**sel, name: value})
+    with pytest.raises(ValueError, match="max_context_len"):
+        pa.pa_paged_decode_attention_q4(**{**_decode_tensors(), "max_context_len": value})
+    with pytest.raises(ValueError, match="max_context_len"):
+        pa.pa_paged_decode_attention_scored(
+            **{**_decode_tensors(128, torch.bfloat16), "sums_out": sums, "sums": sums,
+               "num_new": 1, "max_context_len": value})
+    with pytest.raises(ValueError, match="max_context_len"):
+        pa.pa_paged_decode_scored_workspace_size(2, 8, 4, 128, value)
