@@ -865,7 +865,7 @@ __global__ void __launch_bounds__(kThreads, Lay<NT, HP>::kCtasPerSm)
                             o[2 * v + 1][nt][j] + zu, o[2 * v + 1][nt][j + 2] + zu);
         }
       }
-      if ((v + 1) & (vs - 1)) continue;  // more groups to load first
+      if ((v + 1) & (vs - 1)) continue;  // the pass holds more groups
       consumer_barrier();
       for (int i = threadIdx.x; i < (HP * 8 << lv) << qp.log2_g; i += kConsumers) {
         const int hh = i >> (3 + lv);  // of the CTA's query heads
