@@ -210,3 +210,14 @@ def test_replayed_graph_sees_new_lengths():
     torch.cuda.synchronize()
     got = sums.cpu().numpy().astype(np.float64)
     check(w, got, np.zeros_like(got), 1 << 30, "q4", untouched=0.0)
+
+
+@pytest.mark.parametrize("cache", CACHES)
+@pytest.mark.parametrize("G", [1, 16])
+def test_no_context_at_all(cache, G):
+    """max_context_len 0: the outputs are 0 and no sum is touched."""
+    w = batch(cache, [0, 0, 0], 2, G, 16, seed=14)
+    got, _, err, out = run(w, 1, T=5, max_len=0)
+    assert err == 0
+    assert (out == 0).all()
+    assert (got == -5.0).all()
