@@ -77,6 +77,9 @@ struct Q4Params {
 
 template <int NT, int HP>
 struct Lay {
+  // 16 heads (B = 8, 16K-64K, 4 kv heads): two CTAs with 168 registers and some
+  // spills take 68 us, one without spills 77 (six stages: 78), three 90, two with
+  // four stages 69
   static constexpr int kStages = 3;
   static constexpr int kCtasPerSm = NT == 1 ? 3 : 2;
   static constexpr int kTile = kStageRows / HP;        // tokens per stage
