@@ -187,7 +187,7 @@ pa_status pa_concat_and_cache_mla(const void *kv_c, const void *k_pe, pa_dtype s
  *     out[b, h] = softmax_j(scale * q[b, h] . K_j) @ V_j,   j < L
  * L counts the token just written (write, then attend).  L = 0 gives a
  * zero row.  A block id outside [0, num_blocks) drops its tokens from the
- * softmax.
+ * softmax.  A score of NaN makes its head's output NaN.
  *
  * q, out: [num_seqs, num_q_heads, head_size] bf16, contiguous.
  * k_cache, v_cache: [num_blocks, block_size, num_kv_heads, head_size],

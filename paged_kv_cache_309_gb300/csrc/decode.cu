@@ -674,9 +674,9 @@ __device__ __forceinline__ void epilogue_tc(const DecodeParams& p, uint8_t* smem
     } else {
       const int64_t slot = row * p.num_splits + split;
       *reinterpret_cast<float4*>(p.ws_o + slot * kD + e0) = acc4;
-      // (scored: a NaN sum is carried to the weights)
-      if (e0 == 0)
-        p.ws_lse[slot] = (kScored ? Ls != 0.f : Ls > 0.f) ? fin[2 * h] + log2f(Ls) : -INFINITY;
+      // a NaN sum is carried to the merge (and the weights): where every split held a
+      // NaN, -inf for it would leave the merge nothing and a zero row
+      if (e0 == 0) p.ws_lse[slot] = Ls == 0.f ? -INFINITY : fin[2 * h] + log2f(Ls);
     }
   }
 }
