@@ -542,7 +542,10 @@ pa_status pa_paged_decode_attention_q4(void *out, const void *q, const void *k_c
  *                         softmax_t(scale q[b, h] . K_t)
  *     sums_out[b, g, t] = (t >= L - num_new ? 0 : sums_in[b, g, t]) + w[b, g, t]
  * for t < min(L, sums_len); other elements of sums_out are left as they
- * were.  num_new >= 0: the sequence's last num_new tokens joined the cache
+ * were.  While the workspace's error word has PA_DEVERR_WAIT_TIMEOUT set,
+ * by this call or one before it, no element of sums_out is written: the
+ * caller clears the word and repeats the call.
+ * num_new >= 0: the sequence's last num_new tokens joined the cache
  * since the last call, so their sums start here (1 in a decode loop; any
  * value >= L starts every sum).  A token of a dropped block has weight 0.
  *

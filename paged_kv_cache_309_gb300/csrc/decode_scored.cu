@@ -37,8 +37,13 @@ __global__ void __launch_bounds__(kSumThreads) add_weights_kernel(const DecodePa
   constexpr int kSteps = kSumLoads / kL;
   const int g = blockIdx.y, b = blockIdx.z;
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the scores and sums of logs are there
+  // A wait that ran out in the launches before left tokens without a score (their
+  // places hold an earlier call's): the sums stay as they were, all of them, so that
+  // the call can be repeated.  The caller clears the word.
+  const unsigned err = __ldcg(p.err);
   bool clipped;
   const int L = effective_len(p, b, &clipped);
+  if (err & PA_DEVERR_WAIT_TIMEOUT) return;
   const int end = min(L, w.sums_len);
   const int64_t row = static_cast<int64_t>(b) * p.num_kv_heads + g;
   const int64_t first = static_cast<int64_t>(blockIdx.x) * (kSumThreads * kSteps * kV);
