@@ -496,10 +496,12 @@ __global__ void __launch_bounds__(kThreads, Lay<NT, HP>::kCtasPerSm)
       *abort_flag = 1;
       atomicOr(p.err, PA_DEVERR_WAIT_TIMEOUT);
     }
-    // copies in flight at an early end are waited for (bounded) before the CTA exits
-    if (!ok && lane == 0) {
+    // The last copies are waited for (bounded) before this warp ends, whoever gave up:
+    // consumers whose wait ran out leave with copies in flight, and the CTA's shared
+    // memory must not be handed on before those have landed.
+    if (lane == 0) {
       for (int t = max(0, u - kStages); t < u; ++t)
-        mbar_wait_bounded(&full[t % kStages], (t / kStages) & 1, nullptr);
+        mbar_wait_bounded_long(&full[t % kStages], (t / kStages) & 1, nullptr);
     }
     return;
   }
