@@ -43,9 +43,12 @@
 #include <atomic>
 #include <cmath>
 
-#include "decode_common.cuh"
+#include "pa_internal.cuh"
 
 namespace pa_detail {
+
+using namespace decode;
+
 namespace {
 
 using namespace pa;
@@ -81,6 +84,91 @@ struct TcLayout {
   static constexpr int kBytes = kBarOffset + 3 * kStages * 8 + 16;  // full, empty, mask, flags
   static constexpr int kAlloc = kBytes + 1024;  // room to align the base to 1 KB
 };
+
+// Merge of one (sequence, query head) by one warp: weights 2^(lse_s - max)
+// over the n splits that hold tokens, out = sum_s w_s o_s / sum_s w_s,
+// rounded to bf16.  Partials are read through L2 (__ldcg): other CTAs wrote
+// them during this launch.
+template <bool kScored>
+__device__ __forceinline__ void merge_splits_warp(const DecodeParams& p, int64_t bh, int n,
+                                                  int lane) {
+  const float* lse = p.ws_lse + bh * p.num_splits;
+  const float* o = p.ws_o + bh * p.num_splits * kD;
+  float M = -INFINITY;
+  // (a NaN lse, of a split whose sum is NaN, is carried to the output)
+  for (int s = lane; s < n; s += 32) M = max_nan(M, __ldcg(lse + s));
+#pragma unroll
+  for (int off = 16; off >= 1; off >>= 1) M = max_nan(M, __shfl_xor_sync(0xffffffffu, M, off));
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  float W = 0.f;
+  if (M != -INFINITY) {
+    for (int s0 = 0; s0 < n; s0 += 32) {
+      const int my = s0 + lane;
+      const float wl = my < n ? exp2f(__ldcg(lse + my) - M) : 0.f;
+      const int cnt = min(32, n - s0);
+      int k = 0;
+      for (; k + 8 <= cnt; k += 8) {
+        float4 v[8];
+        float w[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          v[u] = __ldcg(reinterpret_cast<const float4*>(o + static_cast<int64_t>(s0 + k + u) * kD) +
+                        lane);
+          w[u] = __shfl_sync(0xffffffffu, wl, k + u);
+        }
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          W += w[u];
+          acc.x += w[u] * v[u].x;
+          acc.y += w[u] * v[u].y;
+          acc.z += w[u] * v[u].z;
+          acc.w += w[u] * v[u].w;
+        }
+      }
+      for (; k < cnt; ++k) {
+        const float4 v =
+            __ldcg(reinterpret_cast<const float4*>(o + static_cast<int64_t>(s0 + k) * kD) + lane);
+        const float w = __shfl_sync(0xffffffffu, wl, k);
+        W += w;
+        acc.x += w * v.x;
+        acc.y += w * v.y;
+        acc.z += w * v.z;
+        acc.w += w * v.w;
+      }
+    }
+  }
+  if (kScored && lane == 0) p.final_lse[bh] = W == 0.f ? -INFINITY : M + log2f(W);
+  const float inv = W > 0.f ? 1.f / W : 0.f;
+  *reinterpret_cast<uint2*>(p.out + bh * kD + lane * 4) =
+      make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+}
+
+// Counts this CTA's partial in its (sequence, kv head)'s counter; the CTA that
+// completes the count merges the splits of its G query heads and returns the
+// counter to zero.  Every thread of the CTA calls it; last_flag: one int of
+// shared memory nothing else uses.
+template <bool kScored>
+__device__ __forceinline__ void count_and_merge(const DecodeParams& p, int b, int g, int hq0, int G,
+                                                int L, int* last_flag, int warp, int lane) {
+  __syncthreads();  // every partial of this CTA is written
+  const int n_valid = (L + p.tokens_per_split - 1) / p.tokens_per_split;
+  if (threadIdx.x == 0) {
+    __threadfence();
+    unsigned* ctr = p.counters + static_cast<int64_t>(b) * p.num_kv_heads + g;
+    const unsigned prev = atomicAdd(ctr, 1u);
+    const bool last = prev + 1u == static_cast<unsigned>(n_valid);
+    if (last) {
+      atomicExch(ctr, 0u);
+      __threadfence();
+    }
+    *last_flag = last ? 1 : 0;
+  }
+  __syncthreads();
+  if (*last_flag) {
+    for (int h = warp; h < G; h += kThreads / 32)
+      merge_splits_warp<kScored>(p, static_cast<int64_t>(b) * p.num_q_heads + hq0 + h, n_valid, lane);
+  }
+}
 
 // Decode step, fused write: the warp that owns row L-1 of the last tile
 // converts the sequence's new K (lanes 0-15) and V (lanes 16-31) row exactly
@@ -829,7 +917,7 @@ size_t decode_workspace_bytes(int32_t num_seqs, int32_t num_q_heads, int32_t num
   return bytes;
 }
 
-DecodeParams make_decode_params(const DecodeArgs& a) {
+DecodeParams decode::make_decode_params(const DecodeArgs& a) {
   DecodeParams p;
   p.out = static_cast<__nv_bfloat16*>(a.out);
   p.q = static_cast<const __nv_bfloat16*>(a.q);

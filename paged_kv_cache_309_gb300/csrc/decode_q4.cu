@@ -53,9 +53,13 @@
 #include <atomic>
 #include <type_traits>
 
-#include "decode_common.cuh"
+#include "pa_internal.cuh"
 
 namespace pa_detail {
+
+using namespace pa;
+using namespace decode;
+
 namespace {
 
 constexpr int kUnit = 64;          // tokens per unit of the cut (boxes are up to 64 rows)

@@ -8,9 +8,13 @@
 //     sums_out[b, g, t] = (t >= L - num_new ? 0 : sums_in[b, g, t])
 //                         + sum_h 2^(score[b, g, t, h] - lse[b, h])
 // in a fixed order (no atomics).
-#include "decode_common.cuh"
+#include "pa_internal.cuh"
 
 namespace pa_detail {
+
+using namespace pa;
+using namespace decode;
+
 namespace {
 
 constexpr int kSumThreads = 256;

@@ -675,6 +675,87 @@ struct DecodeArgs {
   float* scores;           // accumulated weights (else null): see DecodeParams
   float* final_lse;
 };
+// What the GQA decode kernels (decode.cu, decode_q4.cu, decode_scored.cu) share:
+// their parameters, the clipped context length and the stores of the scores.
+namespace decode {
+
+using namespace pa;
+
+constexpr int kD = 128;                 // head size handled by the decode kernels
+constexpr int kConsumerWarps = 4;
+constexpr int kThreads = (kConsumerWarps + 1) * 32;
+constexpr float kRescaleLog2 = 8.0f;    // lazy-rescale threshold (base-2 units)
+constexpr size_t kWorkspaceHeader = 256;  // error word + padding
+
+struct DecodeParams {
+  __nv_bfloat16* out;
+  const __nv_bfloat16* q;
+  const int32_t* block_tables;
+  const int32_t* context_lens;
+  float* ws_lse;
+  float* ws_o;
+  unsigned* counters;  // [B, H_KV] split arrivals, zero between calls
+  unsigned* err;
+  int64_t num_blocks;
+  int32_t num_q_heads;
+  int32_t num_kv_heads;
+  int32_t block_size;
+  int32_t log2_bs;
+  int32_t max_blocks_per_seq;
+  int32_t num_splits;
+  int32_t tokens_per_split;
+  float scale_log2;
+  const float* k_scale;  // quantised cache: code * k_scale is the value (else null)
+  const float* v_scale;
+  // fused decode step (else null): each sequence's newest K/V row
+  // [B, H_KV, d] bf16, written at slot_mapping[b] before it is attended to
+  const __nv_bfloat16* new_k;
+  const __nv_bfloat16* new_v;
+  const int64_t* slot_mapping;
+  void* k_cache;
+  void* v_cache;
+  // accumulated attention weights (else null): the scores in base 2, -inf
+  // where there is no token, [B, H_KV, score_len, G]; and each query head's
+  // log2-sum-exp [B, H_Q]
+  float* scores;
+  float* final_lse;
+  int64_t score_len;
+};
+
+// context length the kernels use: clipped to the plan and the table
+__device__ __forceinline__ int effective_len(const DecodeParams& p, int b, bool* clipped) {
+  int L = __ldg(p.context_lens + b);
+  L = L < 0 ? 0 : L;
+  const int64_t cap = min(static_cast<int64_t>(p.max_blocks_per_seq) * p.block_size,
+                          static_cast<int64_t>(p.num_splits) * p.tokens_per_split);
+  *clipped = static_cast<int64_t>(L) > cap;
+  return *clipped ? static_cast<int>(cap) : L;
+}
+
+// Scores of one 16-token slice, from the accumulator layout of the score
+// products: this lane holds tokens row and row + 8 of heads h, h + 1 (s[0],
+// s[1] and s[2], s[3]).  Rows at or past `rows` belong to another range.
+__device__ __forceinline__ void store_scores(const DecodeParams& p, int b, int g, int G, int tok0,
+                                             int row, int rows, int h, const float (&s)[4]) {
+  if (h >= G) return;
+  float* dst =
+      p.scores +
+      ((static_cast<int64_t>(b) * p.num_kv_heads + g) * p.score_len + tok0 + row) * G + h;
+#pragma unroll
+  for (int i = 0; i < 2; ++i, dst += 8 * G) {
+    if (row + 8 * i >= rows) break;
+    if (G == 1) {
+      dst[0] = s[2 * i];
+    } else {  // G and h are even
+      *reinterpret_cast<float2*>(dst) = make_float2(s[2 * i], s[2 * i + 1]);
+    }
+  }
+}
+
+// The parameters of a call (workspace split up, scale in base 2).
+DecodeParams make_decode_params(const DecodeArgs& a);
+
+}  // namespace decode
 pa_status launch_paged_decode(const DecodeArgs& a, cudaStream_t stream);
 pa_status launch_paged_decode_q4(const DecodeArgs& a, cudaStream_t stream);  // decode_q4.cu
 // decode_scored.cu: the decode call of a's cache type, then the weights added up
