@@ -18,6 +18,7 @@
  *   pa_paged_decode_attention_scored  decode attention that also adds up each cached
  *                                  token's attention weight
  *   pa_evict_select                which tokens of a row to keep, by those weights
+ *   pa_evict_select_paged          the same where block tables may hold dropped blocks
  *   pa_cache_compact               move the kept rows together through block tables
  *
  * Common rules
@@ -584,7 +585,8 @@ pa_status pa_paged_decode_attention_scored(
  * n = min(L, budget) tokens: first the protected ones (t < num_sink or
  * t >= L - num_recent), then those of the largest sums[b, g, t]; of equal
  * ones the lowest t.  A NaN sum counts as smaller than every number; +0 and
- * -0 are equal.
+ * -0 are equal.  The choice knows no block table: where one holds dropped
+ * blocks, use pa_evict_select_paged.
  *     keep[b, g, 0..n)     = the kept t, ascending; keep[b, g, n..budget) = -1
  *     new_lens[b]          = n
  *     sums_out[b, g, j]    = sums_in[b, g, keep[b, g, j]]  for j < n, other
@@ -603,6 +605,29 @@ pa_status pa_evict_select(int32_t *keep, int32_t *new_lens, float *sums_out,
                           int32_t num_sink, int32_t num_recent, pa_stream_t stream);
 
 /* ------------------------------------------------------------------------
+ * pa_evict_select_paged -- pa_evict_select for sequences whose block tables
+ * may hold dropped blocks.
+ *
+ * A token t < L has no row where its block lies past the table
+ * (t / block_size >= max_blocks_per_seq) or its id outside [0, num_blocks).
+ * Such a token is never kept, protected or not, and a sequence's n is the
+ * smaller of budget and the number of its tokens that have one; the rest is
+ * as in pa_evict_select, which would keep it where it is protected or the
+ * budget leaves room.  pa_cache_compact has no row to move for a kept token
+ * without one, so the row at its new place would stay what it was and be
+ * attended to: with dropped blocks, choose with this call.
+ * block_tables: [num_seqs, max_blocks_per_seq] int32; block_size >= 1.  The
+ * other arguments, limits and errors are pa_evict_select's.
+ * ---------------------------------------------------------------------- */
+pa_status pa_evict_select_paged(int32_t *keep, int32_t *new_lens, float *sums_out,
+                                const float *sums_in, const int32_t *context_lens,
+                                const int32_t *block_tables, int32_t num_seqs,
+                                int32_t num_kv_heads, int32_t sums_len, int32_t budget,
+                                int32_t num_sink, int32_t num_recent, int32_t block_size,
+                                int32_t max_blocks_per_seq, int64_t num_blocks,
+                                pa_stream_t stream);
+
+/* ------------------------------------------------------------------------
  * pa_cache_compact -- move the kept rows together.
  *
  * For every (b, g), j < min(keep_lens[b], keep_len) and t = keep[b, g, j]:
@@ -610,11 +635,14 @@ pa_status pa_evict_select(int32_t *keep, int32_t *new_lens, float *sums_out,
  *         <- row t, read through src_block_tables
  * in k_cache and v_cache (v_cache may be NULL: a K-only or MLA latent cache).
  * A row whose index or block is out of range (t < 0, past a table, a block id outside
- * the pool) is not moved.  All other rows of the pool are left as they were.
+ * the pool) is not moved.  All other rows of the pool are left as they were:
+ * a kept token must have a row (pa_evict_select_paged) and its place a block.
  *
  * In place: pass the same pointer for both tables; keep must then be
  * ascending in each row with keep[b, g, j] >= j (as pa_evict_select writes
- * it) and no two sequences share blocks.  Otherwise the destination blocks
+ * it) and no two sequences share blocks; a table whose first blocks, up to
+ * the kept rows' number, hold a dropped one needs other destination blocks.
+ * Otherwise the destination blocks
  * must be distinct from each other and from every source block.
  * k_cache, v_cache: [num_blocks, block_size, num_kv_heads, row_bytes],
  *   contiguous, any element type; row_bytes a multiple of 16 (256 bf16, 128

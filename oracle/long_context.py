@@ -80,20 +80,25 @@ def decode(q, k, v, table, lens, block, scale, limit=None):
     return out, sums
 
 
-def evict_select(sums, lens, budget, sink, recent):
-    """keep [B, H, budget] int32 (-1 behind the kept), new_lens [B]."""
+def evict_select(sums, lens, budget, sink, recent, table=None, block=1, num_blocks=0):
+    """keep [B, H, budget] int32 (-1 behind the kept), new_lens [B].  With a
+    table, tokens of blocks outside the pool or past it do not take part."""
     B, H, T = sums.shape
     keep = np.full((B, H, budget), -1, np.int32)
     new = np.zeros(B, np.int32)
     for b in range(B):
         L = max(0, min(int(lens[b]), T))
-        new[b] = min(L, budget)
+        there = range(L)
+        if table is not None:
+            there = [t for t in there if t // block < table.shape[1]
+                     and 0 <= table[b, t // block] < num_blocks]
+        new[b] = min(len(there), budget)
         for h in range(H):
             def rank(t):
                 x = float(sums[b, h, t])
                 free = sink <= t < L - recent
                 return (free, np.isnan(x), 0.0 if np.isnan(x) else -x, t)
-            order = sorted(range(L), key=rank)
+            order = sorted(there, key=rank)
             keep[b, h, :new[b]] = sorted(order[:budget])
     return keep, new
 

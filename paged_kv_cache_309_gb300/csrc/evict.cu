@@ -6,7 +6,10 @@
 // and one ordered pass writes the indices of every key above it and of the
 // first ties, ascending, with the sums beside them.  A row is read once: the
 // CTAs of a cluster hold a part of it each in shared memory, and join their
-// digit counts through distributed shared memory.  (One CTA re-reading its row
+// digit counts through distributed shared memory.  Given the block tables (kPaged),
+// tokens of dropped blocks get the lowest key of all and do not count as tokens: a
+// kept one would have no row to move, and the row at its new place, whatever it
+// holds, would be attended to.  (One CTA re-reading its row
 // for every digit: 222 us for 64 rows of 32K-128K, 27 us for 128 rows of 2.3K; so: 49 and 7.3,
 // bound by instruction issue, 0.68 of the cycles, not by the 21 MB read.)
 //
@@ -40,6 +43,38 @@ __device__ __forceinline__ uint32_t order_key(float x) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
+// Whether token t of a sequence has a row (kPaged): its block is in the pool.
+__device__ __forceinline__ bool has_row(const SelectArgs& a, const int32_t* table, int t) {
+  const int blk = (a.block_size & (a.block_size - 1)) == 0 ? t >> (31 - __clz(a.block_size))
+                                                           : t / a.block_size;
+  if (blk >= a.max_blocks) return false;
+  const int id = __ldg(table + blk);
+  return id >= 0 && id < a.num_blocks;
+}
+
+// The order key with room below it for tokens without a row.
+template <bool kPaged>
+__device__ __forceinline__ uint32_t live_key(float x) {
+  const uint32_t k = order_key(x);
+  return kPaged && k == 0u ? 1u : k;  // (the lowest number's key is 0x007FFFFF)
+}
+
+// Tokens below L that have a row, counted by the whole CTA; shared: one word.
+__device__ __forceinline__ int count_live(const SelectArgs& a, const int32_t* table, int L,
+                                          int* shared) {
+  if (threadIdx.x == 0) *shared = 0;
+  __syncthreads();
+  int live = 0;
+  for (int64_t first = static_cast<int64_t>(threadIdx.x) * a.block_size; first < L;
+       first += static_cast<int64_t>(blockDim.x) * a.block_size)
+    if (has_row(a, table, static_cast<int>(first)))
+      live += static_cast<int>(min(static_cast<int64_t>(a.block_size), L - first));
+  live = __reduce_add_sync(0xffffffffu, live);
+  if ((threadIdx.x & 31) == 0) atomicAdd(shared, live);
+  __syncthreads();
+  return *shared;
+}
+
 // Exclusive sums over the CTA's threads of x (two 16-bit counts in one word);
 // total: the sum over all.  warp_sums: 33 words of shared memory.
 __device__ __forceinline__ uint32_t block_scan(uint32_t x, uint32_t* warp_sums, uint32_t& total) {
@@ -71,7 +106,9 @@ __device__ __forceinline__ uint32_t block_scan(uint32_t x, uint32_t* warp_sums, 
 }
 
 // Rows longer than a cluster holds: one CTA per row, re-read for every digit.
+template <bool kPaged>
 __global__ void __launch_bounds__(kSelThreads) evict_select_long_kernel(const SelectArgs a) {
+  __shared__ int live_sum;
   __shared__ uint32_t hist[256];
   __shared__ uint32_t warp_sums[33];
   __shared__ uint32_t found[2];  // digit, rank within it
@@ -79,13 +116,16 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_long_kernel(const Se
   const int b = row / a.num_kv_heads;
   const int tid = threadIdx.x;
   const int L = min(max(__ldg(a.context_lens + b), 0), a.sums_len);
-  const int n = min(L, a.budget);
+  const int32_t* table = kPaged ? a.block_tables + static_cast<int64_t>(b) * a.max_blocks : nullptr;
+  const int live = kPaged ? count_live(a, table, L, &live_sum) : L;
+  const int n = min(live, a.budget);
   if (row == b * a.num_kv_heads && tid == 0) a.new_lens[b] = n;
   int32_t* keep = a.keep + static_cast<int64_t>(row) * a.budget;
   const float* in = a.sums_in + static_cast<int64_t>(row) * a.sums_len;
   float* out = a.sums_out == nullptr ? nullptr : a.sums_out + static_cast<int64_t>(row) * a.sums_len;
   for (int j = n + tid; j < a.budget; j += kSelThreads) keep[j] = -1;
-  if (L <= a.budget) {
+  if (kPaged && n == 0) return;
+  if (n == L) {
     for (int j = tid; j < n; j += kSelThreads) {
       keep[j] = j;
       if (out != nullptr && out != in) out[j] = in[j];
@@ -93,7 +133,8 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_long_kernel(const Se
     return;
   }
   auto key_of = [&](int t, float x) -> uint32_t {
-    return t < a.num_sink || t >= L - a.num_recent ? 0xFFFFFFFFu : order_key(x);
+    if (kPaged && !has_row(a, table, t)) return 0u;
+    return t < a.num_sink || t >= L - a.num_recent ? 0xFFFFFFFFu : live_key<kPaged>(x);
   };
   uint32_t prefix = 0u;
   uint32_t rank = static_cast<uint32_t>(n);  // of the kept, the lowest key's rank from the top
@@ -163,7 +204,10 @@ __device__ __forceinline__ void cluster_store(const uint32_t* local, int rank, u
   asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(x) : "memory");
 }
 
+template <bool kPaged>
 __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const SelectArgs a, int ranks) {
+  constexpr uint32_t kNoRow = 0xFFFFFFFFu;  // a NaN's bits that stand for a token without a row
+  __shared__ int live_sum;
   extern __shared__ float vals[];  // this CTA's part of the row
   __shared__ __align__(8) uint32_t hist[kBins];
   __shared__ uint32_t candidates[kCandidates];
@@ -176,14 +220,17 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const SelectA
   const int b = row / a.num_kv_heads;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int L = min(max(__ldg(a.context_lens + b), 0), a.sums_len);
-  const int n = min(L, a.budget);
+  const int32_t* table = kPaged ? a.block_tables + static_cast<int64_t>(b) * a.max_blocks : nullptr;
+  const int live = kPaged ? count_live(a, table, L, &live_sum) : L;
+  const int n = min(live, a.budget);
   if (row == b * a.num_kv_heads && rank_id == 0 && tid == 0) a.new_lens[b] = n;
   int32_t* keep = a.keep + static_cast<int64_t>(row) * a.budget;
   const float* in = a.sums_in + static_cast<int64_t>(row) * a.sums_len;
   float* out = a.sums_out == nullptr ? nullptr : a.sums_out + static_cast<int64_t>(row) * a.sums_len;
   const int step = ranks * kSelThreads, me = rank_id * kSelThreads + tid;
   for (int64_t j = static_cast<int64_t>(n) + me; j < a.budget; j += step) keep[j] = -1;
-  if (L <= a.budget) {  // (every CTA of the cluster: no barrier is missed)
+  if (kPaged && n == 0) return;  // (here and below every CTA of the cluster: no barrier is missed)
+  if (n == L) {
     for (int j = me; j < n; j += step) {
       keep[j] = j;
       if (out != nullptr && out != in) out[j] = in[j];
@@ -194,7 +241,8 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const SelectA
   const int t0 = min(rank_id * seg, L), size = min(seg, L - t0);
   auto key = [&](int i, float x) -> uint32_t {
     const int t = t0 + i;
-    return t < a.num_sink || t >= L - a.num_recent ? 0xFFFFFFFFu : order_key(x);
+    if (kPaged && __float_as_uint(x) == kNoRow) return 0u;
+    return t < a.num_sink || t >= L - a.num_recent ? 0xFFFFFFFFu : live_key<kPaged>(x);
   };
   auto clear_hist = [&]() { reinterpret_cast<uint2*>(hist)[tid] = make_uint2(0u, 0u); };
   // The digit that holds the key of rank `rank` (counted from the largest), from every
@@ -248,6 +296,10 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const SelectA
     for (int k = 0; k < 8; ++k) {
       const int i = i0 + k * kSelThreads;
       if (i < size) {
+        if (kPaged) {  // (a NaN of the sums with those bits is another NaN)
+          if (!has_row(a, table, t0 + i)) x[k] = __uint_as_float(kNoRow);
+          else if (__float_as_uint(x[k]) == kNoRow) x[k] = __uint_as_float(kNoRow - 1u);
+        }
         vals[i] = x[k];
         atomicAdd(&hist[key(i, x[k]) >> 21], 1u);
       }
@@ -487,7 +539,10 @@ __global__ void __launch_bounds__(kMoveThreads, kInPlace ? 3 : 4)
 
 }  // namespace
 
-pa_status launch_evict_select(const SelectArgs& a, cudaStream_t stream) {
+namespace {
+
+template <bool kPaged>
+pa_status launch_select(const SelectArgs& a, cudaStream_t stream) {
   const unsigned rows = static_cast<unsigned>(a.num_seqs) * static_cast<unsigned>(a.num_kv_heads);
   // CTAs per row: parts of 16K sums are the fastest for a row (131072 sums: 25 us, parts of
   // 32K: 33), but only some 16 clusters of eight run at a time, so where the rows
@@ -502,11 +557,11 @@ pa_status launch_evict_select(const SelectArgs& a, cudaStream_t stream) {
   int ranks = ranks_for(16384);
   if (static_cast<int64_t>(rows) * ranks > sms) ranks = ranks_for(32768);
   if (static_cast<int64_t>(ranks) * kMaxSegment < a.sums_len) {
-    evict_select_long_kernel<<<rows, kSelThreads, 0, stream>>>(a);
+    evict_select_long_kernel<kPaged><<<rows, kSelThreads, 0, stream>>>(a);
     return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
   }
   static std::atomic<uint64_t> smem_raised{0};
-  if (!ensure_smem_limit(evict_select_kernel, kMaxSegment * 4, smem_raised)) return PA_ERR_CUDA;
+  if (!ensure_smem_limit(evict_select_kernel<kPaged>, kMaxSegment * 4, smem_raised)) return PA_ERR_CUDA;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = static_cast<unsigned>(ranks);
@@ -519,11 +574,18 @@ pa_status launch_evict_select(const SelectArgs& a, cudaStream_t stream) {
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, evict_select_kernel, a, ranks) != cudaSuccess) {
+  if (cudaLaunchKernelEx(&cfg, evict_select_kernel<kPaged>, a, ranks) != cudaSuccess) {
     cudaGetLastError();
     return PA_ERR_CUDA;
   }
   return PA_OK;
+}
+
+}  // namespace
+
+pa_status launch_evict_select(const SelectArgs& a, cudaStream_t stream) {
+  return a.block_tables != nullptr ? launch_select<true>(a, stream)
+                                   : launch_select<false>(a, stream);
 }
 
 pa_status launch_cache_compact(CompactArgs a, bool in_place, cudaStream_t stream) {

@@ -662,10 +662,13 @@ pa_status pa_paged_decode_attention_scored(
                                                reinterpret_cast<cudaStream_t>(stream));
 }
 
-pa_status pa_evict_select(int32_t* keep, int32_t* new_lens, float* sums_out,
-                          const float* sums_in, const int32_t* context_lens, int32_t num_seqs,
-                          int32_t num_kv_heads, int32_t sums_len, int32_t budget,
-                          int32_t num_sink, int32_t num_recent, pa_stream_t stream) {
+namespace {
+
+// Checks shared by both choices; fills *a (the tables apart) where there is work.
+pa_status check_select(int32_t* keep, int32_t* new_lens, float* sums_out, const float* sums_in,
+                       const int32_t* context_lens, int32_t num_seqs, int32_t num_kv_heads,
+                       int32_t sums_len, int32_t budget, int32_t num_sink, int32_t num_recent,
+                       pa_detail::SelectArgs* a) {
   if (num_seqs < 0 || num_kv_heads <= 0 || sums_len <= 0 || budget < 1 || num_sink < 0 ||
       num_recent < 0 || static_cast<int64_t>(num_sink) + num_recent > budget)
     return PA_ERR_INVALID;
@@ -682,18 +685,51 @@ pa_status pa_evict_select(int32_t* keep, int32_t* new_lens, float* sums_out,
   if (sums_out != nullptr &&
       partly_overlap(sums_out, sums_in, static_cast<uintptr_t>(rows) * sums_len * 4))
     return PA_ERR_INVALID;
+  a->keep = keep;
+  a->new_lens = new_lens;
+  a->sums_out = sums_out;
+  a->sums_in = sums_in;
+  a->context_lens = context_lens;
+  a->num_seqs = num_seqs;
+  a->num_kv_heads = num_kv_heads;
+  a->sums_len = sums_len;
+  a->budget = budget;
+  a->num_sink = num_sink;
+  a->num_recent = num_recent;
+  return PA_OK;
+}
+
+}  // namespace
+
+pa_status pa_evict_select(int32_t* keep, int32_t* new_lens, float* sums_out,
+                          const float* sums_in, const int32_t* context_lens, int32_t num_seqs,
+                          int32_t num_kv_heads, int32_t sums_len, int32_t budget,
+                          int32_t num_sink, int32_t num_recent, pa_stream_t stream) {
   pa_detail::SelectArgs a{};
-  a.keep = keep;
-  a.new_lens = new_lens;
-  a.sums_out = sums_out;
-  a.sums_in = sums_in;
-  a.context_lens = context_lens;
-  a.num_seqs = num_seqs;
-  a.num_kv_heads = num_kv_heads;
-  a.sums_len = sums_len;
-  a.budget = budget;
-  a.num_sink = num_sink;
-  a.num_recent = num_recent;
+  const pa_status st = check_select(keep, new_lens, sums_out, sums_in, context_lens, num_seqs,
+                                    num_kv_heads, sums_len, budget, num_sink, num_recent, &a);
+  if (st != PA_OK || num_seqs == 0) return st;
+  return pa_detail::launch_evict_select(a, reinterpret_cast<cudaStream_t>(stream));
+}
+
+pa_status pa_evict_select_paged(int32_t* keep, int32_t* new_lens, float* sums_out,
+                                const float* sums_in, const int32_t* context_lens,
+                                const int32_t* block_tables, int32_t num_seqs,
+                                int32_t num_kv_heads, int32_t sums_len, int32_t budget,
+                                int32_t num_sink, int32_t num_recent, int32_t block_size,
+                                int32_t max_blocks_per_seq, int64_t num_blocks,
+                                pa_stream_t stream) {
+  if (block_size <= 0 || max_blocks_per_seq <= 0 || num_blocks < 0) return PA_ERR_INVALID;
+  pa_detail::SelectArgs a{};
+  const pa_status st = check_select(keep, new_lens, sums_out, sums_in, context_lens, num_seqs,
+                                    num_kv_heads, sums_len, budget, num_sink, num_recent, &a);
+  if (st != PA_OK || num_seqs == 0) return st;
+  if (block_tables == nullptr) return PA_ERR_INVALID;
+  if (!aligned(block_tables, 4)) return PA_ERR_ALIGN;
+  a.block_tables = block_tables;
+  a.max_blocks = max_blocks_per_seq;
+  a.block_size = block_size;
+  a.num_blocks = num_blocks;
   return pa_detail::launch_evict_select(a, reinterpret_cast<cudaStream_t>(stream));
 }
 

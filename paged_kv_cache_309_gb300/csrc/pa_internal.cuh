@@ -771,6 +771,9 @@ struct SelectArgs {  // evict.cu
   const float* sums_in;
   const int32_t* context_lens;
   int32_t num_seqs, num_kv_heads, sums_len, budget, num_sink, num_recent;
+  const int32_t* block_tables;  // null: every token below the length is there
+  int32_t max_blocks, block_size;
+  int64_t num_blocks;
 };
 pa_status launch_evict_select(const SelectArgs& a, cudaStream_t stream);
 

@@ -104,6 +104,9 @@ def _load():
     lib.pa_paged_decode_attention_scored.restype = E
     lib.pa_evict_select.argtypes = [P, P, P, P, P, I32, I32, I32, I32, I32, I32, P]
     lib.pa_evict_select.restype = E
+    lib.pa_evict_select_paged.argtypes = [P, P, P, P, P, P, I32, I32, I32, I32, I32, I32, I32, I32,
+                                          I64, P]
+    lib.pa_evict_select_paged.restype = E
     lib.pa_cache_compact.argtypes = [P, P, I32, P, P, I32, P, I32, P, I32, I32, I32, I32, I64, P]
     lib.pa_cache_compact.restype = E
     _lib = lib
@@ -729,6 +732,35 @@ def pa_evict_select(keep, new_lens, sums_out, sums, context_lens, budget, num_si
     their number; sums_out (None, sums itself or another like it) <- their sums."""
     _on_device(keep=keep, new_lens=new_lens, sums=sums, sums_out=sums_out,
                context_lens=context_lens)
+    B, H, tokens, num_sink, num_recent = _select_shapes(keep, new_lens, sums_out, sums,
+                                                        context_lens, budget, num_sink, num_recent)
+    _check(_load().pa_evict_select(_ptr(keep), _ptr(new_lens), _ptr(sums_out), _ptr(sums),
+                                   _ptr(context_lens), B, H, tokens, budget, num_sink,
+                                   num_recent, _stream(stream)), "pa_evict_select")
+
+
+def pa_evict_select_paged(keep, new_lens, sums_out, sums, context_lens, block_tables, budget,
+                          num_sink, num_recent, block_size, num_blocks, stream=None):
+    """pa_evict_select where block_tables [B, max_blocks_per_seq] int32 may hold
+    dropped blocks (ids outside [0, num_blocks)): their tokens are never kept."""
+    _on_device(keep=keep, new_lens=new_lens, sums=sums, sums_out=sums_out,
+               context_lens=context_lens, block_tables=block_tables)
+    B, H, tokens, num_sink, num_recent = _select_shapes(keep, new_lens, sums_out, sums,
+                                                        context_lens, budget, num_sink, num_recent)
+    if block_tables.dtype != torch.int32 or block_tables.dim() != 2 \
+            or block_tables.shape[0] != B or not block_tables.is_contiguous():
+        raise ValueError("block_tables must be int32 [B, max_blocks_per_seq], contiguous")
+    block_size = _i32("block_size", block_size)
+    if not 0 <= num_blocks < 2 ** 63:
+        raise ValueError("num_blocks must be from 0 to 2^63 - 1")
+    _check(_load().pa_evict_select_paged(
+        _ptr(keep), _ptr(new_lens), _ptr(sums_out), _ptr(sums), _ptr(context_lens),
+        _ptr(block_tables), B, H, tokens, budget, num_sink, num_recent, block_size,
+        block_tables.shape[1], int(num_blocks), _stream(stream)), "pa_evict_select_paged")
+
+
+def _select_shapes(keep, new_lens, sums_out, sums, context_lens, budget, num_sink, num_recent):
+    """Checks shared by both choices: (B, H_KV, tokens, num_sink, num_recent)."""
     if keep.dtype != torch.int32 or keep.dim() != 3 or not keep.is_contiguous():
         raise ValueError("keep must be int32 [B, H_KV, budget], contiguous")
     B, H, width = keep.shape
@@ -738,10 +770,7 @@ def pa_evict_select(keep, new_lens, sums_out, sums, context_lens, budget, num_si
     for t, name in ((new_lens, "new_lens"), (context_lens, "context_lens")):
         if t.dtype != torch.int32 or t.numel() != B or not t.is_contiguous():
             raise ValueError(f"{name} must be int32 [B]")
-    num_sink, num_recent = _i32("num_sink", num_sink), _i32("num_recent", num_recent)
-    _check(_load().pa_evict_select(_ptr(keep), _ptr(new_lens), _ptr(sums_out), _ptr(sums),
-                                   _ptr(context_lens), B, H, tokens, budget, num_sink,
-                                   num_recent, _stream(stream)), "pa_evict_select")
+    return B, H, tokens, _i32("num_sink", num_sink), _i32("num_recent", num_recent)
 
 
 def pa_cache_compact(k_cache, v_cache, keep, keep_lens, src_block_tables, dst_block_tables,
