@@ -54,19 +54,21 @@
 #include <type_traits>
 
 #include "pa_internal.cuh"
+#include "q4_cut.h"
 
 namespace pa_detail {
 
 using namespace pa;
 using namespace decode;
+using namespace q4cut;
 
 namespace {
 
-constexpr int kUnit = 64;          // tokens per unit of the cut (boxes are up to 64 rows)
+static_assert(kUnit == 64, "boxes are up to 64 rows, pieces start at multiples of them");
+static_assert(kPartialFloats == kD, "a partial row is a head");
 constexpr int kRow = 80;           // bytes of a cached row of one kv head
 constexpr int kStageRows = 128;    // head rows per stage, 32 per consumer warp
 constexpr float kLift = 7.0f;      // weights are 2^kLift (score - running maximum)
-constexpr int kPieceCost = 2;      // units charged for a sequence's start
 constexpr int kConsumers = kConsumerWarps * 32;
 
 struct Q4Params {
@@ -159,18 +161,10 @@ __device__ __forceinline__ void consumer_barrier() {
 }
 
 // ------------------------------------------------------------ the balanced cut --
-// Units of 64 tokens lie end to end in sequence order; unit t (counted over
-// all sequences) of sequence b sits at cost t + kPieceCost (b + 1), the line is
-// total = units + kPieceCost B long, and its chunk is floor(cost parts / total)
-// with parts = min(C, total): a step of one unit moves at most one chunk on, so
-// no chunk inside a sequence's span is empty.
-__device__ __forceinline__ int chunk_of(int64_t t, int b, int64_t total, int parts) {
-  return static_cast<int>((t + static_cast<int64_t>(kPieceCost) * (b + 1)) * parts / total);
-}
-
+// (the arithmetic and its invariants: q4_cut.h)
 __device__ __forceinline__ int units_of(const DecodeParams& p, int b) {
   bool clipped;
-  return (effective_len(p, b, &clipped) + kUnit - 1) / kUnit;
+  return units_of_len(effective_len(p, b, &clipped));
 }
 
 // Warp 0: the first unit of chunks c and c + 1.  sched: total, first unit of c,
@@ -180,7 +174,7 @@ __device__ __forceinline__ void find_chunk(const Q4Params& q, int c, int chunks,
   const DecodeParams& p = q.d;
   if (q.whole && chunks == q.num_seqs) {  // one sequence per chunk: nothing to cut
     bool clipped;
-    const int n = (effective_len(p, c, &clipped) + kUnit - 1) / kUnit;
+    const int n = units_of_len(effective_len(p, c, &clipped));
     if (clipped && blockIdx.x == 0 && lane == 0) atomicOr(p.err, PA_DEVERR_CONTEXT_CLIPPED);
     if (lane == 0) {
       sched[0] = 1;
@@ -200,24 +194,23 @@ __device__ __forceinline__ void find_chunk(const Q4Params& q, int c, int chunks,
     held[k] = 0;
     if (b < q.num_seqs) {
       bool clipped;
-      held[k] = (effective_len(p, b, &clipped) + kUnit - 1) / kUnit;
+      held[k] = units_of_len(effective_len(p, b, &clipped));
       any_clipped |= clipped;
     }
     units += held[k];
   }
   for (int b = lane + 128; b < q.num_seqs; b += 32) {
     bool clipped;
-    units += (effective_len(p, b, &clipped) + kUnit - 1) / kUnit;
+    units += units_of_len(effective_len(p, b, &clipped));
     any_clipped |= clipped;
   }
 #pragma unroll
   for (int off = 16; off >= 1; off >>= 1) units += __shfl_xor_sync(0xffffffffu, units, off);
   if (c == 0 && blockIdx.x == 0 && any_clipped) atomicOr(p.err, PA_DEVERR_CONTEXT_CLIPPED);
-  const int64_t total = units + static_cast<int64_t>(kPieceCost) * q.num_seqs;
-  const int64_t parts = min(total, static_cast<int64_t>(chunks));
-  // chunk k begins at the first unit whose cost reaches ceil(k total / parts)
-  const int64_t x0 = (c * total + parts - 1) / parts;
-  const int64_t x1 = ((c + 1) * total + parts - 1) / parts;
+  const int64_t total = total_cost(units, q.num_seqs);
+  const int64_t parts = parts_of(total, chunks);
+  const int64_t x0 = chunk_begin_cost(c, total, parts);
+  const int64_t x1 = chunk_begin_cost(c + 1, total, parts);
   int64_t g0 = units, g1 = units, pre0 = 0;
   int b0 = q.num_seqs;
   bool found0 = c >= parts, found1 = c + 1 >= parts;
@@ -237,15 +230,11 @@ __device__ __forceinline__ void find_chunk(const Q4Params& q, int c, int chunks,
       if (lane >= off) incl += y;
     }
     const int64_t pre = base + incl - n;
-    // the cost that decides: of the sequence's last unit (some unit reaches x), or of
-    // its first when sequences stay whole
-    const int64_t cost = pre + (q.whole ? 0 : n - 1) + static_cast<int64_t>(kPieceCost) * (b + 1);
-    const int64_t charge = static_cast<int64_t>(kPieceCost) * (b + 1);
     if (!found0) {
-      const uint32_t hit = __ballot_sync(0xffffffffu, n > 0 && cost >= x0);
+      const uint32_t hit = __ballot_sync(0xffffffffu, begins_in(x0, pre, n, b, q.whole));
       if (hit != 0u) {
         const int l = __ffs(hit) - 1;
-        const int64_t at = q.whole ? pre : max(x0 - charge, pre);
+        const int64_t at = begin_unit(x0, pre, b, q.whole);
         g0 = __shfl_sync(0xffffffffu, at, l);
         pre0 = __shfl_sync(0xffffffffu, pre, l);
         b0 = first + l;
@@ -253,10 +242,10 @@ __device__ __forceinline__ void find_chunk(const Q4Params& q, int c, int chunks,
       }
     }
     if (!found1) {
-      const uint32_t hit = __ballot_sync(0xffffffffu, n > 0 && cost >= x1);
+      const uint32_t hit = __ballot_sync(0xffffffffu, begins_in(x1, pre, n, b, q.whole));
       if (hit != 0u) {
         const int l = __ffs(hit) - 1;
-        const int64_t at = q.whole ? pre : max(x1 - charge, pre);
+        const int64_t at = begin_unit(x1, pre, b, q.whole);
         g1 = __shfl_sync(0xffffffffu, at, l);
         found1 = true;
       }
@@ -287,7 +276,7 @@ __device__ __forceinline__ bool next_piece(const Q4Params& q, Walk& w, Piece& pc
   while (w.t < w.end) {
     bool clipped;
     const int L = effective_len(q.d, w.b, &clipped);
-    const int n = (L + kUnit - 1) / kUnit;
+    const int n = units_of_len(L);
     if (n > 0) {
       const int64_t stop = min(w.end, w.pre + n);
       pc.b = w.b;
@@ -303,11 +292,6 @@ __device__ __forceinline__ bool next_piece(const Q4Params& q, Walk& w, Piece& pc
     ++w.b;
   }
   return false;
-}
-
-// Slot of a split sequence's first piece (the others go to slots c_first, c_first + 1, ...).
-__device__ __forceinline__ int start_slot_of(int chunks, int num_seqs, int b, int c_first) {
-  return chunks - 1 + (num_seqs <= chunks - 1 ? b : c_first);
 }
 
 // Merge of the split sequences' partials: one CTA per query head, for every
@@ -433,7 +417,7 @@ __global__ void __launch_bounds__(kThreads, Lay<NT, HP>::kCtasPerSm)
   // (the merging CTAs may take their places; they wait for this kernel's end)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int64_t total = sched[0];
-  const int parts = static_cast<int>(min(total, static_cast<int64_t>(chunks)));
+  const int parts = static_cast<int>(parts_of(total, chunks));
 
   if (warp == kConsumerWarps) {
     // ------------------------------------------------------------ producer
@@ -838,12 +822,10 @@ __global__ void __launch_bounds__(kThreads, Lay<NT, HP>::kCtasPerSm)
     const int lv = vs == 4 ? 2 : vs - 1;     // log2(vs)
     const int c_first = qp.whole ? c : chunk_of(pc.first, pc.b, total, parts);
     const int c_last = qp.whole ? c : chunk_of(pc.last, pc.b, total, parts);
-    // partial slot: c - 1 for a piece that goes on from chunk c - 1; for a
-    // sequence's first piece one of its own behind those
-    const int slot = c == c_first ? start_slot_of(chunks, qp.num_seqs, pc.b, c_first) : c - 1;
+    const int slot = slot_of_piece(chunks, qp.num_seqs, pc.b, c_first, c);
     if (!qp.whole && c == c_first && threadIdx.x == 0)
       qp.info[static_cast<int64_t>(blockIdx.x) * qp.num_seqs + pc.b] =
-          c_first == c_last ? 0 : c_first << 16 | (c_last - c_first + 1);
+          info_of(c_first, c_last);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -928,25 +910,15 @@ pa_status launch_q4(const CUtensorMap& mk, const CUtensorMap& mv, Q4Params q, in
   static std::atomic<uint64_t> smem_raised{0};
   auto kern = paged_decode_q4_kernel<NT, HP, kScored>;
   if (!ensure_smem_limit(kern, Lay<NT, HP>::kAlloc, smem_raised)) return PA_ERR_CUDA;
-  // one wave of CTAs, as far as the workspace's partial rows (num_seqs * num_splits
-  // per query head, some of them for `info`) hold what the cut can leave: a
-  // piece behind every inner chunk boundary and a first piece for every
-  // sequence that crosses one
   int sms = num_sms_current_device();
   if (sms <= 0) sms = 148;
-  const int32_t heads = q.d.num_kv_heads;
-  int64_t chunks = static_cast<int64_t>(sms) * Lay<NT, HP>::kCtasPerSm / (heads / HP);
-  const int64_t seqs = q.num_seqs, rows = seqs * num_splits - (seqs + kD - 1) / kD;
-  q.whole = num_splits == 1;
-  if (q.whole) {
-    if (chunks > seqs) chunks = seqs;
-  } else if (chunks - 1 + (seqs < chunks - 1 ? seqs : chunks - 1) > rows) {
-    chunks = seqs < rows - seqs ? rows - seqs + 1 : rows / 2 + 1;
-  }
-  if (chunks > 32767) chunks = 32767;  // half of `info`'s word each
-  if (chunks < 1) chunks = 1;
-  q.slots = static_cast<int32_t>(chunks - 1 + (seqs < chunks - 1 ? seqs : chunks - 1));
-  q.info = reinterpret_cast<int32_t*>(q.d.ws_o + static_cast<int64_t>(heads) * q.slots * G * kD);
+  const int32_t heads = q.d.num_kv_heads, seqs = q.num_seqs;
+  const Launch l = launch_of(static_cast<int64_t>(sms) * Lay<NT, HP>::kCtasPerSm / (heads / HP),
+                             seqs, num_splits, heads, G);
+  const int32_t chunks = l.chunks;
+  q.whole = l.whole;
+  q.slots = l.slots;
+  q.info = reinterpret_cast<int32_t*>(q.d.ws_o + l.info_float);
   const dim3 grid(static_cast<unsigned>(heads / HP), static_cast<unsigned>(chunks));
   kern<<<grid, kThreads, Lay<NT, HP>::kAlloc, stream>>>(mk, mv, q, G);
   if (cudaGetLastError() != cudaSuccess) return PA_ERR_CUDA;
@@ -954,7 +926,7 @@ pa_status launch_q4(const CUtensorMap& mk, const CUtensorMap& mv, Q4Params q, in
   const dim3 merge_grid(static_cast<unsigned>(heads * G),
                         static_cast<unsigned>(seqs < 256 ? seqs : 256));
   return launch_dependent(merge_pieces_kernel<HP, kScored>, merge_grid, kMergeWarps * 32, stream, q,
-                          G, static_cast<int>(chunks));
+                          G, chunks);
 }
 
 }  // namespace
