@@ -594,7 +594,7 @@ pa_status pa_paged_decode_attention_scored(
  * sums_in [num_seqs, num_kv_heads, sums_len] fp32 contiguous; sums_out NULL,
  *   the same array, or another of the same shape that does not overlap it.
  * keep [num_seqs, num_kv_heads, budget] int32 contiguous; new_lens
- *   [num_seqs] int32, not context_lens itself (PA_ERR_INVALID).
+ *   [num_seqs] int32, sharing no word with context_lens (PA_ERR_INVALID).
  * budget >= 1; num_sink, num_recent >= 0, num_sink + num_recent <= budget
  *   (else PA_ERR_INVALID).  num_seqs * num_kv_heads of 2^27 or more, sums_len
  *   or budget above 2^30: PA_ERR_UNSUPPORTED.

@@ -673,8 +673,7 @@ pa_status check_select(int32_t* keep, int32_t* new_lens, float* sums_out, const 
       num_recent < 0 || static_cast<int64_t>(num_sink) + num_recent > budget)
     return PA_ERR_INVALID;
   if (num_seqs == 0) return PA_OK;
-  if (keep == nullptr || new_lens == nullptr || sums_in == nullptr || context_lens == nullptr ||
-      new_lens == context_lens)
+  if (keep == nullptr || new_lens == nullptr || sums_in == nullptr || context_lens == nullptr)
     return PA_ERR_INVALID;
   const int64_t rows = static_cast<int64_t>(num_seqs) * num_kv_heads;
   if (rows >= (1ll << 27) || sums_len > (1 << 30) || budget > (1 << 30))
@@ -684,6 +683,10 @@ pa_status check_select(int32_t* keep, int32_t* new_lens, float* sums_out, const 
     return PA_ERR_ALIGN;
   if (sums_out != nullptr &&
       partly_overlap(sums_out, sums_in, static_cast<uintptr_t>(rows) * sums_len * 4))
+    return PA_ERR_INVALID;
+  // a row's CTA writes new_lens while others still read context_lens
+  if (new_lens == context_lens ||
+      partly_overlap(new_lens, context_lens, static_cast<uintptr_t>(num_seqs) * 4))
     return PA_ERR_INVALID;
   a->keep = keep;
   a->new_lens = new_lens;
