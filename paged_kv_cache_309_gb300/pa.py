@@ -188,8 +188,11 @@ def _ptr(t):
 
 
 def _stream(stream):
-    if stream is None:  # (the raw handle: a Stream object costs 3 us)
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    if stream is None:  # the raw handle (a private call) where torch has it: a Stream object costs 3 us
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        if raw is None:
+            return torch.cuda.current_stream().cuda_stream
+        return raw(torch.cuda.current_device())
     if stream.device.index != torch.cuda.current_device():
         raise ValueError(f"stream belongs to {stream.device}, not the current device")
     return stream.cuda_stream
