@@ -562,7 +562,9 @@ pa_status pa_paged_decode_attention_q4(void *out, const void *q, const void *k_c
  *   decode workspace, then one fp32 score for each query head and token and
  *   a log-sum-exp for each query head); otherwise as for
  *   pa_paged_decode_attention (calls that share one agree on num_seqs and
- *   num_kv_heads, for the place of the split counters).  Two launches on
+ *   num_kv_heads, for the place of the split counters).  The size does not
+ *   grow evenly with max_context_len: a workspace for several bounds has the
+ *   largest of their sizes.  Two launches on
  *   `stream` (three over a 4-bit cache).  sums_len above 2^30: PA_ERR_UNSUPPORTED.
  * ---------------------------------------------------------------------- */
 size_t pa_paged_decode_scored_workspace_size(int32_t num_seqs, int32_t num_q_heads,

@@ -9,9 +9,10 @@
 // digit counts through distributed shared memory.  Given the block tables (kPaged),
 // tokens of dropped blocks get the lowest key of all and do not count as tokens: a
 // kept one would have no row to move, and the row at its new place, whatever it
-// holds, would be attended to.  (One CTA re-reading its row
-// for every digit: 222 us for 64 rows of 32K-128K, 27 us for 128 rows of 2.3K; so: 49 and 7.3,
-// bound by instruction issue, 0.68 of the cycles, not by the 21 MB read.)
+// holds, would be attended to (the look-ups: 59 us instead of 49 for 64 rows of 32K-128K).
+// (One CTA re-reading its row for every digit: 222 us for 64 rows of 32K-128K, 27 us for 128
+// rows of 2.3K; so: 49 and 7.3, bound by instruction issue, 0.68 of the cycles, not by the
+// 21 MB read.)
 //
 // Moving.  Row j of the kept list comes from token keep[j].  The places of a
 // chunk of rows are looked up once, a thread per row; then 16-byte units move,

@@ -702,7 +702,8 @@ def pa_paged_decode_attention_scored(out, sums_out, sums, num_new, q, k_cache, v
     """Decode attention (bf16, float8_e4m3fn with optional scales, or uint8
     4-bit caches) that also adds each token's attention weight, summed over a
     kv head's query heads: sums_out [B, H_KV, T] <- sums + weights, the last
-    num_new tokens of a sequence starting from 0.  sums_out may be sums.
+    num_new tokens of a sequence starting from 0.  sums_out may be sums.  While
+    the workspace's error word holds a wait timeout, no sum is written.
     workspace from decode_scored_workspace."""
     B, HQ, HKV, d, bs, nb = _decode_shapes(out, q, k_cache, v_cache, block_tables, context_lens,
                                            workspace)
