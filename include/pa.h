@@ -20,6 +20,11 @@
  *   pa_evict_select                which tokens of a row to keep, by those weights
  *   pa_evict_select_paged          the same where block tables may hold dropped blocks
  *   pa_cache_compact               move the kept rows together through block tables
+ *   pa_rope_and_cache              rotate queries and keys by position, append K/V to a
+ *                                  paged cache
+ *   pa_paged_window_decode_attention   decode attention with a sliding window and a few
+ *                                  first tokens that stay visible
+ *   pa_paged_window_prefill_attention  the same for prompts
  *
  * Common rules
  *   - Every pointer argument except the `*_host` ones is a DEVICE pointer on
@@ -661,6 +666,108 @@ pa_status pa_cache_compact(void *k_cache, void *v_cache, int32_t row_bytes, cons
                            const int32_t *dst_block_tables, int32_t dst_max_blocks,
                            int32_t num_seqs, int32_t num_kv_heads, int32_t block_size,
                            int64_t num_blocks, pa_stream_t stream);
+
+/* ========================================================================
+ * Sliding-window serving: rotation with the cache write, window attention
+ *
+ * No counterpart in the paper's pages: sglang's cache_ops.py has the second
+ * slot table of a sliding window (swa_slot_mapping), not the attention over
+ * it, and writes keys that were rotated before.
+ * ====================================================================== */
+
+/* ------------------------------------------------------------------------
+ * pa_rope_and_cache -- rotate queries and keys by position, append keys and
+ * values to the paged cache, in one launch.
+ *
+ * For every token t with p = positions[t], C_i = cos_sin[p, i] and
+ * S_i = cos_sin[p, rot_dim / 2 + i] (i < rot_dim / 2), a head's row x gives
+ *     interleaved 0:  pairs (x_i, x_{i + rot_dim / 2})
+ *     interleaved 1:  pairs (x_{2 i}, x_{2 i + 1})
+ *     (x, x') -> (x C_i - x' S_i, x' C_i + x S_i)
+ * and its elements from rot_dim on stay as they are.  Products and sums are
+ * fp32, each rounded.  Then
+ *     q_out[t, h]                               = cast(rotated q[t, h])
+ *     key_cache[slot], value_cache[slot], head h = cast(rotated key[t, h] /
+ *                                       k_scale), cast(value[t, h] / v_scale)
+ * with the slot from slot_mapping and swa_slot_mapping, the division, the
+ * casts and the skips of pa_reshape_and_cache (a token without a slot still
+ * has its queries rotated).  A token whose position lies outside
+ * [0, max_positions) is left out: no element of its rows is written.  Two
+ * tokens that resolve to one slot: the row may hold parts of both.
+ *
+ * q, q_out: [num_tokens, num_q_heads, head_size] of src_dtype; q_out may be q
+ *   (with the same stride), else it shares no element with q, key or value.
+ * key, value: [num_tokens, num_kv_heads, head_size] of src_dtype (PA_BF16,
+ *   PA_FP16 or PA_FP32).  *_stride: elements between tokens (a slice of a fused
+ *   projection's output); heads and elements contiguous.
+ * key_cache, value_cache: [num_blocks, block_size, num_kv_heads, head_size]
+ *   of cache_dtype (PA_BF16, PA_FP16, PA_FP32, PA_FP8_E4M3), block_stride
+ *   elements between blocks, the rest contiguous.
+ * cos_sin: [max_positions, rot_dim] fp32, contiguous.  positions,
+ *   slot_mapping: [num_tokens] int64; swa_slot_mapping: NULL or [swa_len] int64.
+ * head_size: a multiple of 8 up to 512; rot_dim: a multiple of 16 from 16 to
+ *   head_size.  num_tokens times the heads above 2^31: PA_ERR_UNSUPPORTED.
+ * Alignment: pointers 16 bytes (positions, slot tables 8); strides multiples of
+ *   8 elements.
+ * Errors: PA_ERR_INVALID, PA_ERR_UNSUPPORTED, PA_ERR_ALIGN, PA_ERR_CUDA.
+ * ---------------------------------------------------------------------- */
+pa_status pa_rope_and_cache(void *q_out, const void *q, const void *key, const void *value,
+                            pa_dtype src_dtype, int64_t num_tokens, int32_t num_q_heads,
+                            int32_t num_kv_heads, int32_t head_size, int64_t q_out_stride,
+                            int64_t q_stride, int64_t key_stride, int64_t value_stride,
+                            const float *cos_sin, const int64_t *positions, int64_t max_positions,
+                            int32_t rot_dim, int32_t interleaved, void *key_cache,
+                            void *value_cache, pa_dtype cache_dtype, int64_t num_blocks,
+                            int32_t block_size, int64_t block_stride, const int64_t *slot_mapping,
+                            const int64_t *swa_slot_mapping, int64_t swa_len, const float *k_scale,
+                            const float *v_scale, pa_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * pa_paged_window_decode_attention -- pa_paged_decode_attention where a
+ * sequence's query sees, of its L = context_lens[b] tokens, only
+ *     t >= L - window  or  t < num_sink
+ * (the last `window` tokens, its own among them, and the first num_sink).
+ * Rows of other tokens are not used, whatever they hold, and their blocks need
+ * not be there: a block id outside the pool drops its tokens as ever.
+ *
+ * window >= 1, num_sink >= 0 (else PA_ERR_INVALID).  cache_dtype PA_BF16
+ * (k_scale, v_scale NULL) or PA_FP8_E4M3 (both NULL: unit scales, or as in
+ * pa_paged_decode_attention_fp8).  max_context_len: a longer context is clipped to it
+ * (and to the table) and flagged PA_DEVERR_CONTEXT_CLIPPED.
+ * workspace: pa_paged_window_decode_workspace_size(...) bytes for the same
+ *   sizes, otherwise as for pa_paged_decode_attention (calls that share one
+ *   agree on num_seqs and num_kv_heads, for the place of the split counters).
+ * Other arguments, limits and errors as there.
+ * ---------------------------------------------------------------------- */
+size_t pa_paged_window_decode_workspace_size(int32_t num_seqs, int32_t num_q_heads,
+                                             int32_t num_kv_heads, int32_t head_size,
+                                             int32_t window, int32_t num_sink,
+                                             int32_t max_context_len);
+
+pa_status pa_paged_window_decode_attention(
+    void *out, const void *q, const void *k_cache, const void *v_cache, pa_dtype cache_dtype,
+    const float *k_scale, const float *v_scale, const int32_t *block_tables,
+    const int32_t *context_lens, int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads,
+    int32_t head_size, int32_t block_size, int32_t max_blocks_per_seq, int64_t num_blocks,
+    int32_t window, int32_t num_sink, float scale, int32_t max_context_len, void *workspace,
+    size_t workspace_bytes, pa_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * pa_paged_window_prefill_attention -- pa_paged_prefill_attention where the
+ * query at position p sees only tokens
+ *     t <= p  and  (t > p - window  or  t < num_sink)
+ * so that a prompt's row equals the window decode call's over the same tokens.
+ * Values of tokens that a row does not see do not reach it, whatever they hold.
+ * window >= 1, num_sink >= 0 (else PA_ERR_INVALID); bf16 caches.
+ * max_blocks_per_seq * block_size above 2^30: PA_ERR_UNSUPPORTED.  Other
+ * arguments, limits and errors as for pa_paged_prefill_attention.
+ * ---------------------------------------------------------------------- */
+pa_status pa_paged_window_prefill_attention(
+    void *out, const void *q, const void *k_cache, const void *v_cache, pa_dtype cache_dtype,
+    const int32_t *block_tables, const int32_t *cu_seqlens_q, const int32_t *context_lens,
+    int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_size,
+    int32_t block_size, int32_t max_blocks_per_seq, int64_t num_blocks, int32_t window,
+    int32_t num_sink, float scale, int32_t max_q_len, unsigned *error_word, pa_stream_t stream);
 
 /* Diagnostic of the failure path every pipeline kernel shares: launches one
  * CTA whose threads wait, with the same bounded wait the pipelines use, on a

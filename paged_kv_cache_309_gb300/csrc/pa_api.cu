@@ -4,6 +4,7 @@
 #include <cmath>
 
 #include "pa_internal.cuh"
+#include "rope_cache.cuh"
 
 namespace pa_detail {
 
@@ -88,6 +89,52 @@ pa_status check_decode(void* out, const void* q, const void* k_cache, const void
   a->v_scale = nullptr;
   a->plan = pa_detail::make_decode_plan(num_seqs, num_kv_heads, max_context_len,
                                         pa_detail::num_sms_current_device());
+  return PA_OK;
+}
+
+// Host-side checks shared by the prefill entry points; fills *a where there is work
+// (num_seqs and max_q_len above 0).
+pa_status check_prefill(void* out, const void* q, const void* k_cache, const void* v_cache,
+                        pa_dtype cache_dtype, const int32_t* block_tables,
+                        const int32_t* cu_seqlens_q, const int32_t* context_lens, int32_t num_seqs,
+                        int32_t num_q_heads, int32_t num_kv_heads, int32_t head_size,
+                        int32_t block_size, int32_t max_blocks_per_seq, int64_t num_blocks,
+                        float scale, int32_t max_q_len, unsigned* error_word,
+                        pa_detail::PrefillArgs* a) {
+  if (num_seqs < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || head_size <= 0 ||
+      block_size <= 0 || max_blocks_per_seq <= 0 || num_blocks <= 0 || max_q_len < 0)
+    return PA_ERR_INVALID;
+  if (num_seqs == 0 || max_q_len == 0) return PA_OK;
+  if (out == nullptr || q == nullptr || k_cache == nullptr || v_cache == nullptr ||
+      block_tables == nullptr || cu_seqlens_q == nullptr || context_lens == nullptr ||
+      error_word == nullptr)
+    return PA_ERR_INVALID;
+  if (num_q_heads % num_kv_heads != 0 || !std::isfinite(scale)) return PA_ERR_INVALID;
+  if (cache_dtype != PA_BF16 || head_size != 128) return PA_ERR_UNSUPPORTED;
+  const int32_t G = num_q_heads / num_kv_heads;
+  if (G != 1 && G != 2 && G != 4 && G != 8 && G != 16) return PA_ERR_UNSUPPORTED;
+  if (block_size < 8 || block_size > 256 || (block_size & (block_size - 1)) != 0)
+    return PA_ERR_UNSUPPORTED;
+  if (num_blocks * block_size >= (1ll << 31)) return PA_ERR_UNSUPPORTED;
+  if (!aligned(out, 16) || !aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) ||
+      !aligned(error_word, 4))
+    return PA_ERR_ALIGN;
+  a->out = out;
+  a->q = q;
+  a->k_cache = k_cache;
+  a->v_cache = v_cache;
+  a->block_tables = block_tables;
+  a->cu_seqlens_q = cu_seqlens_q;
+  a->context_lens = context_lens;
+  a->error_word = error_word;
+  a->num_seqs = num_seqs;
+  a->num_q_heads = num_q_heads;
+  a->num_kv_heads = num_kv_heads;
+  a->block_size = block_size;
+  a->max_blocks_per_seq = max_blocks_per_seq;
+  a->max_q_len = max_q_len;
+  a->num_blocks = num_blocks;
+  a->scale = scale;
   return PA_OK;
 }
 
@@ -401,41 +448,12 @@ pa_status pa_paged_prefill_attention(void* out, const void* q, const void* k_cac
                                      int32_t block_size, int32_t max_blocks_per_seq,
                                      int64_t num_blocks, float scale, int32_t max_q_len,
                                      unsigned* error_word, pa_stream_t stream) {
-  if (num_seqs < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || head_size <= 0 ||
-      block_size <= 0 || max_blocks_per_seq <= 0 || num_blocks <= 0 || max_q_len < 0)
-    return PA_ERR_INVALID;
-  if (num_seqs == 0 || max_q_len == 0) return PA_OK;
-  if (out == nullptr || q == nullptr || k_cache == nullptr || v_cache == nullptr ||
-      block_tables == nullptr || cu_seqlens_q == nullptr || context_lens == nullptr ||
-      error_word == nullptr)
-    return PA_ERR_INVALID;
-  if (num_q_heads % num_kv_heads != 0 || !std::isfinite(scale)) return PA_ERR_INVALID;
-  if (cache_dtype != PA_BF16 || head_size != 128) return PA_ERR_UNSUPPORTED;
-  const int32_t G = num_q_heads / num_kv_heads;
-  if (G != 1 && G != 2 && G != 4 && G != 8 && G != 16) return PA_ERR_UNSUPPORTED;
-  if (block_size < 8 || block_size > 256 || (block_size & (block_size - 1)) != 0)
-    return PA_ERR_UNSUPPORTED;
-  if (num_blocks * block_size >= (1ll << 31)) return PA_ERR_UNSUPPORTED;
-  if (!aligned(out, 16) || !aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) ||
-      !aligned(error_word, 4))
-    return PA_ERR_ALIGN;
   pa_detail::PrefillArgs a{};
-  a.out = out;
-  a.q = q;
-  a.k_cache = k_cache;
-  a.v_cache = v_cache;
-  a.block_tables = block_tables;
-  a.cu_seqlens_q = cu_seqlens_q;
-  a.context_lens = context_lens;
-  a.error_word = error_word;
-  a.num_seqs = num_seqs;
-  a.num_q_heads = num_q_heads;
-  a.num_kv_heads = num_kv_heads;
-  a.block_size = block_size;
-  a.max_blocks_per_seq = max_blocks_per_seq;
-  a.max_q_len = max_q_len;
-  a.num_blocks = num_blocks;
-  a.scale = scale;
+  const pa_status st = check_prefill(out, q, k_cache, v_cache, cache_dtype, block_tables,
+                                     cu_seqlens_q, context_lens, num_seqs, num_q_heads,
+                                     num_kv_heads, head_size, block_size, max_blocks_per_seq,
+                                     num_blocks, scale, max_q_len, error_word, &a);
+  if (st != PA_OK) return st;
   return pa_detail::launch_paged_prefill(a, reinterpret_cast<cudaStream_t>(stream));
 }
 
@@ -774,6 +792,151 @@ pa_status pa_cache_compact(void* k_cache, void* v_cache, int32_t row_bytes, cons
   a.row_units = row_bytes / 16;
   a.num_blocks = num_blocks;
   return pa_detail::launch_cache_compact(a, in_place, reinterpret_cast<cudaStream_t>(stream));
+}
+
+// ------------------------------------------------------- sliding window --
+pa_status pa_rope_and_cache(void* q_out, const void* q, const void* key, const void* value,
+                            pa_dtype src_dtype, int64_t num_tokens, int32_t num_q_heads,
+                            int32_t num_kv_heads, int32_t head_size, int64_t q_out_stride,
+                            int64_t q_stride, int64_t key_stride, int64_t value_stride,
+                            const float* cos_sin, const int64_t* positions, int64_t max_positions,
+                            int32_t rot_dim, int32_t interleaved, void* key_cache,
+                            void* value_cache, pa_dtype cache_dtype, int64_t num_blocks,
+                            int32_t block_size, int64_t block_stride, const int64_t* slot_mapping,
+                            const int64_t* swa_slot_mapping, int64_t swa_len, const float* k_scale,
+                            const float* v_scale, pa_stream_t stream) {
+  if (num_tokens < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || head_size <= 0 || rot_dim <= 0 ||
+      rot_dim > head_size || max_positions < 0 || block_size <= 0 || num_blocks < 0 ||
+      (interleaved != 0 && interleaved != 1))
+    return PA_ERR_INVALID;
+  if (num_tokens == 0) return PA_OK;  // nothing to do; pointers may be null
+  if (q_out == nullptr || q == nullptr || key == nullptr || value == nullptr ||
+      cos_sin == nullptr || positions == nullptr || key_cache == nullptr ||
+      value_cache == nullptr || slot_mapping == nullptr)
+    return PA_ERR_INVALID;
+  if ((k_scale == nullptr) != (v_scale == nullptr)) return PA_ERR_INVALID;
+  if (swa_slot_mapping != nullptr && swa_len < 0) return PA_ERR_INVALID;
+  if (!is_src_dtype(src_dtype) || !is_any_dtype(cache_dtype)) return PA_ERR_UNSUPPORTED;
+  if (head_size % 8 != 0 || head_size > 512 || rot_dim % 16 != 0) return PA_ERR_UNSUPPORTED;
+  const int64_t q_row = static_cast<int64_t>(num_q_heads) * head_size;
+  const int64_t row = static_cast<int64_t>(num_kv_heads) * head_size;
+  if (q_row + 2 * row >= (1ll << 31) || num_blocks >= (1ll << 62) / block_size)
+    return PA_ERR_UNSUPPORTED;
+  if (q_out_stride % 8 != 0 || q_stride % 8 != 0 || key_stride % 8 != 0 || value_stride % 8 != 0 ||
+      block_stride % 8 != 0)
+    return PA_ERR_ALIGN;
+  if (num_tokens > 1 && (q_out_stride < q_row || q_stride < q_row || key_stride < row ||
+                         value_stride < row || (q_out == q && q_out_stride != q_stride)))
+    return PA_ERR_INVALID;
+  if (num_blocks > 1 && block_stride < row * block_size) return PA_ERR_INVALID;
+  if (!aligned(q_out, 16) || !aligned(q, 16) || !aligned(key, 16) || !aligned(value, 16) ||
+      !aligned(cos_sin, 16) || !aligned(key_cache, 16) || !aligned(value_cache, 16) ||
+      !aligned(positions, 8) || !aligned(slot_mapping, 8) || !aligned(swa_slot_mapping, 8) ||
+      !aligned(k_scale, 4) || !aligned(v_scale, 4))
+    return PA_ERR_ALIGN;
+  pa_detail::RopeArgs a{};
+  a.q_out = q_out;
+  a.q = q;
+  a.key = key;
+  a.value = value;
+  a.key_cache = key_cache;
+  a.value_cache = value_cache;
+  a.cos_sin = cos_sin;
+  a.positions = positions;
+  a.slot_mapping = slot_mapping;
+  a.swa = swa_slot_mapping;
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
+  a.swa_len = swa_slot_mapping ? swa_len : 0;
+  a.num_tokens = num_tokens;
+  a.max_positions = max_positions;
+  a.num_slots = num_blocks * block_size;
+  a.q_out_stride = q_out_stride;
+  a.q_stride = q_stride;
+  a.key_stride = key_stride;
+  a.value_stride = value_stride;
+  a.block_stride = block_stride;
+  a.num_q_heads = num_q_heads;
+  a.num_kv_heads = num_kv_heads;
+  a.head_size = head_size;
+  a.rot_dim = rot_dim;
+  a.block_size = block_size;
+  return pa_detail::launch_rope_and_cache(a, src_dtype, cache_dtype, interleaved != 0,
+                                          reinterpret_cast<cudaStream_t>(stream));
+}
+
+// Windows and first tokens of 2^30 and more see every token, as 2^30 does (contexts
+// are at most 2^30).
+static int32_t window_cap(int32_t n) { return n < (1 << 30) ? n : 1 << 30; }
+
+size_t pa_paged_window_decode_workspace_size(int32_t num_seqs, int32_t num_q_heads,
+                                             int32_t num_kv_heads, int32_t head_size,
+                                             int32_t window, int32_t num_sink,
+                                             int32_t max_context_len) {
+  if (num_seqs < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || head_size <= 0 || window < 1 ||
+      num_sink < 0 || max_context_len < 0 || max_context_len > (1 << 30))
+    return 0;
+  const pa_detail::DecodePlan plan = pa_detail::make_window_plan(
+      num_seqs, num_kv_heads, window_cap(window), window_cap(num_sink), max_context_len,
+      pa_detail::num_sms_current_device());
+  return pa_detail::decode_workspace_bytes(num_seqs, num_q_heads, num_kv_heads, head_size, plan);
+}
+
+pa_status pa_paged_window_decode_attention(
+    void* out, const void* q, const void* k_cache, const void* v_cache, pa_dtype cache_dtype,
+    const float* k_scale, const float* v_scale, const int32_t* block_tables,
+    const int32_t* context_lens, int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads,
+    int32_t head_size, int32_t block_size, int32_t max_blocks_per_seq, int64_t num_blocks,
+    int32_t window, int32_t num_sink, float scale, int32_t max_context_len, void* workspace,
+    size_t workspace_bytes, pa_stream_t stream) {
+  if (window < 1 || num_sink < 0 || (k_scale == nullptr) != (v_scale == nullptr) ||
+      (k_scale != nullptr && cache_dtype != PA_FP8_E4M3))
+    return PA_ERR_INVALID;
+  pa_detail::DecodeArgs a{};
+  const pa_status st = check_decode(out, q, k_cache, v_cache, cache_dtype, block_tables,
+                                    context_lens, num_seqs, num_q_heads, num_kv_heads, head_size,
+                                    block_size, max_blocks_per_seq, num_blocks, scale,
+                                    max_context_len, &a);
+  if (st != PA_OK) return st;
+  if (!aligned(block_tables, 4) || !aligned(context_lens, 4) || !aligned(k_scale, 4) ||
+      !aligned(v_scale, 4))
+    return PA_ERR_ALIGN;
+  a.window = window_cap(window);
+  a.num_sink = window_cap(num_sink);
+  a.max_context_len = max_context_len;
+  a.plan = pa_detail::make_window_plan(num_seqs, num_kv_heads, a.window, a.num_sink,
+                                       max_context_len, pa_detail::num_sms_current_device());
+  const size_t need =
+      pa_detail::decode_workspace_bytes(num_seqs, num_q_heads, num_kv_heads, head_size, a.plan);
+  if (workspace == nullptr || workspace_bytes < need) return PA_ERR_WORKSPACE;
+  if (!aligned(workspace, 256)) return PA_ERR_ALIGN;
+  a.workspace = workspace;
+  a.error_word = nullptr;
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
+  return pa_detail::launch_paged_decode(a, reinterpret_cast<cudaStream_t>(stream));
+}
+
+pa_status pa_paged_window_prefill_attention(
+    void* out, const void* q, const void* k_cache, const void* v_cache, pa_dtype cache_dtype,
+    const int32_t* block_tables, const int32_t* cu_seqlens_q, const int32_t* context_lens,
+    int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_size,
+    int32_t block_size, int32_t max_blocks_per_seq, int64_t num_blocks, int32_t window,
+    int32_t num_sink, float scale, int32_t max_q_len, unsigned* error_word, pa_stream_t stream) {
+  if (window < 1 || num_sink < 0) return PA_ERR_INVALID;
+  pa_detail::PrefillArgs a{};
+  const pa_status st = check_prefill(out, q, k_cache, v_cache, cache_dtype, block_tables,
+                                     cu_seqlens_q, context_lens, num_seqs, num_q_heads,
+                                     num_kv_heads, head_size, block_size, max_blocks_per_seq,
+                                     num_blocks, scale, max_q_len, error_word, &a);
+  if (st != PA_OK || num_seqs == 0 || max_q_len == 0) return st;
+  if (static_cast<int64_t>(max_blocks_per_seq) * block_size > (1ll << 30))
+    return PA_ERR_UNSUPPORTED;
+  if (!aligned(block_tables, 4) || !aligned(cu_seqlens_q, 4) || !aligned(context_lens, 4))
+    return PA_ERR_ALIGN;
+  a.window = window_cap(window);
+  a.num_sink = window_cap(num_sink);
+  return pa_detail::launch_paged_prefill(a, reinterpret_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

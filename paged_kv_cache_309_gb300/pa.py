@@ -109,6 +109,17 @@ def _load():
     lib.pa_evict_select_paged.restype = E
     lib.pa_cache_compact.argtypes = [P, P, I32, P, P, I32, P, I32, P, I32, I32, I32, I32, I64, P]
     lib.pa_cache_compact.restype = E
+    lib.pa_rope_and_cache.argtypes = [P, P, P, P, E, I64, I32, I32, I32, I64, I64, I64, I64, P, P,
+                                      I64, I32, I32, P, P, E, I64, I32, I64, P, P, I64, P, P, P]
+    lib.pa_rope_and_cache.restype = E
+    lib.pa_paged_window_decode_workspace_size.argtypes = [I32] * 7
+    lib.pa_paged_window_decode_workspace_size.restype = SZ
+    lib.pa_paged_window_decode_attention.argtypes = [P, P, P, P, E, P, P, P, P, I32, I32, I32, I32,
+                                                     I32, I32, I64, I32, I32, F32, I32, P, SZ, P]
+    lib.pa_paged_window_decode_attention.restype = E
+    lib.pa_paged_window_prefill_attention.argtypes = [P, P, P, P, E, P, P, P, I32, I32, I32, I32,
+                                                      I32, I32, I64, I32, I32, F32, I32, P, P]
+    lib.pa_paged_window_prefill_attention.restype = E
     _lib = lib
     return lib
 
@@ -805,3 +816,132 @@ def pa_cache_compact(k_cache, v_cache, keep, keep_lens, src_block_tables, dst_bl
         _ptr(k_cache), _ptr(v_cache), row * k_cache.element_size(), _ptr(keep), _ptr(keep_lens),
         keep.shape[2], _ptr(src_block_tables), src_block_tables.shape[1], _ptr(dst_block_tables),
         dst_block_tables.shape[1], B, H, bs, nb, _stream(stream)), "pa_cache_compact")
+
+
+# --------------------------------------------------------- sliding window --
+def pa_rope_and_cache(q_out, q, key, value, key_cache, value_cache, cos_sin, positions,
+                      slot_mapping, interleaved=False, swa_slot_mapping=None, k_scale=None,
+                      v_scale=None, stream=None):
+    """q_out <- q [N, H_Q, d] rotated by position; key [N, H, d] rotated and
+    value [N, H, d] written to the caches [num_blocks, bs, H, d] (block stride
+    free) at slot_mapping [N] int64.  cos_sin [max_positions, rot_dim] float32
+    holds each position's cosines, then its sines; positions [N] int64; the
+    first rot_dim elements of a head turn, as pairs (i, i + rot_dim / 2) or,
+    interleaved, (2 i, 2 i + 1).  q, q_out, key and value share a dtype and have
+    free token strides; q_out may be q.  Optional swa table int64,
+    k_scale/v_scale one-element float32 device tensors."""
+    _on_device(q_out=q_out, q=q, key=key, value=value, key_cache=key_cache,
+               value_cache=value_cache, cos_sin=cos_sin, positions=positions,
+               slot_mapping=slot_mapping, swa_slot_mapping=swa_slot_mapping)
+    if k_scale is not None or v_scale is not None:
+        _scales(k_scale, v_scale)
+    N, HQ, d = q.shape
+    H = key.shape[1]
+    kind, shape = q.dtype, key.shape
+    for t, name in ((q_out, "q_out"), (q, "q"), (key, "key"), (value, "value")):
+        _, s1, s2 = t.stride()
+        if t.dtype != kind or s2 != 1 or (s1 != d and t.shape[1] != 1):
+            raise ValueError(f"{name} must share q's dtype, heads and elements contiguous")
+    if q_out.shape != q.shape or shape != (N, H, d) or value.shape != shape:
+        raise ValueError("q_out must match q; key and value must be [N, H, d]")
+    nb, bs, Hc, dc = key_cache.shape
+    strides = key_cache.stride()
+    if (Hc, dc) != (H, d) or strides[1:] != (H * d, d, 1):
+        raise ValueError("key_cache must be [num_blocks, bs, H, d], contiguous inside a block")
+    if value_cache.shape != key_cache.shape or value_cache.stride() != strides \
+            or value_cache.dtype != key_cache.dtype:
+        raise ValueError("value_cache must match key_cache")
+    if cos_sin.dtype != torch.float32 or cos_sin.dim() != 2 or not cos_sin.is_contiguous():
+        raise ValueError("cos_sin must be float32 [max_positions, rot_dim], contiguous")
+    for t, name in ((positions, "positions"), (slot_mapping, "slot_mapping")):
+        if t.dtype != torch.int64 or t.numel() != N or not t.is_contiguous():
+            raise ValueError(f"{name} must be int64 [N]")
+    swa_len = 0
+    if swa_slot_mapping is not None:
+        if swa_slot_mapping.dtype != torch.int64 or not swa_slot_mapping.is_contiguous():
+            raise ValueError("swa_slot_mapping must be int64, contiguous")
+        swa_len = swa_slot_mapping.numel()
+    st = _load().pa_rope_and_cache(
+        _ptr(q_out), _ptr(q), _ptr(key), _ptr(value), _dtype(q), N, HQ, H, d, q_out.stride(0),
+        q.stride(0), key.stride(0), value.stride(0), _ptr(cos_sin), _ptr(positions),
+        cos_sin.shape[0], _i32("rot_dim", cos_sin.shape[1]), int(bool(interleaved)), _ptr(key_cache),
+        _ptr(value_cache), _dtype(key_cache), nb, bs, strides[0], _ptr(slot_mapping),
+        _ptr(swa_slot_mapping), swa_len, _ptr(k_scale), _ptr(v_scale), _stream(stream))
+    _check(st, "pa_rope_and_cache")
+
+
+def pa_paged_window_decode_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_size, window,
+                                          num_sink, max_context_len):
+    window, num_sink = _i32("window", window), _i32("num_sink", num_sink)
+    return int(_load().pa_paged_window_decode_workspace_size(
+        num_seqs, num_q_heads, num_kv_heads, head_size, window, num_sink,
+        _i32("max_context_len", max_context_len)))
+
+
+def window_decode_workspace(num_seqs, num_q_heads, num_kv_heads, head_size, window, num_sink,
+                            max_context_len, device=None):
+    """A zeroed device workspace for pa_paged_window_decode_attention (allocated by torch)."""
+    n = pa_paged_window_decode_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_size,
+                                              window, num_sink, max_context_len)
+    return torch.zeros(max(n, 256), dtype=torch.uint8, device=device or "cuda")
+
+
+def pa_paged_window_decode_attention(out, q, k_cache, v_cache, block_tables, context_lens, window,
+                                     num_sink, scale, max_context_len, workspace, k_scale=None,
+                                     v_scale=None, stream=None):
+    """Decode attention (bf16 caches, or float8_e4m3fn with optional scales)
+    over each sequence's last `window` tokens and its first num_sink; other
+    arguments as for pa_paged_decode_attention, workspace from
+    window_decode_workspace."""
+    B, HQ, HKV, d, bs, nb = _decode_shapes(out, q, k_cache, v_cache, block_tables, context_lens,
+                                           workspace)
+    if k_scale is not None or v_scale is not None:
+        _scales(k_scale, v_scale)
+        if k_cache.dtype != torch.float8_e4m3fn:
+            raise ValueError("k_scale/v_scale apply to an e4m3 cache")
+    window, num_sink = _i32("window", window), _i32("num_sink", num_sink)
+    max_context_len = _i32("max_context_len", max_context_len)
+    dtype = PA_Q4 if k_cache.dtype == torch.uint8 else _dtype(k_cache)
+    st = _load().pa_paged_window_decode_attention(
+        _ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache), dtype, _ptr(k_scale), _ptr(v_scale),
+        _ptr(block_tables), _ptr(context_lens), B, HQ, HKV, d, bs, block_tables.shape[1], nb,
+        window, num_sink, float(scale), max_context_len, _ptr(workspace),
+        workspace.numel() * workspace.element_size(), _stream(stream))
+    _check(st, "pa_paged_window_decode_attention")
+
+
+def pa_paged_window_prefill_attention(out, q, k_cache, v_cache, block_tables, cu_seqlens_q,
+                                      context_lens, window, num_sink, scale, max_q_len,
+                                      error_word, stream=None):
+    """Causal varlen prefill where the query at position p sees tokens
+    t <= p with t > p - window or t < num_sink; other arguments as for
+    pa_paged_prefill_attention."""
+    _word(error_word, "error_word")
+    _on_device(out=out, q=q, k_cache=k_cache, v_cache=v_cache, block_tables=block_tables,
+               cu_seqlens_q=cu_seqlens_q, context_lens=context_lens)
+    if error_word is None:
+        raise ValueError("error_word is required")
+    T, HQ, d = q.shape
+    nb, bs, HKV, dc = k_cache.shape
+    B = context_lens.numel()
+    for t, name in ((q, "q"), (out, "out"), (k_cache, "k_cache"), (v_cache, "v_cache"),
+                    (block_tables, "block_tables"), (cu_seqlens_q, "cu_seqlens_q"),
+                    (context_lens, "context_lens")):
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+    if q.dtype != torch.bfloat16 or out.dtype != torch.bfloat16 or out.shape != q.shape:
+        raise ValueError("q and out must be bf16 [total_new, H_Q, d]")
+    if v_cache.dtype != k_cache.dtype or v_cache.shape != k_cache.shape or dc != d:
+        raise ValueError("v_cache must match k_cache, rows of d elements")
+    if cu_seqlens_q.dtype != torch.int32 or context_lens.dtype != torch.int32 \
+            or cu_seqlens_q.numel() != B + 1:
+        raise ValueError("cu_seqlens_q must be int32 [B + 1], context_lens int32 [B]")
+    if block_tables.dtype != torch.int32 or block_tables.dim() != 2 or block_tables.shape[0] != B:
+        raise ValueError("block_tables must be int32 [B, max_blocks_per_seq]")
+    window, num_sink = _i32("window", window), _i32("num_sink", num_sink)
+    st = _load().pa_paged_window_prefill_attention(
+        _ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache), _dtype(k_cache), _ptr(block_tables),
+        _ptr(cu_seqlens_q), _ptr(context_lens), B, HQ, HKV, d, bs, block_tables.shape[1], nb,
+        window, num_sink, float(scale), _i32("max_q_len", max_q_len), _ptr(error_word),
+        _stream(stream))
+    _check(st, "pa_paged_window_prefill_attention")
