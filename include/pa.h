@@ -735,9 +735,10 @@ pa_status pa_rope_and_cache(void *q_out, const void *q, const void *key, const v
  * pa_paged_decode_attention_fp8).  max_context_len: a longer context is clipped to it
  * (and to the table) and flagged PA_DEVERR_CONTEXT_CLIPPED.
  * workspace: pa_paged_window_decode_workspace_size(...) bytes for the same
- *   sizes, otherwise as for pa_paged_decode_attention (calls that share one
- *   agree on num_seqs and num_kv_heads, for the place of the split counters).
- * Other arguments, limits and errors as there.
+ *   sizes, 256-byte aligned; its first word is the error word, the rest need not be
+ *   zero.  Calls that share one must be ordered on one stream.
+ * One launch, or two where a sequence may be split over CTAs.  q values must be
+ *   finite over an e4m3 cache.  Other arguments, limits and errors as there.
  * ---------------------------------------------------------------------- */
 size_t pa_paged_window_decode_workspace_size(int32_t num_seqs, int32_t num_q_heads,
                                              int32_t num_kv_heads, int32_t head_size,
@@ -759,15 +760,20 @@ pa_status pa_paged_window_decode_attention(
  * so that a prompt's row equals the window decode call's over the same tokens.
  * Values of tokens that a row does not see do not reach it, whatever they hold.
  * window >= 1, num_sink >= 0 (else PA_ERR_INVALID); bf16 caches.
- * max_blocks_per_seq * block_size above 2^30: PA_ERR_UNSUPPORTED.  Other
- * arguments, limits and errors as for pa_paged_prefill_attention.
+ * total_tokens: rows of q and out; new tokens behind them, or past max_q_len of
+ *   their sequence, are not computed.  Rows of out that belong to no sequence are left as
+ *   they were.
+ * max_blocks_per_seq * block_size above 2^30, total_tokens of 2^31 or more:
+ *   PA_ERR_UNSUPPORTED.  Other arguments, limits and errors as for
+ *   pa_paged_prefill_attention.
  * ---------------------------------------------------------------------- */
 pa_status pa_paged_window_prefill_attention(
     void *out, const void *q, const void *k_cache, const void *v_cache, pa_dtype cache_dtype,
     const int32_t *block_tables, const int32_t *cu_seqlens_q, const int32_t *context_lens,
     int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_size,
     int32_t block_size, int32_t max_blocks_per_seq, int64_t num_blocks, int32_t window,
-    int32_t num_sink, float scale, int32_t max_q_len, unsigned *error_word, pa_stream_t stream);
+    int32_t num_sink, float scale, int32_t max_q_len, int64_t total_tokens, unsigned *error_word,
+    pa_stream_t stream);
 
 /* Diagnostic of the failure path every pipeline kernel shares: launches one
  * CTA whose threads wait, with the same bounded wait the pipelines use, on a

@@ -21,7 +21,8 @@ BUILD_DIR = os.path.join(HERE, "_build")
 LIB_PATH = os.path.join(HERE, "libpa.so")
 SOURCES = ["pa_api.cu", "cache_write.cu", "mla_concat.cu", "decode.cu", "mla_decode.cu",
            "mla_decode_tc.cu", "mla_proj.cu", "prefill_tc.cu", "cache_q4.cu", "decode_q4.cu",
-           "decode_scored.cu", "evict.cu", "rope_cache.cu"]
+           "decode_scored.cu", "evict.cu", "rope_cache.cu",
+           "decode_window.cu", "prefill_window.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -224,9 +224,8 @@ __device__ __forceinline__ void epilogue_tc(const DecodeParams& p, uint8_t* smem
                                             int warp, int lane, float out_scale);
 
 // NT: n-tiles of 8 query heads (G <= 8 -> 1, G = 16 -> 2); kFp8: e4m3 cache;
-// kScored: also store the scores and each query head's log2-sum-exp; kWindow: only
-// the rows of the window and the first tokens, as one range of places (WindowRange).
-template <int NT, bool kFp8, bool kScored, bool kWindow>
+// kScored: also store the scores and each query head's log2-sum-exp.
+template <int NT, bool kFp8, bool kScored>
 __global__ void __launch_bounds__(kThreads, (kFp8 && NT == 1) ? 4 : TcLayout<kFp8>::kCtasPerSm)
     paged_decode_split_tc_kernel(const __grid_constant__ CUtensorMap tm_k,
                                  const __grid_constant__ CUtensorMap tm_v, const DecodeParams p,
@@ -253,13 +252,7 @@ __global__ void __launch_bounds__(kThreads, (kFp8 && NT == 1) ? 4 : TcLayout<kFp
   const int hq0 = g * G;
 
   bool clipped;
-  int L = kWindow ? window_len(p, b, &clipped) : effective_len(p, b, &clipped);
-  const int log2_rpb = min(p.log2_bs, 6);  // rows of a copy: a block, or a tile of a longer one
-  WindowRange win;
-  if constexpr (kWindow) {
-    win = window_range(L, max(0, L - p.window), p.num_sink, log2_rpb);
-    L = win.len;  // from here on tokens are places of that range
-  }
+  const int L = effective_len(p, b, &clipped);
   if (clipped && split == 0 && g == 0 && threadIdx.x == 0) atomicOr(p.err, PA_DEVERR_CONTEXT_CLIPPED);
   const int tok_begin = split * p.tokens_per_split;
   const int tok_end = min(tok_begin + p.tokens_per_split, L);
@@ -297,7 +290,7 @@ __global__ void __launch_bounds__(kThreads, (kFp8 && NT == 1) ? 4 : TcLayout<kFp
 
   if (warp == kConsumerWarps) {
     // ------------------------------------------------------------ producer
-    const int rpb = 1 << log2_rpb;
+    const int rpb = bs < kTile ? bs : kTile;
     const int nbox = kTile / rpb;
     const uint64_t pol = l2_policy_evict_first();
     if (lane == 0) {
@@ -310,8 +303,8 @@ __global__ void __launch_bounds__(kThreads, (kFp8 && NT == 1) ? 4 : TcLayout<kFp
     // free stage, so their global-memory latency is off the issue path
     auto tile_bid = [&](int t) -> int {
       const int first = tok_begin + t * kTile + lane * rpb;
-      const int row = kWindow ? win.row(first) : first;
-      return (t < ntiles && lane < nbox && first < tok_end) ? __ldg(bt + (row >> p.log2_bs)) : -1;
+      return (t < ntiles && lane < nbox && first < tok_end) ? __ldg(bt + (first >> p.log2_bs))
+                                                            : -1;
     };
     int bid_next = tile_bid(0);
     bool ok = true;
@@ -330,19 +323,17 @@ __global__ void __launch_bounds__(kThreads, (kFp8 && NT == 1) ? 4 : TcLayout<kFp
       const int nval = min(kTile, tok_end - tok0);
       bool valid = false;
       int rows = 0, bid = -1, row0 = 0;
-      uint64_t seen = ~0ull;  // of the piece's rows, from bit 0 on
       if (lane < nbox) {
-        const int first = kWindow ? win.row(tok0 + lane * rpb) : tok0 + lane * rpb;
+        const int first = tok0 + lane * rpb;
         rows = min(rpb, nval - lane * rpb);
         if (rows > 0) {
           row0 = first & (bs - 1);
           bid = bid_cur;
           valid = bid >= 0 && static_cast<int64_t>(bid) < p.num_blocks;
-          if constexpr (kWindow) seen = win.visible(first, p.num_sink);
         }
       }
       uint64_t bits = 0;
-      if (valid) bits = ((rows >= 64 ? ~0ull : ((1ull << rows) - 1ull)) & seen) << (lane * rpb);
+      if (valid) bits = (rows >= 64 ? ~0ull : ((1ull << rows) - 1ull)) << (lane * rpb);
       const uint32_t lo = __reduce_or_sync(0xffffffffu, static_cast<uint32_t>(bits));
       const uint32_t hi = __reduce_or_sync(0xffffffffu, static_cast<uint32_t>(bits >> 32));
       const uint32_t vb = __ballot_sync(0xffffffffu, valid);
@@ -778,11 +769,11 @@ __device__ __forceinline__ void epilogue_tc(const DecodeParams& p, uint8_t* smem
   }
 }
 
-template <int NT, bool kFp8, bool kScored, bool kWindow = false>
+template <int NT, bool kFp8, bool kScored>
 pa_status launch_split_tc(const CUtensorMap& mk, const CUtensorMap& mv, const DecodeParams& p,
                           dim3 grid, int G, cudaStream_t stream) {
   static std::atomic<uint64_t> smem_raised{0};
-  auto kern = paged_decode_split_tc_kernel<NT, kFp8, kScored, kWindow>;
+  auto kern = paged_decode_split_tc_kernel<NT, kFp8, kScored>;
   constexpr int kSmem = TcLayout<kFp8>::kAlloc;
   if (!ensure_smem_limit(kern, kSmem, smem_raised)) return PA_ERR_CUDA;
   kern<<<grid, kThreads, kSmem, stream>>>(mk, mv, p, G);
@@ -907,16 +898,6 @@ DecodePlan make_decode_plan(int32_t num_seqs, int32_t num_kv_heads, int32_t max_
   return {static_cast<int32_t>(splits), static_cast<int32_t>(tiles_per_split * kTile)};
 }
 
-// A window of W rows and S first tokens touch at most W + S rows and what the two
-// pieces at their ends hold besides (pieces are at most a tile).
-DecodePlan make_window_plan(int32_t num_seqs, int32_t num_kv_heads, int32_t window,
-                            int32_t num_sink, int32_t max_context_len, int32_t num_sms) {
-  const int64_t most = static_cast<int64_t>(window) + num_sink + 2 * kTile;
-  return make_decode_plan(num_seqs, num_kv_heads,
-                          most < max_context_len ? static_cast<int32_t>(most) : max_context_len,
-                          num_sms);
-}
-
 namespace {
 size_t align256(size_t x) { return (x + 255) / 256 * 256; }
 }  // namespace
@@ -970,9 +951,6 @@ DecodeParams decode::make_decode_params(const DecodeArgs& a) {
   p.scores = a.scores;
   p.final_lse = a.final_lse;
   p.score_len = static_cast<int64_t>(a.plan.num_splits) * a.plan.tokens_per_split;
-  p.window = a.window;
-  p.num_sink = a.num_sink;
-  p.max_len = a.max_context_len;
   return p;
 }
 
@@ -995,13 +973,6 @@ pa_status launch_paged_decode(const DecodeArgs& a, cudaStream_t stream) {
   const dim3 grid(static_cast<unsigned>(a.num_kv_heads), static_cast<unsigned>(a.plan.num_splits),
                   static_cast<unsigned>(a.num_seqs));
   const bool scored = a.scores != nullptr;
-  if (a.window > 0) {
-    if (G == 16)
-      return fp8 ? launch_split_tc<2, true, false, true>(mk, mv, p, grid, G, stream)
-                 : launch_split_tc<2, false, false, true>(mk, mv, p, grid, G, stream);
-    return fp8 ? launch_split_tc<1, true, false, true>(mk, mv, p, grid, G, stream)
-               : launch_split_tc<1, false, false, true>(mk, mv, p, grid, G, stream);
-  }
   if (G == 16) {
     if (scored)
       return fp8 ? launch_split_tc<2, true, true>(mk, mv, p, grid, G, stream)

@@ -5,6 +5,7 @@
 
 #include "pa_internal.cuh"
 #include "rope_cache.cuh"
+#include "window.cuh"
 
 namespace pa_detail {
 
@@ -876,10 +877,9 @@ size_t pa_paged_window_decode_workspace_size(int32_t num_seqs, int32_t num_q_hea
   if (num_seqs < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || head_size <= 0 || window < 1 ||
       num_sink < 0 || max_context_len < 0 || max_context_len > (1 << 30))
     return 0;
-  const pa_detail::DecodePlan plan = pa_detail::make_window_plan(
-      num_seqs, num_kv_heads, window_cap(window), window_cap(num_sink), max_context_len,
-      pa_detail::num_sms_current_device());
-  return pa_detail::decode_workspace_bytes(num_seqs, num_q_heads, num_kv_heads, head_size, plan);
+  return pa_detail::window_decode_workspace_bytes(num_seqs, num_q_heads, num_kv_heads,
+                                                  window_cap(window), window_cap(num_sink),
+                                                  max_context_len);
 }
 
 pa_status pa_paged_window_decode_attention(
@@ -901,20 +901,19 @@ pa_status pa_paged_window_decode_attention(
   if (!aligned(block_tables, 4) || !aligned(context_lens, 4) || !aligned(k_scale, 4) ||
       !aligned(v_scale, 4))
     return PA_ERR_ALIGN;
-  a.window = window_cap(window);
-  a.num_sink = window_cap(num_sink);
-  a.max_context_len = max_context_len;
-  a.plan = pa_detail::make_window_plan(num_seqs, num_kv_heads, a.window, a.num_sink,
-                                       max_context_len, pa_detail::num_sms_current_device());
-  const size_t need =
-      pa_detail::decode_workspace_bytes(num_seqs, num_q_heads, num_kv_heads, head_size, a.plan);
-  if (workspace == nullptr || workspace_bytes < need) return PA_ERR_WORKSPACE;
+  const int32_t w = window_cap(window), sinks = window_cap(num_sink);
+  if (workspace == nullptr ||
+      workspace_bytes < pa_detail::window_decode_workspace_bytes(num_seqs, num_q_heads,
+                                                                 num_kv_heads, w, sinks,
+                                                                 max_context_len))
+    return PA_ERR_WORKSPACE;
   if (!aligned(workspace, 256)) return PA_ERR_ALIGN;
   a.workspace = workspace;
   a.error_word = nullptr;
   a.k_scale = k_scale;
   a.v_scale = v_scale;
-  return pa_detail::launch_paged_decode(a, reinterpret_cast<cudaStream_t>(stream));
+  return pa_detail::launch_window_decode(a, w, sinks, max_context_len,
+                                         reinterpret_cast<cudaStream_t>(stream));
 }
 
 pa_status pa_paged_window_prefill_attention(
@@ -922,21 +921,23 @@ pa_status pa_paged_window_prefill_attention(
     const int32_t* block_tables, const int32_t* cu_seqlens_q, const int32_t* context_lens,
     int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_size,
     int32_t block_size, int32_t max_blocks_per_seq, int64_t num_blocks, int32_t window,
-    int32_t num_sink, float scale, int32_t max_q_len, unsigned* error_word, pa_stream_t stream) {
-  if (window < 1 || num_sink < 0) return PA_ERR_INVALID;
+    int32_t num_sink, float scale, int32_t max_q_len, int64_t total_tokens, unsigned* error_word,
+    pa_stream_t stream) {
+  if (window < 1 || num_sink < 0 || total_tokens < 0) return PA_ERR_INVALID;
   pa_detail::PrefillArgs a{};
   const pa_status st = check_prefill(out, q, k_cache, v_cache, cache_dtype, block_tables,
                                      cu_seqlens_q, context_lens, num_seqs, num_q_heads,
                                      num_kv_heads, head_size, block_size, max_blocks_per_seq,
                                      num_blocks, scale, max_q_len, error_word, &a);
   if (st != PA_OK || num_seqs == 0 || max_q_len == 0) return st;
-  if (static_cast<int64_t>(max_blocks_per_seq) * block_size > (1ll << 30))
+  if (static_cast<int64_t>(max_blocks_per_seq) * block_size > (1ll << 30) ||
+      total_tokens >= (1ll << 31))
     return PA_ERR_UNSUPPORTED;
   if (!aligned(block_tables, 4) || !aligned(cu_seqlens_q, 4) || !aligned(context_lens, 4))
     return PA_ERR_ALIGN;
-  a.window = window_cap(window);
-  a.num_sink = window_cap(num_sink);
-  return pa_detail::launch_paged_prefill(a, reinterpret_cast<cudaStream_t>(stream));
+  return pa_detail::launch_window_prefill(
+      {a, total_tokens, window_cap(window), window_cap(num_sink)},
+      reinterpret_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

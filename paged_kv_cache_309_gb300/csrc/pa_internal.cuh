@@ -650,9 +650,6 @@ inline DecodePlan make_scored_plan(int32_t num_seqs, int32_t num_kv_heads,
                                    int32_t max_context_len, int32_t num_sms) {
   return make_decode_plan(num_seqs, num_kv_heads, max_context_len, num_sms, 8);
 }
-// The plan of the window call: the rows that a window may leave, as one range.
-DecodePlan make_window_plan(int32_t num_seqs, int32_t num_kv_heads, int32_t window,
-                            int32_t num_sink, int32_t max_context_len, int32_t num_sms);
 size_t decode_workspace_bytes(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads,
                               int32_t head_size, const DecodePlan& plan);
 
@@ -677,9 +674,6 @@ struct DecodeArgs {
   const int64_t* slot_mapping;
   float* scores;           // accumulated weights (else null): see DecodeParams
   float* final_lse;
-  int32_t window;          // sliding window (0: every token is visible), first tokens that stay
-  int32_t num_sink;        // visible, and the bound that lengths are clipped to
-  int32_t max_context_len;
 };
 // What the GQA decode kernels (decode.cu, decode_q4.cu, decode_scored.cu) share:
 // their parameters, the clipped context length and the stores of the scores.
@@ -726,11 +720,6 @@ struct DecodeParams {
   float* scores;
   float* final_lse;
   int64_t score_len;
-  // sliding window (kernels compiled for one): token t of L is visible where
-  // t >= L - window or t < num_sink; lengths are clipped to max_len
-  int32_t window;
-  int32_t num_sink;
-  int32_t max_len;
 };
 
 // context length the kernels use: clipped to the plan and the table
@@ -741,46 +730,6 @@ __device__ __forceinline__ int effective_len(const DecodeParams& p, int b, bool*
                           static_cast<int64_t>(p.num_splits) * p.tokens_per_split);
   *clipped = static_cast<int64_t>(L) > cap;
   return *clipped ? static_cast<int>(cap) : L;
-}
-
-// the same for a window, whose plan covers fewer rows than the context has: clipped to
-// the caller's bound and the table
-__device__ __forceinline__ int window_len(const DecodeParams& p, int b, bool* clipped) {
-  int L = __ldg(p.context_lens + b);
-  L = L < 0 ? 0 : L;
-  const int64_t cap = min(static_cast<int64_t>(p.max_blocks_per_seq) * p.block_size,
-                          static_cast<int64_t>(p.max_len));
-  *clipped = static_cast<int64_t>(L) > cap;
-  return *clipped ? static_cast<int>(cap) : L;
-}
-
-// The rows that a window leaves, as one range.  Pieces of `rpb` rows (part or all of a
-// block) that hold a first token come first, then those from the one that the
-// window starts in; the pieces between are left out, so places 0 .. len - 1 are rows
-// 0 .. cut - 1, then rows cut + skip and on.
-struct WindowRange {
-  int low;   // first row of the window
-  int cut;   // places below it are the rows of the same number
-  int skip;  // rows left out there
-  int len;   // places
-  __device__ __forceinline__ int row(int place) const { return place < cut ? place : place + skip; }
-  // which of the 64 rows from `first` on are visible
-  __device__ __forceinline__ uint64_t visible(int first, int num_sink) const {
-    return below(num_sink - first) | ~below(low - first);
-  }
-  static __device__ __forceinline__ uint64_t below(int n) {
-    return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1ull;
-  }
-};
-__device__ __forceinline__ WindowRange window_range(int len, int low, int num_sink, int log2_rpb) {
-  WindowRange r;
-  r.low = low;
-  const int sinks = min(num_sink, len);
-  const int first = (sinks + (1 << log2_rpb) - 1) >> log2_rpb;  // pieces with first tokens
-  r.cut = first << log2_rpb;
-  r.skip = max(0, (low >> log2_rpb) - first) << log2_rpb;
-  r.len = len - r.skip;
-  return r;
 }
 
 // Scores of one 16-token slice, from the accumulator layout of the score
@@ -854,8 +803,6 @@ struct PrefillArgs {
   int32_t num_seqs, num_q_heads, num_kv_heads, block_size, max_blocks_per_seq, max_q_len;
   int64_t num_blocks;
   float scale;
-  int32_t window;  // sliding window (0: every token up to the row's own is visible)
-  int32_t num_sink;
 };
 pa_status launch_paged_prefill(const PrefillArgs& a, cudaStream_t stream);  // prefill_tc.cu
 

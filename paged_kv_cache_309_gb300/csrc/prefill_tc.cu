@@ -45,8 +45,6 @@ namespace {
 
 using namespace pa;
 using namespace tc;
-using decode::WindowRange;
-using decode::window_range;
 
 constexpr int kD = 128;
 constexpr int kM = 128;                        // rows per query tile (tokens x heads)
@@ -98,13 +96,6 @@ struct PrefillTcParams {
   int32_t log2_bs;
   int32_t max_blocks_per_seq;
   float scale_log2;
-  // kernels compiled for a sliding window: its width, the first tokens that stay
-  // visible, and the caches as plain arrays
-  int32_t window;
-  int32_t num_sink;
-  int32_t num_kv_heads;
-  const __nv_bfloat16* k_cache;
-  const __nv_bfloat16* v_cache;
 };
 
 // bit c of a tile's 128-bit row mask
@@ -117,9 +108,7 @@ __device__ __forceinline__ bool mask_bit(uint64_t lo, uint64_t hi, int c) {
 // agree on the 128-bit row mask and lane 0 posts it; lane 0 posts the byte
 // count and each lane with a valid piece issues its two boxes (64 head
 // elements each).
-template <bool kWindow>
-__device__ __forceinline__ void issue_tile_half(const PrefillTcParams& p, const WindowRange& win,
-                                                const CUtensorMap* tm,
+__device__ __forceinline__ void issue_tile_half(const PrefillTcParams& p, const CUtensorMap* tm,
                                                 uint8_t* dst, uint64_t* full, uint64_t* mask_slot,
                                                 uint64_t* mask_bar, const int32_t* bt, int g,
                                                 int tok0, int kend, uint64_t pol, int lane) {
@@ -129,19 +118,13 @@ __device__ __forceinline__ void issue_tile_half(const PrefillTcParams& p, const 
   const int nval = min(kTile, kend - tok0);
   bool valid = false;
   int rows = 0, bid = -1, row0 = 0;
-  uint64_t seen_lo = ~0ull, seen_hi = ~0ull;  // of the tile's rows that lie in this piece
   if (lane < nbox) {
-    const int first = kWindow ? win.row(tok0 + lane * rpb) : tok0 + lane * rpb;
+    const int first = tok0 + lane * rpb;
     rows = min(rpb, nval - lane * rpb);
     if (rows > 0) {
       row0 = first & (bs - 1);
       bid = __ldg(bt + (first >> p.log2_bs));
       valid = bid >= 0 && static_cast<int64_t>(bid) < p.num_blocks;
-      if constexpr (kWindow) {
-        const int tile0 = first - lane * rpb;  // the row of place 0 if this piece's run began there
-        seen_lo = win.visible(tile0, p.num_sink);
-        seen_hi = win.visible(tile0 + 64, p.num_sink);
-      }
     }
   }
   // rows of this piece as bits of the 128-bit mask (a piece never straddles
@@ -153,10 +136,6 @@ __device__ __forceinline__ void issue_tile_half(const PrefillTcParams& p, const 
     const int r_hi = rows - r_lo;
     if (r_lo > 0) lo = (r_lo >= 64 ? ~0ull : ((1ull << r_lo) - 1ull)) << start;
     if (r_hi > 0) hi = (r_hi >= 64 ? ~0ull : ((1ull << r_hi) - 1ull)) << max(0, start - 64);
-    if constexpr (kWindow) {
-      lo &= seen_lo;
-      hi &= seen_hi;
-    }
   }
   const uint32_t w0 = __reduce_or_sync(0xffffffffu, static_cast<uint32_t>(lo));
   const uint32_t w1 = __reduce_or_sync(0xffffffffu, static_cast<uint32_t>(lo >> 32));
@@ -180,73 +159,6 @@ __device__ __forceinline__ void issue_tile_half(const PrefillTcParams& p, const 
   }
 }
 
-// One output row by plain loads, a warp to a row (lane: four head elements), over the
-// tokens that the row at position pos sees and no others.  A tile's product
-// multiplies the values of a token that one row sees and another does not by that
-// other row's weight 0, which is NaN for a value that is not finite; a row that
-// comes out NaN without a NaN among its scores is therefore made again here.
-__device__ __noinline__ void window_row_plain(const PrefillTcParams& p, int b, int g, int64_t qrow,
-                                              int pos, int lane) {
-  constexpr int kAhead = 8;
-  const int32_t* bt = p.block_tables + static_cast<int64_t>(b) * p.max_blocks_per_seq;
-  const uint2 qb = __ldg(reinterpret_cast<const uint2*>(p.q + qrow) + lane);
-  const float q[4] = {__uint_as_float(qb.x << 16), __uint_as_float(qb.x & 0xFFFF0000u),
-                      __uint_as_float(qb.y << 16), __uint_as_float(qb.y & 0xFFFF0000u)};
-  float m = -INFINITY, l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
-  const int low = max(0, pos - p.window + 1);
-  const int sinks = min(p.num_sink, low);
-  const int count = sinks + pos + 1 - low;  // visible tokens; j-th: j < sinks ? j : low + j - sinks
-  for (int j0 = 0; j0 < count; j0 += kAhead) {
-    uint2 kb[kAhead], vb[kAhead];
-    bool there[kAhead];
-#pragma unroll
-    for (int i = 0; i < kAhead; ++i) {
-      const int j = j0 + i;
-      const int t = j < sinks ? j : low + j - sinks;
-      const int bid = j < count ? __ldg(bt + (t >> p.log2_bs)) : -1;
-      there[i] = bid >= 0 && static_cast<int64_t>(bid) < p.num_blocks;
-      if (there[i]) {
-        const int64_t row =
-            (static_cast<int64_t>(bid) * p.block_size + (t & (p.block_size - 1))) * p.num_kv_heads + g;
-        kb[i] = __ldg(reinterpret_cast<const uint2*>(p.k_cache + row * kD) + lane);
-        vb[i] = __ldg(reinterpret_cast<const uint2*>(p.v_cache + row * kD) + lane);
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < kAhead; ++i) {
-      if (!there[i]) continue;  // the same in every lane
-      float s = q[0] * __uint_as_float(kb[i].x << 16) + q[1] * __uint_as_float(kb[i].x & 0xFFFF0000u) +
-                q[2] * __uint_as_float(kb[i].y << 16) + q[3] * __uint_as_float(kb[i].y & 0xFFFF0000u);
-#pragma unroll
-      for (int off = 16; off >= 1; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-      s *= p.scale_log2;
-      if (s > m) {
-        const float corr = exp2f(m - s);
-        l *= corr;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[e] *= corr;
-        m = s;
-      }
-      const float w = s == -INFINITY ? 0.f : exp2f(s - m);
-      l += w;
-      o[0] += w * __uint_as_float(vb[i].x << 16);
-      o[1] += w * __uint_as_float(vb[i].x & 0xFFFF0000u);
-      o[2] += w * __uint_as_float(vb[i].y << 16);
-      o[3] += w * __uint_as_float(vb[i].y & 0xFFFF0000u);
-    }
-  }
-  uint2 r = make_uint2(0u, 0u);
-  if (l != 0.f) {
-    const float inv = 1.f / l;
-    r = make_uint2(pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv));
-  }
-  reinterpret_cast<uint2*>(p.out + qrow)[lane] = r;
-}
-
-// kWindow: a row sees the last `window` tokens up to its own and the first num_sink;
-// the CTA's tiles run over the places of the rows that its first row's window and
-// the first tokens leave (WindowRange), and positions are places as well.
-template <bool kWindow>
 __global__ void __launch_bounds__(kThreads, 1)
     paged_prefill_tcgen05_kernel(const __grid_constant__ CUtensorMap tm_k,
                                  const __grid_constant__ CUtensorMap tm_v,
@@ -289,14 +201,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int qt0 = qpair * kQTiles * tpt;  // the CTA's first new token
   if (qt0 >= n) return;
   const int ntok = min(kQTiles * tpt, n - qt0);
-  int pos0 = L - n + qt0;           // position of the CTA's first token
-  int kend = min(L, pos0 + ntok);   // keys 0 .. kend-1 are needed
-  WindowRange win;
-  if constexpr (kWindow) {
-    win = window_range(max(kend, 0), max(0, pos0 - p.window + 1), p.num_sink, min(p.log2_bs, 7));
-    kend = win.len;
-    pos0 -= win.skip;
-  }
+  const int pos0 = L - n + qt0;           // position of the CTA's first token
+  const int kend = min(L, pos0 + ntok);   // keys 0 .. kend-1 are needed
   const int ntiles = kend > 0 ? (kend + kTile - 1) / kTile : 0;
 
   if (threadIdx.x == 0) {
@@ -358,7 +264,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         mbar_wait_bounded_long(&empty[st], ((t / nslots) - 1) & 1, abort_flag));
         if (!ok) break;
       }
-      issue_tile_half<kWindow>(p, win, tm, ring + st * 2 * kChunk, &full[st],
+      issue_tile_half(p, tm, ring + st * 2 * kChunk, &full[st],
                       is_k ? &tile_mask[2 * (t % kMaskSlots)] : nullptr,
                       is_k ? &mask_full[t % kMaskSlots] : nullptr, bt, g, t * kTile, kend, pol,
                       lane);
@@ -448,7 +354,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int tok = qi * tpt + row / G;  // the row's token among the CTA's
     const bool rvalid = tok < ntok;
     const int pos = pos0 + tok;
-    const int low = kWindow ? pos - p.window + 1 : 0;  // the row's window starts here
     const int64_t qrow =
         (static_cast<int64_t>(q0 + qt0 + (rvalid ? tok : 0)) * p.num_q_heads + g * G + row % G) *
         kD;
@@ -478,19 +383,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int c = 0; c < 64; ++c) s[c] *= p.scale_log2;
       }
       const int kc0 = t * kTile + 64 * h;
-      if constexpr (kWindow) {
-        // places up to the row's own, from its window's first on or of first tokens;
-        // places between the first tokens and the CTA's window are not in mw
-        if (kc0 + 63 > pos || (kc0 < low && kc0 + 64 > p.num_sink))
-          mw &= WindowRange::below(pos + 1 - kc0) &
-                (~WindowRange::below(low - kc0) | WindowRange::below(p.num_sink - kc0));
-        if (!rvalid) mw = 0ull;
-        if (mw != ~0ull) {
-#pragma unroll
-          for (int c = 0; c < 64; ++c)
-            if (!((mw >> c) & 1ull)) s[c] = -INFINITY;
-        }
-      } else if (!(rvalid && mw == ~0ull && kc0 + 63 <= pos)) {
+      if (!(rvalid && mw == ~0ull && kc0 + 63 <= pos)) {
 #pragma unroll
         for (int c = 0; c < 64; ++c)
           if (!(rvalid && ((mw >> c) & 1ull) && kc0 + c <= pos)) s[c] = -INFINITY;
@@ -637,15 +530,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ---- epilogue: this thread's output row
       tc_fence_after();
       const float inv = l_run > 0.f ? 1.f / l_run : 0.f;
-      bool nan_row = false;
 #pragma unroll 1
       for (int cq = 0; cq < kD / 32; ++cq) {
         float o[32];
         tc_ld32(o_addr + 32 * cq, o);  // warp-wide: every lane loads
-        if constexpr (kWindow) {
-#pragma unroll
-          for (int i = 0; i < 32; ++i) nan_row |= o[i] != o[i];
-        }
         if (rvalid) {
           uint4* dst = reinterpret_cast<uint4*>(p.out + qrow + 32 * cq);
 #pragma unroll
@@ -654,15 +542,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 pack_bf16x2(o[8 * u + 2] * inv, o[8 * u + 3] * inv),
                                 pack_bf16x2(o[8 * u + 4] * inv, o[8 * u + 5] * inv),
                                 pack_bf16x2(o[8 * u + 6] * inv, o[8 * u + 7] * inv));
-        }
-      }
-      if constexpr (kWindow) {
-        __syncwarp();  // the rows as stored above, before they are written again
-        unsigned again = __ballot_sync(0xffffffffu, nan_row && rvalid && l_run == l_run);
-        for (; again != 0u; again &= again - 1u) {
-          const int src = __ffs(again) - 1;
-          window_row_plain(p, b, g, __shfl_sync(0xffffffffu, qrow, src),
-                           __shfl_sync(0xffffffffu, pos, src) + win.skip, lane);
         }
       }
     }
@@ -719,18 +598,11 @@ pa_status launch_paged_prefill(const PrefillArgs& a, cudaStream_t stream) {
   const int64_t per_cta = static_cast<int64_t>(kQTiles) * p.tokens_per_tile;
   const int64_t qpairs = (static_cast<int64_t>(a.max_q_len) + per_cta - 1) / per_cta;
   if (qpairs > 0x7FFFFFFF) return PA_ERR_UNSUPPORTED;
-  p.window = a.window;
-  p.num_sink = a.num_sink;
-  p.num_kv_heads = a.num_kv_heads;
-  p.k_cache = static_cast<const __nv_bfloat16*>(a.k_cache);
-  p.v_cache = static_cast<const __nv_bfloat16*>(a.v_cache);
+  static std::atomic<uint64_t> smem_raised{0};
+  if (!ensure_smem_limit(paged_prefill_tcgen05_kernel, kAlloc, smem_raised)) return PA_ERR_CUDA;
   const dim3 grid(static_cast<unsigned>(qpairs), static_cast<unsigned>(a.num_kv_heads),
                   static_cast<unsigned>(a.num_seqs));
-  static std::atomic<uint64_t> smem_raised[2];
-  const bool w = a.window > 0;
-  const auto kernel = w ? paged_prefill_tcgen05_kernel<true> : paged_prefill_tcgen05_kernel<false>;
-  if (!ensure_smem_limit(kernel, kAlloc, smem_raised[w])) return PA_ERR_CUDA;
-  kernel<<<grid, kThreads, kAlloc, stream>>>(mk, mv, p);
+  paged_prefill_tcgen05_kernel<<<grid, kThreads, kAlloc, stream>>>(mk, mv, p);
   return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 

@@ -1,0 +1,811 @@
+// prefill_window.cu -- causal varlen prefill attention over the paged cache with a
+// sliding window and a few first tokens that stay visible (tcgen05, accumulators in
+// tensor memory).
+//
+// What is computed: new token j of sequence b sits at position p = L_b - n_b + j
+// and attends to tokens t <= p with t > p - window or t < num_sink; query head h
+// uses kv head h / G.  fp32 online softmax in base 2, weights rounded to bf16 for
+// the second product.
+//
+// An item is two query tiles of 128 rows (128 / G consecutive new tokens x the G
+// query heads of one kv head each) of one sequence; they share every key and value
+// tile.  Its tiles run over the places (window.cuh) of the rows that the first tokens and
+// its first row's window leave.  Windows make items short (a window of 250: three tiles), so
+// CTAs stay: one per SM walks items c, c + grid, ... of all sequences, and while an item's last
+// tiles are weighed and its rows written, the next one's queries, keys and values
+// land and its first score products run.
+//  * TMEM (512 columns): outputs O0, O1 and score tiles S0, S1 of 128 each; tile i's
+//    weights (bf16 pairs) overwrite the upper half of S_i.
+//  * warp 0 loads keys (3 slots) and posts each tile's row mask, warp 2 values (2
+//    slots), warp 3 the query tiles; all by TMA, 128-byte swizzled.
+//  * one thread of warp 1 issues every product: ..., O_i += P_i(t) V(t), S_i(t + 1) =
+//    Q_i K(t + 1)^T, then the other query tile's.  Products of one thread
+//    run in order, so S_i(t + 1) may overwrite P_i(t) without a wait between them.
+//  * warps 4-7 and 8-11 do the softmax of query tiles 0 and 1, one thread per row; a row's
+//    128 scores are held in registers (role warps give theirs up).
+// Every wait is bounded (2 s); a timeout sets an error bit, drains what was issued and
+// frees TMEM before the CTA exits.
+#include <atomic>
+
+#include "tc_ops.cuh"
+#include "window.cuh"
+
+namespace pa_detail {
+namespace {
+
+using namespace pa;
+using namespace tc;
+
+constexpr int kD = 128;
+constexpr int kM = 128;    // rows per query tile (tokens x heads)
+constexpr int kTile = 128; // keys per tile
+constexpr int kKSlots = 3;
+constexpr int kVSlots = 2;
+constexpr int kThreads = 12 * 32;              // 4 role warps + 2 x 4 softmax warps
+constexpr int kChunk = 128 * 128;              // 64 elements of 128 rows: 16 KB
+constexpr int kQOff = 0;                       // query tile i: two chunks
+constexpr int kKOff = 2 * 2 * kChunk;          // key slots: two chunks each
+constexpr int kVOff = kKOff + kKSlots * 2 * kChunk;
+constexpr int kBarOff = kVOff + kVSlots * 2 * kChunk;
+// Mask slot u % 8 is written again for tile u + 8, whose keys need S(u + 5), which is
+// issued after P.V(u + 4), which needs both softmax groups past tile u.
+constexpr int kMaskSlots = 8;
+// q_full, q_empty, s_full, p_full, o_final, o_empty [2] each, k_full, k_empty,
+// v_full, v_empty, mask_full, drain
+constexpr int kNumBars = 6 * 2 + 2 * kKSlots + 2 * kVSlots + kMaskSlots + 1;
+constexpr int kMaskOff = kBarOff + (kNumBars + 1) / 2 * 16;  // two 64-bit words per slot
+constexpr int kMiscOff = kMaskOff + kMaskSlots * 16;
+constexpr int kBytes = kMiscOff + 16;
+constexpr int kAlloc = kBytes + 1024;
+static_assert(kAlloc <= 227 * 1024, "shared memory");
+// Registers: 384 threads are launched with 168 each; 128 role threads keep 96, 256
+// softmax threads get 200 (63488 of the 64512 launched).
+constexpr int kRoleRegs = 96;
+constexpr int kSoftmaxRegs = 200;
+static_assert(128 * kRoleRegs + 256 * kSoftmaxRegs <= kThreads * 168, "registers");
+
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kOCol = 0;      // [0, 256): outputs O0, O1
+constexpr uint32_t kSCol = 256;    // [256, 512): score tiles S0, S1
+constexpr uint32_t kPHalf = 64;    // weights of tile i at kSCol + 128 i + 64
+constexpr uint32_t kIdescS = instr_desc(kM, kTile, false);
+constexpr uint32_t kIdescPV = instr_desc(kM, kD, true);
+constexpr float kRescaleLog2 = 8.0f;
+
+struct Params {
+  __nv_bfloat16* out;
+  const __nv_bfloat16* q;
+  const __nv_bfloat16* k_cache;
+  const __nv_bfloat16* v_cache;
+  const int32_t* block_tables;
+  const int32_t* cu_seqlens_q;
+  const int32_t* context_lens;
+  unsigned* err;
+  int64_t num_blocks;
+  int32_t num_seqs;
+  int32_t total_tokens;
+  int32_t max_q_len;
+  int32_t num_q_heads;
+  int32_t num_kv_heads;
+  int32_t group;
+  int32_t tokens_per_tile;  // kM / group
+  int32_t block_size;
+  int32_t log2_bs;
+  int32_t max_blocks_per_seq;
+  int32_t window;
+  int32_t num_sink;
+  float scale_log2;
+};
+
+// ------------------------------------------------------------------ items --
+struct Item {
+  int b, g;      // sequence, kv head
+  int q_row;     // the item's first row of q
+  int ntok;      // its new tokens
+  int ntiles;    // key tiles (0: no row has a key)
+  int nq;        // query tiles with a row
+  int pos0;      // place of its first token
+  WindowRange win;
+};
+
+// A warp's walk over items first, first + step, ...: items lie sequence by sequence, in a
+// sequence the latest tokens first, kv heads fastest.  Lane l holds sequence
+// chunk + l of the 32 in hand.
+struct Walk {
+  int next, base;  // next item; items before the chunk
+  int chunk;
+  int q0, n, avail, len;  // this lane's sequence: first row, new tokens, those with a row
+  int incl;               // items of the chunk up to and with this lane's
+  __device__ __forceinline__ void load(const Params& p, int lane) {
+    const int b = chunk + lane;
+    q0 = n = avail = len = 0;
+    if (b < p.num_seqs) {
+      q0 = __ldg(p.cu_seqlens_q + b);
+      n = max(__ldg(p.cu_seqlens_q + b + 1) - q0, 0);
+      len = max(__ldg(p.context_lens + b), 0);
+      // (rows outside the array, and tokens past max_q_len, are not there)
+      if (q0 >= 0) avail = max(min(min(n, p.max_q_len), p.total_tokens - q0), 0);
+    }
+    const int per = 2 * p.tokens_per_tile;
+    incl = (avail + per - 1) / per * p.num_kv_heads;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, incl, off);
+      if (lane >= off) incl += y;
+    }
+  }
+  __device__ __forceinline__ Walk(const Params& p, int first, int lane)
+      : next(first), base(0), chunk(0) {
+    load(p, lane);
+  }
+  __device__ __forceinline__ bool get(const Params& p, int step, int lane, Item& it) {
+    for (;;) {
+      const int all = __shfl_sync(0xffffffffu, incl, 31);
+      if (next < base + all) break;
+      base += all;
+      chunk += 32;
+      if (chunk >= p.num_seqs) return false;
+      load(p, lane);
+    }
+    const int at = next - base;
+    next += step;
+    const int l = __ffs(__ballot_sync(0xffffffffu, at < incl)) - 1;
+    const int before = l == 0 ? 0 : __shfl_sync(0xffffffffu, incl, l - 1);
+    const int end = __shfl_sync(0xffffffffu, incl, l);
+    it.b = chunk + l;
+    const int row0 = __shfl_sync(0xffffffffu, q0, l);
+    const int count = __shfl_sync(0xffffffffu, n, l);
+    const int rows = __shfl_sync(0xffffffffu, avail, l);
+    int L = __shfl_sync(0xffffffffu, len, l);
+    const int j = (end - 1 - at) / p.num_kv_heads;  // the item's pair of query tiles
+    it.g = (at - before) % p.num_kv_heads;
+    const int cap = p.max_blocks_per_seq * p.block_size;
+    if (L > cap) {
+      if (j == 0 && it.g == 0 && lane == 0) atomicOr(p.err, PA_DEVERR_CONTEXT_CLIPPED);
+      L = cap;
+    }
+    const int first = 2 * j * p.tokens_per_tile;  // of the sequence's new tokens
+    it.q_row = row0 + first;
+    it.ntok = min(2 * p.tokens_per_tile, rows - first);
+    it.nq = it.ntok > p.tokens_per_tile ? 2 : 1;
+    it.pos0 = L - count + first;
+    const int kend = max(0, min(L, it.pos0 + it.ntok));
+    it.win = window_range(kend, max(0, it.pos0 - p.window + 1), p.num_sink, min(p.log2_bs, 7));
+    it.pos0 -= it.win.skip;
+    it.ntiles = (it.win.len + kTile - 1) / kTile;
+    return true;
+  }
+};
+
+// ------------------------------------------------------------------ loads --
+// The keys or values of one tile: lane i < nbox looks up block piece i; for the
+// keys (mask_slot given) the lanes agree on the 128-bit row mask and lane 0 posts
+// it; lane 0 posts the byte count and each lane with a valid piece issues its
+// two boxes (64 head elements each).
+__device__ __forceinline__ void issue_tile(const Params& p, const Item& it, const CUtensorMap* tm,
+                                           uint8_t* dst, uint64_t* full, uint64_t* mask_slot,
+                                           uint64_t* mask_bar, int place0, uint64_t pol, int lane) {
+  const int bs = p.block_size;
+  const int rpb = bs < kTile ? bs : kTile;
+  const int nbox = kTile / rpb;
+  const int start = lane * rpb;  // of the tile's places
+  int rows = 0, bid = -1, row0 = 0;
+  bool valid = false;
+  uint64_t lo = 0, hi = 0;  // the piece's visible rows as bits of the tile
+  if (lane < nbox) {
+    const int first = it.win.row(place0 + start);
+    rows = min(rpb, it.win.len - place0 - start);
+    if (rows > 0) {
+      row0 = first & (bs - 1);
+      bid = __ldg(p.block_tables + static_cast<int64_t>(it.b) * p.max_blocks_per_seq +
+                  (first >> p.log2_bs));
+      valid = bid >= 0 && static_cast<int64_t>(bid) < p.num_blocks;
+    }
+    if (valid) {
+      const int tile0 = first - start;  // the row of bit 0, if this piece's run began there
+      lo = WindowRange::below(start + rows) & ~WindowRange::below(start) &
+           it.win.visible(tile0, p.num_sink);
+      hi = WindowRange::below(start + rows - 64) & ~WindowRange::below(start - 64) &
+           it.win.visible(tile0 + 64, p.num_sink);
+    }
+  }
+  const uint32_t vb = __ballot_sync(0xffffffffu, valid);
+  if (mask_slot != nullptr) {
+    const uint32_t w0 = __reduce_or_sync(0xffffffffu, static_cast<uint32_t>(lo));
+    const uint32_t w1 = __reduce_or_sync(0xffffffffu, static_cast<uint32_t>(lo >> 32));
+    const uint32_t w2 = __reduce_or_sync(0xffffffffu, static_cast<uint32_t>(hi));
+    const uint32_t w3 = __reduce_or_sync(0xffffffffu, static_cast<uint32_t>(hi >> 32));
+    if (lane == 0) {
+      mask_slot[0] = (static_cast<uint64_t>(w1) << 32) | w0;
+      mask_slot[1] = (static_cast<uint64_t>(w3) << 32) | w2;
+      mbar_arrive(mask_bar);
+    }
+  }
+  if (lane == 0) mbar_arrive_expect_tx(full, static_cast<uint32_t>(__popc(vb) * rpb * 128 * 2));
+  __syncwarp();
+  if (valid) {
+    const int32_t row = bid * bs + row0;
+    uint8_t* st = dst + start * 128;
+    tma_load_3d(st, tm, 0, it.g, row, full, pol);
+    tma_load_3d(st + kChunk, tm, 64, it.g, row, full, pol);
+  }
+}
+
+// One output row by plain loads, a warp to a row (lane: four head elements), over the
+// tokens that the row at position pos sees and no others.  A tile's product
+// multiplies the values of a token that one row sees and another does not by that
+// other row's weight 0, which is NaN for a value that is not finite; a row that
+// comes out NaN without a NaN among its scores is therefore made again here.  Until then
+// its first word is kAgain, a pair of NaN codes that no conversion gives.
+constexpr uint32_t kAgain = 0xFFA5FFA5u;
+__device__ __noinline__ void row_by_plain_loads(const Params& p, int b, int g, int64_t qrow,
+                                                int pos, int lane) {
+  constexpr int kAhead = 8;
+  const int32_t* bt = p.block_tables + static_cast<int64_t>(b) * p.max_blocks_per_seq;
+  const uint2 qb = __ldg(reinterpret_cast<const uint2*>(p.q + qrow) + lane);
+  const float q[4] = {__uint_as_float(qb.x << 16), __uint_as_float(qb.x & 0xFFFF0000u),
+                      __uint_as_float(qb.y << 16), __uint_as_float(qb.y & 0xFFFF0000u)};
+  float m = -INFINITY, l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
+  const int low = max(0, pos - p.window + 1);
+  const int sinks = min(p.num_sink, low);
+  const int count = sinks + pos + 1 - low;  // visible tokens; j-th: j < sinks ? j : low + j - sinks
+  for (int j0 = 0; j0 < count; j0 += kAhead) {
+    uint2 kb[kAhead], vb[kAhead];
+    bool there[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int j = j0 + i;
+      const int t = j < sinks ? j : low + j - sinks;
+      const int bid = j < count ? __ldg(bt + (t >> p.log2_bs)) : -1;
+      there[i] = bid >= 0 && static_cast<int64_t>(bid) < p.num_blocks;
+      if (there[i]) {
+        const int64_t row =
+            (static_cast<int64_t>(bid) * p.block_size + (t & (p.block_size - 1))) * p.num_kv_heads +
+            g;
+        kb[i] = __ldg(reinterpret_cast<const uint2*>(p.k_cache + row * kD) + lane);
+        vb[i] = __ldg(reinterpret_cast<const uint2*>(p.v_cache + row * kD) + lane);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      if (!there[i]) continue;  // the same in every lane
+      float s =
+          q[0] * __uint_as_float(kb[i].x << 16) + q[1] * __uint_as_float(kb[i].x & 0xFFFF0000u) +
+          q[2] * __uint_as_float(kb[i].y << 16) + q[3] * __uint_as_float(kb[i].y & 0xFFFF0000u);
+#pragma unroll
+      for (int off = 16; off >= 1; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
+      s *= p.scale_log2;
+      if (s > m) {
+        const float corr = exp2f(m - s);
+        l *= corr;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[e] *= corr;
+        m = s;
+      }
+      const float w = s == -INFINITY ? 0.f : exp2f(s - m);
+      l += w;
+      o[0] += w * __uint_as_float(vb[i].x << 16);
+      o[1] += w * __uint_as_float(vb[i].x & 0xFFFF0000u);
+      o[2] += w * __uint_as_float(vb[i].y << 16);
+      o[3] += w * __uint_as_float(vb[i].y & 0xFFFF0000u);
+    }
+  }
+  uint2 r = make_uint2(0u, 0u);
+  if (l != 0.f) {
+    const float inv = 1.f / l;
+    r = make_uint2(pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv));
+  }
+  reinterpret_cast<uint2*>(p.out + qrow)[lane] = r;
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+    window_prefill_kernel(const __grid_constant__ CUtensorMap tm_q,
+                          const __grid_constant__ CUtensorMap tm_k,
+                          const __grid_constant__ CUtensorMap tm_v, const Params p) {
+  extern __shared__ __align__(128) uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kBarOff);
+  uint64_t* q_full = bars;                    // [2] query tile i landed
+  uint64_t* q_empty = bars + 2;               // [2] its last score product done (commit)
+  uint64_t* s_full = bars + 4;                // [2] S_i in TMEM (commit)
+  uint64_t* p_full = bars + 6;                // [2] weights of tile i in TMEM (128 threads)
+  uint64_t* o_final = bars + 8;               // [2] the item's products into O_i done (commit)
+  uint64_t* o_empty = bars + 10;              // [2] O_i read (128 threads)
+  uint64_t* k_full = bars + 12;               // [kKSlots]
+  uint64_t* k_empty = k_full + kKSlots;       // [kKSlots] the slot's score products done
+  uint64_t* v_full = k_empty + kKSlots;       // [kVSlots]
+  uint64_t* v_empty = v_full + kVSlots;       // [kVSlots] the slot's output products done
+  uint64_t* mask_full = v_empty + kVSlots;    // [kMaskSlots] row mask posted
+  uint64_t* drain = mask_full + kMaskSlots;   // every product done
+  uint64_t* tile_mask = reinterpret_cast<uint64_t*>(smem + kMaskOff);  // [kMaskSlots][2]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kMiscOff);
+  int* flags = reinterpret_cast<int*>(smem + kMiscOff + 8);
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int step = gridDim.x;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&q_full[i], 1);
+      mbar_init(&q_empty[i], 1);
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_full[i], kM);
+      mbar_init(&o_final[i], 1);
+      mbar_init(&o_empty[i], kM);
+    }
+    for (int s = 0; s < kKSlots; ++s) {
+      mbar_init(&k_full[s], 1);
+      mbar_init(&k_empty[s], 1);
+    }
+    for (int s = 0; s < kVSlots; ++s) {
+      mbar_init(&v_full[s], 1);
+      mbar_init(&v_empty[s], 1);
+    }
+    for (int s = 0; s < kMaskSlots; ++s) mbar_init(&mask_full[s], 1);
+    mbar_init(drain, 1);
+    flags[0] = flags[1] = 0;
+    mbar_init_fence();
+  }
+  if (warp == 1) {  // this warp owns the CTA's tensor memory
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_u32(tmem_slot)),
+                 "r"(kTmemCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  volatile int* abort_flag = flags;
+  uint32_t issued = 0;  // (loading warps) loads requested
+
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRoleRegs));
+    Walk walk(p, blockIdx.x, lane);
+    Item it;
+    bool ok = true;
+    if (warp == 0 || warp == 2) {
+      // ------------------------------------------------ keys (0), values (2)
+      const bool is_k = warp == 0;
+      const CUtensorMap* tm = is_k ? &tm_k : &tm_v;
+      const uint32_t nslots = is_k ? kKSlots : kVSlots;
+      uint64_t* empty = is_k ? k_empty : v_empty;
+      uint64_t* full = is_k ? k_full : v_full;
+      uint8_t* ring = smem + (is_k ? kKOff : kVOff);
+      const uint64_t pol = l2_policy_evict_normal();
+      if (lane == 0) prefetch_tensormap(tm);
+      while (ok && walk.get(p, step, lane, it)) {
+        for (int t = 0; t < it.ntiles; ++t) {
+          const uint32_t st = issued % nslots;
+          if (issued >= nslots) {
+            ok = __all_sync(0xffffffffu, mbar_wait_bounded_long(
+                                             &empty[st], ((issued / nslots) - 1) & 1, abort_flag));
+            if (!ok) break;
+          }
+          const uint32_t ms = issued % kMaskSlots;
+          issue_tile(p, it, tm, ring + st * 2 * kChunk, &full[st],
+                     is_k ? &tile_mask[2 * ms] : nullptr, is_k ? &mask_full[ms] : nullptr,
+                     t * kTile, pol, lane);
+          ++issued;
+        }
+      }
+    } else if (warp == 3) {
+      // ------------------------------------------------------------- queries
+      const uint64_t pol = l2_policy_evict_first();
+      if (lane == 0) prefetch_tensormap(&tm_q);
+      uint32_t count[2] = {0, 0};
+      while (ok && walk.get(p, step, lane, it)) {
+        if (it.ntiles == 0) continue;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          if (i >= it.nq) break;
+          if (count[i] > 0) {
+            ok = __all_sync(0xffffffffu, mbar_wait_bounded_long(&q_empty[i], (count[i] - 1) & 1,
+                                                                abort_flag));
+            if (!ok) break;
+          }
+          if (lane == 0) {
+            uint8_t* dst = smem + kQOff + i * 2 * kChunk;
+            const int32_t row = it.q_row + i * p.tokens_per_tile;
+            mbar_arrive_expect_tx(&q_full[i], 2 * kChunk);
+            tma_load_3d(dst, &tm_q, 0, it.g * p.group, row, &q_full[i], pol);
+            tma_load_3d(dst + kChunk, &tm_q, 64, it.g * p.group, row, &q_full[i], pol);
+          }
+          ++count[i];
+        }
+      }
+      // the last copies are waited for before this warp ends, whoever gave up
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        if (count[i] > 0) mbar_wait_bounded_long(&q_full[i], (count[i] - 1) & 1, nullptr);
+    } else {
+      // ------------------------------------------------------------ products
+      const uint32_t q_base = smem_u32(smem + kQOff);
+      const uint32_t k_base = smem_u32(smem + kKOff);
+      const uint32_t v_base = smem_u32(smem + kVOff);
+      uint32_t u = 0;                       // tiles whose output products are issued
+      uint32_t items[2] = {0, 0};           // items whose first score product is issued
+      auto wait = [&](uint64_t* bar, uint32_t n) {
+        if (ok) ok = mbar_wait_bounded_long(bar, n & 1, abort_flag);
+      };
+      // S_i of tile n of the CTA: 8 k-steps of 16 over the 128 head elements, both
+      // operands K-major 128-byte swizzled (a k-step in a chunk is 32 bytes on)
+      auto score = [&](int i, uint32_t n, bool first, bool last) {
+        if (first) wait(&q_full[i], items[i]++);
+        wait(&k_full[n % kKSlots], n / kKSlots);
+        if (!__all_sync(0xffffffffu, ok)) ok = false;
+        if (ok && lane == 0) {
+          tc_fence_after();
+          const uint32_t qb = q_base + i * 2 * kChunk;
+          const uint32_t kb = k_base + (n % kKSlots) * 2 * kChunk;
+#pragma unroll
+          for (int j = 0; j < kD / 16; ++j)
+            tc_mma_ss(tmem + kSCol + kTile * i,
+                      smem_desc(qb + (j >> 2) * kChunk + 32 * (j & 3), 16, 1024),
+                      smem_desc(kb + (j >> 2) * kChunk + 32 * (j & 3), 16, 1024), kIdescS,
+                      j > 0 ? 1u : 0u);
+          tc_commit(&s_full[i]);
+          if (last) tc_commit(&q_empty[i]);
+        }
+      };
+      // key tiles (0: no item is left) and query tiles of the next item
+      auto next_item = [&](int& nq) -> int {
+        while (walk.get(p, step, lane, it)) {
+          if (it.ntiles > 0) {
+            nq = it.nq;
+            return it.ntiles;
+          }
+        }
+        return 0;
+      };
+      int nq = 0;
+      int ntiles = next_item(nq);
+      if (ntiles > 0) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          if (i < nq) score(i, 0, true, ntiles == 1);
+        if (ok && lane == 0) tc_commit(&k_empty[0]);
+      }
+      uint32_t weighed[2] = {0, 0};  // output products issued per query tile
+      uint32_t done[2] = {0, 0};     // items finished per query tile
+      while (ok && ntiles > 0) {
+        int nxt_nq = 0;
+        const int nxt_ntiles = next_item(nxt_nq);
+        for (int t = 0; ok && t < ntiles; ++t, ++u) {
+          const bool last = t + 1 == ntiles;
+          // the next tile's query tiles: this item's, or those of the next one (or none)
+          const int next_nq = last ? nxt_nq : nq;
+          const bool next_last = last ? nxt_ntiles == 1 : t + 2 == ntiles;
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            if (i < nq) {
+              if (i == 0) wait(&v_full[u % kVSlots], u / kVSlots);
+              wait(&p_full[i], weighed[i]++);
+              if (t == 0 && done[i] > 0) wait(&o_empty[i], done[i] - 1);
+              if (!__all_sync(0xffffffffu, ok)) ok = false;
+              if (ok && lane == 0) {
+                tc_fence_after();
+                // O_i += P_i V: 8 k-steps of 16 keys; P_i from TMEM (bf16 pairs, 8 columns
+                // per k-step), V MN-major (leading offset: next 64 elements = next chunk;
+                // stride offset: next 8 keys = 1 KB)
+                const uint32_t pc = tmem + kSCol + kTile * i + kPHalf;
+                const uint32_t vb = v_base + (u % kVSlots) * 2 * kChunk;
+#pragma unroll
+                for (int kk = 0; kk < kTile / 16; ++kk)
+                  tc_mma_ts(tmem + kOCol + kD * i, pc + 8 * kk,
+                            smem_desc(vb + kk * 2048, kChunk, 1024), kIdescPV,
+                            (t > 0 || kk > 0) ? 1u : 0u);
+                if (last) tc_commit(&o_final[i]);
+                if (i + 1 == nq) tc_commit(&v_empty[u % kVSlots]);
+              }
+              if (last) ++done[i];
+            }
+            if (i < next_nq) score(i, u + 1, last, next_last);
+          }
+          if (ok && next_nq > 0 && lane == 0) tc_commit(&k_empty[(u + 1) % kKSlots]);
+        }
+        ntiles = nxt_ntiles;
+        nq = nxt_nq;
+      }
+      if (lane == 0) {
+        tc_commit(drain);
+        mbar_wait_bounded(drain, 0, nullptr);
+      }
+      __syncwarp();
+    }
+    if (!__all_sync(0xffffffffu, ok) && lane == 0) {
+      *abort_flag = 1;
+      atomicOr(p.err, PA_DEVERR_WAIT_TIMEOUT);
+    }
+  } else {
+    // --------------------------------------------------------------- softmax
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+    const int qi = (warp - 4) >> 2;
+    const int quad = warp & 3;
+    const int row = 32 * quad + lane;  // = TMEM lane
+    const uint32_t lane_addr = static_cast<uint32_t>(32 * quad) << 16;
+    const uint32_t s_addr = tmem + lane_addr + kSCol + kTile * qi;
+    const uint32_t o_addr = tmem + lane_addr + kOCol + kD * qi;
+    const int G = p.group;
+    const int tok = qi * p.tokens_per_tile + row / G;  // the row's token among the item's
+    const bool pos_scale = p.scale_log2 > 0.f;
+    const float sc = pos_scale ? p.scale_log2 : 1.f;
+    Walk walk(p, blockIdx.x, lane);
+    Item it;
+    uint32_t u = 0, mine = 0, done = 0;  // tiles of the CTA, of this query tile; its items
+    bool ok = true;
+    while (ok && walk.get(p, step, lane, it)) {
+      if (qi >= it.nq) {
+        u += it.ntiles;
+        continue;
+      }
+      const bool rvalid = tok < it.ntok;
+      const int pos = it.pos0 + tok;
+      const int low = pos - p.window + 1;  // the row's window starts here
+      const int64_t qrow = (static_cast<int64_t>(it.q_row + (rvalid ? tok : 0)) * p.num_q_heads +
+                            it.g * G + row % G) *
+                           kD;
+      float m_run = -INFINITY, l_run = 0.f;
+      for (int t = 0; t < it.ntiles; ++t, ++u, ++mine) {
+        ok = mbar_wait_bounded(&s_full[qi], mine & 1, abort_flag) &&
+             mbar_wait_bounded(&mask_full[u % kMaskSlots], (u / kMaskSlots) & 1, abort_flag);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        const uint64_t mlo = tile_mask[2 * (u % kMaskSlots)];
+        const uint64_t mhi = tile_mask[2 * (u % kMaskSlots) + 1];
+        tc_fence_after();
+        float s[kTile];
+#pragma unroll
+        for (int c = 0; c < kTile; c += 32) tc_ld32_nowait(s_addr + c, &s[c]);
+        tc_wait_ld();
+        if (!pos_scale) {
+#pragma unroll
+          for (int c = 0; c < kTile; ++c) s[c] *= p.scale_log2;
+        }
+        // places up to the row's own, from its window's first on or of first tokens
+        // (places between the first tokens and the item's window are not in the mask)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int k0 = t * kTile + 64 * h;
+          uint64_t mw = h == 0 ? mlo : mhi;
+          if (k0 + 63 > pos || (k0 < low && k0 + 64 > p.num_sink))
+            mw &= WindowRange::below(pos + 1 - k0) &
+                  (~WindowRange::below(low - k0) | WindowRange::below(p.num_sink - k0));
+          if (!rvalid) mw = 0ull;
+          if (mw != ~0ull) {
+            const uint32_t w[2] = {static_cast<uint32_t>(mw), static_cast<uint32_t>(mw >> 32)};
+#pragma unroll
+            for (int c = 0; c < 64; ++c)
+              if (!((w[c >> 5] >> (c & 31)) & 1u)) s[64 * h + c] = -INFINITY;
+          }
+        }
+        float mq[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int c = 0; c < kTile; c += 8) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) mq[i] = fmax3(mq[i], s[c + 2 * i], s[c + 2 * i + 1]);
+        }
+        const float mx_raw = fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3]));
+        const float mx = pos_scale ? mx_raw * p.scale_log2 : mx_raw;
+        // lazy rescale; tcgen05.ld/st are warp-wide, so the warp rescales together when any
+        // of its rows needs it (the others by 1).  P.V_i(t - 1) came before S_i(t): done.
+        const bool need = mx > m_run + kRescaleLog2;
+        if (__any_sync(0xffffffffu, need)) {
+          const float corr = need ? fast_exp2(m_run - mx) : 1.f;
+          if (t > 0) {
+#pragma unroll 1
+            for (int c = 0; c < kD; c += 32) {
+              float o[32];
+              tc_ld32(o_addr + c, o);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] *= corr;
+              tc_st32u_nowait(o_addr + c, reinterpret_cast<const uint32_t*>(&o[0]));
+            }
+            tc_wait_st();
+          }
+          if (need) {
+            l_run *= corr;
+            m_run = mx;
+          }
+        }
+        // weights 2^(s * scale - m) as bf16 pairs: the A operand of P.V_i, keys 2j, 2j + 1
+        // in column 64 + j.  A masked score is -inf and 2^-inf = +0 (m is taken as 0
+        // while the row has seen no key, so no -inf + inf)
+        const float2 sc2 = make_float2(sc, sc);
+        const float mneg = m_run == -INFINITY ? 0.f : -m_run;
+        const float2 mn2 = make_float2(mneg, mneg);
+        float lsum = 0.f;
+#pragma unroll
+        for (int h = 1; h >= 0; --h) {  // (sums in the order of the call without a window)
+          float2 lq[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+          uint32_t pr[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            const float2 x = ffma2(make_float2(s[64 * h + 2 * i], s[64 * h + 2 * i + 1]), sc2, mn2);
+            const float2 e = make_float2(fast_exp2(x.x), fast_exp2(x.y));
+            lq[i & 1] = fadd2(lq[i & 1], e);
+            pr[i] = pack_bf16x2(e.x, e.y);
+          }
+          tc_st32u_nowait(s_addr + kPHalf + 32 * h, pr);
+          lsum += (lq[0].x + lq[0].y) + (lq[1].x + lq[1].y);
+        }
+        l_run += lsum;
+        tc_wait_st();
+        // keys without a cache row: zero their value rows (0 x NaN would poison P.V), by
+        // query tile 0's threads (P.V_1(t) follows P.V_0(t)); piece j = (key j / 2,
+        // value chunk j % 2), two per thread
+        if (qi == 0 && (mlo != ~0ull || mhi != ~0ull)) {
+          ok = __all_sync(0xffffffffu, mbar_wait_bounded(&v_full[u % kVSlots],
+                                                         (u / kVSlots) & 1, abort_flag));
+          if (!ok) break;
+#pragma unroll
+          for (int hh = 0; hh < 2; ++hh) {
+            const int j = row + kM * hh;
+            const int r = j >> 1;
+            if (!((r < 64 ? mlo >> r : mhi >> (r - 64)) & 1ull)) {
+              uint4* dst = reinterpret_cast<uint4*>(smem + kVOff + (u % kVSlots) * 2 * kChunk +
+                                                    (j & 1) * kChunk + r * 128);
+#pragma unroll
+              for (int i = 0; i < 8; ++i) dst[i] = make_uint4(0u, 0u, 0u, 0u);
+            }
+          }
+          fence_proxy_async_smem();  // generic writes before the tensor core reads them
+        }
+        tc_fence_before();
+        mbar_arrive(&p_full[qi]);
+      }
+      if (!ok) break;
+      if (it.ntiles == 0) {
+        if (rvalid) {  // no key at all: a zero row
+          uint4* dst = reinterpret_cast<uint4*>(p.out + qrow);
+#pragma unroll
+          for (int c = 0; c < kD / 8; ++c) dst[c] = make_uint4(0u, 0u, 0u, 0u);
+        }
+        continue;
+      }
+      // ---- the item's end: this thread's output row
+      ok = __all_sync(0xffffffffu, mbar_wait_bounded(&o_final[qi], done & 1, abort_flag));
+      if (!ok) break;
+      ++done;
+      tc_fence_after();
+      const float inv = l_run > 0.f ? 1.f / l_run : 0.f;
+      bool nan_row = false;
+      float o[kD];
+#pragma unroll
+      for (int c = 0; c < kD; c += 32) tc_ld32_nowait(o_addr + c, &o[c]);
+      tc_wait_ld();
+      tc_fence_before();
+      mbar_arrive(&o_empty[qi]);
+#pragma unroll
+      for (int c = 0; c < kD; ++c) nan_row |= o[c] != o[c];
+      if (rvalid) {
+        uint4* dst = reinterpret_cast<uint4*>(p.out + qrow);
+#pragma unroll
+        for (int c = 0; c < kD / 8; ++c)
+          dst[c] = make_uint4(pack_bf16x2(o[8 * c] * inv, o[8 * c + 1] * inv),
+                              pack_bf16x2(o[8 * c + 2] * inv, o[8 * c + 3] * inv),
+                              pack_bf16x2(o[8 * c + 4] * inv, o[8 * c + 5] * inv),
+                              pack_bf16x2(o[8 * c + 6] * inv, o[8 * c + 7] * inv));
+      }
+      if (nan_row && rvalid && l_run == l_run) {
+        *reinterpret_cast<uint32_t*>(p.out + qrow) = kAgain;
+        flags[1] = 1;
+      }
+    }
+    // rows marked kAgain (by their own thread) are made again, off the loop above
+    __syncwarp();
+    if (ok && *(volatile int*)&flags[1] != 0) {
+      Walk over(p, blockIdx.x, lane);
+      while (over.get(p, step, lane, it)) {
+        if (tok >= it.ntok || it.ntiles == 0) it.ntok = 0;
+        const int64_t qrow =
+            (static_cast<int64_t>(it.q_row + tok) * p.num_q_heads + it.g * G + row % G) * kD;
+        unsigned again = __ballot_sync(
+            0xffffffffu,
+            it.ntok > 0 && *reinterpret_cast<const volatile uint32_t*>(p.out + qrow) == kAgain);
+        for (; again != 0u; again &= again - 1u) {
+          const int src = __ffs(again) - 1;
+          row_by_plain_loads(p, it.b, it.g, __shfl_sync(0xffffffffu, qrow, src),
+                             __shfl_sync(0xffffffffu, it.pos0 + tok, src) + it.win.skip, lane);
+        }
+      }
+    }
+    if (!ok && lane == 0) {
+      *abort_flag = 1;
+      atomicOr(p.err, PA_DEVERR_WAIT_TIMEOUT);
+    }
+  }
+
+  // ---- end: drain on error, free TMEM
+  tc_fence_before();
+  __syncthreads();
+  if (*abort_flag) {
+    if ((warp == 0 || warp == 2) && lane == 0) {
+      uint64_t* full = warp == 0 ? k_full : v_full;
+      const uint32_t nslots = warp == 0 ? kKSlots : kVSlots;
+      for (uint32_t t = issued > nslots ? issued - nslots : 0; t < issued; ++t)
+        mbar_wait_bounded(&full[t % nslots], (t / nslots) & 1, nullptr);
+    }
+    __syncthreads();
+  }
+  if (warp == 1) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
+                 "r"(kTmemCols)
+                 : "memory");
+  }
+}
+
+// [T, H_Q, 128] bf16; box = 64 elements x G heads x 128 / G tokens: the 128 rows of a
+// query tile, tokens slowest
+bool make_q_map(CUtensorMap* map, const void* base, int64_t tokens, int32_t heads, int32_t group) {
+  auto enc = encode_fn();
+  if (enc == nullptr) return false;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(kD), static_cast<cuuint64_t>(heads),
+                              static_cast<cuuint64_t>(tokens)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(kD) * 2,
+                                 static_cast<cuuint64_t>(kD) * 2 * heads};
+  const cuuint32_t box[3] = {64u, static_cast<cuuint32_t>(group),
+                             static_cast<cuuint32_t>(kM / group)};
+  const cuuint32_t es[3] = {1u, 1u, 1u};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box,
+             es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace
+
+pa_status launch_window_prefill(const WindowPrefillArgs& w, cudaStream_t stream) {
+  const PrefillArgs& a = w.p;
+  if (a.num_seqs == 0 || a.max_q_len == 0 || w.total_tokens == 0) return PA_OK;
+  const int32_t G = a.num_q_heads / a.num_kv_heads;
+  const int64_t rows = a.num_blocks * a.block_size;
+  const int32_t box_rows = a.block_size < kTile ? a.block_size : kTile;
+  CUtensorMap mq, mk, mv;
+  if (!make_q_map(&mq, a.q, w.total_tokens, a.num_q_heads, G) ||
+      !make_kv_map_swizzled(&mk, a.k_cache, rows, a.num_kv_heads, box_rows) ||
+      !make_kv_map_swizzled(&mv, a.v_cache, rows, a.num_kv_heads, box_rows))
+    return PA_ERR_CUDA;
+  Params p;
+  p.out = static_cast<__nv_bfloat16*>(a.out);
+  p.q = static_cast<const __nv_bfloat16*>(a.q);
+  p.k_cache = static_cast<const __nv_bfloat16*>(a.k_cache);
+  p.v_cache = static_cast<const __nv_bfloat16*>(a.v_cache);
+  p.block_tables = a.block_tables;
+  p.cu_seqlens_q = a.cu_seqlens_q;
+  p.context_lens = a.context_lens;
+  p.err = a.error_word;
+  p.num_blocks = a.num_blocks;
+  p.num_seqs = a.num_seqs;
+  p.total_tokens = static_cast<int32_t>(w.total_tokens);
+  p.max_q_len = a.max_q_len;
+  p.num_q_heads = a.num_q_heads;
+  p.num_kv_heads = a.num_kv_heads;
+  p.group = G;
+  p.tokens_per_tile = kM / G;
+  p.block_size = a.block_size;
+  p.log2_bs = 0;
+  while ((1 << p.log2_bs) < a.block_size) ++p.log2_bs;
+  p.max_blocks_per_seq = a.max_blocks_per_seq;
+  p.window = w.window;
+  p.num_sink = w.num_sink;
+  p.scale_log2 = a.scale * 1.4426950408889634f;
+  static std::atomic<uint64_t> smem_raised{0};
+  if (!ensure_smem_limit(window_prefill_kernel, kAlloc, smem_raised)) return PA_ERR_CUDA;
+  // one CTA per SM, no more than there can be items
+  int64_t grid = num_sms_current_device();
+  if (grid <= 0) grid = 148;
+  const int64_t per = 2 * p.tokens_per_tile;
+  const int64_t longest = a.max_q_len < w.total_tokens ? a.max_q_len : w.total_tokens;
+  const int64_t most = (longest + per - 1) / per * a.num_seqs;
+  if (most < grid && most * a.num_kv_heads < grid) grid = most * a.num_kv_heads;
+  // items are counted in 32 bits
+  if ((w.total_tokens / per + a.num_seqs + 1) * a.num_kv_heads >= (1ll << 31) - grid)
+    return PA_ERR_UNSUPPORTED;
+  window_prefill_kernel<<<static_cast<unsigned>(grid), kThreads, kAlloc, stream>>>(mq, mk, mv, p);
+  return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+}  // namespace pa_detail

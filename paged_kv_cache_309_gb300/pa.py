@@ -118,7 +118,7 @@ def _load():
                                                      I32, I32, I64, I32, I32, F32, I32, P, SZ, P]
     lib.pa_paged_window_decode_attention.restype = E
     lib.pa_paged_window_prefill_attention.argtypes = [P, P, P, P, E, P, P, P, I32, I32, I32, I32,
-                                                      I32, I32, I64, I32, I32, F32, I32, P, P]
+                                                      I32, I32, I64, I32, I32, F32, I32, I64, P, P]
     lib.pa_paged_window_prefill_attention.restype = E
     _lib = lib
     return lib
@@ -942,6 +942,6 @@ def pa_paged_window_prefill_attention(out, q, k_cache, v_cache, block_tables, cu
     st = _load().pa_paged_window_prefill_attention(
         _ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache), _dtype(k_cache), _ptr(block_tables),
         _ptr(cu_seqlens_q), _ptr(context_lens), B, HQ, HKV, d, bs, block_tables.shape[1], nb,
-        window, num_sink, float(scale), _i32("max_q_len", max_q_len), _ptr(error_word),
+        window, num_sink, float(scale), _i32("max_q_len", max_q_len), T, _ptr(error_word),
         _stream(stream))
     _check(st, "pa_paged_window_prefill_attention")

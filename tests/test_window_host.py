@@ -87,7 +87,7 @@ def test_window_workspace_size(lib):
 
 def _prefill(lib, **kw):
     a = dict(out=FAKE, q=FAKE, kc=FAKE, vc=FAKE, cd=pa.PA_BF16, bt=FAKE, cu=FAKE, cl=FAKE, B=4, HQ=32, HKV=8, d=128,
-             bs=16, mbps=8, nb=64, window=64, sink=4, scale=0.088, mql=64, err=FAKE)
+             bs=16, mbps=8, nb=64, window=64, sink=4, scale=0.088, mql=64, total=256, err=FAKE)
     assert set(kw) <= set(a)
     return lib.pa_paged_window_prefill_attention(*{**a, **kw}.values(), None)
 
@@ -96,7 +96,8 @@ def _prefill(lib, **kw):
     (pa.PA_OK, dict(B=0)), (pa.PA_OK, dict(mql=0)), (INVALID, dict(window=0)), (INVALID, dict(sink=-1)),
     (INVALID, dict(B=0, window=0)), (INVALID, dict(err=None)), (INVALID, dict(cu=None)), (INVALID, dict(HQ=12)),
     (INVALID, dict(mql=-1)), (UNSUPPORTED, dict(cd=pa.PA_FP8_E4M3)), (UNSUPPORTED, dict(d=64)),
-    (UNSUPPORTED, dict(HQ=24)), (UNSUPPORTED, dict(bs=4)), (UNSUPPORTED, dict(mbps=1 << 27)),
+    (UNSUPPORTED, dict(HQ=24)), (UNSUPPORTED, dict(bs=4)), (UNSUPPORTED, dict(mbps=1 << 27)), (INVALID, dict(total=-1)), (UNSUPPORTED, dict(total=1 << 31)),
+    (pa.PA_OK, dict(total=0)),
     (ALIGN, dict(out=FAKE_MIS)), (ALIGN, dict(err=P(0x100002))), (ALIGN, dict(cu=P(0x100002))),
 ])
 def test_window_prefill_rejects(lib, want, kw):
