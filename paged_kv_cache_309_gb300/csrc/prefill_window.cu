@@ -16,8 +16,8 @@
 // land and its first score products run.
 //  * TMEM (512 columns): outputs O0, O1 and score tiles S0, S1 of 128 each; tile i's
 //    weights (bf16 pairs) overwrite the upper half of S_i.
-//  * warp 0 loads keys (3 slots) and posts each tile's row mask, warp 2 values (2
-//    slots), warp 3 the query tiles; all by TMA, 128-byte swizzled.
+//  * warp 0 loads keys and values (K(0), V(0), K(1), ... through five slots) and posts each
+//    tile's row mask, warp 2 the query tiles; all by TMA, 128-byte swizzled.
 //  * one thread of warp 1 issues every product: ..., O_i += P_i(t) V(t), S_i(t + 1) =
 //    Q_i K(t + 1)^T, then the other query tile's.  Products of one thread
 //    run in order, so S_i(t + 1) may overwrite P_i(t) without a wait between them.
@@ -39,20 +39,18 @@ using namespace tc;
 constexpr int kD = 128;
 constexpr int kM = 128;    // rows per query tile (tokens x heads)
 constexpr int kTile = 128; // keys per tile
-constexpr int kKSlots = 3;
-constexpr int kVSlots = 2;
+constexpr int kSlots = 5;  // K(u) is load 2u of the CTA, V(u) load 2u + 1
 constexpr int kThreads = 12 * 32;              // 4 role warps + 2 x 4 softmax warps
 constexpr int kChunk = 128 * 128;              // 64 elements of 128 rows: 16 KB
 constexpr int kQOff = 0;                       // query tile i: two chunks
-constexpr int kKOff = 2 * 2 * kChunk;          // key slots: two chunks each
-constexpr int kVOff = kKOff + kKSlots * 2 * kChunk;
-constexpr int kBarOff = kVOff + kVSlots * 2 * kChunk;
-// Mask slot u % 8 is written again for tile u + 8, whose keys need S(u + 5), which is
-// issued after P.V(u + 4), which needs both softmax groups past tile u.
+constexpr int kRingOff = 2 * 2 * kChunk;       // slots of two chunks
+constexpr int kSlotBytes = 2 * kChunk;
+constexpr int kBarOff = kRingOff + kSlots * kSlotBytes;
+// Mask slot u % 8 is written again for tile u + 8, whose keys (load 2u + 16) need load
+// 2u + 11 = V(u + 5) used, and P.V(u + 5) needs both softmax groups past tile u.
 constexpr int kMaskSlots = 8;
-// q_full, q_empty, s_full, p_full, o_final, o_empty [2] each, k_full, k_empty,
-// v_full, v_empty, mask_full, drain
-constexpr int kNumBars = 6 * 2 + 2 * kKSlots + 2 * kVSlots + kMaskSlots + 1;
+// q_full, q_empty, s_full, p_full, o_final, o_empty [2] each, full, empty, mask_full, drain
+constexpr int kNumBars = 6 * 2 + 2 * kSlots + kMaskSlots + 1;
 constexpr int kMaskOff = kBarOff + (kNumBars + 1) / 2 * 16;  // two 64-bit words per slot
 constexpr int kMiscOff = kMaskOff + kMaskSlots * 16;
 constexpr int kBytes = kMiscOff + 16;
@@ -177,57 +175,93 @@ struct Walk {
   }
 };
 
+// --------------------------------------------------------------- products --
+// The issuing warp stays together and one lane's predicate guards each instruction: in a branch
+// of one lane every operand would be moved to the uniform registers that these
+// instructions read, at ~100 cycles a product.  Descriptors come as two words.
+__device__ __forceinline__ void mma_ss(uint32_t one, uint32_t d, uint32_t a, uint32_t b,
+                                       uint32_t hi, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 da, db;\n\t"
+      "setp.ne.b32 p, %5, 0;\n\tsetp.ne.b32 q, %6, 0;\n\t"
+      "mov.b64 da, {%1, %3};\n\tmov.b64 db, {%2, %3};\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %4, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(hi), "r"(idesc), "r"(accumulate), "r"(one)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t one, uint32_t d, uint32_t a_tmem, uint32_t b,
+                                       uint32_t hi, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 db;\n\t"
+      "setp.ne.b32 p, %5, 0;\n\tsetp.ne.b32 q, %6, 0;\n\t"
+      "mov.b64 db, {%2, %3};\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %4, p;\n\t}" ::"r"(d),
+      "r"(a_tmem), "r"(b), "r"(hi), "r"(idesc), "r"(accumulate), "r"(one)
+      : "memory");
+}
+__device__ __forceinline__ void commit(uint32_t one, uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(
+          smem_u32(bar)),
+      "r"(one)
+      : "memory");
+}
+// one lane of a warp that is together, the same one every time
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r));
+  return r;
+}
+
 // ------------------------------------------------------------------ loads --
-// The keys or values of one tile: lane i < nbox looks up block piece i; for the
-// keys (mask_slot given) the lanes agree on the 128-bit row mask and lane 0 posts
-// it; lane 0 posts the byte count and each lane with a valid piece issues its
-// two boxes (64 head elements each).
-__device__ __forceinline__ void issue_tile(const Params& p, const Item& it, const CUtensorMap* tm,
-                                           uint8_t* dst, uint64_t* full, uint64_t* mask_slot,
-                                           uint64_t* mask_bar, int place0, uint64_t pol, int lane) {
-  const int bs = p.block_size;
-  const int rpb = bs < kTile ? bs : kTile;
-  const int nbox = kTile / rpb;
-  const int start = lane * rpb;  // of the tile's places
-  int rows = 0, bid = -1, row0 = 0;
-  bool valid = false;
-  uint64_t lo = 0, hi = 0;  // the piece's visible rows as bits of the tile
-  if (lane < nbox) {
-    const int first = it.win.row(place0 + start);
-    rows = min(rpb, it.win.len - place0 - start);
-    if (rows > 0) {
-      row0 = first & (bs - 1);
-      bid = __ldg(p.block_tables + static_cast<int64_t>(it.b) * p.max_blocks_per_seq +
-                  (first >> p.log2_bs));
-      valid = bid >= 0 && static_cast<int64_t>(bid) < p.num_blocks;
-    }
-    if (valid) {
-      const int tile0 = first - start;  // the row of bit 0, if this piece's run began there
-      lo = WindowRange::below(start + rows) & ~WindowRange::below(start) &
+// A tile's block pieces: lane i holds piece i % nbox (each looked up by 32 / nbox lanes, which
+// share out its copies): its cache row (-1: nothing of it is there or seen), and the
+// piece's visible rows as bits of the tile.
+struct TilePieces {
+  int row;
+  uint64_t lo, hi;
+};
+__device__ __forceinline__ TilePieces find_pieces(const Params& p, const Item& it, int place0,
+                                                  int log2_rpb, int lane) {
+  TilePieces x;
+  const int rpb = 1 << log2_rpb;
+  const int start = (lane & ((kTile >> log2_rpb) - 1)) << log2_rpb;  // of the tile's places
+  const int first = it.win.row(place0 + start);
+  const int rows = min(rpb, it.win.len - place0 - start);
+  x.row = -1;
+  x.lo = x.hi = 0;
+  if (rows > 0) {
+    const int bid = __ldg(p.block_tables + static_cast<int64_t>(it.b) * p.max_blocks_per_seq +
+                          (first >> p.log2_bs));
+    const int tile0 = first - start;  // the row of bit 0, if this piece's run began there
+    x.lo = WindowRange::below(start + rows) & ~WindowRange::below(start) &
            it.win.visible(tile0, p.num_sink);
-      hi = WindowRange::below(start + rows - 64) & ~WindowRange::below(start - 64) &
+    x.hi = WindowRange::below(start + rows - 64) & ~WindowRange::below(start - 64) &
            it.win.visible(tile0 + 64, p.num_sink);
+    if (bid >= 0 && static_cast<int64_t>(bid) < p.num_blocks && (x.lo | x.hi) != 0) {
+      x.row = bid * p.block_size + (first & (p.block_size - 1));
+    } else {
+      x.lo = x.hi = 0;
     }
   }
-  const uint32_t vb = __ballot_sync(0xffffffffu, valid);
-  if (mask_slot != nullptr) {
-    const uint32_t w0 = __reduce_or_sync(0xffffffffu, static_cast<uint32_t>(lo));
-    const uint32_t w1 = __reduce_or_sync(0xffffffffu, static_cast<uint32_t>(lo >> 32));
-    const uint32_t w2 = __reduce_or_sync(0xffffffffu, static_cast<uint32_t>(hi));
-    const uint32_t w3 = __reduce_or_sync(0xffffffffu, static_cast<uint32_t>(hi >> 32));
-    if (lane == 0) {
-      mask_slot[0] = (static_cast<uint64_t>(w1) << 32) | w0;
-      mask_slot[1] = (static_cast<uint64_t>(w3) << 32) | w2;
-      mbar_arrive(mask_bar);
-    }
-  }
-  if (lane == 0) mbar_arrive_expect_tx(full, static_cast<uint32_t>(__popc(vb) * rpb * 128 * 2));
+  return x;
+}
+// The keys or values of one tile; copy c is half c / nbox (64 head elements) of piece c % nbox.
+__device__ __forceinline__ void load_tile(const CUtensorMap* tm, const TilePieces& x, int g,
+                                          uint8_t* dst, uint64_t* full, int log2_rpb, uint64_t pol,
+                                          int lane) {
+  const int nbox = kTile >> log2_rpb;
+  const uint32_t there = __ballot_sync(0xffffffffu, lane < nbox && x.row >= 0);
+  if (lane == 0)
+    mbar_arrive_expect_tx(full, static_cast<uint32_t>(__popc(there) << (log2_rpb + 8)));
   __syncwarp();
-  if (valid) {
-    const int32_t row = bid * bs + row0;
-    uint8_t* st = dst + start * 128;
-    tma_load_3d(st, tm, 0, it.g, row, full, pol);
-    tma_load_3d(st + kChunk, tm, 64, it.g, row, full, pol);
+  if (lane < 2 * nbox && x.row >= 0) {
+    const int half = lane >= nbox ? 1 : 0;
+    tma_load_3d(dst + half * kChunk + ((lane & (nbox - 1)) << (log2_rpb + 7)), tm, 64 * half, g,
+                x.row, full, pol);
   }
 }
 
@@ -308,14 +342,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* q_full = bars;                    // [2] query tile i landed
   uint64_t* q_empty = bars + 2;               // [2] its last score product done (commit)
   uint64_t* s_full = bars + 4;                // [2] S_i in TMEM (commit)
-  uint64_t* p_full = bars + 6;                // [2] weights of tile i in TMEM (128 threads)
+  uint64_t* p_full = bars + 6;                // [2] weights of tile i in TMEM (4 warps)
   uint64_t* o_final = bars + 8;               // [2] the item's products into O_i done (commit)
-  uint64_t* o_empty = bars + 10;              // [2] O_i read (128 threads)
-  uint64_t* k_full = bars + 12;               // [kKSlots]
-  uint64_t* k_empty = k_full + kKSlots;       // [kKSlots] the slot's score products done
-  uint64_t* v_full = k_empty + kKSlots;       // [kVSlots]
-  uint64_t* v_empty = v_full + kVSlots;       // [kVSlots] the slot's output products done
-  uint64_t* mask_full = v_empty + kVSlots;    // [kMaskSlots] row mask posted
+  uint64_t* o_empty = bars + 10;              // [2] O_i read (4 warps)
+  uint64_t* full = bars + 12;                 // [kSlots] keys or values landed
+  uint64_t* empty = full + kSlots;            // [kSlots] the slot's products done (commit)
+  uint64_t* mask_full = empty + kSlots;       // [kMaskSlots] row mask posted
   uint64_t* drain = mask_full + kMaskSlots;   // every product done
   uint64_t* tile_mask = reinterpret_cast<uint64_t*>(smem + kMaskOff);  // [kMaskSlots][2]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kMiscOff);
@@ -330,17 +362,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&q_full[i], 1);
       mbar_init(&q_empty[i], 1);
       mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i], kM);
+      mbar_init(&p_full[i], 4);
       mbar_init(&o_final[i], 1);
-      mbar_init(&o_empty[i], kM);
+      mbar_init(&o_empty[i], 4);
     }
-    for (int s = 0; s < kKSlots; ++s) {
-      mbar_init(&k_full[s], 1);
-      mbar_init(&k_empty[s], 1);
-    }
-    for (int s = 0; s < kVSlots; ++s) {
-      mbar_init(&v_full[s], 1);
-      mbar_init(&v_empty[s], 1);
+    for (int s = 0; s < kSlots; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
     }
     for (int s = 0; s < kMaskSlots; ++s) mbar_init(&mask_full[s], 1);
     mbar_init(drain, 1);
@@ -357,41 +385,70 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = __reduce_or_sync(0xffffffffu, *tmem_slot);
   volatile int* abort_flag = flags;
-  uint32_t issued = 0;  // (loading warps) loads requested
+  uint32_t issued = 0;  // (warp 0) loads requested
 
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRoleRegs));
     Walk walk(p, blockIdx.x, lane);
     Item it;
     bool ok = true;
-    if (warp == 0 || warp == 2) {
-      // ------------------------------------------------ keys (0), values (2)
-      const bool is_k = warp == 0;
-      const CUtensorMap* tm = is_k ? &tm_k : &tm_v;
-      const uint32_t nslots = is_k ? kKSlots : kVSlots;
-      uint64_t* empty = is_k ? k_empty : v_empty;
-      uint64_t* full = is_k ? k_full : v_full;
-      uint8_t* ring = smem + (is_k ? kKOff : kVOff);
+    if (warp == 0) {
+      // ------------------------------------------------------ keys and values
       const uint64_t pol = l2_policy_evict_normal();
-      if (lane == 0) prefetch_tensormap(tm);
-      while (ok && walk.get(p, step, lane, it)) {
-        for (int t = 0; t < it.ntiles; ++t) {
-          const uint32_t st = issued % nslots;
-          if (issued >= nslots) {
-            ok = __all_sync(0xffffffffu, mbar_wait_bounded_long(
-                                             &empty[st], ((issued / nslots) - 1) & 1, abort_flag));
-            if (!ok) break;
+      const int log2_rpb = min(p.log2_bs, 7);
+      if (lane == 0) {
+        prefetch_tensormap(&tm_k);
+        prefetch_tensormap(&tm_v);
+      }
+      uint32_t slot = 0, phase = 1;  // (the first wait for an empty slot passes)
+      uint32_t u = 0;
+      bool have = walk.get(p, step, lane, it);
+      TilePieces x{};
+      if (have && it.ntiles > 0) x = find_pieces(p, it, 0, log2_rpb, lane);
+      while (ok && have) {
+        const int g = it.g, ntiles = it.ntiles;
+        for (int t = 0; t < ntiles; ++t, ++u) {
+          const TilePieces now = x;
+          // the next tile's blocks are looked up before the waits for slots
+          if (t + 1 < ntiles) {
+            x = find_pieces(p, it, (t + 1) * kTile, log2_rpb, lane);
+          } else {
+            have = walk.get(p, step, lane, it);
+            if (have && it.ntiles > 0) x = find_pieces(p, it, 0, log2_rpb, lane);
           }
-          const uint32_t ms = issued % kMaskSlots;
-          issue_tile(p, it, tm, ring + st * 2 * kChunk, &full[st],
-                     is_k ? &tile_mask[2 * ms] : nullptr, is_k ? &mask_full[ms] : nullptr,
-                     t * kTile, pol, lane);
-          ++issued;
+          const uint32_t w0 = __reduce_or_sync(0xffffffffu, static_cast<uint32_t>(now.lo));
+          const uint32_t w1 = __reduce_or_sync(0xffffffffu, static_cast<uint32_t>(now.lo >> 32));
+          const uint32_t w2 = __reduce_or_sync(0xffffffffu, static_cast<uint32_t>(now.hi));
+          const uint32_t w3 = __reduce_or_sync(0xffffffffu, static_cast<uint32_t>(now.hi >> 32));
+#pragma unroll
+          for (int v = 0; v < 2; ++v) {
+            ok = __all_sync(0xffffffffu,
+                            mbar_wait_bounded_long(&empty[slot], phase, abort_flag));
+            if (!ok) break;
+            if (v == 0 && lane == 0) {
+              uint64_t* m = tile_mask + 2 * (u % kMaskSlots);
+              m[0] = (static_cast<uint64_t>(w1) << 32) | w0;
+              m[1] = (static_cast<uint64_t>(w3) << 32) | w2;
+              mbar_arrive(&mask_full[u % kMaskSlots]);
+            }
+            load_tile(v == 0 ? &tm_k : &tm_v, now, g, smem + kRingOff + slot * kSlotBytes,
+                      &full[slot], log2_rpb, pol, lane);
+            ++issued;
+            if (++slot == kSlots) {
+              slot = 0;
+              phase ^= 1;
+            }
+          }
+          if (!ok) break;
+        }
+        if (ntiles == 0) {
+          have = walk.get(p, step, lane, it);
+          if (have && it.ntiles > 0) x = find_pieces(p, it, 0, log2_rpb, lane);
         }
       }
-    } else if (warp == 3) {
+    } else if (warp == 2) {
       // ------------------------------------------------------------- queries
       const uint64_t pol = l2_policy_evict_first();
       if (lane == 0) prefetch_tensormap(&tm_q);
@@ -420,42 +477,54 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int i = 0; i < 2; ++i)
         if (count[i] > 0) mbar_wait_bounded_long(&q_full[i], (count[i] - 1) & 1, nullptr);
-    } else {
+    } else if (warp == 1) {
       // ------------------------------------------------------------ products
-      const uint32_t q_base = smem_u32(smem + kQOff);
-      const uint32_t k_base = smem_u32(smem + kKOff);
-      const uint32_t v_base = smem_u32(smem + kVOff);
-      uint32_t u = 0;                       // tiles whose output products are issued
+      // Descriptors: the low words differ by (byte offset >> 4), the high words are
+      // fixed, so that a product costs one addition.
+      const uint64_t base = smem_desc(smem_u32(smem), 16, 1024);
+      const uint32_t lo_kmajor = static_cast<uint32_t>(base);
+      const uint32_t hi_word = static_cast<uint32_t>(base >> 32);
+      // V is MN-major: leading offset = the next 64 elements = the next chunk
+      const uint32_t lo_v = static_cast<uint32_t>(smem_desc(smem_u32(smem), kChunk, 1024));
+      const uint32_t one = elect_one();
       uint32_t items[2] = {0, 0};           // items whose first score product is issued
-      auto wait = [&](uint64_t* bar, uint32_t n) {
-        if (ok) ok = mbar_wait_bounded_long(bar, n & 1, abort_flag);
+      uint32_t k_slot = 0, k_phase = 0;     // of the next key tile
+      uint32_t v_slot = 1, v_phase = 0;     // of the next value tile
+      auto advance = [](uint32_t& slot, uint32_t& phase) {
+        slot += 2;
+        if (slot >= kSlots) {
+          slot -= kSlots;
+          phase ^= 1;
+        }
       };
-      // S_i of tile n of the CTA: 8 k-steps of 16 over the 128 head elements, both
-      // operands K-major 128-byte swizzled (a k-step in a chunk is 32 bytes on)
-      auto score = [&](int i, uint32_t n, bool first, bool last) {
+      auto wait = [&](uint64_t* bar, uint32_t n) {
+        if (ok) ok = __all_sync(0xffffffffu, mbar_wait_bounded(bar, n & 1, abort_flag));
+      };
+      // S_i of the key tile in k_slot: 8 k-steps of 16 over the 128 head elements, both operands
+      // K-major 128-byte swizzled (a k-step in a chunk is 32 bytes on)
+      auto score = [&](int i, bool first, bool last) {
         if (first) wait(&q_full[i], items[i]++);
-        wait(&k_full[n % kKSlots], n / kKSlots);
-        if (!__all_sync(0xffffffffu, ok)) ok = false;
-        if (ok && lane == 0) {
+        wait(&full[k_slot], k_phase);
+        if (ok) {
           tc_fence_after();
-          const uint32_t qb = q_base + i * 2 * kChunk;
-          const uint32_t kb = k_base + (n % kKSlots) * 2 * kChunk;
+          const uint32_t qd = lo_kmajor + (kQOff + i * 2 * kChunk) / 16;
+          const uint32_t kd = lo_kmajor + (kRingOff + k_slot * kSlotBytes) / 16;
 #pragma unroll
-          for (int j = 0; j < kD / 16; ++j)
-            tc_mma_ss(tmem + kSCol + kTile * i,
-                      smem_desc(qb + (j >> 2) * kChunk + 32 * (j & 3), 16, 1024),
-                      smem_desc(kb + (j >> 2) * kChunk + 32 * (j & 3), 16, 1024), kIdescS,
-                      j > 0 ? 1u : 0u);
-          tc_commit(&s_full[i]);
-          if (last) tc_commit(&q_empty[i]);
+          for (int j = 0; j < kD / 16; ++j) {
+            const uint32_t off = ((j >> 2) * kChunk + 32 * (j & 3)) / 16;
+            mma_ss(one, tmem + kSCol + kTile * i, qd + off, kd + off, hi_word, kIdescS, j > 0 ? 1u : 0u);
+          }
+          commit(one, &s_full[i]);
+          if (last) commit(one, &q_empty[i]);
         }
       };
       // key tiles (0: no item is left) and query tiles of the next item
       auto next_item = [&](int& nq) -> int {
         while (walk.get(p, step, lane, it)) {
           if (it.ntiles > 0) {
-            nq = it.nq;
-            return it.ntiles;
+            // (by a reduction, whose result is known to be the same in every lane)
+            nq = __reduce_max_sync(0xffffffffu, it.nq);
+            return __reduce_max_sync(0xffffffffu, it.ntiles);
           }
         }
         return 0;
@@ -465,15 +534,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (ntiles > 0) {
 #pragma unroll
         for (int i = 0; i < 2; ++i)
-          if (i < nq) score(i, 0, true, ntiles == 1);
-        if (ok && lane == 0) tc_commit(&k_empty[0]);
+          if (i < nq) score(i, true, ntiles == 1);
+        if (ok) commit(one, &empty[0]);
+        advance(k_slot, k_phase);
       }
       uint32_t weighed[2] = {0, 0};  // output products issued per query tile
       uint32_t done[2] = {0, 0};     // items finished per query tile
       while (ok && ntiles > 0) {
         int nxt_nq = 0;
         const int nxt_ntiles = next_item(nxt_nq);
-        for (int t = 0; ok && t < ntiles; ++t, ++u) {
+        for (int t = 0; ok && t < ntiles; ++t) {
           const bool last = t + 1 == ntiles;
           // the next tile's query tiles: this item's, or those of the next one (or none)
           const int next_nq = last ? nxt_nq : nq;
@@ -481,38 +551,37 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             if (i < nq) {
-              if (i == 0) wait(&v_full[u % kVSlots], u / kVSlots);
+              if (i == 0) wait(&full[v_slot], v_phase);
               wait(&p_full[i], weighed[i]++);
               if (t == 0 && done[i] > 0) wait(&o_empty[i], done[i] - 1);
-              if (!__all_sync(0xffffffffu, ok)) ok = false;
-              if (ok && lane == 0) {
+                    if (ok) {
                 tc_fence_after();
                 // O_i += P_i V: 8 k-steps of 16 keys; P_i from TMEM (bf16 pairs, 8 columns
                 // per k-step), V MN-major (leading offset: next 64 elements = next chunk;
                 // stride offset: next 8 keys = 1 KB)
                 const uint32_t pc = tmem + kSCol + kTile * i + kPHalf;
-                const uint32_t vb = v_base + (u % kVSlots) * 2 * kChunk;
+                const uint32_t vd = lo_v + (kRingOff + v_slot * kSlotBytes) / 16;
 #pragma unroll
                 for (int kk = 0; kk < kTile / 16; ++kk)
-                  tc_mma_ts(tmem + kOCol + kD * i, pc + 8 * kk,
-                            smem_desc(vb + kk * 2048, kChunk, 1024), kIdescPV,
-                            (t > 0 || kk > 0) ? 1u : 0u);
-                if (last) tc_commit(&o_final[i]);
-                if (i + 1 == nq) tc_commit(&v_empty[u % kVSlots]);
+                  mma_ts(one, tmem + kOCol + kD * i, pc + 8 * kk, vd + kk * 2048 / 16, hi_word, kIdescPV,
+                         (t > 0 || kk > 0) ? 1u : 0u);
+                if (last) commit(one, &o_final[i]);
+                if (i + 1 == nq) commit(one, &empty[v_slot]);
               }
               if (last) ++done[i];
             }
-            if (i < next_nq) score(i, u + 1, last, next_last);
+            if (i < next_nq) score(i, last, next_last);
           }
-          if (ok && next_nq > 0 && lane == 0) tc_commit(&k_empty[(u + 1) % kKSlots]);
+          if (ok && next_nq > 0) commit(one, &empty[k_slot]);
+          advance(k_slot, k_phase);
+          advance(v_slot, v_phase);
         }
         ntiles = nxt_ntiles;
         nq = nxt_nq;
       }
-      if (lane == 0) {
-        tc_commit(drain);
-        mbar_wait_bounded(drain, 0, nullptr);
-      }
+      __syncwarp();
+      commit(one, drain);
+      mbar_wait_bounded(drain, 0, nullptr);
       __syncwarp();
     }
     if (!__all_sync(0xffffffffu, ok) && lane == 0) {
@@ -637,15 +706,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         // query tile 0's threads (P.V_1(t) follows P.V_0(t)); piece j = (key j / 2,
         // value chunk j % 2), two per thread
         if (qi == 0 && (mlo != ~0ull || mhi != ~0ull)) {
-          ok = __all_sync(0xffffffffu, mbar_wait_bounded(&v_full[u % kVSlots],
-                                                         (u / kVSlots) & 1, abort_flag));
+          const uint32_t load = 2 * u + 1, vs = load % kSlots;
+          ok = __all_sync(0xffffffffu,
+                          mbar_wait_bounded(&full[vs], (load / kSlots) & 1, abort_flag));
           if (!ok) break;
 #pragma unroll
           for (int hh = 0; hh < 2; ++hh) {
             const int j = row + kM * hh;
             const int r = j >> 1;
             if (!((r < 64 ? mlo >> r : mhi >> (r - 64)) & 1ull)) {
-              uint4* dst = reinterpret_cast<uint4*>(smem + kVOff + (u % kVSlots) * 2 * kChunk +
+              uint4* dst = reinterpret_cast<uint4*>(smem + kRingOff + vs * kSlotBytes +
                                                     (j & 1) * kChunk + r * 128);
 #pragma unroll
               for (int i = 0; i < 8; ++i) dst[i] = make_uint4(0u, 0u, 0u, 0u);
@@ -654,7 +724,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           fence_proxy_async_smem();  // generic writes before the tensor core reads them
         }
         tc_fence_before();
-        mbar_arrive(&p_full[qi]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[qi]);
       }
       if (!ok) break;
       if (it.ntiles == 0) {
@@ -677,7 +748,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int c = 0; c < kD; c += 32) tc_ld32_nowait(o_addr + c, &o[c]);
       tc_wait_ld();
       tc_fence_before();
-      mbar_arrive(&o_empty[qi]);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&o_empty[qi]);
 #pragma unroll
       for (int c = 0; c < kD; ++c) nan_row |= o[c] != o[c];
       if (rvalid) {
@@ -722,11 +794,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   if (*abort_flag) {
-    if ((warp == 0 || warp == 2) && lane == 0) {
-      uint64_t* full = warp == 0 ? k_full : v_full;
-      const uint32_t nslots = warp == 0 ? kKSlots : kVSlots;
-      for (uint32_t t = issued > nslots ? issued - nslots : 0; t < issued; ++t)
-        mbar_wait_bounded(&full[t % nslots], (t / nslots) & 1, nullptr);
+    if (warp == 0 && lane == 0) {
+      for (uint32_t t = issued > kSlots ? issued - kSlots : 0; t < issued; ++t)
+        mbar_wait_bounded(&full[t % kSlots], (t / kSlots) & 1, nullptr);
     }
     __syncthreads();
   }
