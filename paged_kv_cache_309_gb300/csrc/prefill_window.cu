@@ -16,7 +16,7 @@
 // land and its first score products run.
 //  * TMEM (512 columns): outputs O0, O1 and score tiles S0, S1 of 128 each; tile i's
 //    weights (bf16 pairs) overwrite the upper half of S_i.
-//  * warp 0 loads keys and values (K(0), V(0), K(1), ... through five slots) and posts each
+//  * warp 0 loads keys and values (K(0), V(0), K(1), ... through four slots) and posts each
 //    tile's row mask, warp 2 the query tiles; all by TMA, 128-byte swizzled.
 //  * one thread of warp 1 issues every product: ..., O_i += P_i(t) V(t), S_i(t + 1) =
 //    Q_i K(t + 1)^T, then the other query tile's.  Products of one thread
@@ -39,15 +39,18 @@ using namespace tc;
 constexpr int kD = 128;
 constexpr int kM = 128;    // rows per query tile (tokens x heads)
 constexpr int kTile = 128; // keys per tile
-constexpr int kSlots = 5;  // K(u) is load 2u of the CTA, V(u) load 2u + 1
+constexpr int kSlots = 4;  // K(u) is load 2u of the CTA, V(u) load 2u + 1
 constexpr int kThreads = 12 * 32;              // 4 role warps + 2 x 4 softmax warps
 constexpr int kChunk = 128 * 128;              // 64 elements of 128 rows: 16 KB
 constexpr int kQOff = 0;                       // query tile i: two chunks
 constexpr int kRingOff = 2 * 2 * kChunk;       // slots of two chunks
 constexpr int kSlotBytes = 2 * kChunk;
-constexpr int kBarOff = kRingOff + kSlots * kSlotBytes;
+constexpr int kStageOff = kRingOff + kSlots * kSlotBytes;  // 32 half rows per softmax warp
+constexpr int kStageBytes = 32 * 128;
+constexpr int kBarOff = kStageOff + 8 * kStageBytes;
 // Mask slot u % 8 is written again for tile u + 8, whose keys (load 2u + 16) need load
-// 2u + 11 = V(u + 5) used, and P.V(u + 5) needs both softmax groups past tile u.
+// 2u + 12 = K(u + 6) used, and S(u + 6) comes after P.V(u + 5), which needs both softmax
+// groups past tile u.
 constexpr int kMaskSlots = 8;
 // q_full, q_empty, s_full, p_full, o_final, o_empty [2] each, full, empty, mask_full, drain
 constexpr int kNumBars = 6 * 2 + 2 * kSlots + kMaskSlots + 1;
@@ -500,19 +503,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto wait = [&](uint64_t* bar, uint32_t n) {
         if (ok) ok = __all_sync(0xffffffffu, mbar_wait_bounded(bar, n & 1, abort_flag));
       };
-      // S_i of the key tile in k_slot: 8 k-steps of 16 over the 128 head elements, both operands
+      // S_i of the key tile at kd: 8 k-steps of 16 over the 128 head elements, both operands
       // K-major 128-byte swizzled (a k-step in a chunk is 32 bytes on)
-      auto score = [&](int i, bool first, bool last) {
-        if (first) wait(&q_full[i], items[i]++);
-        wait(&full[k_slot], k_phase);
-        if (ok) {
+      auto score = [&](int i, uint32_t kd, bool first, bool last) {
+        if (first) {
+          wait(&q_full[i], items[i]++);
           tc_fence_after();
+        }
+        if (ok) {
           const uint32_t qd = lo_kmajor + (kQOff + i * 2 * kChunk) / 16;
-          const uint32_t kd = lo_kmajor + (kRingOff + k_slot * kSlotBytes) / 16;
 #pragma unroll
           for (int j = 0; j < kD / 16; ++j) {
             const uint32_t off = ((j >> 2) * kChunk + 32 * (j & 3)) / 16;
-            mma_ss(one, tmem + kSCol + kTile * i, qd + off, kd + off, hi_word, kIdescS, j > 0 ? 1u : 0u);
+            mma_ss(one, tmem + kSCol + kTile * i, qd + off, kd + off, hi_word, kIdescS,
+                   j > 0 ? 1u : 0u);
           }
           commit(one, &s_full[i]);
           if (last) commit(one, &q_empty[i]);
@@ -532,9 +536,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       int nq = 0;
       int ntiles = next_item(nq);
       if (ntiles > 0) {
+        wait(&full[0], 0);
+        tc_fence_after();
 #pragma unroll
         for (int i = 0; i < 2; ++i)
-          if (i < nq) score(i, true, ntiles == 1);
+          if (i < nq) score(i, lo_kmajor + kRingOff / 16, true, ntiles == 1);
         if (ok) commit(one, &empty[0]);
         advance(k_slot, k_phase);
       }
@@ -548,33 +554,41 @@ __global__ void __launch_bounds__(kThreads, 1)
           // the next tile's query tiles: this item's, or those of the next one (or none)
           const int next_nq = last ? nxt_nq : nq;
           const bool next_last = last ? nxt_ntiles == 1 : t + 2 == ntiles;
+          // (all that does not hang on the weights comes before the wait for them)
+          const uint32_t vd = lo_v + (kRingOff + v_slot * kSlotBytes) / 16;
+          const uint32_t kd = lo_kmajor + (kRingOff + k_slot * kSlotBytes) / 16;
+          uint64_t* const v_empty = &empty[v_slot];
+          uint64_t* const k_empty = &empty[k_slot];
+          wait(&full[v_slot], v_phase);
+          if (next_nq > 0) wait(&full[k_slot], k_phase);
+          if (t == 0) {
+            if (done[0] > 0) wait(&o_empty[0], done[0] - 1);
+            if (nq > 1 && done[1] > 0) wait(&o_empty[1], done[1] - 1);
+          }
+          advance(k_slot, k_phase);
+          advance(v_slot, v_phase);
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             if (i < nq) {
-              if (i == 0) wait(&full[v_slot], v_phase);
               wait(&p_full[i], weighed[i]++);
-              if (t == 0 && done[i] > 0) wait(&o_empty[i], done[i] - 1);
-                    if (ok) {
-                tc_fence_after();
+              tc_fence_after();
+              if (ok) {
                 // O_i += P_i V: 8 k-steps of 16 keys; P_i from TMEM (bf16 pairs, 8 columns
                 // per k-step), V MN-major (leading offset: next 64 elements = next chunk;
                 // stride offset: next 8 keys = 1 KB)
                 const uint32_t pc = tmem + kSCol + kTile * i + kPHalf;
-                const uint32_t vd = lo_v + (kRingOff + v_slot * kSlotBytes) / 16;
 #pragma unroll
                 for (int kk = 0; kk < kTile / 16; ++kk)
-                  mma_ts(one, tmem + kOCol + kD * i, pc + 8 * kk, vd + kk * 2048 / 16, hi_word, kIdescPV,
-                         (t > 0 || kk > 0) ? 1u : 0u);
+                  mma_ts(one, tmem + kOCol + kD * i, pc + 8 * kk, vd + kk * 2048 / 16, hi_word,
+                         kIdescPV, (t > 0 || kk > 0) ? 1u : 0u);
                 if (last) commit(one, &o_final[i]);
-                if (i + 1 == nq) commit(one, &empty[v_slot]);
+                if (i + 1 == nq) commit(one, v_empty);
               }
               if (last) ++done[i];
             }
-            if (i < next_nq) score(i, last, next_last);
+            if (i < next_nq) score(i, kd, last, next_last);
           }
-          if (ok && next_nq > 0) commit(one, &empty[k_slot]);
-          advance(k_slot, k_phase);
-          advance(v_slot, v_phase);
+          if (ok && next_nq > 0) commit(one, k_empty);
         }
         ntiles = nxt_ntiles;
         nq = nxt_nq;
@@ -635,9 +649,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         // places up to the row's own, from its window's first on or of first tokens
         // (places between the first tokens and the item's window are not in the mask)
+        const int t0 = t * kTile;
+        const bool all_seen = rvalid && (mlo & mhi) == ~0ull && t0 + kTile - 1 <= pos &&
+                              (t0 >= low || t0 + kTile <= p.num_sink);
+        if (!all_seen) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const int k0 = t * kTile + 64 * h;
+          const int k0 = t0 + 64 * h;
           uint64_t mw = h == 0 ? mlo : mhi;
           if (k0 + 63 > pos || (k0 < low && k0 + 64 > p.num_sink))
             mw &= WindowRange::below(pos + 1 - k0) &
@@ -649,6 +667,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int c = 0; c < 64; ++c)
               if (!((w[c >> 5] >> (c & 31)) & 1u)) s[64 * h + c] = -INFINITY;
           }
+        }
         }
         float mq[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
@@ -752,15 +771,31 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) mbar_arrive(&o_empty[qi]);
 #pragma unroll
       for (int c = 0; c < kD; ++c) nan_row |= o[c] != o[c];
-      if (rvalid) {
-        uint4* dst = reinterpret_cast<uint4*>(p.out + qrow);
+      // A thread's row is 256 bytes, far from the next one's: half rows go through shared
+      // memory (16-byte unit c of row r at c ^ (r & 7)), and the warp stores four rows
+      // (128-byte lines) at a time instead of 32 pieces of 16 bytes.
+      uint8_t* stage = smem + kStageOff + (warp - 4) * kStageBytes;
+      const int64_t out_row = rvalid ? qrow : -1;
 #pragma unroll
-        for (int c = 0; c < kD / 8; ++c)
-          dst[c] = make_uint4(pack_bf16x2(o[8 * c] * inv, o[8 * c + 1] * inv),
-                              pack_bf16x2(o[8 * c + 2] * inv, o[8 * c + 3] * inv),
-                              pack_bf16x2(o[8 * c + 4] * inv, o[8 * c + 5] * inv),
-                              pack_bf16x2(o[8 * c + 6] * inv, o[8 * c + 7] * inv));
+      for (int h = 0; h < 2; ++h) {
+        __syncwarp();
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          const float* x = &o[64 * h + 8 * c];
+          *reinterpret_cast<uint4*>(stage + lane * 128 + ((c ^ (lane & 7)) << 4)) =
+              make_uint4(pack_bf16x2(x[0] * inv, x[1] * inv), pack_bf16x2(x[2] * inv, x[3] * inv),
+                         pack_bf16x2(x[4] * inv, x[5] * inv), pack_bf16x2(x[6] * inv, x[7] * inv));
+        }
+        __syncwarp();
+#pragma unroll
+        for (int r0 = 0; r0 < 32; r0 += 4) {
+          const int r = r0 + (lane >> 3), c = lane & 7;
+          const int64_t to = __shfl_sync(0xffffffffu, out_row, r);
+          const uint4 x = *reinterpret_cast<const uint4*>(stage + r * 128 + ((c ^ (r & 7)) << 4));
+          if (to >= 0) *reinterpret_cast<uint4*>(p.out + to + 64 * h + 8 * c) = x;
+        }
       }
+      __syncwarp();  // (kAgain is stored after the row it marks)
       if (nan_row && rvalid && l_run == l_run) {
         *reinterpret_cast<uint32_t*>(p.out + qrow) = kAgain;
         flags[1] = 1;
