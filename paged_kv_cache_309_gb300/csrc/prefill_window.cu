@@ -14,15 +14,18 @@
 // CTAs stay: one per SM walks items c, c + grid, ... of all sequences, and while an item's last
 // tiles are weighed and its rows written, the next one's queries, keys and values
 // land and its first score products run.
-//  * TMEM (512 columns): outputs O0, O1 and score tiles S0, S1 of 128 each; tile i's
-//    weights (bf16 pairs) overwrite the upper half of S_i.
+//  * A key tile (128 places) is weighed in two steps of 64.  TMEM (512 columns): outputs O0, O1
+//    (128 each) and for each query tile two score buffers of 64, so that while the softmax
+//    works on step v, S(v + 1) is there or on its way: with one buffer of 128 a query tile's
+//    softmax and products took turns, and their hand-overs (about 1000 cycles a tile) left
+//    the tensor core idle half the time.  A step's weights (bf16 pairs) overwrite
+//    the first half of its scores.
 //  * warp 0 loads keys and values (K(0), V(0), K(1), ... through four slots) and posts each
 //    tile's row mask, warp 2 the query tiles; all by TMA, 128-byte swizzled.
-//  * one thread of warp 1 issues every product: ..., O_i += P_i(t) V(t), S_i(t + 1) =
-//    Q_i K(t + 1)^T, then the other query tile's.  Products of one thread
-//    run in order, so S_i(t + 1) may overwrite P_i(t) without a wait between them.
-//  * warps 4-7 and 8-11 do the softmax of query tiles 0 and 1, one thread per row; a row's
-//    128 scores are held in registers (role warps give theirs up).
+//  * one thread of warp 1 issues every product: O_i += P_i(v) V(v), S_i(v + 2) = Q_i K(v + 2)^T,
+//    then the other query tile's.  Products of one thread run in order, so S_i(v + 2)
+//    may overwrite P_i(v) without a wait between them.
+//  * warps 4-7 and 8-11 do the softmax of query tiles 0 and 1, one thread per row.
 // Every wait is bounded (2 s); a timeout sets an error bit, drains what was issued and
 // frees TMEM before the CTA exits.
 #include <atomic>
@@ -38,7 +41,8 @@ using namespace tc;
 
 constexpr int kD = 128;
 constexpr int kM = 128;    // rows per query tile (tokens x heads)
-constexpr int kTile = 128; // keys per tile
+constexpr int kTile = 128; // keys per tile of the ring
+constexpr int kStep = 64;  // keys per score buffer
 constexpr int kSlots = 4;  // K(u) is load 2u of the CTA, V(u) load 2u + 1
 constexpr int kThreads = 12 * 32;              // 4 role warps + 2 x 4 softmax warps
 constexpr int kChunk = 128 * 128;              // 64 elements of 128 rows: 16 KB
@@ -49,27 +53,22 @@ constexpr int kStageOff = kRingOff + kSlots * kSlotBytes;  // 32 half rows per s
 constexpr int kStageBytes = 32 * 128;
 constexpr int kBarOff = kStageOff + 8 * kStageBytes;
 // Mask slot u % 8 is written again for tile u + 8, whose keys (load 2u + 16) need load
-// 2u + 12 = K(u + 6) used, and S(u + 6) comes after P.V(u + 5), which needs both softmax
-// groups past tile u.
+// 2u + 12 = K(u + 6) used, and a score product comes after the output product two steps
+// before it, which needs both softmax groups past tile u.
 constexpr int kMaskSlots = 8;
-// q_full, q_empty, s_full, p_full, o_final, o_empty [2] each, full, empty, mask_full, drain
-constexpr int kNumBars = 6 * 2 + 2 * kSlots + kMaskSlots + 1;
+// q_full, q_empty, pv_done, o_empty [2] each, s_full, p_full [2][2], full, empty, mask_full,
+// drain
+constexpr int kNumBars = 4 * 2 + 2 * 4 + 2 * kSlots + kMaskSlots + 1;
 constexpr int kMaskOff = kBarOff + (kNumBars + 1) / 2 * 16;  // two 64-bit words per slot
 constexpr int kMiscOff = kMaskOff + kMaskSlots * 16;
 constexpr int kBytes = kMiscOff + 16;
 constexpr int kAlloc = kBytes + 1024;
 static_assert(kAlloc <= 227 * 1024, "shared memory");
-// Registers: 384 threads are launched with 168 each; 128 role threads keep 96, 256
-// softmax threads get 200 (63488 of the 64512 launched).
-constexpr int kRoleRegs = 96;
-constexpr int kSoftmaxRegs = 200;
-static_assert(128 * kRoleRegs + 256 * kSoftmaxRegs <= kThreads * 168, "registers");
 
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kOCol = 0;      // [0, 256): outputs O0, O1
-constexpr uint32_t kSCol = 256;    // [256, 512): score tiles S0, S1
-constexpr uint32_t kPHalf = 64;    // weights of tile i at kSCol + 128 i + 64
-constexpr uint32_t kIdescS = instr_desc(kM, kTile, false);
+constexpr uint32_t kSCol = 256;    // [256, 512): score buffer b of query tile i at + 128 i + 64 b
+constexpr uint32_t kIdescS = instr_desc(kM, kStep, false);
 constexpr uint32_t kIdescPV = instr_desc(kM, kD, true);
 constexpr float kRescaleLog2 = 8.0f;
 
@@ -104,6 +103,7 @@ struct Item {
   int q_row;     // the item's first row of q
   int ntok;      // its new tokens
   int ntiles;    // key tiles (0: no row has a key)
+  int nsteps;    // steps of 64 places in them
   int nq;        // query tiles with a row
   int pos0;      // place of its first token
   WindowRange win;
@@ -174,6 +174,7 @@ struct Walk {
     it.win = window_range(kend, max(0, it.pos0 - p.window + 1), p.num_sink, min(p.log2_bs, 7));
     it.pos0 -= it.win.skip;
     it.ntiles = (it.win.len + kTile - 1) / kTile;
+    it.nsteps = (it.win.len + kStep - 1) / kStep;
     return true;
   }
 };
@@ -344,11 +345,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kBarOff);
   uint64_t* q_full = bars;                    // [2] query tile i landed
   uint64_t* q_empty = bars + 2;               // [2] its last score product done (commit)
-  uint64_t* s_full = bars + 4;                // [2] S_i in TMEM (commit)
-  uint64_t* p_full = bars + 6;                // [2] weights of tile i in TMEM (4 warps)
-  uint64_t* o_final = bars + 8;               // [2] the item's products into O_i done (commit)
-  uint64_t* o_empty = bars + 10;              // [2] O_i read (4 warps)
-  uint64_t* full = bars + 12;                 // [kSlots] keys or values landed
+  uint64_t* pv_done = bars + 4;               // [2] an output product into O_i done (commit)
+  uint64_t* o_empty = bars + 6;               // [2] O_i read (4 warps)
+  uint64_t* s_full = bars + 8;                // [2][2] scores of buffer b there (commit)
+  uint64_t* p_full = bars + 12;               // [2][2] weights in buffer b (4 warps)
+  uint64_t* full = bars + 16;                 // [kSlots] keys or values landed
   uint64_t* empty = full + kSlots;            // [kSlots] the slot's products done (commit)
   uint64_t* mask_full = empty + kSlots;       // [kMaskSlots] row mask posted
   uint64_t* drain = mask_full + kMaskSlots;   // every product done
@@ -364,10 +365,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < 2; ++i) {
       mbar_init(&q_full[i], 1);
       mbar_init(&q_empty[i], 1);
+      mbar_init(&pv_done[i], 1);
+      mbar_init(&o_empty[i], 4);
+    }
+    for (int i = 0; i < 4; ++i) {
       mbar_init(&s_full[i], 1);
       mbar_init(&p_full[i], 4);
-      mbar_init(&o_final[i], 1);
-      mbar_init(&o_empty[i], 4);
     }
     for (int s = 0; s < kSlots; ++s) {
       mbar_init(&full[s], 1);
@@ -393,12 +396,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t issued = 0;  // (warp 0) loads requested
 
   if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRoleRegs));
-    Walk walk(p, blockIdx.x, lane);
-    Item it;
     bool ok = true;
     if (warp == 0) {
       // ------------------------------------------------------ keys and values
+      Walk walk(p, blockIdx.x, lane);
+      Item it;
       const uint64_t pol = l2_policy_evict_normal();
       const int log2_rpb = min(p.log2_bs, 7);
       if (lane == 0) {
@@ -453,6 +455,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     } else if (warp == 2) {
       // ------------------------------------------------------------- queries
+      Walk walk(p, blockIdx.x, lane);
+      Item it;
       const uint64_t pol = l2_policy_evict_first();
       if (lane == 0) prefetch_tensormap(&tm_q);
       uint32_t count[2] = {0, 0};
@@ -490,108 +494,129 @@ __global__ void __launch_bounds__(kThreads, 1)
       // V is MN-major: leading offset = the next 64 elements = the next chunk
       const uint32_t lo_v = static_cast<uint32_t>(smem_desc(smem_u32(smem), kChunk, 1024));
       const uint32_t one = elect_one();
-      uint32_t items[2] = {0, 0};           // items whose first score product is issued
-      uint32_t k_slot = 0, k_phase = 0;     // of the next key tile
-      uint32_t v_slot = 1, v_phase = 0;     // of the next value tile
-      auto advance = [](uint32_t& slot, uint32_t& phase) {
-        slot += 2;
-        if (slot >= kSlots) {
-          slot -= kSlots;
-          phase ^= 1;
-        }
-      };
       auto wait = [&](uint64_t* bar, uint32_t n) {
         if (ok) ok = __all_sync(0xffffffffu, mbar_wait_bounded(bar, n & 1, abort_flag));
       };
-      // S_i of the key tile at kd: 8 k-steps of 16 over the 128 head elements, both operands
-      // K-major 128-byte swizzled (a k-step in a chunk is 32 bytes on)
-      auto score = [&](int i, uint32_t kd, bool first, bool last) {
-        if (first) {
-          wait(&q_full[i], items[i]++);
+      // A cursor over the steps of all items; scores run two steps ahead of outputs, so each
+      // has its own.  (Counts come by a reduction, whose result is known to be the
+      // same in every lane.)
+      struct Cursor {
+        Walk walk;
+        int step, nsteps, nq;  // of the item in hand; nsteps 0: no more
+        uint32_t slot, phase;  // of its tile's keys or values
+        uint32_t steps[2];     // steps taken per query tile
+        uint32_t items[2];     // items begun per query tile
+      };
+      auto fetch = [&](Cursor& c) {
+        Item x;
+        c.step = c.nsteps = c.nq = 0;
+        while (c.walk.get(p, step, lane, x)) {
+          if (x.ntiles > 0) {
+            c.nsteps = __reduce_max_sync(0xffffffffu, x.nsteps);
+            c.nq = __reduce_max_sync(0xffffffffu, x.nq);
+            break;
+          }
+        }
+      };
+      auto advance = [&](Cursor& c) {
+        const bool last = c.step + 1 == c.nsteps;
+        if ((c.step & 1) || last) {  // on to the next tile
+          c.slot += 2;
+          if (c.slot >= kSlots) {
+            c.slot -= kSlots;
+            c.phase ^= 1;
+          }
+        }
+        if (last) {
+          fetch(c);
+        } else {
+          ++c.step;
+        }
+      };
+      Cursor sc{Walk(p, blockIdx.x, lane), 0, 0, 0, 0, 0, {0, 0}, {0, 0}};
+      fetch(sc);
+      Cursor pv = sc;
+      pv.slot = 1;
+      // S_i of cursor sc's step into the query tile's next buffer: 8 k-steps of 16 over the 128
+      // head elements, both operands K-major 128-byte swizzled (a k-step in a chunk
+      // is 32 bytes on, 64 keys 8 KB)
+      auto score = [&](int i) {
+        if (sc.step == 0) {
+          wait(&q_full[i], sc.items[i]++);
           tc_fence_after();
         }
+        const uint32_t buf = sc.steps[i]++ & 1;
         if (ok) {
           const uint32_t qd = lo_kmajor + (kQOff + i * 2 * kChunk) / 16;
+          const uint32_t kd =
+              lo_kmajor + (kRingOff + sc.slot * kSlotBytes + (sc.step & 1) * (kChunk / 2)) / 16;
+          const uint32_t d = tmem + kSCol + 2 * kStep * i + kStep * buf;
 #pragma unroll
           for (int j = 0; j < kD / 16; ++j) {
             const uint32_t off = ((j >> 2) * kChunk + 32 * (j & 3)) / 16;
-            mma_ss(one, tmem + kSCol + kTile * i, qd + off, kd + off, hi_word, kIdescS,
-                   j > 0 ? 1u : 0u);
+            mma_ss(one, d, qd + off, kd + off, hi_word, kIdescS, j > 0 ? 1u : 0u);
           }
-          commit(one, &s_full[i]);
-          if (last) commit(one, &q_empty[i]);
+          commit(one, &s_full[2 * i + buf]);
+          if (sc.step + 1 == sc.nsteps) commit(one, &q_empty[i]);
         }
       };
-      // key tiles (0: no item is left) and query tiles of the next item
-      auto next_item = [&](int& nq) -> int {
-        while (walk.get(p, step, lane, it)) {
-          if (it.ntiles > 0) {
-            // (by a reduction, whose result is known to be the same in every lane)
-            nq = __reduce_max_sync(0xffffffffu, it.nq);
-            return __reduce_max_sync(0xffffffffu, it.ntiles);
-          }
-        }
-        return 0;
+      auto keys_there = [&]() {
+        if ((sc.step & 1) == 0) wait(&full[sc.slot], sc.phase);
       };
-      int nq = 0;
-      int ntiles = next_item(nq);
-      if (ntiles > 0) {
-        wait(&full[0], 0);
-        tc_fence_after();
+      auto keys_used = [&]() {
+        if (ok && ((sc.step & 1) || sc.step + 1 == sc.nsteps)) commit(one, &empty[sc.slot]);
+        advance(sc);
+      };
+      for (int ahead = 0; ahead < 2; ++ahead) {
+        if (ok && sc.nsteps > 0) {
+          keys_there();
+          tc_fence_after();
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-          if (i < nq) score(i, lo_kmajor + kRingOff / 16, true, ntiles == 1);
-        if (ok) commit(one, &empty[0]);
-        advance(k_slot, k_phase);
+          for (int i = 0; i < 2; ++i)
+            if (i < sc.nq) score(i);
+          keys_used();
+        }
       }
-      uint32_t weighed[2] = {0, 0};  // output products issued per query tile
-      uint32_t done[2] = {0, 0};     // items finished per query tile
-      while (ok && ntiles > 0) {
-        int nxt_nq = 0;
-        const int nxt_ntiles = next_item(nxt_nq);
-        for (int t = 0; ok && t < ntiles; ++t) {
-          const bool last = t + 1 == ntiles;
-          // the next tile's query tiles: this item's, or those of the next one (or none)
-          const int next_nq = last ? nxt_nq : nq;
-          const bool next_last = last ? nxt_ntiles == 1 : t + 2 == ntiles;
-          // (all that does not hang on the weights comes before the wait for them)
-          const uint32_t vd = lo_v + (kRingOff + v_slot * kSlotBytes) / 16;
-          const uint32_t kd = lo_kmajor + (kRingOff + k_slot * kSlotBytes) / 16;
-          uint64_t* const v_empty = &empty[v_slot];
-          uint64_t* const k_empty = &empty[k_slot];
-          wait(&full[v_slot], v_phase);
-          if (next_nq > 0) wait(&full[k_slot], k_phase);
-          if (t == 0) {
-            if (done[0] > 0) wait(&o_empty[0], done[0] - 1);
-            if (nq > 1 && done[1] > 0) wait(&o_empty[1], done[1] - 1);
-          }
-          advance(k_slot, k_phase);
-          advance(v_slot, v_phase);
+      while (ok && pv.nsteps > 0) {
+        // (all that does not hang on the weights comes before the wait for them)
+        if ((pv.step & 1) == 0) wait(&full[pv.slot], pv.phase);
+        if (pv.step == 0) {
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            if (i < nq) {
-              wait(&p_full[i], weighed[i]++);
-              tc_fence_after();
-              if (ok) {
-                // O_i += P_i V: 8 k-steps of 16 keys; P_i from TMEM (bf16 pairs, 8 columns
-                // per k-step), V MN-major (leading offset: next 64 elements = next chunk;
-                // stride offset: next 8 keys = 1 KB)
-                const uint32_t pc = tmem + kSCol + kTile * i + kPHalf;
-#pragma unroll
-                for (int kk = 0; kk < kTile / 16; ++kk)
-                  mma_ts(one, tmem + kOCol + kD * i, pc + 8 * kk, vd + kk * 2048 / 16, hi_word,
-                         kIdescPV, (t > 0 || kk > 0) ? 1u : 0u);
-                if (last) commit(one, &o_final[i]);
-                if (i + 1 == nq) commit(one, v_empty);
-              }
-              if (last) ++done[i];
+            if (i < pv.nq) {
+              if (pv.items[i] > 0) wait(&o_empty[i], pv.items[i] - 1);
+              ++pv.items[i];
             }
-            if (i < next_nq) score(i, kd, last, next_last);
           }
-          if (ok && next_nq > 0) commit(one, k_empty);
         }
-        ntiles = nxt_ntiles;
-        nq = nxt_nq;
+        if (sc.nsteps > 0) keys_there();
+        const uint32_t vd =
+            lo_v + (kRingOff + pv.slot * kSlotBytes + (pv.step & 1) * (kChunk / 2)) / 16;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          if (i < pv.nq) {
+            const uint32_t n = pv.steps[i]++;
+            const uint32_t buf = n & 1;
+            wait(&p_full[2 * i + buf], n >> 1);
+            tc_fence_after();
+            if (ok) {
+              // O_i += P_i V: 4 k-steps of 16 keys; P_i from TMEM (bf16 pairs, 8 columns per
+              // k-step), V MN-major (leading offset: next 64 elements = next chunk;
+              // stride offset: next 8 keys = 1 KB)
+              const uint32_t pc = tmem + kSCol + 2 * kStep * i + kStep * buf;
+#pragma unroll
+              for (int kk = 0; kk < kStep / 16; ++kk)
+                mma_ts(one, tmem + kOCol + kD * i, pc + 8 * kk, vd + kk * 2048 / 16, hi_word,
+                       kIdescPV, (pv.step > 0 || kk > 0) ? 1u : 0u);
+              commit(one, &pv_done[i]);
+              if (i + 1 == pv.nq && ((pv.step & 1) || pv.step + 1 == pv.nsteps))
+                commit(one, &empty[pv.slot]);
+            }
+          }
+          if (i < sc.nq) score(i);
+        }
+        if (sc.nsteps > 0) keys_used();
+        advance(pv);
       }
       __syncwarp();
       commit(one, drain);
@@ -604,12 +629,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     // --------------------------------------------------------------- softmax
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
     const int qi = (warp - 4) >> 2;
     const int quad = warp & 3;
     const int row = 32 * quad + lane;  // = TMEM lane
     const uint32_t lane_addr = static_cast<uint32_t>(32 * quad) << 16;
-    const uint32_t s_addr = tmem + lane_addr + kSCol + kTile * qi;
+    const uint32_t s_addr = tmem + lane_addr + kSCol + 2 * kStep * qi;
     const uint32_t o_addr = tmem + lane_addr + kOCol + kD * qi;
     const int G = p.group;
     const int tok = qi * p.tokens_per_tile + row / G;  // the row's token among the item's
@@ -617,7 +641,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float sc = pos_scale ? p.scale_log2 : 1.f;
     Walk walk(p, blockIdx.x, lane);
     Item it;
-    uint32_t u = 0, mine = 0, done = 0;  // tiles of the CTA, of this query tile; its items
+    uint32_t u = 0, mine = 0;  // tiles of the CTA before the item, steps of this query tile
     bool ok = true;
     while (ok && walk.get(p, step, lane, it)) {
       if (qi >= it.nq) {
@@ -631,58 +655,56 @@ __global__ void __launch_bounds__(kThreads, 1)
                             it.g * G + row % G) *
                            kD;
       float m_run = -INFINITY, l_run = 0.f;
-      for (int t = 0; t < it.ntiles; ++t, ++u, ++mine) {
-        ok = mbar_wait_bounded(&s_full[qi], mine & 1, abort_flag) &&
-             mbar_wait_bounded(&mask_full[u % kMaskSlots], (u / kMaskSlots) & 1, abort_flag);
+      for (int v = 0; v < it.nsteps; ++v, ++mine) {
+        const uint32_t tile = u + (v >> 1);
+        const uint32_t buf = mine & 1;
+        ok = mbar_wait_bounded(&s_full[2 * qi + buf], (mine >> 1) & 1, abort_flag) &&
+             mbar_wait_bounded(&mask_full[tile % kMaskSlots], (tile / kMaskSlots) & 1, abort_flag);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
-        const uint64_t mlo = tile_mask[2 * (u % kMaskSlots)];
-        const uint64_t mhi = tile_mask[2 * (u % kMaskSlots) + 1];
+        const uint64_t mtile = tile_mask[2 * (tile % kMaskSlots) + (v & 1)];
         tc_fence_after();
-        float s[kTile];
-#pragma unroll
-        for (int c = 0; c < kTile; c += 32) tc_ld32_nowait(s_addr + c, &s[c]);
+        float s[kStep];
+        const uint32_t sb = s_addr + kStep * buf;
+        tc_ld32_nowait(sb, &s[0]);
+        tc_ld32_nowait(sb + 32, &s[32]);
         tc_wait_ld();
         if (!pos_scale) {
 #pragma unroll
-          for (int c = 0; c < kTile; ++c) s[c] *= p.scale_log2;
+          for (int c = 0; c < kStep; ++c) s[c] *= p.scale_log2;
         }
         // places up to the row's own, from its window's first on or of first tokens
         // (places between the first tokens and the item's window are not in the mask)
-        const int t0 = t * kTile;
-        const bool all_seen = rvalid && (mlo & mhi) == ~0ull && t0 + kTile - 1 <= pos &&
-                              (t0 >= low || t0 + kTile <= p.num_sink);
-        if (!all_seen) {
+        const int k0 = v * kStep;
+        uint64_t mw = mtile;
+        if (k0 + kStep - 1 > pos || (k0 < low && k0 + kStep > p.num_sink))
+          mw &= WindowRange::below(pos + 1 - k0) &
+                (~WindowRange::below(low - k0) | WindowRange::below(p.num_sink - k0));
+        if (!rvalid) mw = 0ull;
+        if (mw != ~0ull) {
+          const uint32_t w[2] = {static_cast<uint32_t>(mw), static_cast<uint32_t>(mw >> 32)};
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int k0 = t0 + 64 * h;
-          uint64_t mw = h == 0 ? mlo : mhi;
-          if (k0 + 63 > pos || (k0 < low && k0 + 64 > p.num_sink))
-            mw &= WindowRange::below(pos + 1 - k0) &
-                  (~WindowRange::below(low - k0) | WindowRange::below(p.num_sink - k0));
-          if (!rvalid) mw = 0ull;
-          if (mw != ~0ull) {
-            const uint32_t w[2] = {static_cast<uint32_t>(mw), static_cast<uint32_t>(mw >> 32)};
-#pragma unroll
-            for (int c = 0; c < 64; ++c)
-              if (!((w[c >> 5] >> (c & 31)) & 1u)) s[64 * h + c] = -INFINITY;
-          }
-        }
+          for (int c = 0; c < kStep; ++c)
+            if (!((w[c >> 5] >> (c & 31)) & 1u)) s[c] = -INFINITY;
         }
         float mq[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int c = 0; c < kTile; c += 8) {
+        for (int c = 0; c < kStep; c += 8) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) mq[i] = fmax3(mq[i], s[c + 2 * i], s[c + 2 * i + 1]);
         }
         const float mx_raw = fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3]));
         const float mx = pos_scale ? mx_raw * p.scale_log2 : mx_raw;
         // lazy rescale; tcgen05.ld/st are warp-wide, so the warp rescales together when any
-        // of its rows needs it (the others by 1).  P.V_i(t - 1) came before S_i(t): done.
+        // of its rows needs it (the others by 1), once the output product before is done
         const bool need = mx > m_run + kRescaleLog2;
         if (__any_sync(0xffffffffu, need)) {
           const float corr = need ? fast_exp2(m_run - mx) : 1.f;
-          if (t > 0) {
+          if (v > 0) {
+            ok = __all_sync(0xffffffffu,
+                            mbar_wait_bounded(&pv_done[qi], (mine - 1) & 1, abort_flag));
+            if (!ok) break;
+            tc_fence_after();
 #pragma unroll 1
             for (int c = 0; c < kD; c += 32) {
               float o[32];
@@ -699,54 +721,45 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         // weights 2^(s * scale - m) as bf16 pairs: the A operand of P.V_i, keys 2j, 2j + 1
-        // in column 64 + j.  A masked score is -inf and 2^-inf = +0 (m is taken as 0
-        // while the row has seen no key, so no -inf + inf)
+        // in column j.  A masked score is -inf and 2^-inf = +0 (m is taken as 0 while the
+        // row has seen no key, so no -inf + inf)
         const float2 sc2 = make_float2(sc, sc);
         const float mneg = m_run == -INFINITY ? 0.f : -m_run;
         const float2 mn2 = make_float2(mneg, mneg);
-        float lsum = 0.f;
+        float2 lq[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        uint32_t pr[32];
 #pragma unroll
-        for (int h = 1; h >= 0; --h) {  // (sums in the order of the call without a window)
-          float2 lq[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-          uint32_t pr[32];
-#pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            const float2 x = ffma2(make_float2(s[64 * h + 2 * i], s[64 * h + 2 * i + 1]), sc2, mn2);
-            const float2 e = make_float2(fast_exp2(x.x), fast_exp2(x.y));
-            lq[i & 1] = fadd2(lq[i & 1], e);
-            pr[i] = pack_bf16x2(e.x, e.y);
-          }
-          tc_st32u_nowait(s_addr + kPHalf + 32 * h, pr);
-          lsum += (lq[0].x + lq[0].y) + (lq[1].x + lq[1].y);
+        for (int i = 0; i < 32; ++i) {
+          const float2 x = ffma2(make_float2(s[2 * i], s[2 * i + 1]), sc2, mn2);
+          const float2 e = make_float2(fast_exp2(x.x), fast_exp2(x.y));
+          lq[i & 1] = fadd2(lq[i & 1], e);
+          pr[i] = pack_bf16x2(e.x, e.y);
         }
-        l_run += lsum;
+        tc_st32u_nowait(sb, pr);
+        l_run += (lq[0].x + lq[0].y) + (lq[1].x + lq[1].y);
         tc_wait_st();
         // keys without a cache row: zero their value rows (0 x NaN would poison P.V), by
-        // query tile 0's threads (P.V_1(t) follows P.V_0(t)); piece j = (key j / 2,
-        // value chunk j % 2), two per thread
-        if (qi == 0 && (mlo != ~0ull || mhi != ~0ull)) {
-          const uint32_t load = 2 * u + 1, vs = load % kSlots;
+        // query tile 0's threads (P.V_1(v) follows P.V_0(v)): (key row / 2, chunk row % 2)
+        if (qi == 0 && mtile != ~0ull) {
+          const uint32_t load = 2 * tile + 1, vs = load % kSlots;
           ok = __all_sync(0xffffffffu,
                           mbar_wait_bounded(&full[vs], (load / kSlots) & 1, abort_flag));
           if (!ok) break;
+          if (!((mtile >> (row >> 1)) & 1ull)) {
+            uint4* dst = reinterpret_cast<uint4*>(smem + kRingOff + vs * kSlotBytes +
+                                                  (row & 1) * kChunk +
+                                                  (kStep * (v & 1) + (row >> 1)) * 128);
 #pragma unroll
-          for (int hh = 0; hh < 2; ++hh) {
-            const int j = row + kM * hh;
-            const int r = j >> 1;
-            if (!((r < 64 ? mlo >> r : mhi >> (r - 64)) & 1ull)) {
-              uint4* dst = reinterpret_cast<uint4*>(smem + kRingOff + vs * kSlotBytes +
-                                                    (j & 1) * kChunk + r * 128);
-#pragma unroll
-              for (int i = 0; i < 8; ++i) dst[i] = make_uint4(0u, 0u, 0u, 0u);
-            }
+            for (int i = 0; i < 8; ++i) dst[i] = make_uint4(0u, 0u, 0u, 0u);
           }
           fence_proxy_async_smem();  // generic writes before the tensor core reads them
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[qi]);
+        if (lane == 0) mbar_arrive(&p_full[2 * qi + buf]);
       }
       if (!ok) break;
+      u += it.ntiles;
       if (it.ntiles == 0) {
         if (rvalid) {  // no key at all: a zero row
           uint4* dst = reinterpret_cast<uint4*>(p.out + qrow);
@@ -756,9 +769,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         continue;
       }
       // ---- the item's end: this thread's output row
-      ok = __all_sync(0xffffffffu, mbar_wait_bounded(&o_final[qi], done & 1, abort_flag));
+      // (the last two output products may both be under way: a wait by parity tells one phase
+      // from the next only, so each is waited for)
+      ok = (it.nsteps < 2 || mbar_wait_bounded(&pv_done[qi], (mine - 2) & 1, abort_flag)) &&
+           mbar_wait_bounded(&pv_done[qi], (mine - 1) & 1, abort_flag);
+      ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
-      ++done;
       tc_fence_after();
       const float inv = l_run > 0.f ? 1.f / l_run : 0.f;
       bool nan_row = false;
