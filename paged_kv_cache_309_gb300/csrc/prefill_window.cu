@@ -754,6 +754,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           fence_proxy_async_smem();  // generic writes before the tensor core reads them
         }
+        // The wait for the item's last output product tells one phase from the next only, so the
+        // product before it must be done by then: waited for while the last cannot begin.
+        if (v > 0 && v + 1 == it.nsteps) {
+          ok = __all_sync(0xffffffffu,
+                          mbar_wait_bounded(&pv_done[qi], (mine - 1) & 1, abort_flag));
+          if (!ok) break;
+        }
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&p_full[2 * qi + buf]);
@@ -769,11 +776,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         continue;
       }
       // ---- the item's end: this thread's output row
-      // (the last two output products may both be under way: a wait by parity tells one phase
-      // from the next only, so each is waited for)
-      ok = (it.nsteps < 2 || mbar_wait_bounded(&pv_done[qi], (mine - 2) & 1, abort_flag)) &&
-           mbar_wait_bounded(&pv_done[qi], (mine - 1) & 1, abort_flag);
-      ok = __all_sync(0xffffffffu, ok);
+      ok = __all_sync(0xffffffffu, mbar_wait_bounded(&pv_done[qi], (mine - 1) & 1, abort_flag));
       if (!ok) break;
       tc_fence_after();
       const float inv = l_run > 0.f ? 1.f / l_run : 0.f;
