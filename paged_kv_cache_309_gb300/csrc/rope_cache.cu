@@ -24,8 +24,9 @@ namespace {
 
 using namespace pa;
 
-constexpr int kWarps = 8;  // per CTA
-constexpr int kSteps = 4;  // head groups per warp: 8 loads of 16 bytes in flight per lane (16-bit source)
+constexpr int kWarps = 4;  // per CTA
+constexpr int kCtasPerSm = 8;
+constexpr int kSteps = 2;  // head groups per warp: 8 loads of 16 bytes in flight per lane (16-bit source)
 
 // Plain loads: q may be rotated in place, so the rows are not read-only.
 __device__ __forceinline__ uint4 ld16(const void* p) {
@@ -48,46 +49,93 @@ __device__ __forceinline__ Vec8<T> load_chunk(const T* p) {
   return v;
 }
 
-__device__ __forceinline__ void rotate(float& x, float& y, float c, float s) {
-  const float u = __fsub_rn(__fmul_rn(x, c), __fmul_rn(y, s));
-  y = __fadd_rn(__fmul_rn(y, c), __fmul_rn(x, s));
-  x = u;
+// Eight fp32 values as four pairs: paired instructions round each half as the scalar
+// ones do, and halve the instructions (which bound short rows: at 18 a chunk more a
+// batch of 5001 tokens took twice as long).
+struct F2x4 {
+  float2 v[4];
+};
+__device__ __forceinline__ float2 add2_rn(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 ra, rb, rd;\n\t"
+      "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
+      "add.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
 }
-
-// eight cached values of D from fp32, through the division by a scale
-template <typename D>
-__device__ __forceinline__ Vec8<D> to_cache(float (&f)[8], bool scaled, const Divisor& d) {
-  if (scaled) {
-    if constexpr (std::is_same<D, e4m3>::value) {
-      Vec8<float> v = from_f32<float>(f);
-      div8_for_e4m3(v, f, d, fminf(1.7e38f * d.s, 3.0e38f));
-    } else {
+template <typename T>
+__device__ __forceinline__ F2x4 widen(const Vec8<T>& x) {
+  F2x4 r;
+  float f[8];
+  to_f32(x, f);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) f[e] = div_rn(f[e], d);
-    }
+  for (int i = 0; i < 4; ++i) r.v[i] = make_float2(f[2 * i], f[2 * i + 1]);
+  return r;
+}
+template <typename T>
+__device__ __forceinline__ Vec8<T> narrow(const F2x4& x) {
+  if constexpr (std::is_same<T, bf16>::value) {
+    return {make_uint4(pack_bf16x2(x.v[0].x, x.v[0].y), pack_bf16x2(x.v[1].x, x.v[1].y),
+                       pack_bf16x2(x.v[2].x, x.v[2].y), pack_bf16x2(x.v[3].x, x.v[3].y))};
+  } else if constexpr (std::is_same<T, f16>::value) {
+    return {make_uint4(pack_f16x2(x.v[0].x, x.v[0].y), pack_f16x2(x.v[1].x, x.v[1].y),
+                       pack_f16x2(x.v[2].x, x.v[2].y), pack_f16x2(x.v[3].x, x.v[3].y))};
+  } else {
+    const float f[8] = {x.v[0].x, x.v[0].y, x.v[1].x, x.v[1].y,
+                        x.v[2].x, x.v[2].y, x.v[3].x, x.v[3].y};
+    return from_f32<T>(f);
+  }
+}
+// eight cached values of D, through the division by a scale
+template <typename D>
+__device__ __forceinline__ Vec8<D> divided(const F2x4& x, const Divisor& d) {
+  float f[8] = {x.v[0].x, x.v[0].y, x.v[1].x, x.v[1].y, x.v[2].x, x.v[2].y, x.v[3].x, x.v[3].y};
+  if constexpr (std::is_same<D, e4m3>::value) {
+    const Vec8<float> v = from_f32<float>(f);
+    div8_for_e4m3(v, f, d, fminf(1.7e38f * d.s, 3.0e38f));
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f[e] = div_rn(f[e], d);
   }
   return from_f32<D>(f);
 }
 
-template <typename S, typename D, bool kInterleaved>
-__global__ void __launch_bounds__(kWarps * 32) rope_and_cache_kernel(const RopeArgs a) {
+// Rounded products, one by one: a paired mul.rn was joined with the paired add.rn after it (one
+// element in 30 thousand differed).  A paired instruction takes two issue cycles of the
+// pipe, so nothing is lost in the pipe.
+__device__ __forceinline__ float2 product(float2 a, float2 b) {
+  return make_float2(__fmul_rn(a.x, b.x), __fmul_rn(a.y, b.y));
+}
+// Pairs (x, y), the members in separate registers: x c + -(y s) is the rounded difference.
+__device__ __forceinline__ void rotate_apart(float2& x, float2& y, float2 c, float2 s) {
+  const float2 u = add2_rn(product(x, c), product(make_float2(-y.x, -y.y), s));
+  y = add2_rn(product(y, c), product(x, s));
+  x = u;
+}
+// One pair (p.x, p.y): (p.x c + -p.y s, p.y c + p.x s)
+__device__ __forceinline__ float2 rotate_one(float2 p, float c, float s) {
+  return add2_rn(product(p, make_float2(c, c)), product(make_float2(-p.y, p.x), make_float2(s, s)));
+}
+
+template <typename S, typename D, bool kInterleaved, bool kScaled>
+__global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) rope_and_cache_kernel(const RopeArgs a) {
   const int lane = threadIdx.x & 31;
   const uint32_t wid = blockIdx.x * kWarps + (threadIdx.x >> 5);
   const uint32_t t32 = wid / a.parts;
   const int64_t t = t32;
   if (t >= a.num_tokens) return;
-  const int part = static_cast<int>(wid - t32 * a.parts);
+  const int step0 = static_cast<int>(wid - t32 * a.parts) * kSteps;
 
+  // position and slot together; the rows' loads do not wait for them (a padded token's rows are
+  // read in vain), but behind a second slot table, where most tokens may have no slot
   const int64_t pos = __ldg(a.positions + t);
-  if (pos < 0 || pos >= a.max_positions) return;
   int64_t slot = __ldg(a.slot_mapping + t);
   if (a.swa != nullptr && slot >= 0) slot = slot < a.swa_len ? __ldg(a.swa + slot) : -1;
-  if (slot >= a.num_slots) slot = -1;
 
   // this lane's item: its two chunks (element offsets inside a head) and pairs
   const int item = lane & ((1 << a.log2_lanes) - 1);
-  const int rot_items = a.rot_dim >> 4;
-  const bool turned = item < rot_items;
+  const bool turned = item < a.rot_dim >> 4;
   int c0, c1;
   if (turned && !kInterleaved) {
     c0 = 8 * item;
@@ -97,87 +145,93 @@ __global__ void __launch_bounds__(kWarps * 32) rope_and_cache_kernel(const RopeA
     c1 = c0 + 8;
   }
   const bool has0 = c0 < a.head_size, has1 = c1 < a.head_size;
-  float cs[8], sn[8];
-  if (turned) {
-    const float4* row = reinterpret_cast<const float4*>(a.cos_sin + pos * a.rot_dim + 8 * item);
-    const float4* sow = row + (a.rot_dim >> 3);
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const float4 x = __ldg(row + i), y = __ldg(sow + i);
-      cs[4 * i] = x.x, cs[4 * i + 1] = x.y, cs[4 * i + 2] = x.z, cs[4 * i + 3] = x.w;
-      sn[4 * i] = y.x, sn[4 * i + 1] = y.y, sn[4 * i + 2] = y.z, sn[4 * i + 3] = y.w;
-    }
-  }
-
-  const int heads_per_step = 32 >> a.log2_lanes;
-  const int head0 = part * kSteps * heads_per_step + (lane >> a.log2_lanes);
-  const int hq = a.num_q_heads, hk = a.num_kv_heads;
-  const int64_t blk = slot < 0 ? 0
-                      : (a.block_size & (a.block_size - 1)) == 0
-                          ? slot >> (__ffs(a.block_size) - 1)
-                          : slot / a.block_size;
-  const int64_t dst0 =
-      blk * a.block_stride + (slot - blk * a.block_size) * hk * static_cast<int64_t>(a.head_size);
-  auto source = [&](int h) -> const S* {
-    if (h < hq) return static_cast<const S*>(a.q) + t * a.q_stride + h * a.head_size;
-    if (h < hq + hk)
-      return static_cast<const S*>(a.key) + t * a.key_stride + (h - hq) * a.head_size;
-    return static_cast<const S*>(a.value) + t * a.value_stride + (h - hq - hk) * a.head_size;
+  const int log2_heads = 5 - a.log2_lanes;  // heads side by side
+  // a step is such a group of heads of q (the first ones), of k or of v: kind 0, 1, 2
+  auto kind_of = [&](int step) { return step < a.q_steps ? 0 : step < a.q_steps + a.kv_steps ? 1 : 2; };
+  auto head_of = [&](int step, int kind) {
+    const int first = kind == 0 ? 0 : kind == 1 ? a.q_steps : a.q_steps + a.kv_steps;
+    return ((step - first) << log2_heads) + (lane >> a.log2_lanes);
   };
 
   Vec8<S> x[kSteps], y[kSteps];
 #pragma unroll
   for (int i = 0; i < kSteps; ++i) {
-    const int h = head0 + i * heads_per_step;
-    if (h < a.all_heads && (h < hq || slot >= 0)) {
-      const S* src = source(h);
+    const int kind = kind_of(step0 + i), h = head_of(step0 + i, kind);
+    if (h < (kind == 0 ? a.num_q_heads : a.num_kv_heads) &&
+        (kind == 0 || a.swa == nullptr || slot >= 0)) {
+      const S* src = kind == 0   ? static_cast<const S*>(a.q) + t * a.q_stride
+                     : kind == 1 ? static_cast<const S*>(a.key) + t * a.key_stride
+                                 : static_cast<const S*>(a.value) + t * a.value_stride;
+      src += h * a.head_size;
       if (has0) x[i] = load_chunk(src + c0);
       if (has1) y[i] = load_chunk(src + c1);
     }
   }
-  const bool scaled = a.k_scale != nullptr;
-  const Divisor ks = make_divisor(scaled ? __ldg(a.k_scale) : 1.f);
-  const Divisor vs = make_divisor(scaled ? __ldg(a.v_scale) : 1.f);
-  const bool raw = std::is_same<S, D>::value && !scaled;
+  if (pos < 0 || pos >= a.max_positions) return;
+  if (slot >= a.num_slots) slot = -1;
+  float2 cs[4], sn[4];
+  if (turned && kind_of(step0) < 2) {
+    const float4* row = reinterpret_cast<const float4*>(a.cos_sin + pos * a.rot_dim + 8 * item);
+    const float4* sow = row + (a.rot_dim >> 3);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float4 c = __ldg(row + i), s = __ldg(sow + i);
+      cs[2 * i] = make_float2(c.x, c.y), cs[2 * i + 1] = make_float2(c.z, c.w);
+      sn[2 * i] = make_float2(s.x, s.y), sn[2 * i + 1] = make_float2(s.z, s.w);
+    }
+  }
+  const int64_t blk = slot < 0 ? 0
+                      : (a.block_size & (a.block_size - 1)) == 0
+                          ? slot >> (__ffs(a.block_size) - 1)
+                          : slot / a.block_size;
+  const int64_t dst0 = blk * a.block_stride + (slot - blk * a.block_size) * a.num_kv_heads *
+                                                  static_cast<int64_t>(a.head_size);
+  constexpr bool kRaw = std::is_same<S, D>::value && !kScaled;
 #pragma unroll
   for (int i = 0; i < kSteps; ++i) {
-    const int h = head0 + i * heads_per_step;
-    if (h >= a.all_heads || (h >= hq && slot < 0)) continue;
-    const bool is_q = h < hq, is_v = h >= hq + hk;
-    const bool turn = turned && !is_v;
-    float f[8], g[8];
-    to_f32(x[i], f);
-    to_f32(y[i], g);
+    const int kind = kind_of(step0 + i), h = head_of(step0 + i, kind);
+    if (h >= (kind == 0 ? a.num_q_heads : a.num_kv_heads) || (kind != 0 && slot < 0)) continue;
+    F2x4 f, g;
+    const bool turn = turned && kind != 2;
     if (turn) {
+      f = widen(x[i]);
+      g = widen(y[i]);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
+      for (int e = 0; e < 4; ++e) {
         if constexpr (kInterleaved) {
-          if (e < 4) {
-            rotate(f[2 * e], f[2 * e + 1], cs[e], sn[e]);
-          } else {
-            rotate(g[2 * e - 8], g[2 * e - 7], cs[e], sn[e]);
-          }
+          f.v[e] = rotate_one(f.v[e], (e & 1) ? cs[e >> 1].y : cs[e >> 1].x,
+                              (e & 1) ? sn[e >> 1].y : sn[e >> 1].x);
+          g.v[e] = rotate_one(g.v[e], (e & 1) ? cs[2 + (e >> 1)].y : cs[2 + (e >> 1)].x,
+                              (e & 1) ? sn[2 + (e >> 1)].y : sn[2 + (e >> 1)].x);
         } else {
-          rotate(f[e], g[e], cs[e], sn[e]);
+          rotate_apart(f.v[e], g.v[e], cs[e], sn[e]);
         }
       }
     }
-    if (is_q) {
-      S* dst = static_cast<S*>(a.q_out) + t * a.q_out_stride + h * a.head_size;
-      if (has0) store8(dst + c0, turn ? from_f32<S>(f) : x[i]);
-      if (has1) store8(dst + c1, turn ? from_f32<S>(g) : y[i]);
+    // what is not turned keeps its bits where the type stays
+    if (kind == 0 || kRaw) {
+      if (turn) {
+        x[i] = narrow<S>(f);
+        y[i] = narrow<S>(g);
+      }
+      S* dst = kind == 0 ? static_cast<S*>(a.q_out) + t * a.q_out_stride
+                         : static_cast<S*>(kind == 1 ? a.key_cache : a.value_cache) + dst0;
+      dst += h * a.head_size;
+      if (has0) store8(dst + c0, x[i]);
+      if (has1) store8(dst + c1, y[i]);
     } else {
-      const int hh = is_v ? h - hq - hk : h - hq;
-      D* dst = static_cast<D*>(is_v ? a.value_cache : a.key_cache) + dst0 + hh * a.head_size;
-      if (raw && !turn) {  // the bits as they are
-        if constexpr (std::is_same<S, D>::value) {
-          if (has0) store8(dst + c0, x[i]);
-          if (has1) store8(dst + c1, y[i]);
-        }
+      if (!turn) {
+        f = widen(x[i]);
+        g = widen(y[i]);
+      }
+      D* dst = static_cast<D*>(kind == 1 ? a.key_cache : a.value_cache) + dst0 + h * a.head_size;
+      if constexpr (kScaled) {
+        const Divisor d = make_divisor(__ldg(kind == 1 ? a.k_scale : a.v_scale));
+        if (has0) store8(dst + c0, divided<D>(f, d));
+        if (has1) store8(dst + c1, divided<D>(g, d));
       } else {
-        const Divisor& d = is_v ? vs : ks;
-        if (has0) store8(dst + c0, to_cache<D>(f, scaled, d));
-        if (has1) store8(dst + c1, to_cache<D>(g, scaled, d));
+        if (has0) store8(dst + c0, narrow<D>(f));
+        if (has1) store8(dst + c1, narrow<D>(g));
       }
     }
   }
@@ -185,11 +239,12 @@ __global__ void __launch_bounds__(kWarps * 32) rope_and_cache_kernel(const RopeA
 
 template <typename S, typename D>
 pa_status launch_typed(const RopeArgs& a, bool interleaved, unsigned grid, cudaStream_t stream) {
-  if (interleaved) {
-    rope_and_cache_kernel<S, D, true><<<grid, kWarps * 32, 0, stream>>>(a);
-  } else {
-    rope_and_cache_kernel<S, D, false><<<grid, kWarps * 32, 0, stream>>>(a);
-  }
+  const bool scaled = a.k_scale != nullptr;
+  const auto kernel = interleaved ? (scaled ? rope_and_cache_kernel<S, D, true, true>
+                                            : rope_and_cache_kernel<S, D, true, false>)
+                                  : (scaled ? rope_and_cache_kernel<S, D, false, true>
+                                            : rope_and_cache_kernel<S, D, false, false>);
+  kernel<<<grid, kWarps * 32, 0, stream>>>(a);
   return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
@@ -212,9 +267,10 @@ pa_status launch_rope_and_cache(RopeArgs a, pa_dtype src, pa_dtype dst, bool int
   const int items = (a.rot_dim >> 4) + (((a.head_size - a.rot_dim) / 8 + 1) >> 1);
   a.log2_lanes = 0;
   while ((1 << a.log2_lanes) < items) ++a.log2_lanes;
-  a.all_heads = a.num_q_heads + 2 * a.num_kv_heads;
-  const int per_warp = kSteps * (32 >> a.log2_lanes);
-  a.parts = static_cast<uint32_t>((a.all_heads + per_warp - 1) / per_warp);
+  const int heads = 32 >> a.log2_lanes;
+  a.q_steps = (a.num_q_heads + heads - 1) / heads;
+  a.kv_steps = (a.num_kv_heads + heads - 1) / heads;
+  a.parts = static_cast<uint32_t>((a.q_steps + 2 * a.kv_steps + kSteps - 1) / kSteps);
   const int64_t warps = a.num_tokens * a.parts;
   if (warps > 0x7FFFFFFFll) return PA_ERR_UNSUPPORTED;
   const unsigned grid = static_cast<unsigned>((warps + kWarps - 1) / kWarps);

@@ -21,8 +21,9 @@ struct RopeArgs {
   int64_t swa_len, num_tokens, max_positions, num_slots;
   int64_t q_out_stride, q_stride, key_stride, value_stride, block_stride;  // elements
   int32_t num_q_heads, num_kv_heads, head_size, rot_dim, block_size;
-  // set by the launcher: lanes of a head (log2), q + k + v heads, warps per token
-  int32_t log2_lanes, all_heads;
+  // set by the launcher: lanes of a head (log2), steps of q's heads and of k's (and v's),
+  // warps per token
+  int32_t log2_lanes, q_steps, kv_steps;
   uint32_t parts;
 };
 pa_status launch_rope_and_cache(RopeArgs a, pa_dtype src, pa_dtype dst, bool interleaved,
