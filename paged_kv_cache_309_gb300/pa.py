@@ -819,6 +819,29 @@ def pa_cache_compact(k_cache, v_cache, keep, keep_lens, src_block_tables, dst_bl
 
 
 # --------------------------------------------------------- sliding window --
+# These calls come once per layer and token, where the host's time is what counts: their checks
+# read each tensor's properties once, and the messages are made where a check failed.
+def _all_here(*tensors):
+    """Whether every tensor is a CUDA tensor on the current device: that device, else -1."""
+    try:
+        cur = tensors[0].get_device()
+        for t in tensors:
+            if t.get_device() != cur:
+                return -1
+    except AttributeError:
+        return -1
+    return cur if cur >= 0 and cur == torch.cuda.current_device() else -1
+
+
+def _stream_on(device, stream):
+    """_stream for a device already known to be the current one."""
+    if stream is None:
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        if raw is not None:
+            return raw(device)
+    return _stream(stream)
+
+
 def pa_rope_and_cache(q_out, q, key, value, key_cache, value_cache, cos_sin, positions,
                       slot_mapping, interleaved=False, swa_slot_mapping=None, k_scale=None,
                       v_scale=None, stream=None):
@@ -830,44 +853,59 @@ def pa_rope_and_cache(q_out, q, key, value, key_cache, value_cache, cos_sin, pos
     interleaved, (2 i, 2 i + 1).  q, q_out, key and value share a dtype and have
     free token strides; q_out may be q.  Optional swa table int64,
     k_scale/v_scale one-element float32 device tensors."""
-    _on_device(q_out=q_out, q=q, key=key, value=value, key_cache=key_cache,
-               value_cache=value_cache, cos_sin=cos_sin, positions=positions,
-               slot_mapping=slot_mapping, swa_slot_mapping=swa_slot_mapping)
-    if k_scale is not None or v_scale is not None:
-        _scales(k_scale, v_scale)
-    N, HQ, d = q.shape
-    H = key.shape[1]
-    kind, shape = q.dtype, key.shape
-    for t, name in ((q_out, "q_out"), (q, "q"), (key, "key"), (value, "value")):
-        _, s1, s2 = t.stride()
-        if t.dtype != kind or s2 != 1 or (s1 != d and t.shape[1] != 1):
-            raise ValueError(f"{name} must share q's dtype, heads and elements contiguous")
-    if q_out.shape != q.shape or shape != (N, H, d) or value.shape != shape:
+    device = _all_here(q, q_out, key, value, key_cache, value_cache, cos_sin, positions,
+                       slot_mapping)
+    if device < 0:
+        _on_device(q_out=q_out, q=q, key=key, value=value, key_cache=key_cache,
+                   value_cache=value_cache, cos_sin=cos_sin, positions=positions,
+                   slot_mapping=slot_mapping)
+    kind, shape, cache_shape = q.dtype, key.shape, key_cache.shape
+    N, HQ, d = q_shape = q.shape
+    H = shape[1]
+    sq, s1, s2 = q.stride()
+    so, s3, s4 = q_out.stride()
+    sk, s5, s6 = key.stride()
+    sv, s7, s8 = value.stride()
+    if not (s2 == s4 == s6 == s8 == 1 and (s1 == s3 == d or HQ == 1) and (s5 == s7 == d or H == 1)):
+        raise ValueError("q_out, q, key and value: heads and elements must be contiguous")
+    if q_out.dtype != kind or key.dtype != kind or value.dtype != kind:
+        raise ValueError("q_out, key and value must share q's dtype")
+    if q_out.shape != q_shape or shape != (N, H, d) or value.shape != shape:
         raise ValueError("q_out must match q; key and value must be [N, H, d]")
-    nb, bs, Hc, dc = key_cache.shape
+    nb, bs, Hc, dc = cache_shape
     strides = key_cache.stride()
-    if (Hc, dc) != (H, d) or strides[1:] != (H * d, d, 1):
+    sb, r1, r2, r3 = strides
+    if Hc != H or dc != d or r3 != 1 or r2 != d or r1 != H * d:
         raise ValueError("key_cache must be [num_blocks, bs, H, d], contiguous inside a block")
-    if value_cache.shape != key_cache.shape or value_cache.stride() != strides \
-            or value_cache.dtype != key_cache.dtype:
+    cache_kind = key_cache.dtype
+    if value_cache.shape != cache_shape or value_cache.stride() != strides \
+            or value_cache.dtype != cache_kind:
         raise ValueError("value_cache must match key_cache")
     if cos_sin.dtype != torch.float32 or cos_sin.dim() != 2 or not cos_sin.is_contiguous():
         raise ValueError("cos_sin must be float32 [max_positions, rot_dim], contiguous")
-    for t, name in ((positions, "positions"), (slot_mapping, "slot_mapping")):
-        if t.dtype != torch.int64 or t.numel() != N or not t.is_contiguous():
-            raise ValueError(f"{name} must be int64 [N]")
+    if positions.dtype != torch.int64 or positions.numel() != N or not positions.is_contiguous():
+        raise ValueError("positions must be int64 [N]")
+    if slot_mapping.dtype != torch.int64 or slot_mapping.numel() != N \
+            or not slot_mapping.is_contiguous():
+        raise ValueError("slot_mapping must be int64 [N]")
+    swa = ks = vs = None
     swa_len = 0
     if swa_slot_mapping is not None:
+        _on_device(swa_slot_mapping=swa_slot_mapping)
         if swa_slot_mapping.dtype != torch.int64 or not swa_slot_mapping.is_contiguous():
             raise ValueError("swa_slot_mapping must be int64, contiguous")
-        swa_len = swa_slot_mapping.numel()
+        swa, swa_len = swa_slot_mapping.data_ptr(), swa_slot_mapping.numel()
+    if k_scale is not None or v_scale is not None:
+        _scales(k_scale, v_scale)
+        ks, vs = k_scale.data_ptr(), v_scale.data_ptr()
+    most, rot = cos_sin.shape
     st = _load().pa_rope_and_cache(
-        _ptr(q_out), _ptr(q), _ptr(key), _ptr(value), _dtype(q), N, HQ, H, d, q_out.stride(0),
-        q.stride(0), key.stride(0), value.stride(0), _ptr(cos_sin), _ptr(positions),
-        cos_sin.shape[0], _i32("rot_dim", cos_sin.shape[1]), int(bool(interleaved)), _ptr(key_cache),
-        _ptr(value_cache), _dtype(key_cache), nb, bs, strides[0], _ptr(slot_mapping),
-        _ptr(swa_slot_mapping), swa_len, _ptr(k_scale), _ptr(v_scale), _stream(stream))
-    _check(st, "pa_rope_and_cache")
+        q_out.data_ptr(), q.data_ptr(), key.data_ptr(), value.data_ptr(), _dtype(q), N, HQ, H, d,
+        so, sq, sk, sv, cos_sin.data_ptr(), positions.data_ptr(), most, _i32("rot_dim", rot),
+        1 if interleaved else 0, key_cache.data_ptr(), value_cache.data_ptr(), _dtype(key_cache),
+        nb, bs, sb, slot_mapping.data_ptr(), swa, swa_len, ks, vs, _stream_on(device, stream))
+    if st != PA_OK:
+        raise PAError(st, "pa_rope_and_cache")
 
 
 def pa_paged_window_decode_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_size, window,
@@ -886,6 +924,32 @@ def window_decode_workspace(num_seqs, num_q_heads, num_kv_heads, head_size, wind
     return torch.zeros(max(n, 256), dtype=torch.uint8, device=device or "cuda")
 
 
+def _window_shapes(out, q, k_cache, v_cache, block_tables, context_lens, others):
+    """Checks shared by the window attention calls: (device, B, H_Q, H_KV, d, block_size,
+    num_blocks, max_blocks_per_seq)."""
+    device = _all_here(q, out, k_cache, v_cache, block_tables, context_lens, *others)
+    if device < 0:
+        _on_device(out=out, q=q, k_cache=k_cache, v_cache=v_cache, block_tables=block_tables,
+                   context_lens=context_lens)
+    q_shape, shape, kind = q.shape, k_cache.shape, k_cache.dtype
+    _, HQ, d = q_shape
+    nb, bs, HKV, row = shape
+    if not (q.is_contiguous() and out.is_contiguous() and k_cache.is_contiguous()
+            and v_cache.is_contiguous() and block_tables.is_contiguous()
+            and context_lens.is_contiguous()):
+        raise ValueError("out, q, caches, block_tables and lengths must be contiguous")
+    if q.dtype != torch.bfloat16 or out.dtype != torch.bfloat16 or out.shape != q_shape:
+        raise ValueError("q and out must be bf16 and of one shape")
+    if v_cache.dtype != kind or v_cache.shape != shape or row != d:
+        raise ValueError("v_cache must match k_cache, rows of d elements")
+    B = context_lens.numel()
+    if block_tables.dtype != torch.int32 or context_lens.dtype != torch.int32:
+        raise ValueError("block_tables and context_lens must be int32")
+    if block_tables.dim() != 2 or block_tables.shape[0] != B:
+        raise ValueError("block_tables must be [B, max_blocks_per_seq], context_lens [B]")
+    return device, B, HQ, HKV, d, bs, nb, block_tables.shape[1]
+
+
 def pa_paged_window_decode_attention(out, q, k_cache, v_cache, block_tables, context_lens, window,
                                      num_sink, scale, max_context_len, workspace, k_scale=None,
                                      v_scale=None, stream=None):
@@ -893,21 +957,26 @@ def pa_paged_window_decode_attention(out, q, k_cache, v_cache, block_tables, con
     over each sequence's last `window` tokens and its first num_sink; other
     arguments as for pa_paged_decode_attention, workspace from
     window_decode_workspace."""
-    B, HQ, HKV, d, bs, nb = _decode_shapes(out, q, k_cache, v_cache, block_tables, context_lens,
-                                           workspace)
+    device, B, HQ, HKV, d, bs, nb, width = _window_shapes(out, q, k_cache, v_cache, block_tables,
+                                                          context_lens, (workspace,))
+    if device < 0 or not workspace.is_contiguous():
+        _workspace(workspace)
+    if q.shape[0] != B:
+        raise ValueError("q must be [B, H_Q, d]")
+    ks = vs = None
     if k_scale is not None or v_scale is not None:
         _scales(k_scale, v_scale)
         if k_cache.dtype != torch.float8_e4m3fn:
             raise ValueError("k_scale/v_scale apply to an e4m3 cache")
-    window, num_sink = _i32("window", window), _i32("num_sink", num_sink)
-    max_context_len = _i32("max_context_len", max_context_len)
-    dtype = PA_Q4 if k_cache.dtype == torch.uint8 else _dtype(k_cache)
+        ks, vs = k_scale.data_ptr(), v_scale.data_ptr()
     st = _load().pa_paged_window_decode_attention(
-        _ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache), dtype, _ptr(k_scale), _ptr(v_scale),
-        _ptr(block_tables), _ptr(context_lens), B, HQ, HKV, d, bs, block_tables.shape[1], nb,
-        window, num_sink, float(scale), max_context_len, _ptr(workspace),
-        workspace.numel() * workspace.element_size(), _stream(stream))
-    _check(st, "pa_paged_window_decode_attention")
+        out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), _dtype(k_cache), ks,
+        vs, block_tables.data_ptr(), context_lens.data_ptr(), B, HQ, HKV, d, bs, width, nb,
+        _i32("window", window), _i32("num_sink", num_sink), float(scale),
+        _i32("max_context_len", max_context_len), workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), _stream_on(device, stream))
+    if st != PA_OK:
+        raise PAError(st, "pa_paged_window_decode_attention")
 
 
 def pa_paged_window_prefill_attention(out, q, k_cache, v_cache, block_tables, cu_seqlens_q,
@@ -916,32 +985,22 @@ def pa_paged_window_prefill_attention(out, q, k_cache, v_cache, block_tables, cu
     """Causal varlen prefill where the query at position p sees tokens
     t <= p with t > p - window or t < num_sink; other arguments as for
     pa_paged_prefill_attention."""
-    _word(error_word, "error_word")
-    _on_device(out=out, q=q, k_cache=k_cache, v_cache=v_cache, block_tables=block_tables,
-               cu_seqlens_q=cu_seqlens_q, context_lens=context_lens)
     if error_word is None:
         raise ValueError("error_word is required")
-    T, HQ, d = q.shape
-    nb, bs, HKV, dc = k_cache.shape
-    B = context_lens.numel()
-    for t, name in ((q, "q"), (out, "out"), (k_cache, "k_cache"), (v_cache, "v_cache"),
-                    (block_tables, "block_tables"), (cu_seqlens_q, "cu_seqlens_q"),
-                    (context_lens, "context_lens")):
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
-    if q.dtype != torch.bfloat16 or out.dtype != torch.bfloat16 or out.shape != q.shape:
-        raise ValueError("q and out must be bf16 [total_new, H_Q, d]")
-    if v_cache.dtype != k_cache.dtype or v_cache.shape != k_cache.shape or dc != d:
-        raise ValueError("v_cache must match k_cache, rows of d elements")
-    if cu_seqlens_q.dtype != torch.int32 or context_lens.dtype != torch.int32 \
-            or cu_seqlens_q.numel() != B + 1:
-        raise ValueError("cu_seqlens_q must be int32 [B + 1], context_lens int32 [B]")
-    if block_tables.dtype != torch.int32 or block_tables.dim() != 2 or block_tables.shape[0] != B:
-        raise ValueError("block_tables must be int32 [B, max_blocks_per_seq]")
-    window, num_sink = _i32("window", window), _i32("num_sink", num_sink)
+    device, B, HQ, HKV, d, bs, nb, width = _window_shapes(
+        out, q, k_cache, v_cache, block_tables, context_lens, (cu_seqlens_q, error_word))
+    if device < 0:
+        _on_device(cu_seqlens_q=cu_seqlens_q)
+    if device < 0 or error_word.dtype != torch.int32 or error_word.numel() < 1:
+        _word(error_word, "error_word")
+    if cu_seqlens_q.dtype != torch.int32 or cu_seqlens_q.numel() != B + 1 \
+            or not cu_seqlens_q.is_contiguous():
+        raise ValueError("cu_seqlens_q must be int32 [B + 1]")
     st = _load().pa_paged_window_prefill_attention(
-        _ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache), _dtype(k_cache), _ptr(block_tables),
-        _ptr(cu_seqlens_q), _ptr(context_lens), B, HQ, HKV, d, bs, block_tables.shape[1], nb,
-        window, num_sink, float(scale), _i32("max_q_len", max_q_len), T, _ptr(error_word),
-        _stream(stream))
-    _check(st, "pa_paged_window_prefill_attention")
+        out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), _dtype(k_cache),
+        block_tables.data_ptr(), cu_seqlens_q.data_ptr(), context_lens.data_ptr(), B, HQ, HKV, d,
+        bs, width, nb, _i32("window", window), _i32("num_sink", num_sink), float(scale),
+        _i32("max_q_len", max_q_len), q.shape[0], error_word.data_ptr(),
+        _stream_on(device, stream))
+    if st != PA_OK:
+        raise PAError(st, "pa_paged_window_prefill_attention")
