@@ -12,7 +12,8 @@
 // (q4_cut.h, decode_pieces.cuh): one wave of CTAs (two per SM), each with an equal share of all
 // sequences' units of 64 places, walking its pieces with the copy ring running on
 // across them; sequences that lie in one chunk are written directly, the
-// others' pieces are merged by a second, dependent launch.
+// others' pieces are merged by a second, dependent launch.  Where every CTA takes whole
+// sequences in about the same time, nothing is cut.
 //
 // Per tile a producer warp looks up blocks and issues TMA copies (128-byte swizzled);
 // four consumer warps take 16 (bf16, tiles of 64) or 32 (e4m3, tiles of 128) places each:
@@ -82,6 +83,76 @@ struct Lay {
   static_assert(kBarOffset % 8 == 0 && kMaskOffset % 16 == 0 && kSchedOffset % 8 == 0, "aligned");
   static_assert((kAlloc + 1024) * kCtasPerSm <= 228 * 1024, "resident CTAs fit");
 };
+
+// What the pieces of one (sequence, query head) come to: weights 2^(lse - max), by one warp (lane:
+// four head elements).  `slot(i)`: place of piece i; partials are read through L2.
+template <int kAhead, typename Slot>
+__device__ __forceinline__ void merge_row(const DecodeParams& p, int64_t bh, int n, int lane,
+                                          const Slot& slot) {
+  float M = -INFINITY;  // (a NaN lse is carried to the output)
+  for (int i = lane; i < n; i += 32) M = max_nan(M, __ldcg(p.ws_lse + slot(i)));
+#pragma unroll
+  for (int off = 16; off >= 1; off >>= 1) M = max_nan(M, __shfl_xor_sync(0xffffffffu, M, off));
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  float W = 0.f;
+  if (M != -INFINITY) {
+#pragma unroll 1
+    for (int i0 = 0; i0 < n; i0 += kAhead) {
+      float4 v[kAhead];
+      float w[kAhead];
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        if (i0 + k < n) {
+          const int64_t at = slot(i0 + k);
+          v[k] = __ldcg(reinterpret_cast<const float4*>(p.ws_o + at * kD) + lane);
+          w[k] = exp2f(__ldcg(p.ws_lse + at) - M);
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        if (i0 + k < n) {
+          W += w[k];
+          acc.x += w[k] * v[k].x;
+          acc.y += w[k] * v[k].y;
+          acc.z += w[k] * v[k].z;
+          acc.w += w[k] * v[k].w;
+        }
+      }
+    }
+  }
+  const float inv = W == 0.f ? 0.f : 1.f / W;
+  *reinterpret_cast<uint2*>(p.out + bh * kD + lane * 4) =
+      make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+}
+
+// The second launch: a warp per (split sequence, query head); a CTA looks at 32
+// sequences a time and takes every gridDim.y-th.
+constexpr int kMergeThreads = 128;
+__global__ void __launch_bounds__(kMergeThreads)
+    merge_split_kernel(const __grid_constant__ PieceParams qp, int G, int chunks) {
+  const DecodeParams& p = qp.d;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int hq = blockIdx.x * (kMergeThreads / 32) + warp;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (hq >= p.num_q_heads) return;
+  const int g = hq / G;
+  for (int first = blockIdx.y; first < qp.num_seqs; first += 32 * gridDim.y) {
+    const int mine = first + lane * gridDim.y;
+    const int32_t info =
+        mine < qp.num_seqs ? __ldcg(qp.info + static_cast<int64_t>(g) * qp.num_seqs + mine) : 0;
+    for (uint32_t todo = __ballot_sync(0xffffffffu, info != 0); todo != 0u; todo &= todo - 1u) {
+      const int l = __ffs(todo) - 1;
+      const int32_t x = __shfl_sync(0xffffffffu, info, l);
+      const int b = first + l * gridDim.y, c_first = x >> 16;
+      merge_row<8>(p, static_cast<int64_t>(b) * p.num_q_heads + hq, x & 0xFFFF, lane, [&](int i) {
+        return (static_cast<int64_t>(g) * qp.slots +
+                slot_of_piece(chunks, qp.num_seqs, b, c_first, c_first + i)) *
+                   G +
+               hq % G;
+      });
+    }
+  }
+}
 
 template <int NT, bool kFp8>
 __global__ void __launch_bounds__(kThreads, Lay<NT, kFp8>::kCtasPerSm)
@@ -603,9 +674,9 @@ struct WindowPlan {
   size_t lse_offset, o_offset, info_offset, bytes;
 };
 
-// Sequences of up to so many units of 64 places are not cut: a piece's own start and end cost
-// about two units, and the merge is a launch of its own.
-constexpr int64_t kWholeUnits = 4;
+// Cutting costs a second launch and a merge, about as much time as a CTA takes for so many
+// units; a piece's own start and end about two.
+constexpr int64_t kMergeUnits = 6;
 
 WindowPlan plan_of(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads, int32_t window,
                    int32_t num_sink, int32_t max_context_len) {
@@ -617,9 +688,16 @@ WindowPlan plan_of(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads, 
   const int64_t units = (most + kUnit - 1) / kUnit;
   WindowPlan w;
   int64_t chunks = static_cast<int64_t>(sms) * Lay<1, false>::kCtasPerSm / num_kv_heads;
-  w.whole = units <= kWholeUnits;
-  chunks = min64(chunks, w.whole ? num_seqs : units * num_seqs);
   chunks = max64(min64(chunks, kMaxChunks), 1);
+  // Whole sequences where that takes no longer than an even cut with its merge, if the window
+  // makes lengths alike (contexts of twice the window and more); else only short ones.
+  // (64 sequences, window 2000, e4m3: 23 us whole, 31 cut; window 500: 9, 22)
+  const int64_t rounds = (num_seqs + chunks - 1) / chunks;
+  const int64_t piece = units + kPieceCost;
+  const bool alike = max_context_len / 2 >= static_cast<int64_t>(window) + num_sink;
+  w.whole = (alike && rounds * piece <= num_seqs * piece / chunks + kMergeUnits) ||
+            units <= kMergeUnits;
+  chunks = max64(min64(chunks, w.whole ? num_seqs : units * num_seqs), 1);
   if (chunks == 1) w.whole = true;
   w.chunks = static_cast<int32_t>(chunks);
   w.slots = w.whole ? 0 : static_cast<int32_t>(chunks - 1 + min64(num_seqs, chunks - 1));
@@ -642,10 +720,19 @@ pa_status launch(const CUtensorMap& mk, const CUtensorMap& mv, const PieceParams
   kern<<<grid, kThreads, Lay<NT, kFp8>::kAlloc, stream>>>(mk, mv, q, G);
   if (cudaGetLastError() != cudaSuccess) return PA_ERR_CUDA;
   if (q.whole) return PA_OK;  // no sequence is split
-  const dim3 merge_grid(static_cast<unsigned>(q.d.num_q_heads),
-                        static_cast<unsigned>(q.num_seqs < 256 ? q.num_seqs : 256));
-  return launch_dependent(merge_pieces_kernel<1, false>, merge_grid, kMergeWarps * 32, stream, q, G,
-                          chunks);
+  // Pieces per sequence are about chunks / num_seqs and two at its ends: a warp merges few, the
+  // eight warps of a CTA many (one sequence of 18 pieces: 8.3 us in all, 12.7 with a warp;
+  // 64 sequences of two: 46 us with warps, 47 with CTAs).
+  if (chunks > 4 * q.num_seqs) {
+    const dim3 merge_grid(static_cast<unsigned>(q.d.num_q_heads),
+                          static_cast<unsigned>(q.num_seqs < 256 ? q.num_seqs : 256));
+    return launch_dependent(merge_pieces_kernel<1, false>, merge_grid, kMergeWarps * 32, stream, q,
+                            G, chunks);
+  }
+  constexpr int kWarps = kMergeThreads / 32;
+  const dim3 merge_grid(static_cast<unsigned>((q.d.num_q_heads + kWarps - 1) / kWarps),
+                        static_cast<unsigned>(q.num_seqs < 128 ? q.num_seqs : 128));
+  return launch_dependent(merge_split_kernel, merge_grid, kMergeThreads, stream, q, G, chunks);
 }
 
 }  // namespace
