@@ -763,7 +763,8 @@ pa_status pa_paged_window_decode_attention(
  * total_tokens: rows of q and out; new tokens behind them, or past max_q_len of
  *   their sequence, are not computed.  Rows of out that belong to no sequence are left as
  *   they were.
- * max_blocks_per_seq * block_size above 2^30, total_tokens of 2^31 or more:
+ * max_blocks_per_seq * block_size above 2^30, total_tokens of 2^31 or more, or
+ *   total_tokens * num_q_heads / 256 + num_seqs * num_kv_heads above 2^24:
  *   PA_ERR_UNSUPPORTED.  Other arguments, limits and errors as for
  *   pa_paged_prefill_attention.
  * ---------------------------------------------------------------------- */

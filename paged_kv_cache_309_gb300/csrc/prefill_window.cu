@@ -71,6 +71,7 @@ constexpr uint32_t kSCol = 256;    // [256, 512): score buffer b of query tile i
 constexpr uint32_t kIdescS = instr_desc(kM, kStep, false);
 constexpr uint32_t kIdescPV = instr_desc(kM, kD, true);
 constexpr float kRescaleLog2 = 8.0f;
+constexpr int kMaxItems = 1 << 24;  // (queries of 2^24 items are a terabyte)
 
 struct Params {
   __nv_bfloat16* out;
@@ -128,7 +129,9 @@ struct Walk {
       if (q0 >= 0) avail = max(min(min(n, p.max_q_len), p.total_tokens - q0), 0);
     }
     const int per = 2 * p.tokens_per_tile;
-    incl = (avail + per - 1) / per * p.num_kv_heads;
+    // (sequences that share rows of q could add up to any number; the launch takes up to
+    // kMaxItems, so sums of 32 sequences fit)
+    incl = min((avail + per - 1) / per, kMaxItems / p.num_kv_heads) * p.num_kv_heads;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
       const int y = __shfl_up_sync(0xffffffffu, incl, off);
@@ -145,7 +148,7 @@ struct Walk {
       if (next < base + all) break;
       base += all;
       chunk += 32;
-      if (chunk >= p.num_seqs) return false;
+      if (chunk >= p.num_seqs || base > kMaxItems) return false;
       load(p, lane);
     }
     const int at = next - base;
@@ -170,9 +173,13 @@ struct Walk {
     it.ntok = min(2 * p.tokens_per_tile, rows - first);
     it.nq = it.ntok > p.tokens_per_tile ? 2 : 1;
     it.pos0 = L - count + first;
-    const int kend = max(0, min(L, it.pos0 + it.ntok));
-    it.win = window_range(kend, max(0, it.pos0 - p.window + 1), p.num_sink, min(p.log2_bs, 7));
-    it.pos0 -= it.win.skip;
+    const int kend = min(L, it.pos0 + it.ntok);
+    if (kend <= 0) {  // no row has a key (pos0 may be far below zero)
+      it.win = WindowRange{0, 0, 0, 0};
+    } else {
+      it.win = window_range(kend, max(0, it.pos0 - p.window + 1), p.num_sink, min(p.log2_bs, 7));
+      it.pos0 -= it.win.skip;
+    }
     it.ntiles = (it.win.len + kTile - 1) / kTile;
     it.nsteps = (it.win.len + kStep - 1) / kStep;
     return true;
@@ -327,6 +334,8 @@ __device__ __noinline__ void row_by_plain_loads(const Params& p, int b, int g, i
       o[2] += w * __uint_as_float(vb[i].y << 16);
       o[3] += w * __uint_as_float(vb[i].y & 0xFFFF0000u);
     }
+    // (a row that sees a token of NaN values is NaN: done)
+    if (__all_sync(0xffffffffu, o[0] != o[0] && o[1] != o[1] && o[2] != o[2] && o[3] != o[3])) break;
   }
   uint2 r = make_uint2(0u, 0u);
   if (l != 0.f) {
@@ -925,9 +934,7 @@ pa_status launch_window_prefill(const WindowPrefillArgs& w, cudaStream_t stream)
   const int64_t longest = a.max_q_len < w.total_tokens ? a.max_q_len : w.total_tokens;
   const int64_t most = (longest + per - 1) / per * a.num_seqs;
   if (most < grid && most * a.num_kv_heads < grid) grid = most * a.num_kv_heads;
-  // items are counted in 32 bits
-  if ((w.total_tokens / per + a.num_seqs + 1) * a.num_kv_heads >= (1ll << 31) - grid)
-    return PA_ERR_UNSUPPORTED;
+  if ((w.total_tokens / per + a.num_seqs) * a.num_kv_heads > kMaxItems) return PA_ERR_UNSUPPORTED;
   window_prefill_kernel<<<static_cast<unsigned>(grid), kThreads, kAlloc, stream>>>(mq, mk, mv, p);
   return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }

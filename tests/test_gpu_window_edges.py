@@ -1,0 +1,223 @@
+"""GPU tests of the sliding-window calls where sizes and contents leave the ordinary: many
+sequences, every way of cutting a batch, pools past 4 GiB, lengths and offsets that make
+no sense, calls that share rows, and random batches.  Bounds as in test_gpu_window.py."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import window as ow
+from paged_kv_cache_309_gb300 import pa
+from tests.gpu_util import need_gpu
+from tests.test_gpu_window import BF16, E4M3, SCALE, Batch, compare, decode, prefill, queries
+
+pytestmark = pytest.mark.gpu
+
+
+def check_some(lens, hq, h, bs, window, sink, rows, seed, cache=BF16, most=None):
+    batch = Batch(lens, h, bs, seed, cache=cache)
+    q = queries(len(lens), hq, seed + 1)
+    out, ws = decode(batch, q, window, sink, most=most)
+    assert pa.read_device_error(ws) == 0
+    rows = list(rows)
+    ref = ow.decode(q[rows].double().numpy(), *batch.values(), batch.tables[rows], batch.lens[rows], window, sink, SCALE)
+    compare(out[rows], ref, 2.0 ** -16 if cache == BF16 else 2.0 ** -11)
+
+
+@pytest.mark.parametrize("cache", [BF16, E4M3])
+@pytest.mark.parametrize("n,lo,hi,h,window", [
+    (200, 300, 700, 2, 100),    # whole sequences, two and more to a CTA
+    (300, 300, 700, 3, 130),    # more sequences than CTAs of a head
+    (64, 0, 1500, 2, 1000),     # an even cut, few pieces a sequence
+    (40, 2500, 2600, 8, 1024),  # the same with lengths alike
+    (2, 3000, 3000, 1, 2900),   # many pieces a sequence
+    (129, 1, 257, 1, 5000),     # a window that reaches past every context
+])
+def test_every_cut_of_a_batch(n, lo, hi, h, window, cache):
+    lens = np.linspace(lo, hi, n).astype(int).tolist()
+    check_some(lens, 2 * h, h, 16, window, 4, sorted({0, 1, n // 3, n // 2, n - 2, n - 1}), n + window, cache)
+
+
+def test_thousands_of_sequences():
+    lens = (np.arange(3000) % 41).tolist()
+    check_some(lens, 2, 1, 8, 17, 3, range(0, 3000, 97), 1)
+
+
+def test_lengths_that_make_no_sense():
+    """Negative lengths are empty contexts, huge ones are clipped and flagged."""
+    batch = Batch([64, 64, 64, 64], 2, 16, 2)
+    q = queries(4, 4, 3)
+    batch.lens = np.array([-5, 64, 2 ** 31 - 1, -2 ** 31], np.int32)
+    out, ws = decode(batch, q, 20, 4, most=64)
+    assert pa.read_device_error(ws) == pa.PA_DEVERR_CONTEXT_CLIPPED
+    ref = ow.decode(q.double().numpy(), *batch.values(), batch.tables, [0, 64, 64, 0], 20, 4, SCALE)
+    compare(out, ref, 2.0 ** -16)
+
+
+def test_one_block_for_all():
+    """Sequences may share blocks."""
+    batch = Batch([40, 40, 33], 2, 16, 4)
+    batch.tables[:] = batch.tables[:1]
+    q = queries(3, 8, 5)
+    ref = ow.decode(q.double().numpy(), *batch.values(), batch.tables, batch.lens, 30, 2, SCALE)
+    compare(decode(batch, q, 30, 2)[0], ref, 2.0 ** -16)
+
+
+def test_prefill_many_short_sequences():
+    """More sequences than a warp looks at at once, empty ones among them."""
+    rng = np.random.default_rng(6)
+    new = rng.integers(0, 90, 75).tolist()
+    lens = [n + int(rng.integers(0, 200)) for n in new]
+    batch = Batch(lens, 2, 16, 6)
+    q = queries(sum(new), 8, 7)
+    out, starts = prefill(batch, q, new, 60, 4)
+    rows = set(rng.choice(sum(new), 120, replace=False).tolist())
+    ref = ow.prefill(q.double().numpy(), *batch.values(), batch.tables, starts, lens, 60, 4, SCALE, rows)
+    pick = sorted(rows)
+    compare(out[pick], [x[pick] for x in ref], 2.0 ** -8)
+
+
+@pytest.mark.parametrize("starts,lens", [
+    ([0, 50, 20, 90], [50, 70, 70]),                  # a sequence that ends before it starts has no rows
+    ([0, 2 ** 31 - 1, 2 ** 31 - 1, 2 ** 31 - 1], [60, 5, 7]),  # far past the array
+    ([-40, 30, 60, 90], [70, 30, 30]),                # rows before the array
+    ([0, 0, 0, 0], [70, 30, 30]),
+    ([0, 30, 60, 90], [-3, 2 ** 31 - 1, 0]),
+])
+def test_prefill_offsets_that_make_no_sense(starts, lens):
+    """No row outside the array is touched and the call ends; rows of sound sequences are right."""
+    need_gpu()
+    batch = Batch([70, 70, 70], 2, 16, 8)
+    q = queries(120, 4, 9)
+    k, v, bt, _ = batch.device()
+    guard = torch.full((360, 4, 128), 7.0, dtype=BF16, device="cuda")
+    out, dq = guard[120:240], q.cuda()
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    pa.pa_paged_window_prefill_attention(
+        out, dq, k, v, bt, torch.tensor(starts, dtype=torch.int32, device="cuda"),
+        torch.tensor(lens, dtype=torch.int32, device="cuda"), 25, 3, SCALE, 100, err)
+    torch.cuda.synchronize()
+    assert int(err) & ~pa.PA_DEVERR_CONTEXT_CLIPPED == 0
+    assert bool((guard[:120] == 7).all()) and bool((guard[240:] == 7).all())
+    got = out.double().cpu().numpy()
+    cap = batch.tables.shape[1] * 16
+    seen = np.zeros(120, int)
+    for b in range(3):
+        n = max(0, starts[b + 1] - starts[b])
+        for j in range(min(n, 100)):
+            if 0 <= starts[b] and starts[b] + j < 120:
+                seen[starts[b] + j] += 1
+    assert (got[seen == 0] == 7).all()
+    for b in range(3):
+        n, length = max(0, starts[b + 1] - starts[b]), min(max(lens[b], 0), cap)
+        if starts[b] < 0 or lens[b] > cap:
+            continue
+        for j in range(0, min(n, 100, 120 - starts[b]), 7):
+            i = starts[b] + j
+            if seen[i] != 1:
+                continue
+            t = ow.visible(length - n + j, 25, 3)
+            for g in range(2):
+                ref = ow.row(q[i, 2 * g:2 * g + 2].double().numpy(), *(x[:, :, g] for x in batch.values()),
+                             batch.tables[b], t[t < length], SCALE)
+                compare(out[i, 2 * g:2 * g + 2], [ref[0], ref[1], np.full(2, ref[2]), np.full(2, ref[3])], 2.0 ** -8)
+
+
+def test_tokens_past_max_q_len_are_left_out():
+    batch = Batch([90, 40], 2, 16, 10)
+    q = queries(130, 4, 11)
+    k, v, bt, cl = batch.device()
+    out = torch.full((130, 4, 128), 7.0, dtype=BF16, device="cuda")
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    starts = torch.tensor([0, 90, 130], dtype=torch.int32, device="cuda")
+    pa.pa_paged_window_prefill_attention(out, q.cuda(), k, v, bt, starts, cl, 25, 3, SCALE, 50, err)
+    torch.cuda.synchronize()
+    ref = ow.prefill(q.double().numpy(), *batch.values(), batch.tables, [0, 90, 130], batch.lens, 25, 3, SCALE)
+    pick = list(range(50)) + list(range(90, 130))
+    compare(out[pick], [x[pick] for x in ref], 2.0 ** -8)
+    assert bool((out[50:90] == 7).all())
+
+
+@pytest.mark.slow
+def test_pools_past_4_gib():
+    """Rows whose byte offset passes 2^32: written by the append, read by both attention calls."""
+    need_gpu()
+    bs, h, hq, n = 16, 8, 8, 70
+    blocks = 2 ** 32 // (bs * h * 128 * 2) + 8
+    kc, vc = (torch.zeros((blocks, bs, h, 128), dtype=BF16, device="cuda") for _ in range(2))
+    table = torch.tensor([[blocks - 1, blocks - 3, 2, blocks - 7, blocks - 5]], dtype=torch.int32, device="cuda")
+    gen = torch.Generator().manual_seed(12)
+    q, k, v = (torch.randn((n, x, 128), generator=gen).bfloat16().cuda() for x in (hq, h, h))
+    pos = torch.arange(n, device="cuda")
+    slot = table[0].long()[pos // bs] * bs + pos % bs
+    cs = torch.cat([torch.ones(128, 64), torch.zeros(128, 64)], 1).cuda()  # no turn
+    q_out = torch.empty_like(q)
+    pa.pa_rope_and_cache(q_out, q, k, v, kc, vc, cs, pos, slot)
+    assert torch.equal(q_out, q)
+    assert torch.equal(kc.view(-1, h, 128)[slot], k) and torch.equal(vc.view(-1, h, 128)[slot], v)
+    one = [x[None].double().cpu().numpy() for x in (k, v)]
+    flat = [np.zeros((1, 80, h, 128)) for _ in range(2)]
+    for f, x in zip(flat, one):
+        f[:, :n] = x
+    lens, starts = torch.tensor([n], dtype=torch.int32, device="cuda"), torch.tensor([0, n], dtype=torch.int32, device="cuda")
+    out, err = torch.empty_like(q), torch.zeros(1, dtype=torch.int32, device="cuda")
+    pa.pa_paged_window_prefill_attention(out, q, kc, vc, table, starts, lens, 30, 2, SCALE, n, err)
+    qn = q.double().cpu().numpy()
+    ref = ow.prefill(qn, *flat, np.zeros((1, 1), int), [0, n], [n], 30, 2, SCALE)
+    compare(out, ref, 2.0 ** -8)
+    ws = pa.window_decode_workspace(1, hq, h, 128, 30, 2, n)
+    last = torch.empty_like(q[-1:])
+    pa.pa_paged_window_decode_attention(last, q[-1:].contiguous(), kc, vc, table, lens, 30, 2, SCALE, n, ws)
+    compare(last, [x[-1:] for x in ref], 2.0 ** -16)
+
+
+@pytest.mark.parametrize("seed", range(12))
+def test_random_batches(seed):
+    rng = np.random.default_rng(100 + seed)
+    h, g = int(rng.choice([1, 2, 3, 4])), int(rng.choice([1, 2, 4, 8, 16]))
+    bs = int(rng.choice([8, 16, 32, 64, 128, 256]))
+    window, sink = int(np.exp(rng.uniform(0, 7))), int(rng.choice([0, 1, 4, 30, 200]))
+    drop = float(rng.choice([0, 0, 0.2]))
+    lens = [int(np.exp(rng.uniform(0, 6.8))) for _ in range(int(rng.integers(1, 9)))]
+    cache = BF16 if seed % 2 else E4M3
+    batch = Batch(lens, h, bs, seed, cache=cache, drop=drop)
+    q = queries(len(lens), h * g, seed + 1)
+    out, ws = decode(batch, q, window, sink, most=max(lens) + int(rng.integers(0, 500)))
+    ref = ow.decode(q.double().numpy(), *batch.values(), batch.tables, lens, window, sink, SCALE)
+    compare(out, ref, 2.0 ** -16 if cache == BF16 else 2.0 ** -11)
+    batch = Batch(lens, h, bs, seed, drop=drop)
+    new = [int(rng.integers(1, n + 1)) for n in lens]
+    q = queries(sum(new), h * g, seed + 2)
+    out, starts = prefill(batch, q, new, window, sink)
+    rows = set(rng.choice(sum(new), min(sum(new), 60), replace=False).tolist())
+    ref = ow.prefill(q.double().numpy(), *batch.values(), batch.tables, starts, lens, window, sink, SCALE, rows)
+    pick = sorted(rows)
+    compare(out[pick], [x[pick] for x in ref], 2.0 ** -8)
+
+
+def test_calls_on_two_streams_at_once():
+    """Two calls that share caches and lengths, each with its workspace, on two streams."""
+    batch = Batch([900, 2000, 37], 2, 16, 13)
+    q = queries(3, 8, 14)
+    x, _ = decode(batch, q, 600, 4)
+    k, v, bt, cl = batch.device()
+    dq = q.cuda()
+    outs = [torch.zeros_like(x) for _ in range(2)]
+    ws = [pa.window_decode_workspace(3, 8, 2, 128, 600, 4, 2000) for _ in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(50):
+        for i in range(2):
+            pa.pa_paged_window_decode_attention(outs[i], dq, k, v, bt, cl, 600, 4, SCALE, 2000, ws[i], stream=streams[i])
+    torch.cuda.synchronize()
+    assert bool((outs[0] == x).all()) and bool((outs[1] == x).all())
+
+
+@pytest.mark.parametrize("repeat", range(3))
+def test_results_repeat(repeat):
+    """The same call gives the same bits, whatever ran before it."""
+    new = [300, 1, 220, 64]
+    batch = Batch([700, 90, 220, 64], 2, 16, 15)
+    q = queries(sum(new), 8, 16)
+    first, _ = prefill(batch, q, new, 150, 4)
+    for _ in range(20):
+        assert torch.equal(prefill(batch, q, new, 150, 4)[0], first)
