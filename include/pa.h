@@ -728,7 +728,8 @@ pa_status pa_rope_and_cache(void *q_out, const void *q, const void *key, const v
  *     t >= L - window  or  t < num_sink
  * (the last `window` tokens, its own among them, and the first num_sink).
  * Rows of other tokens are not used, whatever they hold, and their blocks need
- * not be there: a block id outside the pool drops its tokens as ever.
+ * not be there: a block id outside the pool drops its tokens as ever.  A score of
+ * -infinity has no weight; a row with no other score is zero.
  *
  * window >= 1, num_sink >= 0 (else PA_ERR_INVALID).  cache_dtype PA_BF16
  * (k_scale, v_scale NULL) or PA_FP8_E4M3 (both NULL: unit scales, or as in
@@ -758,7 +759,8 @@ pa_status pa_paged_window_decode_attention(
  * query at position p sees only tokens
  *     t <= p  and  (t > p - window  or  t < num_sink)
  * so that a prompt's row equals the window decode call's over the same tokens.
- * Values of tokens that a row does not see do not reach it, whatever they hold.
+ * Values of tokens that a row does not see do not reach it, whatever they hold; a
+ * score of -infinity has no weight, and a row with no other is zero.
  * window >= 1, num_sink >= 0 (else PA_ERR_INVALID); bf16 caches.
  * total_tokens: rows of q and out; new tokens behind them, or past max_q_len of
  *   their sequence, are not computed.  Rows of out that belong to no sequence are left as

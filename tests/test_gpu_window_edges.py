@@ -53,6 +53,56 @@ def test_lengths_that_make_no_sense():
     compare(out, ref, 2.0 ** -16)
 
 
+def without_infinite_keys(batch, q, lens, starts, window, sink, infinite):
+    """What ow.decode gives where the tokens infinite(t) have no weight (starts: rows of each sequence)."""
+    hq, g = q.shape[1], q.shape[1] // batch.h
+    refs = [np.zeros(q.shape), np.zeros(q.shape), np.zeros(q.shape[:2]), np.zeros(q.shape[:2])]
+    kc, vc = batch.values()
+    for b, n in enumerate(lens):
+        new = starts[b + 1] - starts[b]
+        for j in range(new):
+            t = np.array([t for t in ow.visible(n - new + j, window, sink) if not infinite(b, t)], np.int64)
+            for h in range(0, hq, g):
+                x = ow.row(q[starts[b] + j, h:h + g].double().numpy(), kc[:, :, h // g], vc[:, :, h // g],
+                           batch.tables[b], t, SCALE)
+                for r, y in zip(refs, x):
+                    r[starts[b] + j, h:h + g] = y
+    return refs
+
+
+def with_infinite_keys(lens, hq, new):
+    """A batch whose queries are positive in element 0, and keys of -inf there: scores of -inf."""
+    def infinite(b, t):
+        return b == 2 or t < 40 or t % 7 == 3 or 150 <= t < 260
+    batch = Batch(lens, 2, 16, 21)
+    for b, n in enumerate(lens):
+        for t in range(n):
+            if infinite(b, t):
+                batch.pools[0][batch.tables[b, t // 16], t % 16, :, 0] = -float("inf")
+    q = queries(new, hq, 22)
+    q[:, :, 0] = q[:, :, 0].abs() + 1
+    return batch, q, infinite
+
+
+@pytest.mark.parametrize("window", [90, 1000])
+def test_decode_scores_of_minus_infinity(window):
+    """They have no weight, first in a row or later; a row of them alone is zero."""
+    lens = [700, 300, 100, 41]
+    batch, q, infinite = with_infinite_keys(lens, 8, 4)
+    out, _ = decode(batch, q, window, 4)
+    compare(out, without_infinite_keys(batch, q, lens, range(5), window, 4, infinite), 2.0 ** -16)
+    assert bool((out[2] == 0).all())
+
+
+@pytest.mark.parametrize("window", [90, 1000])
+def test_prefill_scores_of_minus_infinity(window):
+    lens, new = [400, 300, 100, 41], [300, 300, 100, 1]
+    batch, q, infinite = with_infinite_keys(lens, 4, sum(new))
+    out, starts = prefill(batch, q, new, window, 4)
+    compare(out, without_infinite_keys(batch, q, lens, starts.tolist(), window, 4, infinite), 2.0 ** -8)
+    assert bool((out[600:700] == 0).all())
+
+
 def test_one_block_for_all():
     """Sequences may share blocks."""
     batch = Batch([40, 40, 33], 2, 16, 4)
