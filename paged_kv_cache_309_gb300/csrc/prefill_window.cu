@@ -57,26 +57,27 @@ using namespace tc;
 
 constexpr int kD = 128;
 constexpr int kM = 128;    // rows per query tile (tokens x heads)
-constexpr int kTile = 128; // keys per tile of the ring
-constexpr int kStep = 64;  // keys per score buffer
-constexpr int kSlots = 4;  // K(u) is load 2u of the CTA, V(u) load 2u + 1
+constexpr int kStep = 64;  // keys per step
+constexpr int kSlots = 4;  // of keys, and as many of values: step n of the CTA is in slot n % 4
 constexpr int kThreads = 12 * 32;              // 4 role warps + 2 x 4 softmax warps
-constexpr int kChunk = 128 * 128;              // 64 elements of 128 rows: 16 KB
+constexpr int kChunk = 128 * 128;              // 64 elements of 128 query rows: 16 KB
+constexpr int kHalf = kStep * 128;             // 64 elements of a step's rows: 8 KB
 constexpr int kQOff = 0;                       // query tile i: two chunks
-constexpr int kRingOff = 2 * 2 * kChunk;       // slots of two chunks
-constexpr int kSlotBytes = 2 * kChunk;
-constexpr int kStageOff = kRingOff + kSlots * kSlotBytes;  // 32 half rows per softmax warp
+constexpr int kSlotBytes = 2 * kHalf;
+constexpr int kKOff = 2 * 2 * kChunk;
+constexpr int kVOff = kKOff + kSlots * kSlotBytes;
+constexpr int kStageOff = kVOff + kSlots * kSlotBytes;  // 32 half rows per softmax warp
 constexpr int kStageBytes = 32 * 128;
 constexpr int kBarOff = kStageOff + 8 * kStageBytes;
-// Mask slot u % 8 is written again for tile u + 8, whose keys (load 2u + 16) need load
-// 2u + 12 = K(u + 6) used, and a score product comes after the output product two steps
-// before it, which needs both softmax groups past tile u.
+// Mask slot n % 8 is written again for step n + 8, whose keys need those of step n + 4 used; that
+// score product comes after the output product of step n + 2, which needs the weights of
+// both query tiles' step n + 2.
 constexpr int kMaskSlots = 8;
-// q_full, q_empty, pv_done, o_empty [2] each, s_full, p_full [2][2], full, empty, mask_full,
-// drain
-constexpr int kNumBars = 4 * 2 + 2 * 4 + 2 * kSlots + kMaskSlots + 1;
-constexpr int kMaskOff = kBarOff + (kNumBars + 1) / 2 * 16;  // two 64-bit words per slot
-constexpr int kMiscOff = kMaskOff + kMaskSlots * 16;
+// q_full, q_empty, pv_done, o_empty [2] each, s_full, p_full [2][2], k_full, k_empty, v_full,
+// v_empty, mask_full, drain
+constexpr int kNumBars = 4 * 2 + 2 * 4 + 4 * kSlots + kMaskSlots + 1;
+constexpr int kMaskOff = kBarOff + (kNumBars + 1) / 2 * 16;  // a 64-bit word per slot
+constexpr int kMiscOff = kMaskOff + kMaskSlots * 8;
 constexpr int kBytes = kMiscOff + 16;
 constexpr int kAlloc = kBytes + 1024;
 static_assert(kAlloc <= 227 * 1024, "shared memory");
@@ -87,6 +88,7 @@ constexpr uint32_t kSCol = 256;    // [256, 512): score buffer b of query tile i
 constexpr uint32_t kIdescS = instr_desc(kM, kStep, false);
 constexpr uint32_t kIdescPV = instr_desc(kM, kD, true);
 constexpr float kRescaleLog2 = 8.0f;
+constexpr int kLog2Rows = 6;        // copies are of up to 64 rows
 constexpr int kMaxItems = 1 << 24;  // (queries of 2^24 items are a terabyte)
 
 struct Params {
@@ -119,8 +121,7 @@ struct Item {
   int b, g;      // sequence, kv head
   int q_row;     // the item's first row of q
   int ntok;      // its new tokens
-  int ntiles;    // key tiles (0: no row has a key)
-  int nsteps;    // steps of 64 places in them
+  int nsteps;    // steps of 64 places (0: no row has a key)
   int nq;        // query tiles with a row
   int pos0;      // place of its first token
   WindowRange win;
@@ -193,10 +194,9 @@ struct Walk {
     if (kend <= 0) {  // no row has a key (pos0 may be far below zero)
       it.win = WindowRange{0, 0, 0, 0};
     } else {
-      it.win = window_range(kend, max(0, it.pos0 - p.window + 1), p.num_sink, min(p.log2_bs, 7));
+      it.win = window_range(kend, max(0, it.pos0 - p.window + 1), p.num_sink, min(p.log2_bs, kLog2Rows));
       it.pos0 -= it.win.skip;
     }
-    it.ntiles = (it.win.len + kTile - 1) / kTile;
     it.nsteps = (it.win.len + kStep - 1) / kStep;
     return true;
   }
@@ -206,16 +206,6 @@ struct Walk {
 // The issuing warp stays together and one lane's predicate guards each instruction: in a branch
 // of one lane every operand would be moved to the uniform registers that these
 // instructions read, at ~100 cycles a product.  Descriptors come as two words.
-__device__ __forceinline__ void mma_ss(uint32_t one, uint32_t d, uint32_t a, uint32_t b,
-                                       uint32_t hi, uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t.reg .b64 da, db;\n\t"
-      "setp.ne.b32 p, %5, 0;\n\tsetp.ne.b32 q, %6, 0;\n\t"
-      "mov.b64 da, {%1, %3};\n\tmov.b64 db, {%2, %3};\n\t"
-      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %4, p;\n\t}" ::"r"(d),
-      "r"(a), "r"(b), "r"(hi), "r"(idesc), "r"(accumulate), "r"(one)
-      : "memory");
-}
 __device__ __forceinline__ void mma_ts(uint32_t one, uint32_t d, uint32_t a_tmem, uint32_t b,
                                        uint32_t hi, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
@@ -234,6 +224,35 @@ __device__ __forceinline__ void commit(uint32_t one, uint64_t* bar) {
       "r"(one)
       : "memory");
 }
+// A score product: S = Q K^T over 64 keys, 8 k-steps of 16 over the 128 head elements, both operands
+// K-major 128-byte swizzled (a k-step in a chunk is 32 bytes on).  While it is issued, three
+// barriers are tested (as far as `parity` says): the answers take as long as everything
+// else that goes through shared memory beside the operands' reads, 150 cycles and more.
+struct Tests {
+  uint32_t bar[3], parity[3], done[3];
+};
+__device__ __forceinline__ void score_product(uint32_t one, uint32_t d, uint32_t q, uint32_t k,
+                                              uint32_t hi, uint32_t idesc, Tests& t) {
+#define PA_KSTEP(qoff, koff, acc)                                         \
+  "add.u32 a, %5, " qoff ";\n\tadd.u32 b, %6, " koff ";\n\t"             \
+  "mov.b64 da, {a, %7};\n\tmov.b64 db, {b, %7};\n\t"                     \
+  "@q tcgen05.mma.cta_group::1.kind::f16 [%4], da, db, %8, " acc ";\n\t"
+  asm volatile(
+      "{\n\t.reg .pred q, yes, no, t0, t1, t2;\n\t.reg .b32 a, b;\n\t.reg .b64 da, db;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 t0, [%9], %12;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 t1, [%10], %13;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 t2, [%11], %14;\n\t"
+      "setp.ne.b32 q, %3, 0;\n\tsetp.eq.b32 yes, 0, 0;\n\tsetp.ne.b32 no, 0, 0;\n\t"
+      PA_KSTEP("0", "0", "no") PA_KSTEP("2", "2", "yes") PA_KSTEP("4", "4", "yes")
+      PA_KSTEP("6", "6", "yes") PA_KSTEP("1024", "512", "yes") PA_KSTEP("1026", "514", "yes")
+      PA_KSTEP("1028", "516", "yes") PA_KSTEP("1030", "518", "yes")
+      "selp.u32 %0, 1, 0, t0;\n\tselp.u32 %1, 1, 0, t1;\n\tselp.u32 %2, 1, 0, t2;\n\t}"
+      : "=r"(t.done[0]), "=r"(t.done[1]), "=r"(t.done[2])
+      : "r"(one), "r"(d), "r"(q), "r"(k), "r"(hi), "r"(idesc), "r"(t.bar[0]), "r"(t.bar[1]),
+        "r"(t.bar[2]), "r"(t.parity[0]), "r"(t.parity[1]), "r"(t.parity[2])
+      : "memory");
+#undef PA_KSTEP
+}
 // one lane of a warp that is together, the same one every time
 __device__ __forceinline__ uint32_t elect_one() {
   uint32_t r;
@@ -244,51 +263,41 @@ __device__ __forceinline__ uint32_t elect_one() {
 }
 
 // ------------------------------------------------------------------ loads --
-// A tile's block pieces: lane i holds piece i % nbox (each looked up by 32 / nbox lanes, which
-// share out its copies): its cache row (-1: nothing of it is there or seen), and the
-// piece's visible rows as bits of the tile.
-struct TilePieces {
-  int row;
-  uint64_t lo, hi;
+// A step's block pieces: lane i holds piece i % nbox: its block id (looked up a step before it is
+// used), first row in the block, and rows that an item's query may see, as bits of the step.
+struct Pieces {
+  int bid, row, g;  // (g: the item's kv head)
+  uint64_t seen;
 };
-__device__ __forceinline__ TilePieces find_pieces(const Params& p, const Item& it, int place0,
-                                                  int log2_rpb, int lane) {
-  TilePieces x;
+__device__ __forceinline__ Pieces find_pieces(const Params& p, const Item& it, int place0,
+                                              int log2_rpb, int lane) {
+  Pieces x{-1, 0, it.g, 0};
   const int rpb = 1 << log2_rpb;
-  const int start = (lane & ((kTile >> log2_rpb) - 1)) << log2_rpb;  // of the tile's places
+  const int start = (lane & ((kStep >> log2_rpb) - 1)) << log2_rpb;  // of the step's places
   const int first = it.win.row(place0 + start);
   const int rows = min(rpb, it.win.len - place0 - start);
-  x.row = -1;
-  x.lo = x.hi = 0;
   if (rows > 0) {
-    const int bid = __ldg(p.block_tables + static_cast<int64_t>(it.b) * p.max_blocks_per_seq +
-                          (first >> p.log2_bs));
-    const int tile0 = first - start;  // the row of bit 0, if this piece's run began there
-    x.lo = WindowRange::below(start + rows) & ~WindowRange::below(start) &
-           it.win.visible(tile0, p.num_sink);
-    x.hi = WindowRange::below(start + rows - 64) & ~WindowRange::below(start - 64) &
-           it.win.visible(tile0 + 64, p.num_sink);
-    if (bid >= 0 && static_cast<int64_t>(bid) < p.num_blocks && (x.lo | x.hi) != 0) {
-      x.row = bid * p.block_size + (first & (p.block_size - 1));
-    } else {
-      x.lo = x.hi = 0;
-    }
+    x.bid = __ldg(p.block_tables + static_cast<int64_t>(it.b) * p.max_blocks_per_seq +
+                  (first >> p.log2_bs));
+    x.row = first & (p.block_size - 1);
+    // (visible() from the row of bit 0, if this piece's run began there)
+    x.seen = WindowRange::below(start + rows) & ~WindowRange::below(start) &
+             it.win.visible(first - start, p.num_sink);
   }
   return x;
 }
-// The keys or values of one tile; copy c is half c / nbox (64 head elements) of piece c % nbox.
-__device__ __forceinline__ void load_tile(const CUtensorMap* tm, const TilePieces& x, int g,
-                                          uint8_t* dst, uint64_t* full, int log2_rpb, uint64_t pol,
-                                          int lane) {
-  const int nbox = kTile >> log2_rpb;
-  const uint32_t there = __ballot_sync(0xffffffffu, lane < nbox && x.row >= 0);
+// The keys or values of one step; copy c is half c / nbox (64 head elements) of piece c % nbox.
+__device__ __forceinline__ void load_step(const CUtensorMap* tm, int row, int g, uint8_t* dst,
+                                          uint64_t* full, int log2_rpb, uint64_t pol, int lane) {
+  const int nbox = kStep >> log2_rpb;
+  const uint32_t there = __ballot_sync(0xffffffffu, lane < nbox && row >= 0);
   if (lane == 0)
     mbar_arrive_expect_tx(full, static_cast<uint32_t>(__popc(there) << (log2_rpb + 8)));
   __syncwarp();
-  if (lane < 2 * nbox && x.row >= 0) {
+  if (lane < 2 * nbox && row >= 0) {
     const int half = lane >= nbox ? 1 : 0;
-    tma_load_3d(dst + half * kChunk + ((lane & (nbox - 1)) << (log2_rpb + 7)), tm, 64 * half, g,
-                x.row, full, pol);
+    tma_load_3d(dst + half * kHalf + ((lane & (nbox - 1)) << (log2_rpb + 7)), tm, 64 * half, g, row,
+                full, pol);
   }
 }
 
@@ -374,11 +383,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* o_empty = bars + 6;               // [2] O_i read (4 warps)
   uint64_t* s_full = bars + 8;                // [2][2] scores of buffer b there (commit)
   uint64_t* p_full = bars + 12;               // [2][2] weights in buffer b (4 warps)
-  uint64_t* full = bars + 16;                 // [kSlots] keys or values landed
-  uint64_t* empty = full + kSlots;            // [kSlots] the slot's products done (commit)
-  uint64_t* mask_full = empty + kSlots;       // [kMaskSlots] row mask posted
+  uint64_t* k_full = bars + 16;               // [kSlots] keys landed
+  uint64_t* k_empty = k_full + kSlots;        // [kSlots] their score products done (commit)
+  uint64_t* v_full = k_empty + kSlots;        // [kSlots] values landed
+  uint64_t* v_empty = v_full + kSlots;        // [kSlots] their output products done (commit)
+  uint64_t* mask_full = v_empty + kSlots;     // [kMaskSlots] row mask posted
   uint64_t* drain = mask_full + kMaskSlots;   // every product done
-  uint64_t* tile_mask = reinterpret_cast<uint64_t*>(smem + kMaskOff);  // [kMaskSlots][2]
+  uint64_t* step_mask = reinterpret_cast<uint64_t*>(smem + kMaskOff);  // [kMaskSlots]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kMiscOff);
   int* flags = reinterpret_cast<int*>(smem + kMiscOff + 8);
 
@@ -398,8 +409,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&p_full[i], 4);
     }
     for (int s = 0; s < kSlots; ++s) {
-      mbar_init(&full[s], 1);
-      mbar_init(&empty[s], 1);
+      mbar_init(&k_full[s], 1);
+      mbar_init(&k_empty[s], 1);
+      mbar_init(&v_full[s], 1);
+      mbar_init(&v_empty[s], 1);
     }
     for (int s = 0; s < kMaskSlots; ++s) mbar_init(&mask_full[s], 1);
     mbar_init(drain, 1);
@@ -418,65 +431,59 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = __reduce_or_sync(0xffffffffu, *tmem_slot);
   volatile int* abort_flag = flags;
-  uint32_t issued = 0;  // (warp 0) loads requested
+  uint32_t issued = 0;  // (warps 0, 3) steps whose keys, values are requested
 
   if (warp < 4) {
     bool ok = true;
-    if (warp == 0) {
-      // ------------------------------------------------------ keys and values
+    if (warp == 0 || warp == 3) {
+      // ------------------------------------------- keys (warp 0), values (warp 3)
+      const bool keys = warp == 0;
+      const CUtensorMap* tm = keys ? &tm_k : &tm_v;
+      uint64_t* full = keys ? k_full : v_full;
+      uint64_t* empty = keys ? k_empty : v_empty;
+      uint8_t* slots = smem + (keys ? kKOff : kVOff);
       Walk walk(p, blockIdx.x, lane);
       Item it;
       const uint64_t pol = l2_policy_evict_normal();
-      const int log2_rpb = min(p.log2_bs, 7);
-      if (lane == 0) {
-        prefetch_tensormap(&tm_k);
-        prefetch_tensormap(&tm_v);
-      }
-      uint32_t slot = 0, phase = 1;  // (the first wait for an empty slot passes)
-      uint32_t u = 0;
-      bool have = walk.get(p, step, lane, it);
-      TilePieces x{};
-      if (have && it.ntiles > 0) x = find_pieces(p, it, 0, log2_rpb, lane);
-      while (ok && have) {
-        const int g = it.g, ntiles = it.ntiles;
-        for (int t = 0; t < ntiles; ++t, ++u) {
-          const TilePieces now = x;
-          // the next tile's blocks are looked up before the waits for slots
-          if (t + 1 < ntiles) {
-            x = find_pieces(p, it, (t + 1) * kTile, log2_rpb, lane);
-          } else {
-            have = walk.get(p, step, lane, it);
-            if (have && it.ntiles > 0) x = find_pieces(p, it, 0, log2_rpb, lane);
-          }
-          const uint32_t w0 = __reduce_or_sync(0xffffffffu, static_cast<uint32_t>(now.lo));
-          const uint32_t w1 = __reduce_or_sync(0xffffffffu, static_cast<uint32_t>(now.lo >> 32));
-          const uint32_t w2 = __reduce_or_sync(0xffffffffu, static_cast<uint32_t>(now.hi));
-          const uint32_t w3 = __reduce_or_sync(0xffffffffu, static_cast<uint32_t>(now.hi >> 32));
-#pragma unroll
-          for (int v = 0; v < 2; ++v) {
-            ok = __all_sync(0xffffffffu,
-                            mbar_wait_bounded_long(&empty[slot], phase, abort_flag));
-            if (!ok) break;
-            if (v == 0 && lane == 0) {
-              uint64_t* m = tile_mask + 2 * (u % kMaskSlots);
-              m[0] = (static_cast<uint64_t>(w1) << 32) | w0;
-              m[1] = (static_cast<uint64_t>(w3) << 32) | w2;
-              mbar_arrive(&mask_full[u % kMaskSlots]);
-            }
-            load_tile(v == 0 ? &tm_k : &tm_v, now, g, smem + kRingOff + slot * kSlotBytes,
-                      &full[slot], log2_rpb, pol, lane);
-            ++issued;
-            if (++slot == kSlots) {
-              slot = 0;
-              phase ^= 1;
-            }
-          }
+      const int log2_rpb = min(p.log2_bs, kLog2Rows);
+      if (lane == 0) prefetch_tensormap(tm);
+      bool have = true;
+      int at = 0;
+      it.nsteps = 0;
+      // the next step's pieces, looked up before the wait for a slot
+      auto next = [&]() {
+        while (at == it.nsteps) {
+          have = walk.get(p, step, lane, it);
+          at = 0;
+          if (!have) return Pieces{-1, 0, 0, 0};
+        }
+        return find_pieces(p, it, at++ * kStep, log2_rpb, lane);
+      };
+      Pieces x = next();
+      while (have) {
+        const Pieces now = x;
+        x = next();
+        const bool there =
+            now.bid >= 0 && static_cast<int64_t>(now.bid) < p.num_blocks && now.seen != 0;
+        const uint32_t n = issued;
+        const uint32_t slot = n % kSlots;
+        if (n >= kSlots) {
+          ok = __all_sync(0xffffffffu, mbar_wait_bounded_long(&empty[slot], (n / kSlots - 1) & 1,
+                                                              abort_flag));
           if (!ok) break;
         }
-        if (ntiles == 0) {
-          have = walk.get(p, step, lane, it);
-          if (have && it.ntiles > 0) x = find_pieces(p, it, 0, log2_rpb, lane);
+        if (keys) {
+          const uint64_t seen = there ? now.seen : 0;
+          const uint32_t w0 = __reduce_or_sync(0xffffffffu, static_cast<uint32_t>(seen));
+          const uint32_t w1 = __reduce_or_sync(0xffffffffu, static_cast<uint32_t>(seen >> 32));
+          if (lane == 0) {
+            step_mask[n % kMaskSlots] = (static_cast<uint64_t>(w1) << 32) | w0;
+            mbar_arrive(&mask_full[n % kMaskSlots]);
+          }
         }
+        load_step(tm, there ? now.bid * p.block_size + now.row : -1, now.g,
+                  slots + slot * kSlotBytes, &full[slot], log2_rpb, pol, lane);
+        ++issued;
       }
     } else if (warp == 2) {
       // ------------------------------------------------------------- queries
@@ -486,7 +493,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) prefetch_tensormap(&tm_q);
       uint32_t count[2] = {0, 0};
       while (ok && walk.get(p, step, lane, it)) {
-        if (it.ntiles == 0) continue;
+        if (it.nsteps == 0) continue;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           if (i >= it.nq) break;
@@ -516,8 +523,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t base = smem_desc(smem_u32(smem), 16, 1024);
       const uint32_t lo_kmajor = static_cast<uint32_t>(base);
       const uint32_t hi_word = static_cast<uint32_t>(base >> 32);
-      // V is MN-major: leading offset = the next 64 elements = the next chunk
-      const uint32_t lo_v = static_cast<uint32_t>(smem_desc(smem_u32(smem), kChunk, 1024));
+      // V is MN-major: leading offset = the next 64 elements
+      const uint32_t lo_v = static_cast<uint32_t>(smem_desc(smem_u32(smem), kHalf, 1024));
       const uint32_t one = elect_one();
       auto wait = [&](uint64_t* bar, uint32_t n) {
         if (ok) ok = __all_sync(0xffffffffu, mbar_wait_bounded(bar, n & 1, abort_flag));
@@ -528,15 +535,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       struct Cursor {
         Walk walk;
         int step, nsteps, nq;  // of the item in hand; nsteps 0: no more
-        uint32_t slot, phase;  // of its tile's keys or values
-        uint32_t steps[2];     // steps taken per query tile
+        uint32_t n;            // steps before it
+        uint32_t steps[2];     // the same per query tile
         uint32_t items[2];     // items begun per query tile
       };
       auto fetch = [&](Cursor& c) {
         Item x;
         c.step = c.nsteps = c.nq = 0;
         while (c.walk.get(p, step, lane, x)) {
-          if (x.ntiles > 0) {
+          if (x.nsteps > 0) {
             c.nsteps = __reduce_max_sync(0xffffffffu, x.nsteps);
             c.nq = __reduce_max_sync(0xffffffffu, x.nq);
             break;
@@ -544,67 +551,110 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       };
       auto advance = [&](Cursor& c) {
-        const bool last = c.step + 1 == c.nsteps;
-        if ((c.step & 1) || last) {  // on to the next tile
-          c.slot += 2;
-          if (c.slot >= kSlots) {
-            c.slot -= kSlots;
-            c.phase ^= 1;
-          }
-        }
-        if (last) {
+        ++c.n;
+        if (c.step + 1 == c.nsteps) {
           fetch(c);
         } else {
           ++c.step;
         }
       };
-      Cursor sc{Walk(p, blockIdx.x, lane), 0, 0, 0, 0, 0, {0, 0}, {0, 0}};
+      Cursor sc{Walk(p, blockIdx.x, lane), 0, 0, 0, 0, {0, 0}, {0, 0}};
       fetch(sc);
       Cursor pv = sc;
-      pv.slot = 1;
-      // S_i of cursor sc's step into the query tile's next buffer: 8 k-steps of 16 over the 128
-      // head elements, both operands K-major 128-byte swizzled (a k-step in a chunk
-      // is 32 bytes on, 64 keys 8 KB)
-      auto score = [&](int i) {
+      // What is known of the barriers that come next (see Tests)
+      Tests tests{};
+      bool have_p[2] = {false, false}, have_k = false, have_v = false;
+#pragma unroll
+      for (int t = 0; t < 3; ++t) tests.bar[t] = smem_u32(drain);
+      auto test_weights = [&](int i, uint32_t n) {
+        tests.bar[0] = smem_u32(&p_full[2 * i + (n & 1)]);
+        tests.parity[0] = (n >> 1) & 1;
+      };
+      auto test_loads = [&](uint32_t k, uint32_t v) {
+        tests.bar[1] = smem_u32(&k_full[k % kSlots]);
+        tests.parity[1] = (k / kSlots) & 1;
+        tests.bar[2] = smem_u32(&v_full[v % kSlots]);
+        tests.parity[2] = (v / kSlots) & 1;
+      };
+      // S_i of a step (the n-th) with the keys of slot k, into buffer n % 2
+      auto score = [&](int i, uint32_t n, uint32_t k) {
+        const uint32_t buf = n & 1;
+        score_product(one, tmem + kSCol + 2 * kStep * i + kStep * buf,
+                      lo_kmajor + (kQOff + i * 2 * kChunk) / 16,
+                      lo_kmajor + (kKOff + (k % kSlots) * kSlotBytes) / 16, hi_word, kIdescS, tests);
+        commit(one, &s_full[2 * i + buf]);
+      };
+      // O_i += P_i V: 4 k-steps of 16 keys; P_i from TMEM (bf16 pairs, 8 columns per k-step), V
+      // MN-major (stride offset: next 8 keys = 1 KB)
+      auto output = [&](int i, uint32_t n, uint32_t v, bool add) {
+        const uint32_t pc = tmem + kSCol + 2 * kStep * i + kStep * (n & 1);
+        const uint32_t vd = lo_v + (kVOff + (v % kSlots) * kSlotBytes) / 16;
+#pragma unroll
+        for (int kk = 0; kk < kStep / 16; ++kk)
+          mma_ts(one, tmem + kOCol + kD * i, pc + 8 * kk, vd + kk * 2048 / 16, hi_word, kIdescPV,
+                 add || kk > 0 ? 1u : 0u);
+        commit(one, &pv_done[i]);
+      };
+      // the scores of cursor sc's step in query tile i
+      auto next_score = [&](int i) {
         if (sc.step == 0) {
           wait(&q_full[i], sc.items[i]++);
           tc_fence_after();
         }
-        const uint32_t buf = sc.steps[i]++ & 1;
-        if (ok) {
-          const uint32_t qd = lo_kmajor + (kQOff + i * 2 * kChunk) / 16;
-          const uint32_t kd =
-              lo_kmajor + (kRingOff + sc.slot * kSlotBytes + (sc.step & 1) * (kChunk / 2)) / 16;
-          const uint32_t d = tmem + kSCol + 2 * kStep * i + kStep * buf;
-#pragma unroll
-          for (int j = 0; j < kD / 16; ++j) {
-            const uint32_t off = ((j >> 2) * kChunk + 32 * (j & 3)) / 16;
-            mma_ss(one, d, qd + off, kd + off, hi_word, kIdescS, j > 0 ? 1u : 0u);
-          }
-          commit(one, &s_full[2 * i + buf]);
-          if (sc.step + 1 == sc.nsteps) commit(one, &q_empty[i]);
-        }
-      };
-      auto keys_there = [&]() {
-        if ((sc.step & 1) == 0) wait(&full[sc.slot], sc.phase);
-      };
-      auto keys_used = [&]() {
-        if (ok && ((sc.step & 1) || sc.step + 1 == sc.nsteps)) commit(one, &empty[sc.slot]);
-        advance(sc);
+        if (!ok) return;
+        score(i, sc.steps[i]++, sc.n);
+        if (sc.step + 1 == sc.nsteps) commit(one, &q_empty[i]);
+        if (i + 1 == sc.nq) commit(one, &k_empty[sc.n % kSlots]);
       };
       for (int ahead = 0; ahead < 2; ++ahead) {
         if (ok && sc.nsteps > 0) {
-          keys_there();
+          wait(&k_full[sc.n % kSlots], sc.n / kSlots);
           tc_fence_after();
 #pragma unroll
           for (int i = 0; i < 2; ++i)
-            if (i < sc.nq) score(i);
-          keys_used();
+            if (i < sc.nq) next_score(i);
+          advance(sc);
         }
       }
       while (ok && pv.nsteps > 0) {
-        // (all that does not hang on the weights comes before the wait for them)
-        if ((pv.step & 1) == 0) wait(&full[pv.slot], pv.phase);
+        // In the middle of an item, where neither cursor comes to its end, a step is this:
+        if (pv.nq == 2 && pv.step > 0 && sc.step == pv.step + 2) {
+          uint32_t k = sc.n, v = pv.n, n0 = pv.steps[0], n1 = pv.steps[1];
+          const int steps = sc.nsteps - 1 - sc.step;
+          for (int left = steps; ok && left > 0; --left) {
+            if (!have_v) wait(&v_full[v % kSlots], v / kSlots);
+            if (!have_k) wait(&k_full[k % kSlots], k / kSlots);
+            if (!have_p[0]) wait(&p_full[n0 & 1], n0 >> 1);
+            tc_fence_after();
+            if (!ok) break;
+            output(0, n0, v, true);
+            test_weights(1, n1);
+            score(0, n0, k);
+            ++n0;
+            if (!__all_sync(0xffffffffu, tests.done[0])) wait(&p_full[2 + (n1 & 1)], n1 >> 1);
+            tc_fence_after();
+            if (!ok) break;
+            output(1, n1, v, true);
+            commit(one, &v_empty[v % kSlots]);
+            test_weights(0, n0);
+            test_loads(k + 1, v + 1);
+            score(1, n1, k);
+            commit(one, &k_empty[k % kSlots]);
+            ++n1, ++k, ++v;
+            have_p[0] = __all_sync(0xffffffffu, tests.done[0]);
+            have_k = __all_sync(0xffffffffu, tests.done[1]);
+            have_v = __all_sync(0xffffffffu, tests.done[2]);
+          }
+          if (!ok) break;
+          if (steps > 0) {
+            sc.n = k, pv.n = v;
+            sc.steps[0] = sc.steps[0] + (n0 - pv.steps[0]);
+            sc.steps[1] = sc.steps[1] + (n1 - pv.steps[1]);
+            pv.steps[0] = n0, pv.steps[1] = n1;
+            sc.step += steps, pv.step += steps;
+          }
+        }
+        if (!have_v) wait(&v_full[pv.n % kSlots], pv.n / kSlots);
         if (pv.step == 0) {
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
@@ -614,33 +664,38 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
-        if (sc.nsteps > 0) keys_there();
-        const uint32_t vd =
-            lo_v + (kRingOff + pv.slot * kSlotBytes + (pv.step & 1) * (kChunk / 2)) / 16;
+        if (sc.nsteps > 0 && !have_k) wait(&k_full[sc.n % kSlots], sc.n / kSlots);
+        have_k = have_v = false;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           if (i < pv.nq) {
             const uint32_t n = pv.steps[i]++;
-            const uint32_t buf = n & 1;
-            wait(&p_full[2 * i + buf], n >> 1);
+            if (!have_p[i]) wait(&p_full[2 * i + (n & 1)], n >> 1);
+            have_p[i] = false;
             tc_fence_after();
             if (ok) {
-              // O_i += P_i V: 4 k-steps of 16 keys; P_i from TMEM (bf16 pairs, 8 columns per
-              // k-step), V MN-major (leading offset: next 64 elements = next chunk;
-              // stride offset: next 8 keys = 1 KB)
-              const uint32_t pc = tmem + kSCol + 2 * kStep * i + kStep * buf;
-#pragma unroll
-              for (int kk = 0; kk < kStep / 16; ++kk)
-                mma_ts(one, tmem + kOCol + kD * i, pc + 8 * kk, vd + kk * 2048 / 16, hi_word,
-                       kIdescPV, (pv.step > 0 || kk > 0) ? 1u : 0u);
-              commit(one, &pv_done[i]);
-              if (i + 1 == pv.nq && ((pv.step & 1) || pv.step + 1 == pv.nsteps))
-                commit(one, &empty[pv.slot]);
+              output(i, n, pv.n, pv.step > 0);
+              if (i + 1 == pv.nq) commit(one, &v_empty[pv.n % kSlots]);
             }
           }
-          if (i < sc.nq) score(i);
+          if (i < sc.nq && ok) {
+            const bool other = i == 0 && pv.nq == 2;
+            test_weights(other ? 1 : 0, other ? pv.steps[1] : pv.steps[0]);
+            test_loads(sc.n + 1, pv.n + 1);
+            next_score(i);
+            const bool there = __all_sync(0xffffffffu, tests.done[0]);
+            if (other) {
+              have_p[1] = there;
+            } else {
+              have_p[0] = there;
+            }
+            if (i + 1 == sc.nq) {
+              have_k = __all_sync(0xffffffffu, tests.done[1]);
+              have_v = __all_sync(0xffffffffu, tests.done[2]);
+            }
+          }
         }
-        if (sc.nsteps > 0) keys_used();
+        if (sc.nsteps > 0) advance(sc);
         advance(pv);
       }
       __syncwarp();
@@ -666,11 +721,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float sc = pos_scale ? p.scale_log2 : 1.f;
     Walk walk(p, blockIdx.x, lane);
     Item it;
-    uint32_t u = 0, mine = 0;  // tiles of the CTA before the item, steps of this query tile
+    uint32_t u = 0, mine = 0;  // steps of the CTA before the item, of this query tile
     bool ok = true;
     while (ok && walk.get(p, step, lane, it)) {
       if (qi >= it.nq) {
-        u += it.ntiles;
+        u += it.nsteps;
         continue;
       }
       const bool rvalid = tok < it.ntok;
@@ -681,13 +736,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                            kD;
       float m_run = -INFINITY, l_run = 0.f;
       for (int v = 0; v < it.nsteps; ++v, ++mine) {
-        const uint32_t tile = u + (v >> 1);
+        const uint32_t n = u + v;
         const uint32_t buf = mine & 1;
-        ok = mbar_wait_bounded(&s_full[2 * qi + buf], (mine >> 1) & 1, abort_flag) &&
-             mbar_wait_bounded(&mask_full[tile % kMaskSlots], (tile / kMaskSlots) & 1, abort_flag);
+        // (the mask is long there; it is looked at while the scores may not be)
+        ok = mbar_wait_bounded(&mask_full[n % kMaskSlots], (n / kMaskSlots) & 1, abort_flag);
+        const uint64_t seen = step_mask[n % kMaskSlots];
+        ok = ok && mbar_wait_bounded(&s_full[2 * qi + buf], (mine >> 1) & 1, abort_flag);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
-        const uint64_t mtile = tile_mask[2 * (tile % kMaskSlots) + (v & 1)];
         tc_fence_after();
         float s[kStep];
         const uint32_t sb = s_addr + kStep * buf;
@@ -701,7 +757,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // places up to the row's own, from its window's first on or of first tokens
         // (places between the first tokens and the item's window are not in the mask)
         const int k0 = v * kStep;
-        uint64_t mw = mtile;
+        uint64_t mw = seen;
         if (k0 + kStep - 1 > pos || (k0 < low && k0 + kStep > p.num_sink))
           mw &= WindowRange::below(pos + 1 - k0) &
                 (~WindowRange::below(low - k0) | WindowRange::below(p.num_sink - k0));
@@ -765,15 +821,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_wait_st();
         // keys without a cache row: zero their value rows (0 x NaN would poison P.V), by
         // query tile 0's threads (P.V_1(v) follows P.V_0(v)): (key row / 2, chunk row % 2)
-        if (qi == 0 && mtile != ~0ull) {
-          const uint32_t load = 2 * tile + 1, vs = load % kSlots;
+        if (qi == 0 && seen != ~0ull) {
+          const uint32_t slot = n % kSlots;
           ok = __all_sync(0xffffffffu,
-                          mbar_wait_bounded(&full[vs], (load / kSlots) & 1, abort_flag));
+                          mbar_wait_bounded(&v_full[slot], (n / kSlots) & 1, abort_flag));
           if (!ok) break;
-          if (!((mtile >> (row >> 1)) & 1ull)) {
-            uint4* dst = reinterpret_cast<uint4*>(smem + kRingOff + vs * kSlotBytes +
-                                                  (row & 1) * kChunk +
-                                                  (kStep * (v & 1) + (row >> 1)) * 128);
+          if (!((seen >> (row >> 1)) & 1ull)) {
+            uint4* dst = reinterpret_cast<uint4*>(smem + kVOff + slot * kSlotBytes +
+                                                  (row & 1) * kHalf + (row >> 1) * 128);
 #pragma unroll
             for (int i = 0; i < 8; ++i) dst[i] = make_uint4(0u, 0u, 0u, 0u);
           }
@@ -791,8 +846,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(&p_full[2 * qi + buf]);
       }
       if (!ok) break;
-      u += it.ntiles;
-      if (it.ntiles == 0) {
+      u += it.nsteps;
+      if (it.nsteps == 0) {
         if (rvalid) {  // no key at all: a zero row
           uint4* dst = reinterpret_cast<uint4*>(p.out + qrow);
 #pragma unroll
@@ -850,7 +905,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (ok && *(volatile int*)&flags[1] != 0) {
       Walk over(p, blockIdx.x, lane);
       while (over.get(p, step, lane, it)) {
-        if (tok >= it.ntok || it.ntiles == 0) it.ntok = 0;
+        if (tok >= it.ntok || it.nsteps == 0) it.ntok = 0;
         const int64_t qrow =
             (static_cast<int64_t>(it.q_row + tok) * p.num_q_heads + it.g * G + row % G) * kD;
         unsigned again = __ballot_sync(
@@ -873,9 +928,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   if (*abort_flag) {
-    if (warp == 0 && lane == 0) {
+    if ((warp == 0 || warp == 3) && lane == 0) {
       for (uint32_t t = issued > kSlots ? issued - kSlots : 0; t < issued; ++t)
-        mbar_wait_bounded(&full[t % kSlots], (t / kSlots) & 1, nullptr);
+        mbar_wait_bounded(&(warp == 0 ? k_full : v_full)[t % kSlots], (t / kSlots) & 1, nullptr);
     }
     __syncthreads();
   }
@@ -911,7 +966,7 @@ pa_status launch_window_prefill(const WindowPrefillArgs& w, cudaStream_t stream)
   if (a.num_seqs == 0 || a.max_q_len == 0 || w.total_tokens == 0) return PA_OK;
   const int32_t G = a.num_q_heads / a.num_kv_heads;
   const int64_t rows = a.num_blocks * a.block_size;
-  const int32_t box_rows = a.block_size < kTile ? a.block_size : kTile;
+  const int32_t box_rows = a.block_size < kStep ? a.block_size : kStep;
   CUtensorMap mq, mk, mv;
   if (!make_q_map(&mq, a.q, w.total_tokens, a.num_q_heads, G) ||
       !make_kv_map_swizzled(&mk, a.k_cache, rows, a.num_kv_heads, box_rows) ||
