@@ -74,8 +74,8 @@ constexpr int kBarOff = kStageOff + 8 * kStageBytes;
 // both query tiles' step n + 2.
 constexpr int kMaskSlots = 8;
 // q_full, q_empty, pv_done, o_empty [2] each, s_full, p_full [2][2], k_full, k_empty, v_full,
-// v_empty, mask_full, drain
-constexpr int kNumBars = 4 * 2 + 2 * 4 + 4 * kSlots + kMaskSlots + 1;
+// v_empty, drain
+constexpr int kNumBars = 4 * 2 + 2 * 4 + 4 * kSlots + 1;
 constexpr int kMaskOff = kBarOff + (kNumBars + 1) / 2 * 16;  // a 64-bit word per slot
 constexpr int kMiscOff = kMaskOff + kMaskSlots * 8;
 constexpr int kBytes = kMiscOff + 16;
@@ -387,9 +387,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* k_empty = k_full + kSlots;        // [kSlots] their score products done (commit)
   uint64_t* v_full = k_empty + kSlots;        // [kSlots] values landed
   uint64_t* v_empty = v_full + kSlots;        // [kSlots] their output products done (commit)
-  uint64_t* mask_full = v_empty + kSlots;     // [kMaskSlots] row mask posted
-  uint64_t* drain = mask_full + kMaskSlots;   // every product done
-  uint64_t* step_mask = reinterpret_cast<uint64_t*>(smem + kMaskOff);  // [kMaskSlots]
+  uint64_t* drain = v_empty + kSlots;         // every product done
+  volatile uint64_t* step_mask =
+      reinterpret_cast<volatile uint64_t*>(smem + kMaskOff);  // [kMaskSlots]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kMiscOff);
   int* flags = reinterpret_cast<int*>(smem + kMiscOff + 8);
 
@@ -414,7 +414,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&v_full[s], 1);
       mbar_init(&v_empty[s], 1);
     }
-    for (int s = 0; s < kMaskSlots; ++s) mbar_init(&mask_full[s], 1);
     mbar_init(drain, 1);
     flags[0] = flags[1] = 0;
     mbar_init_fence();
@@ -476,10 +475,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint64_t seen = there ? now.seen : 0;
           const uint32_t w0 = __reduce_or_sync(0xffffffffu, static_cast<uint32_t>(seen));
           const uint32_t w1 = __reduce_or_sync(0xffffffffu, static_cast<uint32_t>(seen >> 32));
-          if (lane == 0) {
-            step_mask[n % kMaskSlots] = (static_cast<uint64_t>(w1) << 32) | w0;
-            mbar_arrive(&mask_full[n % kMaskSlots]);
-          }
+          // (read once the scores are there: they wait for the keys, which are asked for after this)
+          if (lane == 0) step_mask[n % kMaskSlots] = (static_cast<uint64_t>(w1) << 32) | w0;
         }
         load_step(tm, there ? now.bid * p.block_size + now.row : -1, now.g,
                   slots + slot * kSlotBytes, &full[slot], log2_rpb, pol, lane);
@@ -738,12 +735,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int v = 0; v < it.nsteps; ++v, ++mine) {
         const uint32_t n = u + v;
         const uint32_t buf = mine & 1;
-        // (the mask is long there; it is looked at while the scores may not be)
-        ok = mbar_wait_bounded(&mask_full[n % kMaskSlots], (n / kMaskSlots) & 1, abort_flag);
-        const uint64_t seen = step_mask[n % kMaskSlots];
-        ok = ok && mbar_wait_bounded(&s_full[2 * qi + buf], (mine >> 1) & 1, abort_flag);
-        ok = __all_sync(0xffffffffu, ok);
+        ok = __all_sync(0xffffffffu, mbar_wait_bounded(&s_full[2 * qi + buf], (mine >> 1) & 1,
+                                                       abort_flag));
         if (!ok) break;
+        const uint64_t seen = step_mask[n % kMaskSlots];
         tc_fence_after();
         float s[kStep];
         const uint32_t sb = s_addr + kStep * buf;
