@@ -116,6 +116,35 @@ struct Params {
   float scale_log2;
 };
 
+// 16 columns of this thread's TMEM lane, without waiting
+__device__ __forceinline__ void st16(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+// Waits for this thread's stores to TMEM, and tells whether a barrier's phase is complete: the
+// two take their time side by side.
+__device__ __forceinline__ bool wait_st_and_test(uint64_t* bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred t;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 t, [%1], %2;\n\t"
+      "tcgen05.wait::st.sync.aligned;\n\t"
+      "selp.u32 %0, 1, 0, t;\n\t}"
+      : "=r"(done)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return done != 0;
+}
+// max of three, NaN if one of them is
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
 // ------------------------------------------------------------------ items --
 struct Item {
   int b, g;      // sequence, kv head
@@ -527,37 +556,56 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (ok) ok = __all_sync(0xffffffffu, mbar_wait_bounded(bar, n & 1, abort_flag));
       };
       // A cursor over the steps of all items; scores run two steps ahead of outputs, so each
-      // has its own.  (Counts come by a reduction, whose result is known to be the
-      // same in every lane.)
+      // has its own.  (What a walk says comes by a reduction, whose result is known to
+      // be the same in every lane.)
       struct Cursor {
-        Walk walk;
         int step, nsteps, nq;  // of the item in hand; nsteps 0: no more
         uint32_t n;            // steps before it
         uint32_t steps[2];     // the same per query tile
         uint32_t items[2];     // items begun per query tile
       };
-      auto fetch = [&](Cursor& c) {
+      Walk walk(p, blockIdx.x, lane);
+      int after = -1;  // the item after the scores' one: 4 steps + query tiles; 0 none, -1 not known yet
+      auto look_ahead = [&]() {
         Item x;
-        c.step = c.nsteps = c.nq = 0;
-        while (c.walk.get(p, step, lane, x)) {
-          if (x.nsteps > 0) {
-            c.nsteps = __reduce_max_sync(0xffffffffu, x.nsteps);
-            c.nq = __reduce_max_sync(0xffffffffu, x.nq);
-            break;
-          }
-        }
+        if (after >= 0) return;
+        after = 0;
+        while (after == 0 && walk.get(p, step, lane, x))
+          if (x.nsteps > 0) after = __reduce_max_sync(0xffffffffu, 4 * x.nsteps + x.nq);
       };
-      auto advance = [&](Cursor& c) {
-        ++c.n;
-        if (c.step + 1 == c.nsteps) {
-          fetch(c);
+      int begun[2] = {0, 0};  // items that the scores have come to and the outputs have not
+      auto take = [&](Cursor& c, int item) {
+        c.step = 0;
+        c.nsteps = item >> 2;
+        c.nq = item & 3;
+      };
+      Cursor sc{0, 0, 0, 0, {0, 0}, {0, 0}};
+      auto next_scores = [&]() {
+        look_ahead();
+        take(sc, after);
+        if (begun[0] == 0) {
+          begun[0] = after;
         } else {
-          ++c.step;
+          begun[1] = after;
         }
+        if (after > 0) after = -1;
       };
-      Cursor sc{Walk(p, blockIdx.x, lane), 0, 0, 0, 0, {0, 0}, {0, 0}};
-      fetch(sc);
+      auto advance_scores = [&]() {
+        ++sc.n;
+        if (++sc.step == sc.nsteps) next_scores();
+      };
       Cursor pv = sc;
+      auto next_outputs = [&]() {
+        take(pv, begun[0]);
+        begun[0] = begun[1];
+        begun[1] = 0;
+      };
+      auto advance_outputs = [&]() {
+        ++pv.n;
+        if (++pv.step == pv.nsteps) next_outputs();
+      };
+      next_scores();
+      next_outputs();
       // What is known of the barriers that come next (see Tests)
       Tests tests{};
       bool have_p[2] = {false, false}, have_k = false, have_v = false;
@@ -610,7 +658,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int i = 0; i < 2; ++i)
             if (i < sc.nq) next_score(i);
-          advance(sc);
+          advance_scores();
         }
       }
       while (ok && pv.nsteps > 0) {
@@ -653,6 +701,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (!have_v) wait(&v_full[pv.n % kSlots], pv.n / kSlots);
         if (pv.step == 0) {
+          look_ahead();  // (a wait follows in any case)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             if (i < pv.nq) {
@@ -692,8 +741,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
-        if (sc.nsteps > 0) advance(sc);
-        advance(pv);
+        advance_outputs();
+        if (sc.nsteps > 0) advance_scores();
       }
       __syncwarp();
       commit(one, drain);
@@ -718,11 +767,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float sc = pos_scale ? p.scale_log2 : 1.f;
     Walk walk(p, blockIdx.x, lane);
     Item it;
+    bool scores = false;  // (of the next step are there)
     uint32_t u = 0, mine = 0;  // steps of the CTA before the item, of this query tile
     bool ok = true;
-    while (ok && walk.get(p, step, lane, it)) {
+    bool have = walk.get(p, step, lane, it);
+    while (ok && have) {
       if (qi >= it.nq) {
         u += it.nsteps;
+        have = walk.get(p, step, lane, it);
         continue;
       }
       const bool rvalid = tok < it.ntok;
@@ -735,9 +787,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int v = 0; v < it.nsteps; ++v, ++mine) {
         const uint32_t n = u + v;
         const uint32_t buf = mine & 1;
-        ok = __all_sync(0xffffffffu, mbar_wait_bounded(&s_full[2 * qi + buf], (mine >> 1) & 1,
-                                                       abort_flag));
-        if (!ok) break;
+        if (!__all_sync(0xffffffffu, scores)) {
+          ok = __all_sync(0xffffffffu, mbar_wait_bounded(&s_full[2 * qi + buf], (mine >> 1) & 1,
+                                                         abort_flag));
+          if (!ok) break;
+        }
         const uint64_t seen = step_mask[n % kMaskSlots];
         tc_fence_after();
         float s[kStep];
@@ -757,19 +811,23 @@ __global__ void __launch_bounds__(kThreads, 1)
           mw &= WindowRange::below(pos + 1 - k0) &
                 (~WindowRange::below(low - k0) | WindowRange::below(p.num_sink - k0));
         if (!rvalid) mw = 0ull;
+        auto largest = [&]() {
+          float mq[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int c = 0; c < kStep; c += 8) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) mq[i] = fmax3(mq[i], s[c + 2 * i], s[c + 2 * i + 1]);
+          }
+          return fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3]));
+        };
+        float mx_raw = largest();  // (first, as the mask takes longer to come than the scores)
         if (mw != ~0ull) {
           const uint32_t w[2] = {static_cast<uint32_t>(mw), static_cast<uint32_t>(mw >> 32)};
 #pragma unroll
           for (int c = 0; c < kStep; ++c)
             if (!((w[c >> 5] >> (c & 31)) & 1u)) s[c] = -INFINITY;
+          mx_raw = largest();
         }
-        float mq[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-        for (int c = 0; c < kStep; c += 8) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) mq[i] = fmax3(mq[i], s[c + 2 * i], s[c + 2 * i + 1]);
-        }
-        const float mx_raw = fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3]));
         const float mx = pos_scale ? mx_raw * p.scale_log2 : mx_raw;
         // lazy rescale; tcgen05.ld/st are warp-wide, so the warp rescales together when any
         // of its rows needs it (the others by 1), once the output product before is done
@@ -810,10 +868,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float2 e = make_float2(fast_exp2(x.x), fast_exp2(x.y));
           lq[i & 1] = fadd2(lq[i & 1], e);
           pr[i] = pack_bf16x2(e.x, e.y);
+          if (i == 15) st16(sb, pr);
         }
-        tc_st32u_nowait(sb, pr);
+        st16(sb + 16, pr + 16);
         l_run += (lq[0].x + lq[0].y) + (lq[1].x + lq[1].y);
-        tc_wait_st();
+        // (tested meanwhile: the next step's scores)
+        scores = wait_st_and_test(&s_full[2 * qi + (buf ^ 1)], ((mine + 1) >> 1) & 1);
         // keys without a cache row: zero their value rows (0 x NaN would poison P.V), by
         // query tile 0's threads (P.V_1(v) follows P.V_0(v)): (key row / 2, chunk row % 2)
         if (qi == 0 && seen != ~0ull) {
@@ -842,7 +902,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok) break;
       u += it.nsteps;
-      if (it.nsteps == 0) {
+      const bool none = it.nsteps == 0;
+      have = walk.get(p, step, lane, it);  // (the next item, while the last product runs)
+      if (none) {
         if (rvalid) {  // no key at all: a zero row
           uint4* dst = reinterpret_cast<uint4*>(p.out + qrow);
 #pragma unroll
@@ -855,7 +917,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
       tc_fence_after();
       const float inv = l_run > 0.f ? 1.f / l_run : 0.f;
-      bool nan_row = false;
       float o[kD];
 #pragma unroll
       for (int c = 0; c < kD; c += 32) tc_ld32_nowait(o_addr + c, &o[c]);
@@ -863,8 +924,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&o_empty[qi]);
+      float nan_max = -INFINITY;  // NaN where an element is
 #pragma unroll
-      for (int c = 0; c < kD; ++c) nan_row |= o[c] != o[c];
+      for (int c = 0; c < kD; c += 2) nan_max = max3_nan(nan_max, o[c], o[c + 1]);
+      const bool nan_row = nan_max != nan_max;
       // A thread's row is 256 bytes, far from the next one's: half rows go through shared
       // memory (16-byte unit c of row r at c ^ (r & 7)), and the warp stores four rows
       // (128-byte lines) at a time instead of 32 pieces of 16 bytes.
