@@ -8,39 +8,41 @@
 // the second product.
 //
 // An item is two query tiles of 128 rows (128 / G consecutive new tokens x the G
-// query heads of one kv head each) of one sequence; they share every key and value
-// tile.  Its tiles run over the places (window.cuh) of the rows that the first tokens and
-// its first row's window leave.  Windows make items short (a window of 250: three tiles), so
-// CTAs stay: one per SM walks items c, c + grid, ... of all sequences, and while an item's last
-// tiles are weighed and its rows written, the next one's queries, keys and values
-// land and its first score products run.
-//  * A key tile (128 places) is weighed in two steps of 64.  TMEM (512 columns): outputs O0, O1
-//    (128 each) and for each query tile two score buffers of 64, so that while the softmax
-//    works on step v, S(v + 1) is there or on its way: with one buffer of 128 a query tile's
-//    softmax and products took turns, and their hand-overs (about 1000 cycles a tile) left
-//    the tensor core idle half the time.  A step's weights (bf16 pairs) overwrite
-//    the first half of its scores.
-//  * warp 0 loads keys and values (K(0), V(0), K(1), ... through four slots) and posts each
-//    tile's row mask, warp 2 the query tiles; all by TMA, 128-byte swizzled.
+// query heads of one kv head each) of one sequence; they share every key and value.
+// Its steps of 64 keys run over the places (window.cuh) of the rows that the first tokens
+// and its first row's window leave.  Windows make items short (a window of 250: five
+// steps), so CTAs stay: one per SM walks items c, c + grid, ... of all sequences, and while
+// an item's last steps are weighed and its rows written, the next one's queries, keys and
+// values land and its first score products run.
+//  * TMEM (512 columns): outputs O0, O1 (128 each) and for each query tile two score
+//    buffers of 64, so that while the softmax works on step v, S(v + 1) is there or on
+//    its way.  A step's weights (bf16 pairs) overwrite the first half of its scores.
+//  * warps 0 and 3 load keys and values, four steps ahead (one warp for both came too late:
+//    1680 us where two take 1190), warp 0 posts each step's row mask; warp 2 loads the
+//    query tiles; all by TMA, 128-byte swizzled.
 //  * one thread of warp 1 issues every product: O_i += P_i(v) V(v), S_i(v + 2) = Q_i K(v + 2)^T,
 //    then the other query tile's.  Products of one thread run in order, so S_i(v + 2)
-//    may overwrite P_i(v) without a wait between them.  (Two warps, one per query tile:
-//    1361 us where one takes 1339.)
+//    may overwrite P_i(v) without a wait between them.  The core holds a few products ahead,
+//    about 100 cycles of work, so what this warp does besides must be short: the middle of
+//    an item is a loop of its own, and barriers are asked before their answers matter.
 //  * warps 4-7 and 8-11 do the softmax of query tiles 0 and 1, one thread per row.
-// What bounds it: the softmax warps' chain.  A step of both query tiles takes 1940 cycles: 1282 of
-// the tensor core (2 x (385 + 256)), 1024 of the arithmetic pipes (two warps on each
-// quarter of the SM, 512 of them exponentials at 4 cycles a warp's); with two
-// warps a quarter neither is kept busy through loads of scores, votes and
-// hand-overs (the issue slots are used in 43% of the cycles).
+// What bounds it (cycles of a step of both query tiles, on a long prompt): products 1240 alone
+// (2 x (370 + 256): a score product of 64 keys reads as many bytes of shared memory as it has
+// cycles), 1500 beside copies and hand-overs; the softmax warps' chain of scores, maximum,
+// exponentials, weights and barriers 850 alone, 1250 and 400 of hand-overs where two
+// warps of a quarter of the SM run in step: some 1700 in all.  Without the softmax's
+// arithmetic the kernel takes 1075 us instead of 1190.
 // Measured (GPU time, L2 cold; heads q / kv):
-//  * 4 prompts of 8192, window 4096, 32 / 8: 1339 us, 1.23 PFLOP/s over visible pairs
+//  * 4 prompts of 8192, window 4096, 32 / 8: 1190 us, 1.39 PFLOP/s over visible pairs
 //    (a CTA per item and products issued from a branch of one lane: 1903);
-//  * 8 chunks of 512 behind up to 6000, window 1024, 16 / 8: 51 us (73); its 256 items
+//  * 8 chunks of 512 behind up to 6000, window 1024, 16 / 8: 46 us (73); its 256 items
 //    take two rounds of the 152 SMs;
-//  * 5 prompts of 1000 .. 6001, window 250, 16 / 2: 68.5 us (147);
-//  * a few short rows: 10.3 us, a chain of lengths, block ids, copies and products.
-// Score buffers of 128 keys: 1311, 53 and 80 us; four softmax groups that split a step's
-// keys or take steps in turn: 1471 and 1568; weights handed over by halves: 1347.
+//  * 5 prompts of 1000 .. 6001, window 250, 16 / 2: 68 us (147), half of it starts and ends
+//    of items;
+//  * a few short rows: 9.6 us, a chain of lengths, block ids, copies and products.
+// Slower: the two warps of a quarter kept apart by a barrier (1375), the next scores read before
+// the weights are handed over (1360), next queries brought to L2 (no gain); before the loads
+// were split, two issuing warps, one buffer of 128 keys, four softmax groups.
 //
 // Every wait is bounded (2 s); a timeout sets an error bit, drains what was issued and
 // frees TMEM before the CTA exits.
@@ -223,7 +225,8 @@ struct Walk {
     if (kend <= 0) {  // no row has a key (pos0 may be far below zero)
       it.win = WindowRange{0, 0, 0, 0};
     } else {
-      it.win = window_range(kend, max(0, it.pos0 - p.window + 1), p.num_sink, min(p.log2_bs, kLog2Rows));
+      it.win = window_range(kend, max(0, it.pos0 - p.window + 1), p.num_sink,
+                            min(p.log2_bs, kLog2Rows));
       it.pos0 -= it.win.skip;
     }
     it.nsteps = (it.win.len + kStep - 1) / kStep;
@@ -255,8 +258,8 @@ __device__ __forceinline__ void commit(uint32_t one, uint64_t* bar) {
 }
 // A score product: S = Q K^T over 64 keys, 8 k-steps of 16 over the 128 head elements, both operands
 // K-major 128-byte swizzled (a k-step in a chunk is 32 bytes on).  While it is issued, three
-// barriers are tested (as far as `parity` says): the answers take as long as everything
-// else that goes through shared memory beside the operands' reads, 150 cycles and more.
+// barriers are asked whether their phase of that parity is complete: beside the operands'
+// reads of shared memory an answer takes 150 cycles and more.
 struct Tests {
   uint32_t bar[3], parity[3], done[3];
 };
