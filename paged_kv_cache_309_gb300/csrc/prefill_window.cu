@@ -256,9 +256,9 @@ __device__ __forceinline__ void commit(uint32_t one, uint64_t* bar) {
       "r"(one)
       : "memory");
 }
-// A score product: S = Q K^T over 64 keys, 8 k-steps of 16 over the 128 head elements, both operands
-// K-major 128-byte swizzled (a k-step in a chunk is 32 bytes on).  While it is issued, three
-// barriers are asked whether their phase of that parity is complete: beside the operands'
+// A score product: S = Q K^T over 64 keys, 8 k-steps of 16 over the 128 head elements, both
+// operands K-major 128-byte swizzled (a k-step in a chunk is 32 bytes on).  While it is
+// issued, three barriers are asked whether their phase of that parity is complete: beside the operands'
 // reads of shared memory an answer takes 150 cycles and more.
 struct Tests {
   uint32_t bar[3], parity[3], done[3];
@@ -392,7 +392,8 @@ __device__ __noinline__ void row_by_plain_loads(const Params& p, int b, int g, i
       o[3] += w * __uint_as_float(vb[i].y & 0xFFFF0000u);
     }
     // (a row that sees a token of NaN values is NaN: done)
-    if (__all_sync(0xffffffffu, o[0] != o[0] && o[1] != o[1] && o[2] != o[2] && o[3] != o[3])) break;
+    const bool all_nan = o[0] != o[0] && o[1] != o[1] && o[2] != o[2] && o[3] != o[3];
+    if (__all_sync(0xffffffffu, all_nan)) break;
   }
   uint2 r = make_uint2(0u, 0u);
   if (l != 0.f) {
@@ -402,6 +403,9 @@ __device__ __noinline__ void row_by_plain_loads(const Params& p, int b, int g, i
   reinterpret_cast<uint2*>(p.out + qrow)[lane] = r;
 }
 
+// kPositive: scale > 0, which goes into the exponentials' products; else scores are multiplied
+// first (64 products a step that are not there otherwise, and their instructions: 1% of a long prompt)
+template <bool kPositive>
 __global__ void __launch_bounds__(kThreads, 1)
     window_prefill_kernel(const __grid_constant__ CUtensorMap tm_q,
                           const __grid_constant__ CUtensorMap tm_k,
@@ -507,7 +511,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint64_t seen = there ? now.seen : 0;
           const uint32_t w0 = __reduce_or_sync(0xffffffffu, static_cast<uint32_t>(seen));
           const uint32_t w1 = __reduce_or_sync(0xffffffffu, static_cast<uint32_t>(seen >> 32));
-          // (read once the scores are there: they wait for the keys, which are asked for after this)
+          // (read once the scores are there, which wait for the keys, asked for after this)
           if (lane == 0) step_mask[n % kMaskSlots] = (static_cast<uint64_t>(w1) << 32) | w0;
         }
         load_step(tm, there ? now.bid * p.block_size + now.row : -1, now.g,
@@ -568,7 +572,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t items[2];     // items begun per query tile
       };
       Walk walk(p, blockIdx.x, lane);
-      int after = -1;  // the item after the scores' one: 4 steps + query tiles; 0 none, -1 not known yet
+      // the item after the scores' one as 4 steps + query tiles; 0: none, -1: not known yet
+      int after = -1;
       auto look_ahead = [&]() {
         Item x;
         if (after >= 0) return;
@@ -629,7 +634,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t buf = n & 1;
         score_product(one, tmem + kSCol + 2 * kStep * i + kStep * buf,
                       lo_kmajor + (kQOff + i * 2 * kChunk) / 16,
-                      lo_kmajor + (kKOff + (k % kSlots) * kSlotBytes) / 16, hi_word, kIdescS, tests);
+                      lo_kmajor + (kKOff + (k % kSlots) * kSlotBytes) / 16, hi_word, kIdescS,
+                      tests);
         commit(one, &s_full[2 * i + buf]);
       };
       // O_i += P_i V: 4 k-steps of 16 keys; P_i from TMEM (bf16 pairs, 8 columns per k-step), V
@@ -766,8 +772,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t o_addr = tmem + lane_addr + kOCol + kD * qi;
     const int G = p.group;
     const int tok = qi * p.tokens_per_tile + row / G;  // the row's token among the item's
-    const bool pos_scale = p.scale_log2 > 0.f;
-    const float sc = pos_scale ? p.scale_log2 : 1.f;
+    const float sc = kPositive ? p.scale_log2 : 1.f;
     Walk walk(p, blockIdx.x, lane);
     Item it;
     bool scores = false;  // (of the next step are there)
@@ -802,7 +807,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_ld32_nowait(sb, &s[0]);
         tc_ld32_nowait(sb + 32, &s[32]);
         tc_wait_ld();
-        if (!pos_scale) {
+        if constexpr (!kPositive) {
 #pragma unroll
           for (int c = 0; c < kStep; ++c) s[c] *= p.scale_log2;
         }
@@ -831,7 +836,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!((w[c >> 5] >> (c & 31)) & 1u)) s[c] = -INFINITY;
           mx_raw = largest();
         }
-        const float mx = pos_scale ? mx_raw * p.scale_log2 : mx_raw;
+        const float mx = kPositive ? mx_raw * p.scale_log2 : mx_raw;
         // lazy rescale; tcgen05.ld/st are warp-wide, so the warp rescales together when any
         // of its rows needs it (the others by 1), once the output product before is done
         const bool need = mx > m_run + kRescaleLog2;
@@ -1020,6 +1025,15 @@ bool make_q_map(CUtensorMap* map, const void* base, int64_t tokens, int32_t head
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+template <bool kPositive>
+pa_status launch(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv,
+                 const Params& p, unsigned grid, cudaStream_t stream) {
+  static std::atomic<uint64_t> smem_raised{0};
+  if (!ensure_smem_limit(window_prefill_kernel<kPositive>, kAlloc, smem_raised)) return PA_ERR_CUDA;
+  window_prefill_kernel<kPositive><<<grid, kThreads, kAlloc, stream>>>(mq, mk, mv, p);
+  return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
 }  // namespace
 
 pa_status launch_window_prefill(const WindowPrefillArgs& w, cudaStream_t stream) {
@@ -1057,8 +1071,6 @@ pa_status launch_window_prefill(const WindowPrefillArgs& w, cudaStream_t stream)
   p.window = w.window;
   p.num_sink = w.num_sink;
   p.scale_log2 = a.scale * 1.4426950408889634f;
-  static std::atomic<uint64_t> smem_raised{0};
-  if (!ensure_smem_limit(window_prefill_kernel, kAlloc, smem_raised)) return PA_ERR_CUDA;
   // one CTA per SM, no more than there can be items
   int64_t grid = num_sms_current_device();
   if (grid <= 0) grid = 148;
@@ -1067,8 +1079,8 @@ pa_status launch_window_prefill(const WindowPrefillArgs& w, cudaStream_t stream)
   const int64_t most = (longest + per - 1) / per * a.num_seqs;
   if (most < grid && most * a.num_kv_heads < grid) grid = most * a.num_kv_heads;
   if ((w.total_tokens / per + a.num_seqs) * a.num_kv_heads > kMaxItems) return PA_ERR_UNSUPPORTED;
-  window_prefill_kernel<<<static_cast<unsigned>(grid), kThreads, kAlloc, stream>>>(mq, mk, mv, p);
-  return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+  return p.scale_log2 > 0.f ? launch<true>(mq, mk, mv, p, static_cast<unsigned>(grid), stream)
+                            : launch<false>(mq, mk, mv, p, static_cast<unsigned>(grid), stream);
 }
 
 }  // namespace pa_detail

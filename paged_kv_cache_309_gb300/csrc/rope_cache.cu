@@ -156,7 +156,9 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) rope_and_cache_kernel
   const bool has0 = c0 < a.head_size, has1 = c1 < a.head_size;
   const int log2_heads = 5 - a.log2_lanes;  // heads side by side
   // a step is such a group of heads of q (the first ones), of k or of v: kind 0, 1, 2
-  auto kind_of = [&](int step) { return step < a.q_steps ? 0 : step < a.q_steps + a.kv_steps ? 1 : 2; };
+  auto kind_of = [&](int step) {
+    return step < a.q_steps ? 0 : step < a.q_steps + a.kv_steps ? 1 : 2;
+  };
   auto head_of = [&](int step, int kind) {
     const int first = kind == 0 ? 0 : kind == 1 ? a.q_steps : a.q_steps + a.kv_steps;
     return ((step - first) << log2_heads) + (lane >> a.log2_lanes);

@@ -103,6 +103,21 @@ def test_prefill_scores_of_minus_infinity(window):
     assert bool((out[600:700] == 0).all())
 
 
+@pytest.mark.parametrize("scale", [-SCALE, 0.0, 3.0])
+def test_any_scale(scale, monkeypatch):
+    """Scores may be turned round or all be equal; a scale of 3 leaves few tokens with a weight."""
+    monkeypatch.setattr("tests.test_gpu_window.SCALE", scale)
+    lens, new = [400, 300, 33], [200, 300, 1]
+    for cache, r in ((BF16, 2.0 ** -16), (E4M3, 2.0 ** -11)):
+        batch, q = Batch(lens, 2, 16, 23, cache=cache), queries(3, 8, 24)
+        out, _ = decode(batch, q, 130, 4)
+        compare(out, ow.decode(q.double().numpy(), *batch.values(), batch.tables, lens, 130, 4, scale), r)
+    batch, q = Batch(lens, 2, 16, 25), queries(sum(new), 8, 26)
+    out, starts = prefill(batch, q, new, 130, 4)
+    ref = ow.prefill(q.double().numpy(), *batch.values(), batch.tables, starts, lens, 130, 4, scale)
+    compare(out, ref, 2.0 ** -8)
+
+
 def test_one_block_for_all():
     """Sequences may share blocks."""
     batch = Batch([40, 40, 33], 2, 16, 4)
