@@ -18,7 +18,7 @@
 //    buffers of 64, so that while the softmax works on step v, S(v + 1) is there or on
 //    its way.  A step's weights (bf16 pairs) overwrite the first half of its scores.
 //  * warps 0 and 3 load keys and values, four steps ahead (one warp for both came too late:
-//    1680 us where two take 1190), warp 0 posts each step's row mask; warp 2 loads the
+//    1680 us where two took 1300), warp 0 posts each step's row mask; warp 2 loads the
 //    query tiles; all by TMA, 128-byte swizzled.
 //  * one thread of warp 1 issues every product: O_i += P_i(v) V(v), S_i(v + 2) = Q_i K(v + 2)^T,
 //    then the other query tile's.  Products of one thread run in order, so S_i(v + 2)
@@ -30,19 +30,22 @@
 // (2 x (370 + 256): a score product of 64 keys reads as many bytes of shared memory as it has
 // cycles), 1500 beside copies and hand-overs; the softmax warps' chain of scores, maximum,
 // exponentials, weights and barriers 850 alone, 1250 and 400 of hand-overs where two
-// warps of a quarter of the SM run in step: some 1700 in all.  Without the softmax's
-// arithmetic the kernel takes 1075 us instead of 1190.
+// warps of a quarter of the SM run in step: some 1700 in all.  Warps wait for
+// instructions more than for anything else (1.9 warps an issue): loops are kept short.
+// Without the softmax's arithmetic the kernel takes 1075 us instead of 1190.
 // Measured (GPU time, L2 cold; heads q / kv):
-//  * 4 prompts of 8192, window 4096, 32 / 8: 1190 us, 1.39 PFLOP/s over visible pairs
+//  * 4 prompts of 8192, window 4096, 32 / 8: 1160 us, 1.42 PFLOP/s over visible pairs
 //    (a CTA per item and products issued from a branch of one lane: 1903);
 //  * 8 chunks of 512 behind up to 6000, window 1024, 16 / 8: 46 us (73); its 256 items
 //    take two rounds of the 152 SMs;
-//  * 5 prompts of 1000 .. 6001, window 250, 16 / 2: 68 us (147), half of it starts and ends
-//    of items;
+//  * 5 prompts of 1000 .. 6001, window 250, 16 / 2: 67 us (147): an item of five steps takes
+//    14700 cycles, 4000 of them from its last weights to the next one's first (product, rows
+//    read and written, first step), the other steps at an item's ends 2450 each;
 //  * a few short rows: 9.6 us, a chain of lengths, block ids, copies and products.
 // Slower: the two warps of a quarter kept apart by a barrier (1375), the next scores read before
-// the weights are handed over (1360), next queries brought to L2 (no gain); before the loads
-// were split, two issuing warps, one buffer of 128 keys, four softmax groups.
+// the weights are handed over (1360), both query tiles' products in one rolled body (1245),
+// rows stored straight from registers (narrow window 75), next queries brought to L2 (no gain);
+// before the loads were split, two issuing warps, one buffer of 128 keys, four softmax groups.
 //
 // Every wait is bounded (2 s); a timeout sets an error bit, drains what was issued and
 // frees TMEM before the CTA exits.
@@ -258,8 +261,8 @@ __device__ __forceinline__ void commit(uint32_t one, uint64_t* bar) {
 }
 // A score product: S = Q K^T over 64 keys, 8 k-steps of 16 over the 128 head elements, both
 // operands K-major 128-byte swizzled (a k-step in a chunk is 32 bytes on).  While it is
-// issued, three barriers are asked whether their phase of that parity is complete: beside the operands'
-// reads of shared memory an answer takes 150 cycles and more.
+// issued, three barriers are asked whether their phase of that parity is complete: beside the
+// operands' reads of shared memory an answer takes 150 cycles and more.
 struct Tests {
   uint32_t bar[3], parity[3], done[3];
 };
@@ -404,7 +407,8 @@ __device__ __noinline__ void row_by_plain_loads(const Params& p, int b, int g, i
 }
 
 // kPositive: scale > 0, which goes into the exponentials' products; else scores are multiplied
-// first (64 products a step that are not there otherwise, and their instructions: 1% of a long prompt)
+// first (64 products a step; where they are not used their instructions alone cost 1% of a long
+// prompt)
 template <bool kPositive>
 __global__ void __launch_bounds__(kThreads, 1)
     window_prefill_kernel(const __grid_constant__ CUtensorMap tm_q,
