@@ -259,6 +259,23 @@ def test_random_batches(seed):
     compare(out[pick], [x[pick] for x in ref], 2.0 ** -8)
 
 
+@pytest.mark.parametrize("seed", range(8))
+def test_prefill_short_items(seed):
+    """Items of one step and few, of one and two query tiles in turn, empty sequences between them."""
+    rng = np.random.default_rng(300 + seed)
+    n, h, g = int(rng.integers(20, 50)), int(rng.integers(1, 4)), int(rng.choice([1, 2, 4, 8, 16]))
+    new = [int(x) for x in rng.integers(0, int(rng.choice([3, 40, 130, 300])) + 1, n - 1)] + [5]
+    lens = [a + int(x) for a, x in zip(new, rng.integers(0, int(rng.choice([1, 70, 500])), n))]
+    window, sink = int(rng.choice([1, 2, 17, 64, 65, 130])), int(rng.choice([0, 1, 5, 64, 70]))
+    batch = Batch(lens, h, int(rng.choice([8, 16, 64, 256])), seed, drop=0.1)
+    q = queries(sum(new), h * g, seed + 1)
+    out, starts = prefill(batch, q, new, window, sink)
+    rows = sorted(rng.choice(sum(new), min(sum(new), 60), replace=False).tolist())
+    ref = ow.prefill(q.double().numpy(), *batch.values(), batch.tables, starts, lens, window, sink, SCALE, set(rows))
+    compare(out[rows], [x[rows] for x in ref], 2.0 ** -8)
+    assert bool((prefill(batch, q, new, window, sink)[0] == out).all())
+
+
 def test_calls_on_two_streams_at_once():
     """Two calls that share caches and lengths, each with its workspace, on two streams."""
     batch = Batch([900, 2000, 37], 2, 16, 13)
