@@ -34,14 +34,14 @@
 // instructions more than for anything else (1.9 warps an issue): loops are kept short.
 // Without the softmax's arithmetic the kernel takes 1075 us instead of 1190.
 // Measured (GPU time, L2 cold; heads q / kv):
-//  * 4 prompts of 8192, window 4096, 32 / 8: 1160 us, 1.42 PFLOP/s over visible pairs
+//  * 4 prompts of 8192, window 4096, 32 / 8: 1150 us, 1.44 PFLOP/s over visible pairs
 //    (a CTA per item and products issued from a branch of one lane: 1903);
-//  * 8 chunks of 512 behind up to 6000, window 1024, 16 / 8: 46 us (73); its 256 items
+//  * 8 chunks of 512 behind up to 6000, window 1024, 16 / 8: 45 us (73); its 256 items
 //    take two rounds of the 152 SMs;
-//  * 5 prompts of 1000 .. 6001, window 250, 16 / 2: 67 us (147): an item of five steps takes
+//  * 5 prompts of 1000 .. 6001, window 250, 16 / 2: 66 us (147): an item of five steps takes
 //    14700 cycles, 4000 of them from its last weights to the next one's first (product, rows
 //    read and written, first step), the other steps at an item's ends 2450 each;
-//  * a few short rows: 9.6 us, a chain of lengths, block ids, copies and products.
+//  * a few short rows: 9.4 us, a chain of lengths, block ids, copies and products.
 // Slower: the two warps of a quarter kept apart by a barrier (1375), the next scores read before
 // the weights are handed over (1360), both query tiles' products in one rolled body (1245),
 // rows stored straight from registers (narrow window 75), next queries brought to L2 (no gain);
@@ -406,6 +406,12 @@ __device__ __noinline__ void row_by_plain_loads(const Params& p, int b, int g, i
   reinterpret_cast<uint2*>(p.out + qrow)[lane] = r;
 }
 
+// A wait of the issuing warp that is not over at once.  A call: the loop in line at each of its
+// waits cost 1% to 3%, as instructions between those that are needed.
+__device__ __noinline__ bool wait_on(uint64_t* bar, uint32_t parity, int* flags) {
+  return mbar_wait_bounded(bar, parity, flags);
+}
+
 // kPositive: scale > 0, which goes into the exponentials' products; else scores are multiplied
 // first (64 products a step; where they are not used their instructions alone cost 1% of a long
 // prompt)
@@ -564,7 +570,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t lo_v = static_cast<uint32_t>(smem_desc(smem_u32(smem), kHalf, 1024));
       const uint32_t one = elect_one();
       auto wait = [&](uint64_t* bar, uint32_t n) {
-        if (ok) ok = __all_sync(0xffffffffu, mbar_wait_bounded(bar, n & 1, abort_flag));
+        if (ok && !__all_sync(0xffffffffu, mbar_try_wait(bar, n & 1)))
+          ok = __all_sync(0xffffffffu, wait_on(bar, n & 1, flags));
       };
       // A cursor over the steps of all items; scores run two steps ahead of outputs, so each
       // has its own.  (What a walk says comes by a reduction, whose result is known to
@@ -823,23 +830,19 @@ __global__ void __launch_bounds__(kThreads, 1)
           mw &= WindowRange::below(pos + 1 - k0) &
                 (~WindowRange::below(low - k0) | WindowRange::below(p.num_sink - k0));
         if (!rvalid) mw = 0ull;
-        auto largest = [&]() {
-          float mq[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-          for (int c = 0; c < kStep; c += 8) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) mq[i] = fmax3(mq[i], s[c + 2 * i], s[c + 2 * i + 1]);
-          }
-          return fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3]));
-        };
-        float mx_raw = largest();  // (first, as the mask takes longer to come than the scores)
         if (mw != ~0ull) {
           const uint32_t w[2] = {static_cast<uint32_t>(mw), static_cast<uint32_t>(mw >> 32)};
 #pragma unroll
           for (int c = 0; c < kStep; ++c)
             if (!((w[c >> 5] >> (c & 31)) & 1u)) s[c] = -INFINITY;
-          mx_raw = largest();
         }
+        float mq[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int c = 0; c < kStep; c += 8) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) mq[i] = fmax3(mq[i], s[c + 2 * i], s[c + 2 * i + 1]);
+        }
+        const float mx_raw = fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3]));
         const float mx = kPositive ? mx_raw * p.scale_log2 : mx_raw;
         // lazy rescale; tcgen05.ld/st are warp-wide, so the warp rescales together when any
         // of its rows needs it (the others by 1), once the output product before is done
