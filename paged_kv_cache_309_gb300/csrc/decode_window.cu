@@ -45,11 +45,12 @@ namespace pa_detail {
 
 using namespace pa;
 using namespace decode;
-using namespace q4cut;
 using namespace pieces;
+using namespace windowcut;
 
 namespace {
 
+static_assert(kHeaderBytes == kWorkspaceHeader, "one header for all workspaces");
 constexpr int kLog2Rows = 6;  // copies are of up to 64 rows
 // A running maximum before the first score: finite, so that a score of -inf (a masked place, or an
 // infinite key) has the weight 2^(-inf - m) = 0 then too.
@@ -73,7 +74,6 @@ struct WindowRows {
 template <int NT, bool kFp8>
 struct Lay {
   static constexpr int kStages = 3;
-  static constexpr int kCtasPerSm = 2;
   static constexpr int kSlices = kFp8 ? 2 : 1;         // of 16 places per warp and tile
   static constexpr int kTile = kConsumerWarps * 16 * kSlices;
   static constexpr int kRowBytes = kFp8 ? 128 : 256;
@@ -169,7 +169,7 @@ __global__ void __launch_bounds__(kMergeThreads)
 }
 
 template <int NT, bool kFp8>
-__global__ void __launch_bounds__(kThreads, Lay<NT, kFp8>::kCtasPerSm)
+__global__ void __launch_bounds__(kThreads, kCtasPerSm)
     window_decode_kernel(const __grid_constant__ CUtensorMap tm_k,
                          const __grid_constant__ CUtensorMap tm_v,
                          const __grid_constant__ PieceParams qp, int G) {
@@ -673,49 +673,11 @@ __global__ void __launch_bounds__(kThreads, Lay<NT, kFp8>::kCtasPerSm)
   }
 }
 
-// The launch's cut and what it needs of the workspace: header, log-sum-exp partials, output
-// partials, info words.
-struct WindowPlan {
-  int32_t chunks;
-  int32_t slots;
-  bool whole;
-  size_t lse_offset, o_offset, info_offset, bytes;
-};
-
-// Cutting costs a second launch and a merge, about as much time as a CTA takes for so many
-// units; a piece's own start and end about two.
-constexpr int64_t kMergeUnits = 6;
-
 WindowPlan plan_of(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads, int32_t window,
                    int32_t num_sink, int32_t max_context_len) {
-  int sms = num_sms_current_device();
-  if (sms <= 0) sms = 148;
-  // a window of W rows and S first tokens touch at most W + S rows and what the pieces at
-  // their ends hold besides
-  const int64_t most = min64(static_cast<int64_t>(window) + num_sink + 2 * kUnit, max_context_len);
-  const int64_t units = (most + kUnit - 1) / kUnit;
-  WindowPlan w;
-  int64_t chunks = static_cast<int64_t>(sms) * Lay<1, false>::kCtasPerSm / num_kv_heads;
-  chunks = max64(min64(chunks, kMaxChunks), 1);
-  // Whole sequences where that takes no longer than an even cut with its merge, if the window
-  // makes lengths alike (contexts of twice the window and more); else only short ones.
-  // (64 sequences, window 2000, e4m3: 23 us whole, 31 cut; window 500: 9, 22)
-  const int64_t rounds = (num_seqs + chunks - 1) / chunks;
-  const int64_t piece = units + kPieceCost;
-  const bool alike = max_context_len / 2 >= static_cast<int64_t>(window) + num_sink;
-  w.whole = (alike && rounds * piece <= num_seqs * piece / chunks + kMergeUnits) ||
-            units <= kMergeUnits;
-  chunks = max64(min64(chunks, w.whole ? num_seqs : units * num_seqs), 1);
-  if (chunks == 1) w.whole = true;
-  w.chunks = static_cast<int32_t>(chunks);
-  w.slots = w.whole ? 0 : static_cast<int32_t>(chunks - 1 + min64(num_seqs, chunks - 1));
-  auto align256 = [](size_t x) { return (x + 255) / 256 * 256; };
-  const size_t rows = static_cast<size_t>(num_q_heads) * w.slots;
-  w.lse_offset = kWorkspaceHeader;
-  w.o_offset = w.lse_offset + align256(rows * 4);
-  w.info_offset = w.o_offset + rows * kD * 4;
-  w.bytes = w.info_offset + (w.whole ? 0 : static_cast<size_t>(num_kv_heads) * num_seqs * 4);
-  return w;
+  const int sms = num_sms_current_device();
+  return window_plan(sms > 0 ? sms : 148, num_seqs, num_q_heads, num_kv_heads, window, num_sink,
+                     max_context_len);
 }
 
 template <int NT, bool kFp8>
