@@ -735,9 +735,11 @@ pa_status pa_rope_and_cache(void *q_out, const void *q, const void *key, const v
  * (k_scale, v_scale NULL) or PA_FP8_E4M3 (both NULL: unit scales, or as in
  * pa_paged_decode_attention_fp8).  max_context_len: a longer context is clipped to it
  * (and to the table) and flagged PA_DEVERR_CONTEXT_CLIPPED.
- * workspace: pa_paged_window_decode_workspace_size(...) bytes for the same
- *   sizes, 256-byte aligned; its first word is the error word, the rest need not be
- *   zero.  Calls that share one must be ordered on one stream.
+ * workspace: pa_paged_window_decode_workspace_size(...) bytes, 256-byte
+ *   aligned; its first word is the error word, the rest need not be zero.  The size
+ *   never falls as num_seqs, window, num_sink or max_context_len grow, so a
+ *   workspace for the largest of them serves every smaller call over the same heads.
+ *   Calls that share one must be ordered on one stream.
  * One launch, or two where a sequence may be split over CTAs.  q values must be
  *   finite over an e4m3 cache.  Other arguments, limits and errors as there.
  * ---------------------------------------------------------------------- */

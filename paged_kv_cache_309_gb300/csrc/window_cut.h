@@ -77,15 +77,18 @@ PA_CUT_FN WindowPlan window_plan(int32_t sms, int32_t num_seqs, int32_t num_q_he
   const bool alike = max_context_len / 2 >= static_cast<int64_t>(window) + num_sink;
   w.whole = (alike && rounds * piece <= num_seqs * piece / chunks + kMergeUnits) ||
             units <= kMergeUnits;
-  chunks = max64(min64(chunks, w.whole ? num_seqs : units * num_seqs), 1);
-  if (chunks == 1) w.whole = true;
-  w.chunks = static_cast<int32_t>(chunks);
-  w.slots = w.whole ? 0 : static_cast<int32_t>(chunks - 1 + min64(num_seqs, chunks - 1));
+  const int64_t cut = max64(min64(chunks, units * num_seqs), 1);
+  if (cut == 1) w.whole = true;
+  w.chunks = static_cast<int32_t>(w.whole ? max64(min64(chunks, num_seqs), 1) : cut);
+  // The workspace is that of an even cut also where sequences stay whole: so it never shrinks as
+  // num_seqs, window, num_sink or max_context_len grow, and one of the largest batch
+  // serves all others.
+  w.slots = static_cast<int32_t>(cut - 1 + min64(num_seqs, cut - 1));
   const size_t rows = static_cast<size_t>(num_q_heads) * w.slots;
   w.lse_offset = kHeaderBytes;
   w.o_offset = w.lse_offset + (rows * 4 + 255) / 256 * 256;
   w.info_offset = w.o_offset + rows * kPartialFloats * 4;
-  w.bytes = w.info_offset + (w.whole ? 0 : static_cast<size_t>(num_kv_heads) * num_seqs * 4);
+  w.bytes = w.info_offset + static_cast<size_t>(num_kv_heads) * num_seqs * 4;
   return w;
 }
 

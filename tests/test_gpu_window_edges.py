@@ -303,3 +303,23 @@ def test_results_repeat(repeat):
     first, _ = prefill(batch, q, new, 150, 4)
     for _ in range(20):
         assert torch.equal(prefill(batch, q, new, 150, 4)[0], first)
+
+
+@pytest.mark.parametrize("cache", [BF16, E4M3])
+def test_one_workspace_for_batches_of_every_size(cache):
+    """A workspace of the largest batch, taken once, serves the smaller ones, cut or whole."""
+    need_gpu()
+    top, most, window, sink = 130, 900, 300, 4
+    ws = pa.window_decode_workspace(top, 16, 4, 128, window, sink, most)
+    ws.fill_(255)
+    ws[:4] = 0
+    r = 2.0 ** -16 if cache == BF16 else 2.0 ** -11
+    for n in (130, 64, 33, 20, 7, 1):
+        lens = np.linspace(min(n, 2) * 200, most, n).astype(int).tolist()
+        batch = Batch(lens, 4, 16, n, cache=cache)
+        q = queries(n, 16, n + 1)
+        out, _ = decode(batch, q, window, sink, ws=ws)
+        rows = sorted({0, n // 2, n - 1})
+        ref = ow.decode(q[rows].double().numpy(), *batch.values(), batch.tables[rows], batch.lens[rows], window, sink, SCALE)
+        compare(out[rows], ref, r)
+    assert pa.read_device_error(ws) == 0

@@ -140,3 +140,22 @@ def test_pieces_end_inside_the_workspace(cut):
         assert len(set(cuts[:, 6].tolist())) == len(cuts) and ((cuts[:, 6] >= 0) & (cuts[:, 6] < slots)).all()
         split += len(cuts) > 0
     assert split > 100
+
+
+def test_a_workspace_of_a_larger_batch_serves_a_smaller_one():
+    """The size never falls as sequences, window, first tokens or contexts grow."""
+    pabuild.build()
+    size = pa.library().pa_paged_window_decode_workspace_size
+    rng = np.random.default_rng(3)
+    for H, HQ in ((8, 32), (4, 32), (1, 1), (2, 32), (40, 160)):
+        for window, most in ((4096, 32768), (500, 1500), (2000, 8192), (100, 400), (5000, 5000)):
+            row = [size(B, HQ, H, 128, window, 4, most) for B in range(0, 400)]
+            assert row == sorted(row)
+            row = [size(36, HQ, H, 128, window, 4, n) for n in range(0, 20000, 50)]
+            assert row == sorted(row)
+            row = [size(36, HQ, H, 128, n, 4, most) for n in range(1, 10000, 33)]
+            assert row == sorted(row)
+    for _ in range(2000):
+        B, HQ, H, window, sink, most = sizes(rng)
+        less = [int(rng.integers(1, x + 1)) for x in (B, window, sink + 1, most)]
+        assert size(less[0], HQ, H, 128, less[1], less[2] - 1, less[3]) <= size(B, HQ, H, 128, window, sink, most)
