@@ -674,10 +674,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
 }
 
 WindowPlan plan_of(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads, int32_t window,
-                   int32_t num_sink, int32_t max_context_len) {
+                   int32_t num_sink, int32_t max_context_len, bool e4m3) {
   const int sms = num_sms_current_device();
   return window_plan(sms > 0 ? sms : 148, num_seqs, num_q_heads, num_kv_heads, window, num_sink,
-                     max_context_len);
+                     max_context_len, e4m3);
 }
 
 template <int NT, bool kFp8>
@@ -709,7 +709,9 @@ pa_status launch(const CUtensorMap& mk, const CUtensorMap& mv, const PieceParams
 
 size_t window_decode_workspace_bytes(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads,
                                      int32_t window, int32_t num_sink, int32_t max_context_len) {
-  return plan_of(num_seqs, num_q_heads, num_kv_heads, window, num_sink, max_context_len).bytes;
+  // (the size does not depend on the cache's type)
+  return plan_of(num_seqs, num_q_heads, num_kv_heads, window, num_sink, max_context_len, false)
+      .bytes;
 }
 
 pa_status launch_window_decode(const DecodeArgs& a, int32_t window, int32_t num_sink,
@@ -726,7 +728,7 @@ pa_status launch_window_decode(const DecodeArgs& a, int32_t window, int32_t num_
       !make(&mv, a.v_cache, rows, a.num_kv_heads, box_rows))
     return PA_ERR_CUDA;
   const WindowPlan w = plan_of(a.num_seqs, a.num_q_heads, a.num_kv_heads, window, num_sink,
-                               max_context_len);
+                               max_context_len, fp8);
   PieceParams q{};
   q.d = make_decode_params(a);
   uint8_t* ws = static_cast<uint8_t*>(a.workspace);

@@ -55,13 +55,44 @@ struct WindowPlan {
   size_t lse_offset, o_offset, info_offset, bytes;
 };
 
-// Cutting costs a second launch and a merge, about as much time as a CTA takes for so many
-// units; a piece's own start and end about two.
-constexpr int64_t kMergeUnits = 6;
+// Whether sequences stay whole, by the time of either way in ns.  A CTA takes kUnitTime for a
+// unit, all of them together no less than kUnitMemory for each unit of each kv head; a cut adds a
+// second launch and the merge of its partial rows.  Fitted to both ways of 4776 batches (1 .. 256
+// sequences, 1 .. 16 kv heads, 1 .. 16 query heads each, windows 300 .. 16384; rms 6 %): the
+// choice then costs 0.5 % over the better way in the mean.  Both sides, us whole / cut:
+//  * bf16, 8 kv heads, window 1000: 8 sequences 20.1 / 13.4, 20 21.4 / 21.8, 36 27.0 / 31.6,
+//    40 (a second round) 46.0 / 34.2;
+//  * e4m3, 4 kv heads, window 2000: 16 sequences 20.6 / 16.1, 48 24.3 / 25.1, 63 25.9 / 30.9,
+//    76 28.7 / 31.5, 80 49.4 / 35.2;
+//  * e4m3, 1 kv head, window 300: 72 sequences 7.5 / 15.8; bf16, 8 kv heads, window 16384: 8
+//    sequences 260 / 90.
+struct Times {
+  double unit, memory;
+};
+constexpr Times kBf16Times{1000.0, 5.0}, kE4m3Times{550.0, 2.6};
+constexpr double kMergeTime = 4800.0, kPartialTime = 0.7;
+constexpr int kShortUnits = 6;  // so few are never cut (one sequence of them: 6 us whole, 8 cut)
+
+// chunks: of a whole wave; cut: of an even cut.  units: of the longest sequence, which the window
+// makes the ordinary one.  A second round of whole sequences is uneven where some are
+// shorter after all (16384, 64 of 21 .. 49152 tokens: 697 / 513), so it has to be a short one.
+PA_CUT_FN bool stay_whole(int64_t chunks, int64_t cut, int64_t num_seqs, int64_t q_heads,
+                          int64_t kv_heads, int64_t units, bool e4m3) {
+  const Times t = e4m3 ? kE4m3Times : kBf16Times;
+  const double one = units * t.unit, all = static_cast<double>(kv_heads) * units * t.memory;
+  auto longer = [](double a, double b) { return a > b ? a : b; };
+  const int64_t full = num_seqs / chunks, rest = num_seqs % chunks;
+  const double whole =
+      full * longer(one, chunks * all) + (rest > 0 ? longer(one, rest * all) : 0.0);
+  const double merge =
+      kMergeTime + kPartialTime * q_heads * static_cast<double>(cut + min64(num_seqs, cut));
+  const double even = longer(num_seqs * one / cut, num_seqs * all) + merge;
+  return whole <= even && (num_seqs <= chunks || one <= 1.5 * merge);
+}
 
 PA_CUT_FN WindowPlan window_plan(int32_t sms, int32_t num_seqs, int32_t num_q_heads,
                                  int32_t num_kv_heads, int32_t window, int32_t num_sink,
-                                 int32_t max_context_len) {
+                                 int32_t max_context_len, bool e4m3) {
   // a window of W rows and S first tokens touch at most W + S rows and what the pieces at
   // their ends hold besides
   const int64_t most = min64(static_cast<int64_t>(window) + num_sink + 2 * kUnit, max_context_len);
@@ -69,15 +100,11 @@ PA_CUT_FN WindowPlan window_plan(int32_t sms, int32_t num_seqs, int32_t num_q_he
   WindowPlan w;
   int64_t chunks = static_cast<int64_t>(sms) * kCtasPerSm / num_kv_heads;
   chunks = max64(min64(chunks, kMaxChunks), 1);
-  // Whole sequences where that takes no longer than an even cut with its merge, if the window
-  // makes lengths alike (contexts of twice the window and more); else only short ones.
-  // (64 sequences, window 2000, e4m3: 23 us whole, 31 cut; window 500: 9, 22)
-  const int64_t rounds = (num_seqs + chunks - 1) / chunks;
-  const int64_t piece = units + kPieceCost;
-  const bool alike = max_context_len / 2 >= static_cast<int64_t>(window) + num_sink;
-  w.whole = (alike && rounds * piece <= num_seqs * piece / chunks + kMergeUnits) ||
-            units <= kMergeUnits;
   const int64_t cut = max64(min64(chunks, units * num_seqs), 1);
+  // (contexts of less than twice the window: lengths differ, and an even cut wins)
+  const bool alike = max_context_len / 2 >= static_cast<int64_t>(window) + num_sink;
+  w.whole = units <= kShortUnits ||
+            (alike && stay_whole(chunks, cut, num_seqs, num_q_heads, num_kv_heads, units, e4m3));
   if (cut == 1) w.whole = true;
   w.chunks = static_cast<int32_t>(w.whole ? max64(min64(chunks, num_seqs), 1) : cut);
   // The workspace is that of an even cut also where sequences stay whole: so it never shrinks as

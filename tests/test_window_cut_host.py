@@ -34,8 +34,8 @@ extern "C" int places(int len, int low, int sink, int log2_rpb, int32_t* row, ui
   return r.len;
 }
 extern "C" void plan(int32_t sms, int32_t B, int32_t HQ, int32_t H, int32_t window, int32_t sink, int32_t most,
-                     int64_t* out) {
-  const auto w = windowcut::window_plan(sms, B, HQ, H, window, sink, most);
+                     int32_t e4m3, int64_t* out) {
+  const auto w = windowcut::window_plan(sms, B, HQ, H, window, sink, most, e4m3);
   const int64_t row[7] = {w.chunks, w.slots, w.whole, (int64_t)w.lse_offset, (int64_t)w.o_offset,
                           (int64_t)w.info_offset, (int64_t)w.bytes};
   for (int i = 0; i < 7; ++i) out[i] = row[i];
@@ -55,7 +55,7 @@ def cut(tmp_path_factory):
     lib = ctypes.CDLL(str(d / "cut.so"))
     P, I32 = ctypes.c_void_p, ctypes.c_int32
     lib.places.argtypes = [I32] * 4 + [P, P, I32]
-    lib.plan.argtypes = [I32] * 7 + [P]
+    lib.plan.argtypes = [I32] * 8 + [P]
     lib.cut_pieces.argtypes = [P, I32, I32, I32, P, ctypes.c_int64]
     lib.cut_pieces.restype = ctypes.c_int64
     return lib
@@ -68,9 +68,9 @@ def places(cut, length, low, sink, log2_rpb):
     return row[:n], seen[:n].astype(bool)
 
 
-def plan(cut, *args):
+def plan(cut, *args, e4m3=False, sms=SMS):
     out = np.zeros(7, np.int64)
-    cut.plan(SMS, *args, out.ctypes.data)
+    cut.plan(sms, *args, e4m3, out.ctypes.data)
     return out.tolist()
 
 
@@ -116,7 +116,8 @@ def test_pieces_end_inside_the_workspace(cut):
     split = 0
     for _ in range(1500):
         B, HQ, H, window, sink, most = sizes(rng)
-        chunks, slots, whole, lse, o, info, size = plan(cut, B, HQ, H, window, sink, most)
+        chunks, slots, whole, lse, o, info, size = plan(cut, B, HQ, H, window, sink, most,
+                                                         e4m3=bool(rng.integers(2)))
         assert 1 <= chunks <= 32767 and lse >= 256 and o % 256 == 0 and info % 4 == 0
         assert lse + HQ * slots * 4 <= o and o + HQ * slots * 512 <= info
         nbytes = lib.pa_paged_window_decode_workspace_size(B, HQ, H, 128, window, sink, most)
@@ -159,3 +160,29 @@ def test_a_workspace_of_a_larger_batch_serves_a_smaller_one():
         B, HQ, H, window, sink, most = sizes(rng)
         less = [int(rng.integers(1, x + 1)) for x in (B, window, sink + 1, most)]
         assert size(less[0], HQ, H, 128, less[1], less[2] - 1, less[3]) <= size(B, HQ, H, 128, window, sink, most)
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_the_choice_does_not_flip_back(cut, e4m3):
+    """Within one wave, a batch that is cut stays cut as sequences are removed, for every window."""
+    both = 0
+    for H, HQ in ((8, 32), (8, 16), (4, 32), (2, 16), (1, 8), (1, 16), (16, 16)):
+        for window in (300, 500, 1000, 1024, 2000, 4096, 16384):
+            whole = [plan(cut, B, HQ, H, window, 4, 4 * window, e4m3=e4m3, sms=152)[2]
+                     for B in range(1, 304 // H + 1)]
+            assert whole == sorted(whole), (H, window)
+            both += 0 < sum(whole) < len(whole)
+    assert both > 20
+
+
+@pytest.mark.parametrize("e4m3,H,HQ,window,sequences", [
+    # (us whole and cut of these batches stand at the choice; the times differ by a tenth and more)
+    (False, 8, 16, 1000, {8: 0, 36: 1, 40: 0, 48: 0}),
+    (True, 4, 32, 2000, {16: 0, 60: 1, 63: 1, 64: 1, 76: 1, 80: 0, 96: 0}),
+    (True, 1, 16, 300, {56: 1, 72: 1, 128: 1}),
+    (True, 8, 16, 1000, {4: 0, 28: 1, 36: 1, 40: 0}),
+    (False, 8, 16, 16384, {1: 0, 8: 0, 24: 0, 48: 0, 80: 0}),
+])
+def test_the_choice_is_the_faster_way(cut, e4m3, H, HQ, window, sequences):
+    for B, want in sequences.items():
+        assert plan(cut, B, HQ, H, window, 4, 3 * (window + 4), e4m3=e4m3, sms=152)[2] == want, B
