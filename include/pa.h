@@ -762,7 +762,11 @@ pa_status pa_paged_window_decode_attention(
  *     t <= p  and  (t > p - window  or  t < num_sink)
  * so that a prompt's row equals the window decode call's over the same tokens.
  * Values of tokens that a row does not see do not reach it, whatever they hold; a
- * score of -infinity has no weight, and a row with no other is zero.
+ * score of -infinity has no weight, and a row with no other is zero.  An element
+ * that is not finite in the values of a token that a row sees makes that element
+ * of the row not finite.  Rows that do not see a token of such values which
+ * others of their tile see are computed twice: a few such tokens cost about half
+ * a call more, many of them (every row is computed again) up to 50 times a call.
  * window >= 1, num_sink >= 0 (else PA_ERR_INVALID); bf16 caches.
  * total_tokens: rows of q and out; new tokens behind them, or past max_q_len of
  *   their sequence, are not computed.  Rows of out that belong to no sequence are left as

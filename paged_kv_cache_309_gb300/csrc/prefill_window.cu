@@ -50,6 +50,7 @@
 // Every wait is bounded (2 s); a timeout sets an error bit, drains what was issued and
 // frees TMEM before the CTA exits.
 #include <atomic>
+#include <climits>
 
 #include "tc_ops.cuh"
 #include "window.cuh"
@@ -336,74 +337,352 @@ __device__ __forceinline__ void load_step(const CUtensorMap* tm, int row, int g,
   }
 }
 
-// One output row by plain loads, a warp to a row (lane: four head elements), over the
-// tokens that the row at position pos sees and no others.  A tile's product
-// multiplies the values of a token that one row sees and another does not by that
-// other row's weight 0, which is NaN for a value that is not finite; a row that
-// comes out NaN without a NaN among its scores is therefore made again here.  Until then
-// its first word is kAgain, a pair of NaN codes that no conversion gives.
-constexpr uint32_t kAgain = 0xFFA5FFA5u;
-__device__ __noinline__ void row_by_plain_loads(const Params& p, int b, int g, int64_t qrow,
-                                                int pos, int lane) {
-  constexpr int kAhead = 8;
-  const int32_t* bt = p.block_tables + static_cast<int64_t>(b) * p.max_blocks_per_seq;
-  const uint2 qb = __ldg(reinterpret_cast<const uint2*>(p.q + qrow) + lane);
-  const float q[4] = {__uint_as_float(qb.x << 16), __uint_as_float(qb.x & 0xFFFF0000u),
-                      __uint_as_float(qb.y << 16), __uint_as_float(qb.y & 0xFFFF0000u)};
-  float m = -INFINITY, l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
-  const int low = max(0, pos - p.window + 1);
-  const int sinks = min(p.num_sink, low);
-  const int count = sinks + pos + 1 - low;  // visible tokens; j-th: j < sinks ? j : low + j - sinks
-  for (int j0 = 0; j0 < count; j0 += kAhead) {
-    uint2 kb[kAhead], vb[kAhead];
-    bool there[kAhead];
+// ------------------------------------------------------- rows made again --
+// A tile's product multiplies the values of a token that one row sees and another does not by that
+// other row's weight 0, which is NaN for a value that is not finite.  Items with such rows are
+// marked, and when all are done the softmax warps make the rows again that do not see some token
+// of such values: the scan of an item's values finds the newest of these tokens and the oldest
+// behind the first ones, and a row sees all of them where the newest is no newer than the row and the
+// oldest not before its window.  (Such rows stay as they are.)  Tiles of 128 rows by
+// mma.sync, 16 rows to a warp, over memory that keys, values and queries have left.  Elements that are
+// not finite enter the product as 0; where a row sees one of them, whatever its weight, its
+// output takes the infinity or NaN on: two more products of ones and zeros, of the elements
+// +inf and -inf (NaN is both), say which.
+// Measured on 4 prompts of 8192 (window 4096, 32 / 8 heads; 1.16 ms without): one infinite element
+// 1.75 ms, one token of NaN 1.9, an infinite element in a first token 1.3, one in every 64th token
+// (all rows are made again) 22 to 25, all values +inf 54, all NaN 3.8 (rows of NaN are done).
+// Rows made again one by one took 214 ms for the one token.
+constexpr int kAgainPitch = 256 + 16;             // bytes between rows: eight fall into all 32 banks
+constexpr int kAgainKV = kM * kAgainPitch;        // behind the queries two buffers of keys and values
+constexpr int kAgainBuffer = 2 * kStep * kAgainPitch;
+// newest, oldest, and per buffer a stamp for every 16 keys: of the step that has such a value there
+constexpr int kAgainMisc = kAgainKV + 2 * kAgainBuffer;
+static_assert(kAgainMisc + 40 <= kStageOff, "inside the memory of queries, keys and values");
+constexpr int kSoftmaxThreads = 8 * 32;
+
+__device__ __forceinline__ void softmax_barrier() {
+  asm volatile("bar.sync 1, %0;" ::"n"(kSoftmaxThreads) : "memory");
+}
+// the same, and whether every thread came with `x`
+__device__ __forceinline__ bool softmax_all(bool x) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred a, b;\n\tsetp.ne.u32 a, %1, 0;\n\t"
+      "bar.red.and.pred b, 1, %2, a;\n\tselp.u32 %0, 1, 0, b;\n\t}"
+      : "=r"(r)
+      : "r"(x ? 1u : 0u), "n"(kSoftmaxThreads)
+      : "memory");
+  return r != 0;
+}
+// 16 bytes from global memory, or zeros, without waiting
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(there ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ bool not_finite(uint32_t pair) {
+  return (pair & 0x7F80u) == 0x7F80u || (pair & 0x7F800000u) == 0x7F800000u;
+}
+// Of a pair of bf16: finite values (others 0); ones where it is +inf or NaN; -inf or NaN
+__device__ __forceinline__ void apart(uint32_t pair, uint32_t& finite, uint32_t& up,
+                                      uint32_t& down) {
+  finite = pair;
+  up = down = 0u;
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) {
-      const int j = j0 + i;
-      const int t = j < sinks ? j : low + j - sinks;
-      const int bid = j < count ? __ldg(bt + (t >> p.log2_bs)) : -1;
-      there[i] = bid >= 0 && static_cast<int64_t>(bid) < p.num_blocks;
-      if (there[i]) {
-        const int64_t row =
-            (static_cast<int64_t>(bid) * p.block_size + (t & (p.block_size - 1))) * p.num_kv_heads +
-            g;
-        kb[i] = __ldg(reinterpret_cast<const uint2*>(p.k_cache + row * kD) + lane);
-        vb[i] = __ldg(reinterpret_cast<const uint2*>(p.v_cache + row * kD) + lane);
+  for (int h = 0; h < 2; ++h) {
+    const uint32_t x = (pair >> (16 * h)) & 0xFFFFu;
+    if ((x & 0x7F80u) == 0x7F80u) {
+      finite &= h ? 0x0000FFFFu : 0xFFFF0000u;
+      if (x != 0xFF80u) up |= 0x3F80u << (16 * h);
+      if (x != 0x7F80u) down |= 0x3F80u << (16 * h);
+    }
+  }
+}
+// one of 32 bits for an item, by its first row of q and out (in heads)
+__device__ __forceinline__ unsigned item_bit(int64_t first) {
+  return 1u << ((static_cast<uint32_t>(first) * 2654435761u) >> 27);
+}
+// A step's rows from the pieces that find_pieces gave (the same in every lane for one place)
+struct StepRows {
+  Pieces x;
+  uint64_t seen;
+  __device__ __forceinline__ StepRows(const Params& p, const Item& it, int v, int log2_rpb,
+                                      int lane)
+      : x(find_pieces(p, it, v * kStep, log2_rpb, lane)) {
+    if (x.bid < 0 || static_cast<int64_t>(x.bid) >= p.num_blocks) x.seen = 0ull;
+    const uint32_t lo = __reduce_or_sync(0xffffffffu, static_cast<uint32_t>(x.seen));
+    const uint32_t hi = __reduce_or_sync(0xffffffffu, static_cast<uint32_t>(x.seen >> 32));
+    seen = (static_cast<uint64_t>(hi) << 32) | lo;
+  }
+  // element offset of place r's row in the caches; called by whole warps
+  __device__ __forceinline__ int64_t offset(const Params& p, int r, int log2_rpb) const {
+    const int bid = __shfl_sync(0xffffffffu, x.bid, r >> log2_rpb);
+    const int row = __shfl_sync(0xffffffffu, x.row, r >> log2_rpb);
+    return ((static_cast<int64_t>(bid) * p.block_size + row + (r & ((1 << log2_rpb) - 1))) *
+                p.num_kv_heads +
+            x.g) *
+           kD;
+  }
+};
+
+// The rows of one query tile that do not see all of the tokens newest .. oldest
+__device__ __noinline__ void tile_again(const Params& p, uint8_t* smem, const Item& it, int tile,
+                                        int newest, int oldest, int& serial) {
+  const int t = threadIdx.x - (kThreads - kSoftmaxThreads);
+  const int warp = t >> 5, lane = t & 31;
+  const int G = p.group, log2_rpb = min(p.log2_bs, kLog2Rows);
+  const int tok0 = tile * p.tokens_per_tile;
+  const int toks = min(p.tokens_per_tile, it.ntok - tok0);
+  const uint32_t base = smem_u32(smem);
+  volatile int* stamps = reinterpret_cast<volatile int*>(smem + kAgainMisc) + 2;
+  const int c16 = lane & 15, half = lane >> 4;  // 16 lanes to a row of 256 bytes
+  auto row_of = [&](int r) {  // element offset of tile row r in q and out
+    return (static_cast<int64_t>(it.q_row + tok0 + r / G) * p.num_q_heads + it.g * G + r % G) * kD;
+  };
+#pragma unroll 1
+  for (int r = 2 * warp + half; r < kM; r += 16) {
+    const bool there = r / G < toks;
+    copy16(base + r * kAgainPitch + 16 * c16, p.q + (there ? row_of(r) + 8 * c16 : 0), there);
+  }
+  // this warp's eight rows of a step's keys and values
+  auto request = [&](int v, const StepRows& s) {
+    const uint32_t dst = base + kAgainKV + (v & 1) * kAgainBuffer + 16 * c16;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int r = 8 * warp + 2 * k + half;
+      const int64_t at = s.offset(p, r, log2_rpb);
+      const bool there = (s.seen >> r) & 1ull;
+      copy16(dst + r * kAgainPitch, p.k_cache + (there ? at + 8 * c16 : 0), there);
+      copy16(dst + (kStep + r) * kAgainPitch, p.v_cache + (there ? at + 8 * c16 : 0), there);
+    }
+  };
+  // rows 16 warp + lane / 4 and eight more of the tile: this lane's
+  const int gq = lane >> 2, tq = lane & 3;
+  int pos[2];
+  bool again[2];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const int r = 16 * warp + gq + 8 * j;
+    pos[j] = it.pos0 + tok0 + r / G;
+    again[j] = r / G < toks && (newest > pos[j] || oldest <= pos[j] - p.window);
+  }
+  float o[16][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+#pragma unroll
+  for (int n = 0; n < 16; ++n)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[n][i] = 0.f;
+  const int lo8 = lane & 7, hi8 = (lane >> 3) & 1;
+  const uint32_t q_addr = base + (16 * warp + lo8 + 8 * hi8) * kAgainPitch + 16 * half;
+  const uint32_t k_row = (lo8 + 8 * half) * kAgainPitch + 16 * hi8;
+  const uint32_t v_row = (kStep + lo8 + 8 * hi8) * kAgainPitch + 16 * half;
+
+  StepRows next(p, it, 0, log2_rpb, lane);
+  uint64_t seen = next.seen;
+  request(0, next);
+  asm volatile("cp.async.commit_group;" ::: "memory");
+  next = StepRows(p, it, 1, log2_rpb, lane);
+#pragma unroll 1
+  for (int v = 0; v < it.nsteps; ++v) {
+    const uint64_t seen_now = seen;
+    if (v + 1 < it.nsteps) {
+      seen = next.seen;
+      request(v + 1, next);
+      next = StepRows(p, it, v + 2, log2_rpb, lane);
+    }
+    asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 1;" ::: "memory");
+    const uint8_t* buf = smem + kAgainKV + (v & 1) * kAgainBuffer;
+    bool bad = false;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int r = 8 * warp + 2 * k + half;
+      const uint4 x = *reinterpret_cast<const uint4*>(buf + (kStep + r) * kAgainPitch + 16 * c16);
+      bad |= not_finite(x.x) || not_finite(x.y) || not_finite(x.z) || not_finite(x.w);
+    }
+    volatile int* stamp = stamps + 4 * (serial & 1);
+    ++serial;
+    if (bad) stamp[warp >> 1] = serial;
+    softmax_barrier();
+    const uint32_t at = base + kAgainKV + (v & 1) * kAgainBuffer;
+    float s[8][4];
+#pragma unroll
+    for (int n = 0; n < 8; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s[n][i] = 0.f;
+#pragma unroll
+    for (int kk = 0; kk < 8; ++kk) {
+      uint32_t a[4];
+      ldsm_x4(q_addr + 32 * kk, a);
+#pragma unroll
+      for (int n = 0; n < 4; ++n) {
+        uint32_t b[4];
+        ldsm_x4(at + k_row + 16 * n * kAgainPitch + 32 * kk, b);
+        mma_bf16_16816(s[2 * n], a, b[0], b[1]);
+        mma_bf16_16816(s[2 * n + 1], a, b[2], b[3]);
       }
     }
+    // which of the step's places this lane's rows see (as in the first pass)
+    const int k0 = v * kStep;
+    uint64_t mw[2];
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) {
-      if (!there[i]) continue;  // the same in every lane
-      float s =
-          q[0] * __uint_as_float(kb[i].x << 16) + q[1] * __uint_as_float(kb[i].x & 0xFFFF0000u) +
-          q[2] * __uint_as_float(kb[i].y << 16) + q[3] * __uint_as_float(kb[i].y & 0xFFFF0000u);
-#pragma unroll
-      for (int off = 16; off >= 1; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-      s *= p.scale_log2;
-      if (s > m) {
-        const float corr = exp2f(m - s);
-        l *= corr;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[e] *= corr;
-        m = s;
-      }
-      const float w = s == -INFINITY ? 0.f : exp2f(s - m);
-      l += w;
-      o[0] += w * __uint_as_float(vb[i].x << 16);
-      o[1] += w * __uint_as_float(vb[i].x & 0xFFFF0000u);
-      o[2] += w * __uint_as_float(vb[i].y << 16);
-      o[3] += w * __uint_as_float(vb[i].y & 0xFFFF0000u);
+    for (int j = 0; j < 2; ++j) {
+      const int low = pos[j] - p.window + 1;
+      mw[j] = seen_now & WindowRange::below(pos[j] + 1 - k0) &
+              (~WindowRange::below(low - k0) | WindowRange::below(p.num_sink - k0));
     }
-    // (a row that sees a token of NaN values is NaN: done)
-    const bool all_nan = o[0] != o[0] && o[1] != o[1] && o[2] != o[2] && o[3] != o[3];
-    if (__all_sync(0xffffffffu, all_nan)) break;
+    float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+    for (int n = 0; n < 8; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int c = 8 * n + 2 * tq + (i & 1);
+        s[n][i] = (mw[i >> 1] >> c) & 1ull ? s[n][i] * p.scale_log2 : -INFINITY;
+        mx[i >> 1] = fmaxf(mx[i >> 1], s[n][i]);
+      }
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      mx[j] = fmaxf(mx[j], __shfl_xor_sync(0xffffffffu, mx[j], 1));
+      mx[j] = fmaxf(mx[j], __shfl_xor_sync(0xffffffffu, mx[j], 2));
+      mx[j] = fmaxf(m[j], mx[j]);
+      // (no key so far: m and mx are -inf, nothing to rescale)
+      const float corr = mx[j] == m[j] ? 1.f : fast_exp2(m[j] - mx[j]);
+      m[j] = mx[j];
+      l[j] *= corr;
+#pragma unroll
+      for (int n = 0; n < 16; ++n) {
+        o[n][2 * j] *= corr;
+        o[n][2 * j + 1] *= corr;
+      }
+      if (mx[j] == -INFINITY) mx[j] = 0.f;
+    }
+#pragma unroll
+    for (int kk = 0; kk < kStep / 16; ++kk) {
+      const bool special = stamp[kk] == serial;
+      // weights of 16 keys, and ones where the row sees the key, as A operands
+      uint32_t a[4], ones[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int n = 2 * kk + (i >> 1), j = i & 1;
+        const float e0 = fast_exp2(s[n][2 * j] - mx[j]), e1 = fast_exp2(s[n][2 * j + 1] - mx[j]);
+        l[j] += e0 + e1;
+        a[i] = pack_bf16x2(e0, e1);
+        const uint32_t w = static_cast<uint32_t>(mw[j] >> (8 * n + 2 * tq));
+        ones[i] = (w & 1u ? 0x3F80u : 0u) | (w & 2u ? 0x3F800000u : 0u);
+      }
+#pragma unroll
+      for (int n = 0; n < 8; ++n) {
+        uint32_t b[4];
+        ldsm_x4_trans(at + v_row + 16 * kk * kAgainPitch + 32 * n, b);
+        if (special) {
+          uint32_t up[4], down[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) apart(b[i], b[i], up[i], down[i]);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            float plus[4] = {0.f, 0.f, 0.f, 0.f}, minus[4] = {0.f, 0.f, 0.f, 0.f};
+            mma_bf16_16816(plus, ones, up[2 * h], up[2 * h + 1]);
+            mma_bf16_16816(minus, ones, down[2 * h], down[2 * h + 1]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              if (plus[i] > 0.f) o[2 * n + h][i] += INFINITY;
+              if (minus[i] > 0.f) o[2 * n + h][i] -= INFINITY;
+            }
+          }
+        }
+        mma_bf16_16816(o[2 * n], a, b[0], b[1]);
+        mma_bf16_16816(o[2 * n + 1], a, b[2], b[3]);
+      }
+    }
+    // (the buffer is free for the step after the next; rows that are all NaN are done)
+    bool done = true;
+#pragma unroll
+    for (int n = 0; n < 16; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) done &= o[n][i] != o[n][i] || !again[i >> 1];
+    if (softmax_all(done)) break;
   }
-  uint2 r = make_uint2(0u, 0u);
-  if (l != 0.f) {
-    const float inv = 1.f / l;
-    r = make_uint2(pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv));
+  asm volatile("cp.async.wait_group 0;" ::: "memory");  // (those of a step that was not taken)
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    l[j] += __shfl_xor_sync(0xffffffffu, l[j], 1);
+    l[j] += __shfl_xor_sync(0xffffffffu, l[j], 2);
+    if (!again[j]) continue;
+    const float inv = l[j] == 0.f ? 0.f : 1.f / l[j];
+    __nv_bfloat16* dst = p.out + row_of(16 * warp + gq + 8 * j) + 2 * tq;
+#pragma unroll
+    for (int n = 0; n < 16; ++n)
+      *reinterpret_cast<uint32_t*>(dst + 8 * n) =
+          pack_bf16x2(o[n][2 * j] * inv, o[n][2 * j + 1] * inv);
   }
-  reinterpret_cast<uint2*>(p.out + qrow)[lane] = r;
+}
+
+// The marked items of this CTA, by the softmax warps.  (No arguments but the kernel's: with more of
+// them, or called before the CTA's last barrier, long prompts took 1 % and the smallest 5 %
+// more where nothing was marked.)
+__device__ __noinline__ void rows_again(const Params& p) {
+  extern __shared__ __align__(128) uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  const int* flags = reinterpret_cast<const int*>(smem + kMiscOff + 8);
+  if (threadIdx.x < kThreads - kSoftmaxThreads || flags[0] != 0) return;
+  const unsigned marked = static_cast<unsigned>(flags[1]);
+  const int t = threadIdx.x - (kThreads - kSoftmaxThreads);
+  const int warp = t >> 5, lane = t & 31;
+  const int log2_rpb = min(p.log2_bs, kLog2Rows);
+  int* misc = reinterpret_cast<int*>(smem + kAgainMisc);
+  int serial = 0;  // steps of all tiles so far, for the stamps
+  if (t < 8) misc[2 + t] = 0;
+  Walk walk(p, blockIdx.x, lane);
+  Item it;
+  while (walk.get(p, gridDim.x, lane, it)) {
+    if (it.nsteps == 0 ||
+        (marked & item_bit(static_cast<int64_t>(it.q_row) * p.num_q_heads + it.g * p.group)) == 0u)
+      continue;
+    softmax_barrier();  // (misc of the item before is read)
+    if (t == 0) {
+      misc[0] = -1;
+      misc[1] = INT_MAX;
+    }
+    softmax_barrier();
+    int newest = -1, oldest = INT_MAX;  // places of tokens with values that are not finite
+    for (int v = warp; v < it.nsteps; v += kSoftmaxThreads / 32) {
+      const StepRows rows(p, it, v, log2_rpb, lane);
+#pragma unroll 1
+      for (int r0 = 0; r0 < kStep; r0 += 16) {
+        uint4 x[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int r = r0 + 2 * k + (lane >> 4);
+          const int64_t at = rows.offset(p, r, log2_rpb);
+          x[k] = make_uint4(0u, 0u, 0u, 0u);
+          if ((rows.seen >> r) & 1ull)
+            x[k] = __ldg(reinterpret_cast<const uint4*>(p.v_cache + at) + (lane & 15));
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int place = v * kStep + r0 + 2 * k + (lane >> 4);
+          if (not_finite(x[k].x) || not_finite(x[k].y) || not_finite(x[k].z) ||
+              not_finite(x[k].w)) {
+            newest = max(newest, place);
+            if (place >= p.num_sink) oldest = min(oldest, place);
+          }
+        }
+      }
+    }
+    newest = __reduce_max_sync(0xffffffffu, newest);
+    oldest = __reduce_min_sync(0xffffffffu, oldest);
+    if (lane == 0) {
+      atomicMax(&misc[0], newest);
+      atomicMin(&misc[1], oldest);
+    }
+    softmax_barrier();
+    newest = *const_cast<volatile int*>(&misc[0]);
+    oldest = *const_cast<volatile int*>(&misc[1]);
+    for (int i = 0; i < it.nq; ++i) {
+      const int first = it.pos0 + i * p.tokens_per_tile;
+      const int last = it.pos0 + min((i + 1) * p.tokens_per_tile, it.ntok) - 1;
+      if (newest > first || oldest <= last - p.window)
+        tile_again(p, smem, it, i, newest, oldest, serial);
+    }
+  }
 }
 
 // A wait of the issuing warp that is not over at once.  A call: the loop in line at each of its
@@ -967,29 +1246,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (to >= 0) *reinterpret_cast<uint4*>(p.out + to + 64 * h + 8 * c) = x;
         }
       }
-      __syncwarp();  // (kAgain is stored after the row it marks)
-      if (nan_row && rvalid && l_run == l_run) {
-        *reinterpret_cast<uint32_t*>(p.out + qrow) = kAgain;
-        flags[1] = 1;
-      }
-    }
-    // rows marked kAgain (by their own thread) are made again, off the loop above
-    __syncwarp();
-    if (ok && *(volatile int*)&flags[1] != 0) {
-      Walk over(p, blockIdx.x, lane);
-      while (over.get(p, step, lane, it)) {
-        if (tok >= it.ntok || it.nsteps == 0) it.ntok = 0;
-        const int64_t qrow =
-            (static_cast<int64_t>(it.q_row + tok) * p.num_q_heads + it.g * G + row % G) * kD;
-        unsigned again = __ballot_sync(
-            0xffffffffu,
-            it.ntok > 0 && *reinterpret_cast<const volatile uint32_t*>(p.out + qrow) == kAgain);
-        for (; again != 0u; again &= again - 1u) {
-          const int src = __ffs(again) - 1;
-          row_by_plain_loads(p, it.b, it.g, __shfl_sync(0xffffffffu, qrow, src),
-                             __shfl_sync(0xffffffffu, it.pos0 + tok, src) + it.win.skip, lane);
-        }
-      }
+      if (nan_row && rvalid && l_run == l_run)
+        atomicOr(reinterpret_cast<unsigned*>(&flags[1]),
+                 item_bit(qrow / kD - static_cast<int64_t>(tok) * p.num_q_heads - row % G));
     }
     if (!ok && lane == 0) {
       *abort_flag = 1;
@@ -1013,6 +1272,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                  "r"(kTmemCols)
                  : "memory");
   }
+  if (flags[1] != 0) rows_again(p);
 }
 
 // [T, H_Q, 128] bf16; box = 64 elements x G heads x 128 / G tokens: the 128 rows of a

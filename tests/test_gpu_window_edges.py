@@ -323,3 +323,113 @@ def test_one_workspace_for_batches_of_every_size(cache):
         ref = ow.decode(q[rows].double().numpy(), *batch.values(), batch.tables[rows], batch.lens[rows], window, sink, SCALE)
         compare(out[rows], ref, r)
     assert pa.read_device_error(ws) == 0
+
+
+def with_bad_values(batch, rng, tokens):
+    """Sets elements of the values of `tokens` tokens a sequence to infinities and NaN; gives the caches
+    with these elements 0 and, of all elements, which are +inf or NaN and which -inf or NaN."""
+    pool = batch.pools[1]
+    for b, n in enumerate(batch.lens):
+        for t in rng.choice(int(n), min(int(n), tokens), replace=False):
+            blk = batch.tables[b, t // batch.bs]
+            if not 0 <= blk < pool.shape[0]:
+                continue
+            for _ in range(int(rng.integers(1, 4))):
+                what = float(rng.choice([np.inf, -np.inf, np.nan]))
+                h, e = int(rng.integers(batch.h)), int(rng.integers(128))
+                if rng.random() < 0.2:
+                    pool[blk, t % batch.bs, h] = what
+                else:
+                    pool[blk, t % batch.bs, h, e] = what
+    k, v = batch.values()
+    nan = np.isnan(v)
+    return [k, np.where(np.isfinite(v), v, 0.0)], (v == np.inf) | nan, (v == -np.inf) | nan
+
+
+def check_bad_values(batch, q, new, window, sink, rng, tokens, rows=80):
+    caches, up, down = with_bad_values(batch, rng, tokens)
+    out, starts = prefill(batch, q, new, window, sink)
+    pick = sorted(rng.choice(sum(new), min(sum(new), rows), replace=False).tolist())
+    ref = ow.prefill(q.double().numpy(), *caches, batch.tables, starts, batch.lens, window, sink, SCALE, set(pick))
+    g = q.shape[1] // batch.h
+    sees = np.zeros((2,) + tuple(q.shape), bool)  # whether a row's element has seen +inf, -inf
+    for b, n in enumerate(batch.lens):
+        for j in range(new[b]):
+            i = int(starts[b]) + j
+            if i not in set(pick):
+                continue
+            t = ow.visible(int(n) - new[b] + j, window, sink)
+            blk = batch.tables[b][t // batch.bs] if len(t) else np.zeros(0, int)
+            there = (blk >= 0) & (blk < up.shape[0])
+            for s, x in zip(sees, (up, down)):
+                s[i] = x[blk[there], t[there] % batch.bs].any(0).repeat(g, 0)
+    got = out[pick].double().cpu().numpy()
+    up, down = sees[0][pick], sees[1][pick]
+    assert np.isnan(got[up & down]).all()
+    assert (got[up & ~down] == np.inf).all() and (got[down & ~up] == -np.inf).all()
+    good = ~(up | down)
+    out_, mag, size, total = (x[pick] for x in ref)
+    bound = 2.0 ** -8 * np.abs(out_) + (2.0 ** -15 * size[..., None] + 2.0 ** -8 + 2.0 ** -14) * mag \
+        + 2.0 ** -24 * total[..., None]
+    err = np.abs(np.where(good, got, 0.0) - np.where(good, out_, 0.0))
+    assert np.isfinite(got[good]).all() and (err[good] <= bound[good]).all()
+    return int((~good).sum()), int(good.sum())
+
+
+@pytest.mark.parametrize("seed", range(16))
+def test_prefill_values_that_are_not_finite(seed):
+    """Single elements and whole heads of tokens, infinities of both signs and NaN: the elements of the rows
+    that see them take them on, all others are as if they were 0."""
+    rng = np.random.default_rng(500 + seed)
+    h, g = int(rng.choice([1, 2, 3])), int(rng.choice([1, 2, 4, 8, 16]))
+    bs = int(rng.choice([8, 16, 64, 256]))
+    window, sink = int(rng.choice([1, 30, 64, 200, 1000])), int(rng.choice([0, 1, 5, 70]))
+    new = [int(x) for x in rng.integers(1, 500, 3)]
+    lens = [n + int(rng.choice([0, 7, 300])) for n in new]
+    batch = Batch(lens, h, bs, seed, drop=float(rng.choice([0, 0.1])))
+    q = queries(sum(new), h * g, seed + 1)
+    bad, good = check_bad_values(batch, q, new, window, sink, rng, int(rng.choice([1, 3, 10, 1000])))
+    assert bad + good > 0
+
+
+def test_prefill_values_that_are_not_finite_over_many_items():
+    """Several items to a CTA, some of them marked; a scale below zero; more tokens than n."""
+    rng = np.random.default_rng(7)
+    lens, new = [3000, 90, 2500], [3000, 100, 1200]
+    batch = Batch(lens, 4, 16, 31)
+    bad, good = check_bad_values(batch, queries(sum(new), 16, 32), new, 700, 4, rng, 4, rows=120)
+    assert bad > 0 and good > 0
+    batch = Batch(lens, 8, 32, 33)
+    bad, good = check_bad_values(batch, queries(sum(new), 8, 34), new, 5000, 0, rng, 2, rows=60)
+    assert bad > 0 and good > 0
+
+
+def test_a_value_that_is_not_finite_does_not_make_the_call_slow():
+    """One infinite element in two prompts costs a few passes over the items at the edges of its
+    visibility; when every row that sees it was made again by itself the call took 160 times as long."""
+    need_gpu()
+    n, window, h, hq, bs = 4096, 2048, 8, 32, 16
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    kc, vc = (torch.randn((2 * n // bs, bs, h, 128), generator=gen, device="cuda").bfloat16() for _ in range(2))
+    q = torch.randn((2 * n, hq, 128), generator=gen, device="cuda").bfloat16()
+    bt = torch.arange(2 * n // bs, dtype=torch.int32, device="cuda").view(2, -1)
+    starts = torch.tensor([0, n, 2 * n], dtype=torch.int32, device="cuda")
+    lens = torch.tensor([n, n], dtype=torch.int32, device="cuda")
+    out, err = torch.empty_like(q), torch.zeros(1, dtype=torch.int32, device="cuda")
+
+    def took():
+        best = 1e9
+        for _ in range(3):
+            a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+            a.record()
+            pa.pa_paged_window_prefill_attention(out, q, kc, vc, bt, starts, lens, window, 4, SCALE, n, err)
+            b.record()
+            torch.cuda.synchronize()
+            best = min(best, a.elapsed_time(b))
+        return best
+
+    took()
+    clean = took()
+    vc[1500 // bs, 1500 % bs, :, 7] = float("inf")
+    one = took()
+    assert int(err) == 0 and one < 10 * clean + 1.0, (clean, one)
