@@ -768,6 +768,7 @@ pa_status pa_paged_window_decode_attention(
  * others of their tile see are computed twice: a few such tokens cost about half
  * a call more, many of them (every row is computed again) up to 50 times a call.
  * window >= 1, num_sink >= 0 (else PA_ERR_INVALID); bf16 caches.
+ * q and out share no memory (PA_ERR_INVALID).
  * total_tokens: rows of q and out; new tokens behind them, or past max_q_len of
  *   their sequence, are not computed.  Rows of out that belong to no sequence are left as
  *   they were.

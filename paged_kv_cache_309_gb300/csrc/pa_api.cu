@@ -35,10 +35,14 @@ namespace {
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
-// whether two arrays of `size` bytes share part of their range but not all of it
-bool partly_overlap(const void* x, const void* y, uintptr_t size) {
+// whether two arrays of `size` bytes share part of their range
+bool overlap(const void* x, const void* y, uintptr_t size) {
   const uintptr_t a = reinterpret_cast<uintptr_t>(x), b = reinterpret_cast<uintptr_t>(y);
-  return a != b && a < b + size && b < a + size;
+  return a < b + size && b < a + size;
+}
+// the same, but not all of it
+bool partly_overlap(const void* x, const void* y, uintptr_t size) {
+  return x != y && overlap(x, y, size);
 }
 
 bool is_src_dtype(pa_dtype d) { return d == PA_BF16 || d == PA_FP16 || d == PA_FP32; }
@@ -935,6 +939,9 @@ pa_status pa_paged_window_prefill_attention(
     return PA_ERR_UNSUPPORTED;
   if (!aligned(block_tables, 4) || !aligned(cu_seqlens_q, 4) || !aligned(context_lens, 4))
     return PA_ERR_ALIGN;
+  // (queries are read again for rows that are made again, after other rows are written)
+  if (overlap(out, q, static_cast<uintptr_t>(total_tokens) * num_q_heads * head_size * 2))
+    return PA_ERR_INVALID;
   return pa_detail::launch_window_prefill(
       {a, total_tokens, window_cap(window), window_cap(num_sink)},
       reinterpret_cast<cudaStream_t>(stream));

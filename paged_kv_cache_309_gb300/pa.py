@@ -983,8 +983,8 @@ def pa_paged_window_prefill_attention(out, q, k_cache, v_cache, block_tables, cu
                                       context_lens, window, num_sink, scale, max_q_len,
                                       error_word, stream=None):
     """Causal varlen prefill where the query at position p sees tokens
-    t <= p with t > p - window or t < num_sink; other arguments as for
-    pa_paged_prefill_attention."""
+    t <= p with t > p - window or t < num_sink; out shares no memory with q;
+    other arguments as for pa_paged_prefill_attention."""
     if error_word is None:
         raise ValueError("error_word is required")
     device, B, HQ, HKV, d, bs, nb, width = _window_shapes(

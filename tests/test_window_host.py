@@ -141,3 +141,12 @@ def test_places_cover_what_is_seen():
         assert rows == sorted(set(rows)) and (not rows or rows[-1] == length - 1)
         assert set(ow.visible(length - 1, window, sink).tolist()) <= set(rows)
         assert places <= window + sink + 2 * 64
+
+
+def test_window_prefill_refuses_outputs_over_its_queries(lib):
+    """Rows beside values that are not finite are made from their queries a second time, after others
+    are written: in place they would come out wrong."""
+    size = 256 * 32 * 128 * 2
+    q = 1 << 28
+    for out in (q, q + size - 256, q - size + 256, q + 256):
+        assert _prefill(lib, q=P(q), out=P(out)) == INVALID
