@@ -740,6 +740,7 @@ pa_status pa_rope_and_cache(void *q_out, const void *q, const void *key, const v
  *   never falls as num_seqs, window, num_sink or max_context_len grow, so a
  *   workspace for the largest of them serves every smaller call over the same heads.
  *   Calls that share one must be ordered on one stream.
+ * num_seqs 0: PA_OK, nothing to do; pointers may be NULL.
  * One launch, or two where a sequence may be split over CTAs.  q values must be
  *   finite over an e4m3 cache.  Other arguments, limits and errors as there.
  * ---------------------------------------------------------------------- */
@@ -771,7 +772,8 @@ pa_status pa_paged_window_decode_attention(
  * q and out share no memory (PA_ERR_INVALID).
  * total_tokens: rows of q and out; new tokens behind them, or past max_q_len of
  *   their sequence, are not computed.  Rows of out that belong to no sequence are left as
- *   they were.
+ *   they were.  total_tokens 0 (or num_seqs or max_q_len 0): PA_OK, nothing to do;
+ *   pointers may be NULL.
  * max_blocks_per_seq * block_size above 2^30, total_tokens of 2^31 or more, or
  *   total_tokens * num_q_heads / 256 + num_seqs * num_kv_heads above 2^24:
  *   PA_ERR_UNSUPPORTED.  Other arguments, limits and errors as for

@@ -48,6 +48,14 @@ bool partly_overlap(const void* x, const void* y, uintptr_t size) {
 bool is_src_dtype(pa_dtype d) { return d == PA_BF16 || d == PA_FP16 || d == PA_FP32; }
 bool is_any_dtype(pa_dtype d) { return is_src_dtype(d) || d == PA_FP8_E4M3; }
 
+bool decode_sizes_valid(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads,
+                        int32_t head_size, int32_t block_size, int32_t max_blocks_per_seq,
+                        int64_t num_blocks, int32_t max_context_len) {
+  return num_seqs >= 0 && num_q_heads > 0 && num_kv_heads > 0 && head_size > 0 &&
+         block_size > 0 && max_blocks_per_seq > 0 && num_blocks > 0 && max_context_len >= 0 &&
+         max_context_len <= (1 << 30);
+}
+
 // Host-side checks shared by the decode entry points; fills *a (all but the
 // workspace) on success.
 pa_status check_decode(void* out, const void* q, const void* k_cache, const void* v_cache,
@@ -56,9 +64,8 @@ pa_status check_decode(void* out, const void* q, const void* k_cache, const void
                        int32_t num_kv_heads, int32_t head_size, int32_t block_size,
                        int32_t max_blocks_per_seq, int64_t num_blocks, float scale,
                        int32_t max_context_len, pa_detail::DecodeArgs* a, bool allow_q4 = false) {
-  if (num_seqs < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || head_size <= 0 ||
-      block_size <= 0 || max_blocks_per_seq <= 0 || num_blocks <= 0 || max_context_len < 0 ||
-      max_context_len > (1 << 30))
+  if (!decode_sizes_valid(num_seqs, num_q_heads, num_kv_heads, head_size, block_size,
+                          max_blocks_per_seq, num_blocks, max_context_len))
     return PA_ERR_INVALID;
   if (out == nullptr || q == nullptr || k_cache == nullptr || v_cache == nullptr ||
       block_tables == nullptr || context_lens == nullptr)
@@ -896,6 +903,10 @@ pa_status pa_paged_window_decode_attention(
   if (window < 1 || num_sink < 0 || (k_scale == nullptr) != (v_scale == nullptr) ||
       (k_scale != nullptr && cache_dtype != PA_FP8_E4M3))
     return PA_ERR_INVALID;
+  if (num_seqs == 0 &&
+      decode_sizes_valid(num_seqs, num_q_heads, num_kv_heads, head_size, block_size,
+                         max_blocks_per_seq, num_blocks, max_context_len))
+    return PA_OK;  // nothing to do; pointers may be null
   pa_detail::DecodeArgs a{};
   const pa_status st = check_decode(out, q, k_cache, v_cache, cache_dtype, block_tables,
                                     context_lens, num_seqs, num_q_heads, num_kv_heads, head_size,
@@ -928,6 +939,7 @@ pa_status pa_paged_window_prefill_attention(
     int32_t num_sink, float scale, int32_t max_q_len, int64_t total_tokens, unsigned* error_word,
     pa_stream_t stream) {
   if (window < 1 || num_sink < 0 || total_tokens < 0) return PA_ERR_INVALID;
+  if (total_tokens == 0) max_q_len = max_q_len < 0 ? max_q_len : 0;  // no row: nothing to do
   pa_detail::PrefillArgs a{};
   const pa_status st = check_prefill(out, q, k_cache, v_cache, cache_dtype, block_tables,
                                      cu_seqlens_q, context_lens, num_seqs, num_q_heads,

@@ -433,3 +433,23 @@ def test_a_value_that_is_not_finite_does_not_make_the_call_slow():
     vc[1500 // bs, 1500 % bs, :, 7] = float("inf")
     one = took()
     assert int(err) == 0 and one < 10 * clean + 1.0, (clean, one)
+
+
+def test_empty_batches():
+    """No sequence, no token: the calls return and write nothing (torch gives such tensors no address)."""
+    need_gpu()
+    kc, vc = (torch.zeros((4, 16, 2, 128), dtype=BF16, device="cuda") for _ in range(2))
+    i32 = dict(dtype=torch.int32, device="cuda")
+    ws = pa.window_decode_workspace(0, 8, 2, 128, 30, 4, 64)
+    none = torch.zeros((0, 8, 128), dtype=BF16, device="cuda")
+    pa.pa_paged_window_decode_attention(none.clone(), none, kc, vc, torch.zeros((0, 4), **i32), torch.zeros(0, **i32),
+                                        30, 4, SCALE, 64, ws)
+    err = torch.zeros(1, **i32)
+    pa.pa_paged_window_prefill_attention(none.clone(), none, kc, vc, torch.zeros((2, 4), **i32),
+                                         torch.zeros(3, **i32), torch.full((2,), 5, **i32), 30, 4, SCALE, 64, err)
+    pa.pa_paged_window_prefill_attention(none.clone(), none, kc, vc, torch.zeros((0, 4), **i32),
+                                         torch.zeros(1, **i32), torch.zeros(0, **i32), 30, 4, SCALE, 0, err)
+    pa.pa_rope_and_cache(none.clone(), none, none[:, :2], none[:, :2], kc, vc, torch.zeros((8, 64), device="cuda"),
+                         torch.zeros(0, dtype=torch.int64, device="cuda"), torch.zeros(0, dtype=torch.int64, device="cuda"))
+    torch.cuda.synchronize()
+    assert int(err) == 0 and pa.read_device_error(ws) == 0 and not bool(kc.any() or vc.any())

@@ -150,3 +150,17 @@ def test_window_prefill_refuses_outputs_over_its_queries(lib):
     q = 1 << 28
     for out in (q, q + size - 256, q - size + 256, q + 256):
         assert _prefill(lib, q=P(q), out=P(out)) == INVALID
+
+
+def test_empty_batches_are_nothing_to_do(lib):
+    """Tensors without an element have no address: a batch of no sequence and a prompt batch of no row
+    pass with null pointers; sizes are checked all the same."""
+    none = dict(out=None, q=None, bt=None, cl=None, ws=None, wsb=0)
+    assert _decode(lib, B=0, **none) == pa.PA_OK
+    assert _decode(lib, B=0, **none, cd=pa.PA_FP8_E4M3) == pa.PA_OK
+    for kw in (dict(HQ=0), dict(nb=0), dict(window=0), dict(sink=-1), dict(maxctx=-1), dict(ksc=FAKE)):
+        assert _decode(lib, **{**dict(B=0), **none, **kw}) == INVALID
+    assert _prefill(lib, total=0, out=None, q=None) == pa.PA_OK
+    assert _prefill(lib, total=0, out=None, q=None, B=0, bt=None, cl=None) == pa.PA_OK
+    for kw in (dict(HKV=0), dict(mql=-1), dict(window=0), dict(nb=0)):
+        assert _prefill(lib, **{**dict(total=0, out=None, q=None), **kw}) == INVALID
