@@ -761,7 +761,10 @@ pa_status pa_paged_window_decode_attention(
  * pa_paged_window_prefill_attention -- pa_paged_prefill_attention where the
  * query at position p sees only tokens
  *     t <= p  and  (t > p - window  or  t < num_sink)
- * so that a prompt's row equals the window decode call's over the same tokens.
+ * which are those that the window decode call's query sees at the same position.
+ * The two calls' rows differ by rounding: here each weight enters the second
+ * product as one bf16 (off by 2^-8 of it at most), decode carries about
+ * 16 bits of it, and sums run in another order.
  * Values of tokens that a row does not see do not reach it, whatever they hold; a
  * score of -infinity has no weight, and a row with no other is zero.  An element
  * that is not finite in the values of a token that a row sees makes that element

@@ -4,8 +4,10 @@
 //
 // What is computed: new token j of sequence b sits at position p = L_b - n_b + j
 // and attends to tokens t <= p with t > p - window or t < num_sink; query head h
-// uses kv head h / G.  fp32 online softmax in base 2, weights rounded to bf16 for
-// the second product.
+// uses kv head h / G.  fp32 online softmax in base 2, sums of weights in fp32.  Each weight is
+// rounded to one bf16 for the second product, as in the plain prefill: as two terms (decode's
+// way) it would take two products of the tensor core instead of one, a half more in all, where
+// products are what bounds a long prompt.  It costs a relative error of 0.0020 instead of 0.0015.
 //
 // An item is two query tiles of 128 rows (128 / G consecutive new tokens x the G
 // query heads of one kv head each) of one sequence; they share every key and value.
@@ -399,8 +401,8 @@ __device__ __forceinline__ void apart(uint32_t pair, uint32_t& finite, uint32_t&
   }
 }
 // one of 32 bits for an item, by its first row of q and out (in heads)
-__device__ __forceinline__ unsigned item_bit(int64_t first) {
-  return 1u << ((static_cast<uint32_t>(first) * 2654435761u) >> 27);
+__device__ __forceinline__ unsigned item_bit(uint32_t first) {
+  return 1u << ((first * 2654435761u) >> 27);
 }
 // A step's rows from the pieces that find_pieces gave (the same in every lane for one place)
 struct StepRows {
@@ -634,7 +636,8 @@ __device__ __noinline__ void rows_again(const Params& p) {
   Item it;
   while (walk.get(p, gridDim.x, lane, it)) {
     if (it.nsteps == 0 ||
-        (marked & item_bit(static_cast<int64_t>(it.q_row) * p.num_q_heads + it.g * p.group)) == 0u)
+        (marked & item_bit(static_cast<uint32_t>(it.q_row) * p.num_q_heads + it.g * p.group)) ==
+            0u)
       continue;
     softmax_barrier();  // (misc of the item before is read)
     if (t == 0) {
@@ -1248,7 +1251,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (nan_row && rvalid && l_run == l_run)
         atomicOr(reinterpret_cast<unsigned*>(&flags[1]),
-                 item_bit(qrow / kD - static_cast<int64_t>(tok) * p.num_q_heads - row % G));
+                 item_bit(static_cast<uint32_t>(qrow / kD) -
+                          static_cast<uint32_t>(tok) * p.num_q_heads - row % G));
     }
     if (!ok && lane == 0) {
       *abort_flag = 1;

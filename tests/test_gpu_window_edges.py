@@ -453,3 +453,21 @@ def test_empty_batches():
                          torch.zeros(0, dtype=torch.int64, device="cuda"), torch.zeros(0, dtype=torch.int64, device="cuda"))
     torch.cuda.synchronize()
     assert int(err) == 0 and pa.read_device_error(ws) == 0 and not bool(kc.any() or vc.any())
+
+
+@pytest.mark.parametrize("window,sink", [(1, 0), (50, 4), (300, 70), (5000, 0)])
+def test_prompt_rows_and_decode_see_the_same_tokens(window, sink):
+    """A prompt's rows beside the decode call's at the same positions: within the sum of both bounds."""
+    n, picks = 420, [0, 1, 49, 50, 51, 63, 64, 200, 299, 300, 419]
+    batch = Batch([n], 2, 16, 40)
+    q = queries(n, 8, 41)
+    x, _ = prefill(batch, q, [n], window, sink)
+    # the same tokens as a batch of contexts that end at these positions
+    batch.tables = np.repeat(batch.tables, len(picks), 0)
+    batch.lens = np.array([p + 1 for p in picks], np.int32)
+    y, _ = decode(batch, q[picks], window, sink)
+    out, mag, size, total = ow.decode(q[picks].double().numpy(), *batch.values(), batch.tables, batch.lens, window, sink,
+                                      SCALE)
+    bound = 2.0 ** -7 * np.abs(out) + (2.0 ** -14 * size[..., None] + 2.0 ** -8 + 2.0 ** -16 + 2.0 ** -13) * mag \
+        + 2.0 ** -23 * total[..., None]
+    assert (np.abs((x[picks].double() - y.double()).cpu().numpy()) <= bound).all()
