@@ -12,8 +12,8 @@
 // (q4_cut.h, decode_pieces.cuh): one wave of CTAs (two per SM), each with an equal share of all
 // sequences' units of 64 places, walking its pieces with the copy ring running on
 // across them; sequences that lie in one chunk are written directly, the
-// others' pieces are merged by a second, dependent launch.  Where every CTA takes whole
-// sequences in about the same time, nothing is cut.
+// others' pieces are merged by a second, dependent launch.  Where that would take longer than
+// whole sequences to a CTA, nothing is cut (window_cut.h).
 //
 // Per tile a producer warp looks up blocks and issues TMA copies (128-byte swizzled);
 // four consumer warps take 16 (bf16, tiles of 64) or 32 (e4m3, tiles of 128) places each:
@@ -22,15 +22,15 @@
 // bf16 terms; e4m3 codes go to fp16 (exact), q after a power of two and weights in
 // fp16, 2^7 above the running maximum's scale so that they keep 11 bits down to 2^-21 of it.
 //
-// Measured (GPU time of both launches, L2 cold):
-//  * 64 sequences of 512 .. 4096 tokens, window 1024, 8 kv heads, bf16: 45.8 us for 258 MB
+// Measured (GPU time of both launches, perf/gpu_times.py):
+//  * 64 sequences of 512 .. 4096 tokens, window 1024, 8 kv heads, bf16: 45.9 us for 258 MB
 //    (a CTA per sequence, head and range of places: 86.8);
-//  * 8 of 32768 .. 131072, window 16384, 8 kv heads: 84.3 us for 539 MB, 6.4 TB/s (127.8);
-//  * e4m3, 64 of 512 .. 8192, window 2000, 4 kv heads, whole sequences: 22.4 us for
+//  * 8 of 32768 .. 131072, window 16384, 8 kv heads: 84.4 us for 539 MB, 6.4 TB/s (127.8);
+//  * e4m3, 64 of 512 .. 8192, window 2000, 4 kv heads, whole sequences: 22.7 us for
 //    122 MB (cut and merged 33.4; a CTA per range 55.4).  Three or four CTAs an SM
 //    changed nothing;
 //  * the smallest call is a chain of launch, lengths, block ids, first copy and the join
-//    of four warps: 3.8 us.
+//    of four warps: 3.9 us.
 // A merge by whichever CTA came last instead of a second launch gained nothing.
 //
 // Every mbarrier wait is bounded (2 s); after a timeout the error bit is set, the

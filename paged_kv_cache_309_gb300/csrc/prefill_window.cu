@@ -7,7 +7,7 @@
 // uses kv head h / G.  fp32 online softmax in base 2, sums of weights in fp32.  Each weight is
 // rounded to one bf16 for the second product, as in the plain prefill: as two terms (decode's
 // way) it would take two products of the tensor core instead of one, a half more in all, where
-// products are what bounds a long prompt.  It costs a relative error of 0.0020 instead of 0.0015.
+// products are what bounds a long prompt.  It costs a relative error of 0.0022 instead of 0.0016.
 //
 // An item is two query tiles of 128 rows (128 / G consecutive new tokens x the G
 // query heads of one kv head each) of one sequence; they share every key and value.
@@ -33,17 +33,17 @@
 // cycles), 1500 beside copies and hand-overs; the softmax warps' chain of scores, maximum,
 // exponentials, weights and barriers 850 alone, 1250 and 400 of hand-overs where two
 // warps of a quarter of the SM run in step: some 1700 in all.  Warps wait for
-// instructions more than for anything else (1.9 warps an issue): loops are kept short.
-// Without the softmax's arithmetic the kernel takes 1075 us instead of 1190.
-// Measured (GPU time, L2 cold; heads q / kv):
-//  * 4 prompts of 8192, window 4096, 32 / 8: 1150 us, 1.44 PFLOP/s over visible pairs
-//    (a CTA per item and products issued from a branch of one lane: 1903);
-//  * 8 chunks of 512 behind up to 6000, window 1024, 16 / 8: 45 us (73); its 256 items
+// instructions more than for anything else (1.8 warps an issue): loops are kept short.
+// Measured (GPU time, perf/gpu_times.py; heads q / kv):
+//  * 4 prompts of 8192, window 4096, 32 / 8: 1205 us back to back (1155 after a pause), 1.37
+//    PFLOP/s over visible pairs (a CTA per item and products issued from a branch of one
+//    lane: 1903);
+//  * 8 chunks of 512 behind up to 6000, window 1024, 16 / 8: 45.5 us (73); its 256 items
 //    take two rounds of the 152 SMs;
-//  * 5 prompts of 1000 .. 6001, window 250, 16 / 2: 66 us (147): an item of five steps takes
+//  * 5 prompts of 1000 .. 6001, window 250, 16 / 2: 67 us (147): an item of five steps takes
 //    14700 cycles, 4000 of them from its last weights to the next one's first (product, rows
 //    read and written, first step), the other steps at an item's ends 2450 each;
-//  * a few short rows: 9.4 us, a chain of lengths, block ids, copies and products.
+//  * a few short rows: 9.5 us, a chain of lengths, block ids, copies and products.
 // Slower: the two warps of a quarter kept apart by a barrier (1375), the next scores read before
 // the weights are handed over (1360), both query tiles' products in one rolled body (1245),
 // rows stored straight from registers (narrow window 75), next queries brought to L2 (no gain);

@@ -15,15 +15,17 @@
 // heads), so a lane keeps the same item for every head and its 16 cosines and
 // sines are loaded once per warp.
 //
-// Bounds and what was measured (GPU time, L2 cold):
+// Bounds and what was measured (GPU time, perf/gpu_times.py):
 //  * a long batch moves bytes: 32768 tokens, 32 q and 8 kv heads of 128, bf16, take
-//    129 us for 823 MB, 6.4 TB/s.  A warp that walked over all steps of its token
+//    130 us for 823 MB, 6.3 TB/s.  A warp that walked over all steps of its token
 //    took 140 us, one that waited for position and slot before its rows' loads 185;
 //  * a short one is a chain of two loads and a store (position, table row, row
 //    out): 64 tokens, 1.9 us (3.5 us with a warp per token).  The rows
 //    are therefore loaded before the position and slot are there;
-//  * short rows that are divided into e4m3 are bound by issued instructions: 5001
-//    tokens, 12.8 us (20.2 us before pairs of sums and the steps of one kind).
+//  * 5001 tokens of 10 / 5 heads of 96 divided into e4m3 take 12.9 us (20.2 before pairs of sums
+//    and the steps of one kind): issue slots are 64 % used, by warps of which half the lanes' places
+//    hold an item (6 items in 8 lanes, heads of a kind in groups of four: 120 items a token in
+//    256 places).
 #include <type_traits>
 
 #include "pa_internal.cuh"
