@@ -57,9 +57,11 @@ struct WindowPlan {
 
 // Whether sequences stay whole, by the time of either way in ns.  A CTA takes kUnitTime for a
 // unit, all of them together no less than kUnitMemory for each unit of each kv head; a cut adds a
-// second launch and the merge of its partial rows.  Fitted to both ways of 4776 batches (1 .. 256
-// sequences, 1 .. 16 kv heads, 1 .. 16 query heads each, windows 300 .. 16384; rms 6 %): the
-// choice then costs 0.5 % over the better way in the mean.  Both sides, us whole / cut:
+// second launch and the merge of its partial rows.  Fitted to both ways of 4776 batches, timed in a
+// copy of the launch that is told which (1 .. 256 sequences, 1 .. 16 kv heads, 1 .. 16 query heads
+// each, windows 300 .. 16384, contexts of two to three windows or of any length up to three; rms
+// 6 %): the choice costs 0.4 % over the better way in the mean, more than a tenth in 0.8 % of
+// them.  Both sides, us whole / cut:
 //  * bf16, 8 kv heads, window 1000: 8 sequences 20.1 / 13.4, 20 21.4 / 21.8, 36 27.0 / 31.6,
 //    40 (a second round) 46.0 / 34.2;
 //  * e4m3, 4 kv heads, window 2000: 16 sequences 20.6 / 16.1, 48 24.3 / 25.1, 63 25.9 / 30.9,
@@ -74,8 +76,9 @@ constexpr double kMergeTime = 4800.0, kPartialTime = 0.7;
 constexpr int kShortUnits = 6;  // so few are never cut (one sequence of them: 6 us whole, 8 cut)
 
 // chunks: of a whole wave; cut: of an even cut.  units: of the longest sequence, which the window
-// makes the ordinary one.  A second round of whole sequences is uneven where some are
-// shorter after all (16384, 64 of 21 .. 49152 tokens: 697 / 513), so it has to be a short one.
+// makes the ordinary one.  Where some are shorter after all, whole sequences are uneven, a second
+// round of them more so (window 16384, 64 of 21 .. 49152 tokens: 697 / 513): what that can
+// cost, a sequence's time, is held against what a cut costs.
 PA_CUT_FN bool stay_whole(int64_t chunks, int64_t cut, int64_t num_seqs, int64_t q_heads,
                           int64_t kv_heads, int64_t units, bool e4m3) {
   const Times t = e4m3 ? kE4m3Times : kBf16Times;
@@ -87,7 +90,7 @@ PA_CUT_FN bool stay_whole(int64_t chunks, int64_t cut, int64_t num_seqs, int64_t
   const double merge =
       kMergeTime + kPartialTime * q_heads * static_cast<double>(cut + min64(num_seqs, cut));
   const double even = longer(num_seqs * one / cut, num_seqs * all) + merge;
-  return whole <= even && (num_seqs <= chunks || one <= 1.5 * merge);
+  return whole <= even && one <= (num_seqs <= chunks ? 5.0 : 1.5) * merge;
 }
 
 PA_CUT_FN WindowPlan window_plan(int32_t sms, int32_t num_seqs, int32_t num_q_heads,

@@ -182,6 +182,7 @@ def test_the_choice_does_not_flip_back(cut, e4m3):
     (True, 1, 16, 300, {56: 1, 72: 1, 128: 1}),
     (True, 8, 16, 1000, {4: 0, 28: 1, 36: 1, 40: 0}),
     (False, 8, 16, 16384, {1: 0, 8: 0, 24: 0, 48: 0, 80: 0}),
+    (True, 4, 32, 16384, {56: 0, 60: 0}),  # (of uneven contexts)
 ])
 def test_the_choice_is_the_faster_way(cut, e4m3, H, HQ, window, sequences):
     for B, want in sequences.items():
